@@ -75,6 +75,7 @@ typedef enum {
 #define PKV_DEV_ERR_POSITION 0x4 /* append position's logical block >= max_blocks_per_row */
 #define PKV_DEV_ERR_TIMEOUT 0x8  /* a bounded wait inside a kernel gave up (the call's output is invalid) */
 #define PKV_DEV_ERR_PLAN 0x10    /* a decode plan made for another launch size was passed (nothing was done) */
+#define PKV_DEV_ERR_MASK 0x20    /* a row has more drafted nodes than its mask has bits (row skipped) */
 
 /* Human-readable name of a pkv_status.  Never null; static storage. */
 const char* pkv_status_string(int status);
@@ -425,6 +426,170 @@ int paged_attention_decode_planned(void* out, const void* q, void* k_pool, void*
                                    size_t plan_bytes, void* workspace, size_t workspace_bytes,
                                    unsigned flags, int32_t* dev_err, cudaStream_t stream);
 
+/*
+ * A step of several new tokens per row, drafted as a tree (speculative
+ * decoding).  The pages have no counterpart; the definitions below are this
+ * library's.  As in paged_attention_prefill, the rows' new tokens (nodes) are
+ * packed: q_start is device int32 [rows + 1], q_start[0] = 0, row r's nodes
+ * are q_start[r] .. q_start[r+1]-1 (C_r of them, possibly 0), seq_lens[r]
+ * counts the row's tokens including them, and node i occupies the row's
+ * logical position P_r + i, P_r = seq_lens[r] - C_r.  total_q (host value)
+ * sizes the launch; nodes at and behind q_start[rows], when total_q is
+ * larger, are left alone.  A step is
+ *     paged_kv_rope_append   rotate the nodes' queries and keys, write K and V
+ *     paged_attention_tree   attend, each node to the cache and its ancestors
+ *     paged_kv_tree_commit   once the accepted path is known, move its K and V
+ *                            to positions P_r, P_r + 1, ...
+ * A row with C_r < 0, C_r > seq_lens[r] or seq_lens[r] > max_seq_len is
+ * skipped by each of them (nothing of it is written) and flagged
+ * PKV_DEV_ERR_SEQ_LEN.
+ */
+
+/* Rotary frequencies and their fixed-point form (host functions, no GPU).
+ *
+ * pkv_rope_frequencies -- freqs[i], i < rot_dim / 2: the angle in radians by
+ * which pair i turns from one position to the next.
+ *     PKV_ROPE_SCALING_NONE      f_i = base^(-2 i / rot_dim)
+ *     PKV_ROPE_SCALING_LINEAR    f_i / factor (positions interpolated)
+ *     PKV_ROPE_SCALING_BASE      f_i of base * factor^(rot_dim / (rot_dim - 2)):
+ *                                the slowest pair is interpolated by factor,
+ *                                the fastest unchanged
+ *     PKV_ROPE_SCALING_BY_PARTS  g f_i + (1 - g) f_i / factor, with
+ *                                g = clamp((n_i - low) / (high - low), 0, 1) and
+ *                                n_i = original_len f_i / 2 pi, the turns that
+ *                                pair i makes over the original context: pairs
+ *                                of more than `high` turns stay, pairs of fewer
+ *                                than `low` are interpolated
+ * rot_dim even, base > 1, factor >= 1 (unused by NONE); original_len, low <
+ * high are used by BY_PARTS alone.  PKV_ERR_INVALID_ARG otherwise.
+ *
+ * pkv_rope_rates -- rates[i] = freqs[i] / 2 pi as a fraction of a turn in 64
+ * bits (modulo a turn), the form in which paged_kv_rope_append takes the
+ * frequencies: position * rate modulo 2^64 is the angle modulo a turn with no
+ * rounding, however far the position.  Any finite frequencies may be given.
+ */
+#define PKV_ROPE_SCALING_NONE 0
+#define PKV_ROPE_SCALING_LINEAR 1
+#define PKV_ROPE_SCALING_BASE 2
+#define PKV_ROPE_SCALING_BY_PARTS 3
+int pkv_rope_frequencies(double* freqs, int rot_dim, double base, int scaling, double factor,
+                         double original_len, double low, double high);
+int pkv_rope_rates(uint64_t* rates, const double* freqs, int n);
+
+/*
+ * paged_kv_rope_append -- rotary positions on the step's queries and keys,
+ * and its keys and values written to their slots; one launch.
+ *
+ * With p = rope_positions[g] of token g (or, where rope_positions is null,
+ * its logical position) and (c, s) = mscale * (cos, sin)(p * f_i), each pair
+ * (a, b) of the first rot_dim dims of every query and key head becomes
+ * (a c - b s, a s + b c); dims from rot_dim on pass through unchanged.
+ *     PKV_ROPE_HALF         pair i is dims (i, i + rot_dim / 2)
+ *     PKV_ROPE_INTERLEAVED  pair i is dims (2 i, 2 i + 1)
+ * (In a tree rope_positions is P_r + the node's depth, its logical position
+ * P_r + its index.)  Computed in binary32 and rounded once.
+ *
+ * q: fp16, token g's heads at q + g * q_stride (elements; a multiple of 8, at
+ * least q_heads * head_dim), so q, k_new and v_new may be views of one
+ * projection's output; q_out: fp16 [total_q][q_heads][head_dim], contiguous.
+ * q_out == q is allowed when q_stride == q_heads * head_dim.  q_heads == 0
+ * (q, q_out unused) writes keys and values only.  k_new, v_new: fp16, strides
+ * likewise, at least kv_heads * head_dim.
+ * Pools: fp16 when k_scale == v_scale == null (values copied bit-exactly),
+ * else E4M3 as in paged_kv_append_fp8: a value is stored as
+ * paged_kv_append_fp8 stores it, a key as the nearest E4M3 value of the
+ * binary32 quotient of its rotated binary32 value and the scale.
+ * rates: device uint64 [rot_dim / 2] from pkv_rope_rates.  A position past the
+ * table sets PKV_DEV_ERR_POSITION and a block id out of range
+ * PKV_DEV_ERR_BLOCK_ID; that token's key and value are not written (its query
+ * is rotated).  Two tokens naming one slot is a caller error, as in
+ * paged_kv_append.
+ *
+ * head_dim a multiple of 8, rot_dim a multiple of 16 and at most head_dim and
+ * 1024, (q_heads + 2 kv_heads) * head_dim below 131072, num_blocks *
+ * block_size below 2^31 (PKV_ERR_UNSUPPORTED otherwise); all buffers 16-byte
+ * aligned.
+ */
+#define PKV_ROPE_HALF 0
+#define PKV_ROPE_INTERLEAVED 1
+int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, const float* k_scale,
+                         const float* v_scale, const int32_t* block_tables,
+                         const int32_t* seq_lens, const int32_t* q_start,
+                         const int32_t* rope_positions, const uint64_t* rates, const void* q,
+                         const void* k_new, const void* v_new, int64_t q_stride, int64_t k_stride,
+                         int64_t v_stride, int rows, int total_q, int q_heads, int kv_heads,
+                         int head_dim, int rot_dim, int layout, float mscale, int block_size,
+                         int max_blocks_per_row, int num_blocks, int max_seq_len,
+                         int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * paged_attention_tree -- attention of each row's nodes over its cached
+ * tokens and the nodes that the mask lets them see.
+ *
+ * Node i of row r (g = q_start[r] + i) sees every cached token t < P_r, and
+ * node j of its row iff j < C_r and bit j % 32 of mask[g][j / 32] is set
+ * (a node sees itself only if its own bit is set); with mask == null it sees
+ * nodes 0 .. i, a chain.  With K_t and V_t read through the row's table,
+ *     out[g][h][:] = sum_t softmax_t(scale * q[g][h] . K_t) * V_t[:]
+ * over the tokens it sees, head h reading KV head h / (q_heads / kv_heads).  A
+ * node that sees nothing gives zeros.  Tokens that a node does not see do not
+ * reach its output whatever they hold (infinities and NaN included).
+ * q, out: fp16 [total_q][q_heads][head_dim].  mask: device uint32
+ * [total_q][mask_words]; a row of more than 32 * mask_words nodes is skipped
+ * and flagged PKV_DEV_ERR_MASK.  Pools: fp16 when k_scale == v_scale == null,
+ * else E4M3 codes with one scale per KV head (as in
+ * paged_attention_decode_fp8).  A table entry out of range sets
+ * PKV_DEV_ERR_BLOCK_ID and its tokens are skipped.
+ *
+ * Supported: head_dim 128, any group q_heads / kv_heads, block_size a multiple
+ * of 16, rows <= 1024, mask_words <= 32 (PKV_ERR_UNSUPPORTED otherwise).
+ * workspace: paged_attention_tree_workspace_size(...) bytes of device memory,
+ * 256-byte aligned; see paged_attention_tree_workspace_size.
+ */
+int paged_attention_tree(void* out, const void* q, const void* k_pool, const void* v_pool,
+                         const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                         const int32_t* seq_lens, const int32_t* q_start, const uint32_t* mask,
+                         int mask_words, int rows, int total_q, int q_heads, int kv_heads,
+                         int head_dim, int block_size, float scale, int max_blocks_per_row,
+                         int num_blocks, int max_seq_len, void* workspace,
+                         size_t workspace_bytes, int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * paged_attention_tree_workspace_size -- bytes of workspace for these sizes
+ * (0 for invalid sizes).  It holds partial results of rows cut between thread
+ * blocks while a call runs; calls that share a workspace must be ordered.
+ */
+size_t paged_attention_tree_workspace_size(int rows, int total_q, int q_heads, int kv_heads,
+                                           int head_dim, int block_size);
+
+/*
+ * paged_kv_tree_commit -- the accepted path's keys and values move to the
+ * row's next positions, in every layer, and the rows' new lengths come out.
+ *
+ * path: device int32 [rows][max_path]; path[r][0 .. path_lens[r]) are the
+ * accepted nodes of row r, strictly increasing node indices below C_r.  For
+ * each j < path_lens[r], each layer and both pools, the slot of position
+ * P_r + j becomes a bit-exact copy of what the slot of P_r + path[r][j] held
+ * before the call.  new_seq_lens (may be null; must not overlap seq_lens):
+ * device int32 [rows], new_seq_lens[r] = P_r + path_lens[r].  A path that is
+ * no such list, or path_lens[r] outside [0, min(max_path, C_r)], skips the row
+ * (its new length too) and sets PKV_DEV_ERR_POSITION; a table entry out of
+ * range skips that copy and sets PKV_DEV_ERR_BLOCK_ID.  Blocks that the moved
+ * positions lie in must not be shared between rows (copy-on-write first, as
+ * for any write).
+ *
+ * Pools: [layers][num_blocks][block_size][kv_heads][head_dim] of elt_bytes
+ * (2: fp16, 1: E4M3) each, one block table for all layers; layers == 1 for a
+ * single layer's pools.  head_dim * elt_bytes a multiple of 16.
+ * pkv_bm_truncate is the block manager's side of a commit.
+ */
+int paged_kv_tree_commit(void* k_pool, void* v_pool, const int32_t* block_tables,
+                         const int32_t* seq_lens, const int32_t* q_start, const int32_t* path,
+                         const int32_t* path_lens, int32_t* new_seq_lens, int layers, int rows,
+                         int max_path, int kv_heads, int head_dim, int elt_bytes, int block_size,
+                         int max_blocks_per_row, int num_blocks, int max_seq_len,
+                         int32_t* dev_err, cudaStream_t stream);
+
 /* Bytes of the static device scratch behind paged_attention_decode_noalloc
  * (8 MiB, held by every GPU that loads the library until the process exits). */
 #define PKV_NOALLOC_WORKSPACE_BYTES ((size_t)8 << 20)
@@ -562,6 +727,13 @@ int pkv_bm_admit(pkv_block_manager* bm, int64_t seq_id, int prompt_len, int max_
  * needed and none is free, PKV_ERR_STATE past max_blocks_per_row. */
 int pkv_bm_append_slot(pkv_block_manager* bm, int64_t seq_id, int32_t* position_out,
                        int32_t* cow_src_out, int32_t* cow_dst_out);
+
+/*
+ * pkv_bm_truncate -- set the sequence's length back to new_len <= its length
+ * (PKV_ERR_INVALID_ARG otherwise): the host's side of paged_kv_tree_commit.  Its blocks stay
+ * with it, so the next pkv_bm_append_slot calls reuse them.
+ */
+int pkv_bm_truncate(pkv_block_manager* bm, int64_t seq_id, int new_len);
 
 /* Release a finished sequence: every block it references loses one
  * reference; blocks at zero go back to the free list (no data moves). */

@@ -43,13 +43,14 @@ def _L():
         L.pkv_bm_release_prefix.argtypes = [P, I32]
         L.pkv_bm_admit.argtypes = [P, I64, I, I, I32, I]
         L.pkv_bm_append_slot.argtypes = [P, I64, PI32, PI32, PI32]
+        L.pkv_bm_truncate.argtypes = [P, I64, I]
         L.pkv_bm_free.argtypes = [P, I64]
         L.pkv_bm_table.argtypes = [P, I64, P, PI32]
         L.pkv_bm_stats.argtypes = [P, ctypes.POINTER(Stats)]
         L.pkv_bm_refcount.argtypes = [P, I32, PI32]
         L.pkv_bm_inject_pop_failure.argtypes = [P, I]
         for fn in ("pkv_bm_create", "pkv_bm_register_prefix", "pkv_bm_release_prefix",
-                   "pkv_bm_admit", "pkv_bm_append_slot", "pkv_bm_free", "pkv_bm_table",
+                   "pkv_bm_admit", "pkv_bm_append_slot", "pkv_bm_truncate", "pkv_bm_free", "pkv_bm_table",
                    "pkv_bm_stats", "pkv_bm_refcount", "pkv_bm_inject_pop_failure"):
             getattr(L, fn).restype = I
         _declared = True
@@ -113,6 +114,10 @@ class BlockManager:
         _check("pkv_bm_append_slot", _L().pkv_bm_append_slot(self._h, seq_id, ctypes.byref(pos),
                                                              ctypes.byref(src), ctypes.byref(dst)))
         return pos.value, ((src.value, dst.value) if src.value >= 0 else None)
+
+    def truncate(self, seq_id: int, new_len: int) -> None:
+        """Set the sequence's length back to ``new_len`` (its blocks stay)."""
+        _check("pkv_bm_truncate", _L().pkv_bm_truncate(self._h, seq_id, new_len))
 
     def free(self, seq_id: int) -> None:
         _check("pkv_bm_free", _L().pkv_bm_free(self._h, seq_id))

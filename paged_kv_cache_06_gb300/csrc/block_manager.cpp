@@ -191,6 +191,15 @@ int pkv_bm_append_slot(pkv_block_manager* bm, int64_t seq_id, int32_t* position_
     return PKV_OK;
 }
 
+int pkv_bm_truncate(pkv_block_manager* bm, int64_t seq_id, int new_len) {
+    if (!bm) return PKV_ERR_INVALID_ARG;
+    auto it = bm->seqs.find(seq_id);
+    if (it == bm->seqs.end()) return PKV_ERR_NOT_FOUND;
+    if (new_len < 0 || new_len > it->second.len) return PKV_ERR_INVALID_ARG;
+    it->second.len = new_len;
+    return PKV_OK;
+}
+
 int pkv_bm_free(pkv_block_manager* bm, int64_t seq_id) {
     if (!bm) return PKV_ERR_INVALID_ARG;
     auto it = bm->seqs.find(seq_id);

@@ -96,6 +96,19 @@ def _declare(L: ctypes.CDLL) -> None:
     L.paged_attention_decode_planned.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, F,
                                                  I, I, I, P, S, P, S, ctypes.c_uint, P, P]
     L.paged_attention_decode_planned.restype = I
+    D, L64 = ctypes.c_double, ctypes.c_int64
+    L.pkv_rope_frequencies.argtypes = [P, I, D, I, D, D, D, D]
+    L.pkv_rope_frequencies.restype = I
+    L.pkv_rope_rates.argtypes = [P, P, I]
+    L.pkv_rope_rates.restype = I
+    L.paged_kv_rope_append.argtypes = [P] * 13 + [L64, L64, L64] + [I] * 7 + [F, I, I, I, I, P, P]
+    L.paged_kv_rope_append.restype = I
+    L.paged_attention_tree.argtypes = [P] * 10 + [I] * 7 + [F, I, I, I, P, S, P, P]
+    L.paged_attention_tree.restype = I
+    L.paged_attention_tree_workspace_size.argtypes = [I, I, I, I, I, I]
+    L.paged_attention_tree_workspace_size.restype = S
+    L.paged_kv_tree_commit.argtypes = [P] * 8 + [I] * 10 + [P, P]
+    L.paged_kv_tree_commit.restype = I
     L.pkv_debug_set_decode_hooks.argtypes = [ctypes.c_uint, P]
     L.pkv_debug_set_decode_hooks.restype = I
 
@@ -458,6 +471,263 @@ def decode_planned(out, q, k_pool, v_pool, block_tables, seq_lens, scale: float,
         plan_buf.numel(), _ptr(workspace), workspace.numel(), PKV_FLAG_PDL if pdl else 0,
         _ptr(dev_err), _stream(stream))
     _check("paged_attention_decode_planned", st)
+
+
+# ---------------------------------------------------------------------------
+# A step of several new tokens per row, drafted as a tree.  These calls run on
+# the device that holds their tensors (all on one device, checked) and, unless
+# a stream is given, on that device's current stream.
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
+
+
+class _on:
+    """Makes the device of the (name, tensor) pairs current for a launch."""
+
+    def __init__(self, *named):
+        named = [(n, t) for n, t in named if t is not None]
+        dev = named[0][1].device
+        for n, t in named:
+            if t.device != dev:
+                raise ValueError(f"{n} is on {t.device}, {named[0][0]} on {dev}")
+        self._guard = torch.cuda.device(dev)
+
+    def __enter__(self):
+        self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        return self._guard.__exit__(*exc)
+
+
+def _need_shape(t: torch.Tensor, name: str, shape) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_tokens(t: torch.Tensor, name: str, heads: int, dim: int) -> None:
+    """fp16 [tokens][heads][dim]; only the tokens may be strided (a view of a
+    projection's output)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens][{heads}][{dim}], got {tuple(t.shape)}")
+    if t.numel() and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}'s heads and dims must be contiguous")
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    # the stride of a single token means nothing
+    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
+
+
+def _need_pools(k_pool, v_pool, k_scale, v_scale, ndim: int = 4) -> None:
+    """Both pools fp16 without scales, or both E4M3 codes with both scales."""
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go together")
+    dt = torch.float16 if k_scale is None else torch.uint8
+    _need(k_pool, "k_pool", dt, ndim)
+    _need(v_pool, "v_pool", dt, ndim)
+    _need_shape(v_pool, "v_pool", k_pool.shape)
+    if k_scale is not None:
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _need(t, n, torch.float32, 1)
+            _need_shape(t, n, (k_pool.shape[-2],))
+
+
+def _need_rows(block_tables, seq_lens, q_start) -> int:
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    _need(q_start, "q_start", torch.int32, 1)
+    rows = seq_lens.shape[0]
+    if block_tables.shape[0] != rows:
+        raise ValueError("block_tables must have a row per seq_len")
+    if q_start.shape[0] != rows + 1:
+        raise ValueError("q_start must have rows + 1 entries")
+    return rows
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
+                     factor: float = 1.0, original_len: float = 0.0, low: float = 1.0,
+                     high: float = 32.0) -> torch.Tensor:
+    """pkv_rope_frequencies: radians a position of each rotated pair, as a CPU
+    float64 tensor [rot_dim // 2].  scaling: "none", "linear", "base" or
+    "by_parts" (include/paged_kv.h has the formulas)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    out = torch.empty(max(0, rot_dim // 2), dtype=torch.float64)
+    st = lib().pkv_rope_frequencies(_ptr(out), int(rot_dim), float(base), ROPE_SCALINGS[scaling],
+                                    float(factor), float(original_len), float(low), float(high))
+    _check("pkv_rope_frequencies", st)
+    return out
+
+
+def rope_rates(freqs: torch.Tensor, device="cuda") -> torch.Tensor:
+    """pkv_rope_rates: the frequencies as 64-bit fractions of a turn (int64
+    tensor on ``device`` holding the unsigned words), which rope_append takes."""
+    if freqs.dim() != 1:
+        raise ValueError(f"freqs must have 1 dim, got {tuple(freqs.shape)}")
+    f = freqs.detach().to(device="cpu", dtype=torch.float64).contiguous()
+    out = torch.empty(f.shape[0], dtype=torch.int64)
+    _check("pkv_rope_rates", lib().pkv_rope_rates(_ptr(out), _ptr(f), f.shape[0]))
+    return out.to(device)
+
+
+def rope_append(k_pool, v_pool, block_tables, seq_lens, q_start, k_new, v_new, rates,
+                max_seq_len: int, layout: str = "half", q=None, q_out=None, rope_positions=None,
+                mscale: float = 1.0, k_scale=None, v_scale=None, dev_err=None, stream=None):
+    """paged_kv_rope_append: rotary positions on the step's queries (``q`` into
+    ``q_out``; both None to leave them out) and keys, and its keys and values
+    written to the rows' blocks (FP8 pools when the scales are given).  q,
+    k_new and v_new may be strided along the tokens."""
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    _need_pools(k_pool, v_pool, k_scale, v_scale)
+    rows = _need_rows(block_tables, seq_lens, q_start)
+    nb, bs, hk, d = k_pool.shape
+    _need_tokens(k_new, "k_new", hk, d)
+    _need_tokens(v_new, "v_new", hk, d)
+    total = k_new.shape[0]
+    _need_shape(v_new, "v_new", k_new.shape)
+    _need(rates, "rates", torch.int64, 1)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    hq = 0
+    if q is not None:
+        _need(q_out, "q_out", torch.float16, 3)
+        hq = q_out.shape[1]
+        _need_shape(q_out, "q_out", (total, hq, d))
+        _need_tokens(q, "q", hq, d)
+        _need_shape(q, "q", (total, hq, d))
+    if rope_positions is not None:
+        _need(rope_positions, "rope_positions", torch.int32, 1)
+        _need_shape(rope_positions, "rope_positions", (total,))
+    _need_err(dev_err)
+    with _on(("k_pool", k_pool), ("v_pool", v_pool), ("k_scale", k_scale), ("v_scale", v_scale),
+             ("block_tables", block_tables), ("seq_lens", seq_lens), ("q_start", q_start),
+             ("k_new", k_new), ("v_new", v_new), ("rates", rates), ("q", q), ("q_out", q_out),
+             ("rope_positions", rope_positions), ("dev_err", dev_err)):
+        st = lib().paged_kv_rope_append(
+            _ptr(q_out), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), _ptr(rope_positions), _ptr(rates),
+            _ptr(q), _ptr(k_new), _ptr(v_new), 0 if q is None else _token_stride(q),
+            _token_stride(k_new), _token_stride(v_new), rows, total, hq, hk, d,
+            2 * rates.shape[0], ROPE_LAYOUTS[layout], float(mscale), bs, block_tables.shape[1], nb,
+            int(max_seq_len), _ptr(dev_err), _stream(stream))
+    _check("paged_kv_rope_append", st)
+
+
+def tree_mask(parents, q_start, words: Optional[int] = None) -> torch.Tensor:
+    """The mask of drafted trees, on the CPU: node i sees itself and its
+    ancestors.  parents: per node of the packed step, its parent's index within
+    the row (below the node's own), or -1 for a child of the cached tokens.
+    Returns int32 [total][words] (words: 32 nodes each; default as needed)."""
+    par = [int(x) for x in parents]
+    qs = [int(x) for x in q_start]
+    if not qs or qs[0] != 0 or qs[-1] != len(par) or any(b < a for a, b in zip(qs, qs[1:])):
+        raise ValueError("q_start must rise from 0 to the number of nodes")
+    most = max([b - a for a, b in zip(qs, qs[1:])], default=0)
+    need = max(1, (most + 31) // 32)
+    words = need if words is None else int(words)
+    if words < need:
+        raise ValueError(f"{most} nodes need {need} mask words, got {words}")
+    bits = []
+    for a, b in zip(qs, qs[1:]):
+        for i in range(b - a):
+            p = par[a + i]
+            if not -1 <= p < i:
+                raise ValueError(f"node {i} of a row has parent {p}")
+            bits.append((bits[a + p] if p >= 0 else 0) | (1 << i))
+    out = torch.tensor([[(x >> (32 * w)) & 0xffffffff for w in range(words)] for x in bits],
+                       dtype=torch.int64).reshape(len(bits), words)
+    return torch.where(out >= 1 << 31, out - (1 << 32), out).to(torch.int32)
+
+
+def tree_workspace_size(rows: int, total_q: int, q_heads: int, kv_heads: int, head_dim: int,
+                        block_size: int) -> int:
+    return int(lib().paged_attention_tree_workspace_size(rows, total_q, q_heads, kv_heads,
+                                                         head_dim, block_size))
+
+
+def alloc_tree_workspace(rows, total_q, q_heads, kv_heads, head_dim, block_size, device="cuda"):
+    """A zero-filled tree-attention workspace of the size the C ABI asks for."""
+    n = tree_workspace_size(rows, total_q, q_heads, kv_heads, head_dim, block_size)
+    if n == 0:
+        raise ValueError("invalid sizes for a tree workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def tree_attention(out, q, k_pool, v_pool, block_tables, seq_lens, q_start, scale: float,
+                   max_seq_len: int, workspace, mask=None, k_scale=None, v_scale=None,
+                   dev_err=None, stream=None):
+    """paged_attention_tree: each row's drafted nodes attend to its cached
+    tokens and to the nodes their mask lets them see (``mask`` None: a chain;
+    FP8 pools when the scales are given)."""
+    _need(out, "out", torch.float16, 3)
+    _need(q, "q", torch.float16, 3)
+    _need_shape(out, "out", q.shape)
+    _need_pools(k_pool, v_pool, k_scale, v_scale)
+    rows = _need_rows(block_tables, seq_lens, q_start)
+    _need(workspace, "workspace", torch.uint8, 1)
+    total, hq, d = q.shape
+    nb, bs, hk, dk = k_pool.shape
+    if dk != d:
+        raise ValueError(f"q has head_dim {d}, the pools {dk}")
+    words = 0
+    if mask is not None:
+        _need(mask, "mask", torch.int32, 2)
+        words = mask.shape[1]
+        _need_shape(mask, "mask", (total, words))
+    _need_err(dev_err)
+    with _on(("out", out), ("q", q), ("k_pool", k_pool), ("v_pool", v_pool), ("k_scale", k_scale),
+             ("v_scale", v_scale), ("block_tables", block_tables), ("seq_lens", seq_lens),
+             ("q_start", q_start), ("mask", mask), ("workspace", workspace), ("dev_err", dev_err)):
+        st = lib().paged_attention_tree(
+            _ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), _ptr(mask), words, rows, total, hq,
+            hk, d, bs, float(scale), block_tables.shape[1], nb, int(max_seq_len), _ptr(workspace),
+            workspace.numel(), _ptr(dev_err), _stream(stream))
+    _check("paged_attention_tree", st)
+
+
+def tree_commit(k_pool, v_pool, block_tables, seq_lens, q_start, path, path_lens,
+                max_seq_len: int, new_seq_lens=None, dev_err=None, stream=None):
+    """paged_kv_tree_commit: the accepted path's keys and values move to the
+    rows' next positions.  Pools: one layer's [num_blocks][block_size][kv_heads]
+    [head_dim], or all layers' with a leading [layers]; fp16, or uint8 (E4M3).
+    ``new_seq_lens`` (int32 [rows]) receives the rows' new lengths."""
+    if not isinstance(k_pool, torch.Tensor):
+        raise TypeError("k_pool must be a torch.Tensor")
+    if k_pool.dtype not in (torch.float16, torch.uint8):
+        raise TypeError(f"k_pool must be {torch.float16} or {torch.uint8}, got {k_pool.dtype}")
+    ndim = 5 if k_pool.dim() == 5 else 4
+    _need(k_pool, "k_pool", k_pool.dtype, ndim)
+    _need(v_pool, "v_pool", k_pool.dtype, ndim)
+    _need_shape(v_pool, "v_pool", k_pool.shape)
+    rows = _need_rows(block_tables, seq_lens, q_start)
+    _need(path, "path", torch.int32, 2)
+    _need(path_lens, "path_lens", torch.int32, 1)
+    if path.shape[0] != rows or path_lens.shape[0] != rows:
+        raise ValueError("path and path_lens must have a row per seq_len")
+    if new_seq_lens is not None:
+        _need(new_seq_lens, "new_seq_lens", torch.int32, 1)
+        _need_shape(new_seq_lens, "new_seq_lens", (rows,))
+    _need_err(dev_err)
+    layers = k_pool.shape[0] if ndim == 5 else 1
+    nb, bs, hk, d = k_pool.shape[-4:]
+    with _on(("k_pool", k_pool), ("v_pool", v_pool), ("block_tables", block_tables),
+             ("seq_lens", seq_lens), ("q_start", q_start), ("path", path), ("path_lens", path_lens),
+             ("new_seq_lens", new_seq_lens), ("dev_err", dev_err)):
+        st = lib().paged_kv_tree_commit(
+            _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start),
+            _ptr(path), _ptr(path_lens), _ptr(new_seq_lens), layers, rows, path.shape[1], hk, d,
+            k_pool.element_size(), bs, block_tables.shape[1], nb, int(max_seq_len), _ptr(dev_err),
+            _stream(stream))
+    _check("paged_kv_tree_commit", st)
 
 
 def check_error(dev_err: torch.Tensor, stream=None) -> int:
