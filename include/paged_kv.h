@@ -440,9 +440,9 @@ int paged_attention_decode_planned(void* out, const void* q, void* k_pool, void*
  *     paged_attention_tree   attend, each node to the cache and its ancestors
  *     paged_kv_tree_commit   once the accepted path is known, move its K and V
  *                            to positions P_r, P_r + 1, ...
- * A row with C_r < 0, C_r > seq_lens[r] or seq_lens[r] > max_seq_len is
- * skipped by each of them (nothing of it is written) and flagged
- * PKV_DEV_ERR_SEQ_LEN.
+ * A row with C_r < 0, C_r > seq_lens[r] or seq_lens[r] > max_seq_len (or, in
+ * the first two, nodes past total_q) is skipped by each of them (nothing of it
+ * is written) and flagged PKV_DEV_ERR_SEQ_LEN.
  */
 
 /* Rotary frequencies and their fixed-point form (host functions, no GPU).
@@ -556,8 +556,12 @@ int paged_attention_tree(void* out, const void* q, const void* k_pool, const voi
 
 /*
  * paged_attention_tree_workspace_size -- bytes of workspace for these sizes
- * (0 for invalid sizes).  It holds partial results of rows cut between thread
- * blocks while a call runs; calls that share a workspace must be ordered.
+ * (0 for invalid sizes): partial results of rows cut between thread blocks,
+ * and the words by which the blocks that hold one row's pieces find each other.
+ * Zero-filled once after allocation; every call that completes without
+ * PKV_DEV_ERR_TIMEOUT leaves it ready for the next (after one that timed out,
+ * zero-fill it again).  Calls that share a workspace must be ordered; calls on
+ * separate workspaces may overlap.
  */
 size_t paged_attention_tree_workspace_size(int rows, int total_q, int q_heads, int kv_heads,
                                            int head_dim, int block_size);

@@ -58,8 +58,11 @@ struct AppendArgs {
     const void* k_new;
     const void* v_new;
 };
-// Cached tiled tensor map (128-byte swizzle) over a 3-D array: dims and box
-// innermost first, strides in bytes of dims 1 and 2.
+// Tiled tensor map (128-byte swizzle) over a 3-D array: dims and box innermost
+// first, strides in bytes of dims 1 and 2.
+int encode_map_3d(const void* base, CUtensorMapDataType dtype, const int64_t dims[3],
+                  const int64_t strides[2], const int box[3], CUtensorMap* out);
+// The same, kept for later calls with the same arguments.
 int tiled_map_3d(const void* base, CUtensorMapDataType dtype, const int64_t dims[3],
                  const int64_t strides[2], const int box[3], CUtensorMap* out);
 

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
         int slot = -2, pos = 0;  // -2: the token is left alone; -1: only its keys and values are
         if (r >= 0) {
             const int q0 = p.q_start[r], C = p.q_start[r + 1] - q0, L = p.seq_lens[r];
-            if (C < 0 || L < C || L > p.limit) {
+            if (C < 0 || L < C || L > p.limit || q0 < 0 || q0 > p.total - C) {
                 if ((tid & 31) == 0) flag_error(p.dev_err, PKV_DEV_ERR_SEQ_LEN);
             } else if (g >= q0 && g - q0 < C) {
                 pos = L - C + (g - q0);

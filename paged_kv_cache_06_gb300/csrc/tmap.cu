@@ -52,6 +52,21 @@ struct MapKeyHash {
 
 }  // namespace
 
+int encode_map_3d(const void* base, CUtensorMapDataType dtype, const int64_t dims[3],
+                  const int64_t strides[2], const int box[3], CUtensorMap* out) {
+    EncodeFn enc = encode_fn();
+    if (!enc) return PKV_ERR_CUDA;
+    const cuuint64_t d[3] = {(cuuint64_t)dims[0], (cuuint64_t)dims[1], (cuuint64_t)dims[2]};
+    const cuuint64_t st[2] = {(cuuint64_t)strides[0], (cuuint64_t)strides[1]};
+    const cuuint32_t bx[3] = {(cuuint32_t)box[0], (cuuint32_t)box[1], (cuuint32_t)box[2]};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    if (enc(out, dtype, 3, const_cast<void*>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return PKV_ERR_CUDA;
+    return PKV_OK;
+}
+
 int tiled_map_3d(const void* base, CUtensorMapDataType dtype, const int64_t dims[3],
                  const int64_t strides[2], const int box[3], CUtensorMap* out) {
     static std::mutex mu;
@@ -64,17 +79,9 @@ int tiled_map_3d(const void* base, CUtensorMapDataType dtype, const int64_t dims
         *out = it->second;
         return PKV_OK;
     }
-    EncodeFn enc = encode_fn();
-    if (!enc) return PKV_ERR_CUDA;
     CUtensorMap m;
-    const cuuint64_t d[3] = {(cuuint64_t)dims[0], (cuuint64_t)dims[1], (cuuint64_t)dims[2]};
-    const cuuint64_t st[2] = {(cuuint64_t)strides[0], (cuuint64_t)strides[1]};
-    const cuuint32_t bx[3] = {(cuuint32_t)box[0], (cuuint32_t)box[1], (cuuint32_t)box[2]};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    if (enc(&m, dtype, 3, const_cast<void*>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return PKV_ERR_CUDA;
+    const int st = encode_map_3d(base, dtype, dims, strides, box, &m);
+    if (st != PKV_OK) return st;
     if (cache.size() > 4096) cache.clear();
     cache.emplace(key, m);
     *out = m;

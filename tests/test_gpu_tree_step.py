@@ -11,7 +11,9 @@ Tolerances are worst-case sums of the roundings that the operators are allowed
 * attention: with A = sum_t p_t |v_t|, weights rounded to fp16 give h A; a
   score's dot product is off by at most 130 u scale sum_d |q_d k_d| =: e, which
   moves weights and their sum by 2 e A; exponent and normalisation 8 u A; sums
-  over L tokens L u A at most; the output h |ref| + 2^-25.
+  over L tokens L u A at most; a weight below fp16's normal range is off by
+  2^-25 of the row's reference weight, sum_t |v_t| 2^-25 in all; the output
+  h |ref| + 2^-25.
 """
 import math
 
@@ -141,8 +143,9 @@ def tree_ref(step, q, seen, scale, skip=None):
         p = torch.where(l > 0, p / torch.where(l > 0, l, torch.ones_like(l)), torch.zeros_like(p))
         o, big = p @ vz, p @ vz.abs()
         e = 130 * U * abs(scale) * (x.abs() @ kz.abs().transpose(1, 2)).where(vis, torch.zeros(())).amax(-1, keepdim=True)
+        low = 2.0 ** -25 * (vis.double() @ vz.abs())
         out[a:a + n] = o.permute(1, 0, 2)
-        tol[a:a + n] = (H * o.abs() + (H + 2 * e + (8 + step.lens[r]) * U) * big + 2.0 ** -25).permute(1, 0, 2)
+        tol[a:a + n] = (H * o.abs() + (H + 2 * e + (8 + step.lens[r]) * U) * big + low + 2.0 ** -25).permute(1, 0, 2)
     return out, tol
 
 
@@ -823,5 +826,5 @@ def test_a_drafted_step_end_to_end(cuda_device, fp8):
         e = scale * ((qr.abs() + qd) @ kd.transpose(1, 2) + qd @ kr.abs().transpose(1, 2)).amax(-1, keepdim=True)
         e = e + 130 * U * scale * (qr.abs() @ kr.abs().transpose(1, 2)).amax(-1, keepdim=True)
         grow = torch.expm1(2 * e)           # every weight over the sum: within e^(2 e)
-        tol = H * want.abs() + grow * big + (1 + grow) * ((H + (8 + n) * U) * big + p @ vd) + 2.0 ** -25
+        tol = H * want.abs() + grow * big + (1 + grow) * ((H + (8 + n) * U) * big + p @ vd) + 2.0 ** -25 * (1 + v.abs().sum(1, keepdim=True))
         check(out[r:r + 1], want.permute(1, 0, 2), tol.permute(1, 0, 2), f"row {r}")
