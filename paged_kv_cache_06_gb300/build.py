@@ -1,8 +1,10 @@
-"""Build libpagedkv.so in-tree from csrc/ (nvcc for sm_103a, g++ for host code).
+"""Build libpagedkv.so in-tree from csrc/ (nvcc for sm_103a, g++ for host code),
+and the Python binding of the drafted step's calls, ``_binding.so``.
 
 Translation units compile in parallel into ``_build/`` and link into
-``paged_kv_cache_06_gb300/libpagedkv.so``.  Rebuilds only when a source or
-header is newer than the library.  Usage: ``python -m
+``paged_kv_cache_06_gb300/libpagedkv.so``; ``csrc/python/`` compiles against the
+installed torch's headers into ``_binding.so`` beside it, which links to it.
+Rebuilds only when a source or header is newer than the products.  Usage: ``python -m
 paged_kv_cache_06_gb300.build [--force]``.
 """
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libpagedkv.so")
+BINDING_SRC = os.path.join(CSRC, "python", "binding.cpp")
+BINDING_PATH = os.path.join(HERE, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -48,20 +53,36 @@ def _inputs():
     cu, cpp = sources()
     hdr = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
-    return cu + cpp + hdr
+    return cu + cpp + hdr + [BINDING_SRC]
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(BINDING_PATH)):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return any(os.path.getmtime(p) > t for p in _inputs())
+
+
+def _torch_dir() -> str:
+    """The installed torch's folder, without importing it."""
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _binding_flags():
+    torch_inc = os.path.join(_torch_dir(), "include")
+    return ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+            "-isystem", torch_inc, "-isystem", os.path.join(torch_inc, "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(_cuda_home(), "include"),
+            "-isystem", sysconfig.get_config_var("INCLUDEPY")]
 
 
 def _compile(src: str, verbose: bool, ptxas_info: bool) -> str:
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
     cuda_inc = os.path.join(_cuda_home(), "include")
-    if src.endswith(".cu"):
+    if src == BINDING_SRC:
+        cmd = [os.environ.get("CXX", "g++"), *_binding_flags(), "-c", src, "-o", obj]
+    elif src.endswith(".cu"):
         cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                "-I", INCLUDE, "-c", src, "-o", obj]
         if ptxas_info:
@@ -83,9 +104,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     cu, cpp = sources()
-    srcs = cu + cpp
+    srcs = [BINDING_SRC] + cu + cpp  # the slowest first
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose, ptxas_info), srcs))
+        binding, *objs = ex.map(lambda s: _compile(s, verbose, ptxas_info), srcs)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     lib_dir = os.path.join(_cuda_home(), "lib64")
     cmd = [_nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
@@ -94,6 +115,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if res.returncode != 0:
         raise RuntimeError(f"linking libpagedkv.so failed:\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding, "-L", HERE, "-l:libpagedkv.so",
+           "-Wl,-rpath,$ORIGIN", "-L", torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-L", lib_dir, "-lcudart", f"-Wl,-rpath,{torch_lib}", f"-Wl,-rpath,{lib_dir}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"linking _binding.so failed:\n{res.stderr}")
+    os.replace(tmp, BINDING_PATH)
     return LIB_PATH
 
 

@@ -16,6 +16,8 @@ Tensors (torch, on the GPU):
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import Optional
@@ -26,6 +28,7 @@ from . import build as _build
 
 _lock = threading.Lock()
 _lib = None
+_ext = None
 
 PKV_OK = 0
 STATUS_NAMES = {}
@@ -49,6 +52,22 @@ def lib() -> ctypes.CDLL:
             _declare(L)
             _lib = L
     return _lib
+
+
+def binding():
+    """The C++ binding module of the drafted step's calls (loads the library
+    first, which it links against)."""
+    global _ext
+    lib()
+    with _lock:
+        if _ext is None:
+            path = _build.BINDING_PATH
+            loader = importlib.machinery.ExtensionFileLoader(f"{__package__}._binding", path)
+            spec = importlib.util.spec_from_file_location(loader.name, path, loader=loader)
+            module = importlib.util.module_from_spec(spec)
+            loader.exec_module(module)
+            _ext = module
+    return _ext
 
 
 def _declare(L: ctypes.CDLL) -> None:
@@ -474,81 +493,13 @@ def decode_planned(out, q, k_pool, v_pool, block_tables, seq_lens, scale: float,
 
 
 # ---------------------------------------------------------------------------
-# A step of several new tokens per row, drafted as a tree.  These calls run on
+# A step of several new tokens per row, drafted as a tree.  These calls check
+# and unpack their arguments in the C++ binding (csrc/python/binding.cpp), run on
 # the device that holds their tensors (all on one device, checked) and, unless
 # a stream is given, on that device's current stream.
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
-
-
-class _on:
-    """Makes the device of the (name, tensor) pairs current for a launch."""
-
-    def __init__(self, *named):
-        named = [(n, t) for n, t in named if t is not None]
-        dev = named[0][1].device
-        for n, t in named:
-            if t.device != dev:
-                raise ValueError(f"{n} is on {t.device}, {named[0][0]} on {dev}")
-        self._guard = torch.cuda.device(dev)
-
-    def __enter__(self):
-        self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        return self._guard.__exit__(*exc)
-
-
-def _need_shape(t: torch.Tensor, name: str, shape) -> None:
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _need_tokens(t: torch.Tensor, name: str, heads: int, dim: int) -> None:
-    """fp16 [tokens][heads][dim]; only the tokens may be strided (a view of a
-    projection's output)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype != torch.float16:
-        raise TypeError(f"{name} must be {torch.float16}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens][{heads}][{dim}], got {tuple(t.shape)}")
-    if t.numel() and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)):
-        raise ValueError(f"{name}'s heads and dims must be contiguous")
-
-
-def _token_stride(t: torch.Tensor) -> int:
-    # the stride of a single token means nothing
-    return int(t.stride(0)) if t.shape[0] > 1 else int(t.shape[1] * t.shape[2])
-
-
-def _need_pools(k_pool, v_pool, k_scale, v_scale, ndim: int = 4) -> None:
-    """Both pools fp16 without scales, or both E4M3 codes with both scales."""
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale go together")
-    dt = torch.float16 if k_scale is None else torch.uint8
-    _need(k_pool, "k_pool", dt, ndim)
-    _need(v_pool, "v_pool", dt, ndim)
-    _need_shape(v_pool, "v_pool", k_pool.shape)
-    if k_scale is not None:
-        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _need(t, n, torch.float32, 1)
-            _need_shape(t, n, (k_pool.shape[-2],))
-
-
-def _need_rows(block_tables, seq_lens, q_start) -> int:
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    _need(q_start, "q_start", torch.int32, 1)
-    rows = seq_lens.shape[0]
-    if block_tables.shape[0] != rows:
-        raise ValueError("block_tables must have a row per seq_len")
-    if q_start.shape[0] != rows + 1:
-        raise ValueError("q_start must have rows + 1 entries")
-    return rows
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
@@ -584,41 +535,14 @@ def rope_append(k_pool, v_pool, block_tables, seq_lens, q_start, k_new, v_new, r
     ``q_out``; both None to leave them out) and keys, and its keys and values
     written to the rows' blocks (FP8 pools when the scales are given).  q,
     k_new and v_new may be strided along the tokens."""
-    if layout not in ROPE_LAYOUTS:
+    code = ROPE_LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
-    _need_pools(k_pool, v_pool, k_scale, v_scale)
-    rows = _need_rows(block_tables, seq_lens, q_start)
-    nb, bs, hk, d = k_pool.shape
-    _need_tokens(k_new, "k_new", hk, d)
-    _need_tokens(v_new, "v_new", hk, d)
-    total = k_new.shape[0]
-    _need_shape(v_new, "v_new", k_new.shape)
-    _need(rates, "rates", torch.int64, 1)
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    hq = 0
-    if q is not None:
-        _need(q_out, "q_out", torch.float16, 3)
-        hq = q_out.shape[1]
-        _need_shape(q_out, "q_out", (total, hq, d))
-        _need_tokens(q, "q", hq, d)
-        _need_shape(q, "q", (total, hq, d))
-    if rope_positions is not None:
-        _need(rope_positions, "rope_positions", torch.int32, 1)
-        _need_shape(rope_positions, "rope_positions", (total,))
-    _need_err(dev_err)
-    with _on(("k_pool", k_pool), ("v_pool", v_pool), ("k_scale", k_scale), ("v_scale", v_scale),
-             ("block_tables", block_tables), ("seq_lens", seq_lens), ("q_start", q_start),
-             ("k_new", k_new), ("v_new", v_new), ("rates", rates), ("q", q), ("q_out", q_out),
-             ("rope_positions", rope_positions), ("dev_err", dev_err)):
-        st = lib().paged_kv_rope_append(
-            _ptr(q_out), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), _ptr(rope_positions), _ptr(rates),
-            _ptr(q), _ptr(k_new), _ptr(v_new), 0 if q is None else _token_stride(q),
-            _token_stride(k_new), _token_stride(v_new), rows, total, hq, hk, d,
-            2 * rates.shape[0], ROPE_LAYOUTS[layout], float(mscale), bs, block_tables.shape[1], nb,
-            int(max_seq_len), _ptr(dev_err), _stream(stream))
-    _check("paged_kv_rope_append", st)
+    st = (_ext or binding()).rope_append(
+        k_pool, v_pool, block_tables, seq_lens, q_start, k_new, v_new, rates, max_seq_len, code, q,
+        q_out, rope_positions, mscale, k_scale, v_scale, dev_err, stream)
+    if st:
+        _check("paged_kv_rope_append", st)
 
 
 def tree_mask(parents, q_start, words: Optional[int] = None) -> torch.Tensor:
@@ -667,31 +591,11 @@ def tree_attention(out, q, k_pool, v_pool, block_tables, seq_lens, q_start, scal
     """paged_attention_tree: each row's drafted nodes attend to its cached
     tokens and to the nodes their mask lets them see (``mask`` None: a chain;
     FP8 pools when the scales are given)."""
-    _need(out, "out", torch.float16, 3)
-    _need(q, "q", torch.float16, 3)
-    _need_shape(out, "out", q.shape)
-    _need_pools(k_pool, v_pool, k_scale, v_scale)
-    rows = _need_rows(block_tables, seq_lens, q_start)
-    _need(workspace, "workspace", torch.uint8, 1)
-    total, hq, d = q.shape
-    nb, bs, hk, dk = k_pool.shape
-    if dk != d:
-        raise ValueError(f"q has head_dim {d}, the pools {dk}")
-    words = 0
-    if mask is not None:
-        _need(mask, "mask", torch.int32, 2)
-        words = mask.shape[1]
-        _need_shape(mask, "mask", (total, words))
-    _need_err(dev_err)
-    with _on(("out", out), ("q", q), ("k_pool", k_pool), ("v_pool", v_pool), ("k_scale", k_scale),
-             ("v_scale", v_scale), ("block_tables", block_tables), ("seq_lens", seq_lens),
-             ("q_start", q_start), ("mask", mask), ("workspace", workspace), ("dev_err", dev_err)):
-        st = lib().paged_attention_tree(
-            _ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_tables), _ptr(seq_lens), _ptr(q_start), _ptr(mask), words, rows, total, hq,
-            hk, d, bs, float(scale), block_tables.shape[1], nb, int(max_seq_len), _ptr(workspace),
-            workspace.numel(), _ptr(dev_err), _stream(stream))
-    _check("paged_attention_tree", st)
+    st = (_ext or binding()).tree_attention(
+        out, q, k_pool, v_pool, block_tables, seq_lens, q_start, scale, max_seq_len, workspace,
+        mask, k_scale, v_scale, dev_err, stream)
+    if st:
+        _check("paged_attention_tree", st)
 
 
 def tree_commit(k_pool, v_pool, block_tables, seq_lens, q_start, path, path_lens,
@@ -700,34 +604,11 @@ def tree_commit(k_pool, v_pool, block_tables, seq_lens, q_start, path, path_lens
     rows' next positions.  Pools: one layer's [num_blocks][block_size][kv_heads]
     [head_dim], or all layers' with a leading [layers]; fp16, or uint8 (E4M3).
     ``new_seq_lens`` (int32 [rows]) receives the rows' new lengths."""
-    if not isinstance(k_pool, torch.Tensor):
-        raise TypeError("k_pool must be a torch.Tensor")
-    if k_pool.dtype not in (torch.float16, torch.uint8):
-        raise TypeError(f"k_pool must be {torch.float16} or {torch.uint8}, got {k_pool.dtype}")
-    ndim = 5 if k_pool.dim() == 5 else 4
-    _need(k_pool, "k_pool", k_pool.dtype, ndim)
-    _need(v_pool, "v_pool", k_pool.dtype, ndim)
-    _need_shape(v_pool, "v_pool", k_pool.shape)
-    rows = _need_rows(block_tables, seq_lens, q_start)
-    _need(path, "path", torch.int32, 2)
-    _need(path_lens, "path_lens", torch.int32, 1)
-    if path.shape[0] != rows or path_lens.shape[0] != rows:
-        raise ValueError("path and path_lens must have a row per seq_len")
-    if new_seq_lens is not None:
-        _need(new_seq_lens, "new_seq_lens", torch.int32, 1)
-        _need_shape(new_seq_lens, "new_seq_lens", (rows,))
-    _need_err(dev_err)
-    layers = k_pool.shape[0] if ndim == 5 else 1
-    nb, bs, hk, d = k_pool.shape[-4:]
-    with _on(("k_pool", k_pool), ("v_pool", v_pool), ("block_tables", block_tables),
-             ("seq_lens", seq_lens), ("q_start", q_start), ("path", path), ("path_lens", path_lens),
-             ("new_seq_lens", new_seq_lens), ("dev_err", dev_err)):
-        st = lib().paged_kv_tree_commit(
-            _ptr(k_pool), _ptr(v_pool), _ptr(block_tables), _ptr(seq_lens), _ptr(q_start),
-            _ptr(path), _ptr(path_lens), _ptr(new_seq_lens), layers, rows, path.shape[1], hk, d,
-            k_pool.element_size(), bs, block_tables.shape[1], nb, int(max_seq_len), _ptr(dev_err),
-            _stream(stream))
-    _check("paged_kv_tree_commit", st)
+    st = (_ext or binding()).tree_commit(
+        k_pool, v_pool, block_tables, seq_lens, q_start, path, path_lens, max_seq_len,
+        new_seq_lens, dev_err, stream)
+    if st:
+        _check("paged_kv_tree_commit", st)
 
 
 def check_error(dev_err: torch.Tensor, stream=None) -> int:

@@ -419,13 +419,14 @@ def test_two_streams_and_captured_graphs(cuda_device):
     torch.cuda.synchronize()
     for i in range(2):
         assert torch.equal(outs[i], want[i])
-    # graphs on one workspace
+    # graphs on one workspace, of the larger step's size
+    shared = max(ws, key=lambda x: x.numel())
     graphs = []
     for i in range(2):
         outs[i].fill_(float("nan"))
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            call(i, ws[0])
+            call(i, shared)
         graphs.append(g)
     for k in range(4):
         graphs[k % 2].replay()
