@@ -8,38 +8,51 @@
 // group.  S = Q K^T, an online softmax in base 2 and 32 bits over tiles of 128
 // tokens, O += P V; the mask only touches the tiles that hold nodes.
 //
-// Work.  A unit is 128 flat rows of one (row, KV head) and walks the row's
-// tokens in 128-token tiles.  All units' 64-token granules, in (row, KV head,
-// rows, token) order, are cut into equal contiguous ranges, one per block, one
-// block per SM, whatever the mix of lengths (the host never reads them); a cut
-// that falls within a few granules of a unit's border moves to it, which spares
-// a partial result of 64 KB for a little imbalance.
+// Work.  A unit is 128 flat rows (an M block) of one (row, KV head) and walks the
+// row's tokens in 128-token tiles; a job is one tile.  The units' 64-token
+// granules, in (row, KV head, M block, token) order, are cut into equal
+// contiguous ranges, one per thread block, one block per SM, whatever the mix of
+// lengths (the host never reads them); a cut that falls within a few granules
+// of a unit's border moves to it, which spares a partial result of 64 KB for a
+// little imbalance.  Rows of several M blocks: M block m belongs to plane
+// m % planes, the blocks are shared out over the planes by their work, and each
+// plane is a sequence of its own.  Planes of equal work are walked in step, so
+// the M blocks of a row read its cache at the same time, from DRAM once: in one
+// sequence, 64 rows of 4096 tokens and 64 nodes took three times the traffic.
 //
-// Units cut over P blocks.  Each piece stores its partial result (reference
-// maxima, row sums, unnormalised output in 32 bits) and counts itself as
-// arrived.  A block walks its range from the last unit to the first, so a piece
-// that others continue is stored first, and merges last: its warps wait a
-// little for the unit's other pieces and then claim jobs (some rows by eight
-// dims), each merged over the pieces in order, so the result does not depend on
-// who does it.  The block that arrives last waits for nobody and does whatever
-// is unclaimed; the others give up after a while.  So no block's progress
-// depends on another block running, and two calls can share the GPU.  The last
-// warp to leave a unit sets its words back to zero.
+// Units cut over P blocks.  A block walks its range from the last unit to the
+// first, so a piece that others continue comes first.  It stores its partial
+// result (reference maxima, row sums, unnormalised output in 32 bits).  Of two
+// pieces the second folds the first's partial into its own result when it is
+// done: the block before, which started earlier, stored it long ago.  Of more
+// pieces each stores its partial and counts itself, and in the end each block
+// waits for its cut units' other pieces and merges its share of each (some rows
+// by some dims), over the pieces in order, so the result does not depend on
+// time.  A block that has waited
+// kHelpNs gives its share up, and the block that arrives last, which waits for
+// nobody, does what was given up: so no block's progress depends on another
+// one running, and two calls can share the GPU.  The counts return to zero by
+// themselves (a wrapping increment on arrival and one on departure).
 //
-// Warp roles (each walks the same segments):
-//   warps 0-7   softmax: warps w and w + 4 share flat rows 32 (w % 4) .. (TMEM
-//               lanes); half hf = w / 4 takes 64 of a tile's tokens and 64 of
-//               the output's dims;
+// Warp roles (each walks the same segments, a unit's part in the block's range):
+//   warps 0-7   softmax, in two groups of four that take alternate jobs: one
+//               flat row a thread (TMEM lane), its 128 scores in two halves.
+//               Both groups share the accumulator; a job's reference maximum
+//               goes to the other group as soon as it is known, before the
+//               exponentials;
 //   warp 8      queries (cp.async) and S issue;  warp 9  PV issue;
-//   fp16 pools: warp 10 K tiles, warp 11 V halves, by TMA, one box of 16, 32 or
-//               64 consecutive tokens of a page a copy;
-//   FP8 pools:  warps 10-13 load the codes, widen them (exactly) to fp16 and
-//               store them where a copy would have put them; the scales go into
-//               the score scale and the normalisation.
-// The rings (three K slots of 128 tokens, five V slots of 64) and the three S
-// buffers are those of the prefill kernel, as are the bounded waits: a block
-// that gives up flags the error, tells its other warps to stop, and lets its
-// copies in flight land before it frees tensor memory.
+//   warps 10/11 K / V by TMA, one box of 16, 32 or 64 tokens of a page a copy;
+//               fp16 pools straight into the operand rings;
+//   warps 12-15 (FP8 pools) widen the codes, exactly, from rings of their own
+//               into the operand rings; the scales go into the score scale and
+//               the normalisation.
+// A job's 128 x 128 exponentials take 1024 clocks (16 a clock and SM), its two
+// products as many; one group for all jobs also waits, loads and stores in
+// turn, 2000 clocks a job.  A wait and its commits cost an issuing warp some 150
+// clocks that nothing hides, so tiles of 64 tokens ran at half the rate.
+// Every wait is bounded: a block that gives up flags the error, tells its other
+// warps to stop, and lets its copies and products in flight finish before it
+// frees tensor memory.
 //
 // What is not seen.  Scores of tokens a flat row does not see become -inf
 // before the maximum.  A weight of zero times an infinity or NaN in V would
@@ -58,40 +71,53 @@ namespace pkv {
 namespace tree {
 using namespace tc;
 
-constexpr int kRows = 128;     // flat rows of a unit: TMEM lanes
-constexpr int kTile = 128;     // tokens of a step
-constexpr int kGranule = 64;   // tokens: the grain of the work split
-constexpr int kKSlots = 3;     // K ring, 128 tokens a slot
-constexpr int kVSlots = 5;     // V ring, 64 tokens a slot
-constexpr int kSBufs = 3;      // S buffers in TMEM
+constexpr int kRows = 128;     // flat rows of an M block: TMEM lanes
+constexpr int kTile = 128;     // tokens of a tile
+constexpr int kGrain = 64;     // tokens of a granule: the grain of the work split, and of V's slots
 constexpr int kSoftWarps = 8;
-constexpr int kSIssue = 8, kPvIssue = 9, kLoad = 10;  // warp roles
-constexpr int kConvWarps = 4;  // FP8: warps that load and widen
+constexpr int kSIssue = 8, kPvIssue = 9, kLoad = 10, kConv = 12;  // warp roles
+constexpr int kConvWarps = 4;
 constexpr int kMaxRows = 1024;
 constexpr int kMaxGrid = 192;  // blocks: one per SM, at most this many
 constexpr int kMaxWords = 32;  // mask words: up to 1024 nodes a row
-constexpr int kHeadInts = 32;  // ints between two units' words: arrived, next job, left
-constexpr int kMinGranules = 4;  // of a block's range and of a moved cut
-constexpr uint32_t kHalfQ = kRows * 128;      // 128 flat rows x 64 dims
-constexpr uint32_t kKHalf = kTile * 128;      // 128 tokens x 64 dims
-constexpr uint32_t kKSlot = 2 * kKHalf;
-constexpr uint32_t kVHalf = 64 * 128;         // 64 tokens x 64 dims
-constexpr uint32_t kVSlot = 2 * kVHalf;
+constexpr int kHeadInts = 32;  // ints between two units' words: count, then given-up blocks' bits
+constexpr int kUnitCost = 4;   // granules that a unit's queries, first scores and output cost in time
+constexpr int kMinSlack = 4;   // granules: a cut this near a unit's border moves to it
+static_assert(kMinSlack >= kUnitCost, "a cut that stays lies past the unit's fixed cost");
+constexpr uint32_t kHalfQ = kRows * 128;   // 128 flat rows x 64 dims
+constexpr uint32_t kQBlock = 2 * kHalfQ;
+constexpr uint32_t kKHalf = kTile * 128;   // 128 tokens x 64 dims
+constexpr uint32_t kKSlot = 2 * kKHalf;    // a K tile: dims lo, hi
+constexpr uint32_t kVHalf = kGrain * 128;  // 64 tokens x 64 dims
+constexpr uint32_t kVSlot = 2 * kVHalf;    // half a V tile: dims lo, hi
+constexpr uint32_t kRaw = kGrain * 128;    // a granule of codes
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0;    // S buffers [0, 128), [128, 256), [256, 384)
-constexpr uint32_t kColO = 384;  // O [384, 512)
-// A partial: m[128], l[128], then O as [32 groups of 4 dims][128 rows][4].
+// A partial of one M block: m[128], l[128], then O as [32 groups of 4 dims][128 rows][4].
 constexpr int kPartFloats = 2 * kRows + kRows * kHeadDim;
 constexpr uint64_t kHelpNs = 100000;  // how long a block waits for a unit's other pieces
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kSBufs = 3;        // S buffers of 128 columns
+constexpr uint32_t kColS = 128;  // above the accumulator's 128 columns
+
+constexpr int kPlanes = 4;  // at most
 
 template <bool kFp8>
-__host__ __device__ constexpr int threads() { return (kLoad + (kFp8 ? kConvWarps : 2)) * 32; }
+__host__ __device__ constexpr int threads() { return (kConv + (kFp8 ? kConvWarps : 0)) * 32; }
+
+// The planes: M block m of a row belongs to plane m % n; magic = 2^32 / n, rounded up.
+struct Planes {
+    int n;
+    uint32_t magic;
+    // A row's M blocks in a plane (a row has fewer than 2^28).
+    __device__ __forceinline__ int blocks(int flat, int plane) const {
+        const int m = (flat + kRows - 1) / kRows - plane;
+        return m <= 0 ? 0 : n == 1 ? m : (int)__umulhi((uint32_t)(m + n - 1), magic);
+    }
+};
 
 struct Params {
     const __half* q;
     __half* out;
-    const void* k_pool;
     const void* v_pool;
     const float* k_scale;
     const float* v_scale;
@@ -101,90 +127,154 @@ struct Params {
     const uint32_t* mask;
     int words;
     int rows, total, hq, hk, group, bs, mbpr, nb, limit;
+    Planes planes;
     int box;       // tokens per copy
     float scale;
-    int out_v8;    // out is 32-byte aligned: 32-byte stores
     float* part;   // [grid][2][kPartFloats]
     int* heads;    // [grid][kHeadInts], zero between calls: of the cut unit that starts in a block
     int32_t* dev_err;
 };
 
+// Shared memory.
+template <bool kFp8>
 struct Smem {
-    static constexpr uint32_t q = 0;                               // Q lo, Q hi
-    static constexpr uint32_t kring = q + 2 * kHalfQ;
-    static constexpr uint32_t vring = kring + kKSlots * kKSlot;
-    static constexpr uint32_t bars = vring + kVSlots * kVSlot;
-    static constexpr uint32_t tmem = bars + 40 * 8;
-    static constexpr uint32_t misc = tmem + 16;                    // first unit [8], abort flag at 7
-    static constexpr uint32_t bad = misc + 32;                     // [8] tiles: 16-token groups not to be seen
-    static constexpr uint32_t odd = bad + 32;                      // [2][kMaxWords] nodes whose V is no number
-    static constexpr uint32_t xch = odd + 2 * kMaxWords * 4;       // row maxima [2][2][128], sums [2][128]
-    static constexpr uint32_t rowc = xch + 6 * kRows * 4;          // per row: nodes
+    static constexpr int kslots = kFp8 ? 2 : 3;  // tiles
+    static constexpr int vslots = kFp8 ? 4 : 5;  // granules (4 at least: see the wait for V's tiles that hold nodes)
+    static constexpr int raws = kFp8 ? 3 : 0;    // granules of codes, of K and of V
+    static constexpr uint32_t q = 0;
+    static constexpr uint32_t kring = q + kQBlock;
+    static constexpr uint32_t vring = kring + kslots * kKSlot;
+    static constexpr uint32_t kraw = vring + vslots * kVSlot;
+    static constexpr uint32_t vraw = kraw + raws * kRaw;
+    static constexpr uint32_t bars = vraw + raws * kRaw;
+    static constexpr uint32_t tmem = bars + 64 * 8;
+    // last unit [6], range [2], abort, odd V; then of each of two cut units what this block took
+    // over of it [6], the verdict, its pieces, the first block, the count, and r, k, t
+    static constexpr uint32_t misc = tmem + 16;
+    static constexpr uint32_t bad = misc + 192;                    // [32] granules: 16-token groups not to be seen
+    static constexpr uint32_t ref = bad + 128;                     // [2] jobs' reference maxima [128]
+    static constexpr uint32_t sum = ref + 2 * kRows * 4;           // [2 groups] last references, row sums [128]
+    static constexpr uint32_t rowc = sum + 4 * kRows * 4;          // per row: nodes
     static constexpr uint32_t rowp = rowc + kMaxRows * 4;          // per row: cached tokens
-    static constexpr uint32_t rowq = rowp + kMaxRows * 4;          // per row: q_start
     // the scan's scratch lives in the K ring: it is read before the first copy is issued
     static constexpr uint32_t part = kring;
-    static constexpr uint32_t pre = part + 1024 * 4;
-    __host__ __device__ static constexpr uint32_t total() { return rowq + kMaxRows * 4 + 1024; }
+    static constexpr uint32_t total = rowp + kMaxRows * 4 + 1024;
+    static_assert(kring % 1024 == 0 && vring % 1024 == 0 && kraw % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+    static_assert(total <= 232448, "shared memory per block");
+    static_assert(kslots * kKSlot + vslots * kVSlot >= kPartFloats * 4, "a partial fits the rings");
+    static_assert(vslots >= 4, "two tiles before this one, a slot of it was filled for the last time");
+    static_assert(2 * (kslots + vslots + 2 * raws) + 3 * kSBufs + 16 <= 64, "barriers");
 };
-static_assert(Smem::kring % 1024 == 0 && Smem::vring % 1024 == 0 && (Smem::q + kHalfQ) % 1024 == 0,
-              "swizzled tiles need 1024-byte alignment");
-static_assert(Smem::pre + (kMaxRows + 1) * 4 <= Smem::kring + kKSlots * kKSlot, "scan scratch fits the K ring");
-static_assert(Smem::total() <= 232448, "shared memory per block");
 
-// A unit: flat rows 128 t .. of KV head k of row r, its first granule U and its
-// n granules.
+// a / b for 0 <= a < 2^31, 0 < b: a float quotient (off by 2^-21 of it at most,
+// 1024), that of the remainder (off by one), and the last step.
+__device__ __forceinline__ int div_of(int a, int b) {
+    const float rb = __fdividef(1.f, (float)b);
+    int q = (int)((float)a * rb);
+    q += __float2int_rn((float)(a - q * b) * rb);
+    const int r = a - q * b;
+    return r < 0 ? q - 1 : r >= b ? q + 1 : q;
+}
+
+// A unit: M block plane + planes t of KV head k of row r, its place U in the
+// plane's sequence and its n granules; there it takes n + kUnitCost.
 struct Unit {
     int r, k, t, U, n;
+    __device__ __forceinline__ int end() const { return U + n + kUnitCost; }
 };
 
-// How the granules of all units are cut: raw cut c lies at floor(W c / G); one
-// within `slack` granules of a border of the unit it falls in moves there.
+__device__ __noinline__ int cut_at(int x, int W, int G, int quo, int rem);
+
+// How a plane's sequence of units, W long, is cut over its G blocks: raw cut c lies at
+// floor(W c / G); one within `slack` of a border of its unit moves there.
 struct Split {
-    int W, G, slack;
-    __device__ __forceinline__ int raw(int c) const { return (int)((int64_t)W * c / G); }
-    __device__ __forceinline__ int moved(int x, const Unit& u) const {
-        const int d0 = x - u.U, d1 = u.U + u.n - x;
-        if (min(d0, d1) > slack) return x;
-        return d0 <= d1 ? u.U : u.U + u.n;
+    int W, G, slack, quo, rem;
+    __device__ __forceinline__ void set(int w, int blocks) {
+        W = w;
+        G = min(blocks, max(w, 1));
+        quo = W / G;
+        rem = W - quo * G;
+        slack = max(kMinSlack, quo / 16);
     }
-    // The pieces of unit u (1: whole) and the block that holds the first one.
+    __device__ __forceinline__ int raw(int c) const { return quo * c + div_of(rem * c, G); }
+    __device__ __forceinline__ int moved(int x, const Unit& u) const {
+        const int d0 = x - u.U, d1 = u.end() - x;
+        if (min(d0, d1) > slack) return x;
+        return d0 <= d1 ? u.U : u.end();
+    }
+    // The pieces of unit u (1: whole) and the plane's block that holds the first one.
     __device__ __forceinline__ int pieces(const Unit& u, int& first) const {
-        const int64_t a = u.U + slack + 1, b = u.U + u.n - slack - 1;  // cuts that stay lie in a .. b
-        const int lo = (int)((a * G + W - 1) / W), hi = (int)(((b + 1) * G + W - 1) / W) - 1;
+        const int a = u.U + slack + 1, b = u.end() - slack;  // cuts that stay lie in [a, b)
+        if (a >= b) return 1;
+        const int lo = cut_at(a, W, G, quo, rem), hi = cut_at(b, W, G, quo, rem);
         first = lo - 1;
-        return a <= b && hi >= lo ? hi - lo + 2 : 1;
+        return hi - lo + 1;
     }
 };
 
-// The units of a block's range [s0, s1), last to first; [e0, e1): the granules
-// of the present unit that lie in it.
+// The first raw cut at x or behind it: the quotient's float estimate is off by
+// one at most (there are at most kMaxGrid cuts).
+__device__ __noinline__ int cut_at(int x, int W, int G, int quo, int rem) {
+    int c = (int)__fdividef((float)x * (float)G, (float)W);
+#pragma unroll 1
+    while (c > 0 && quo * (c - 1) + div_of(rem * (c - 1), G) >= x) --c;
+#pragma unroll 1
+    while (quo * c + div_of(rem * c, G) < x) ++c;
+    return c;
+}
+
+// The unit (r, k, t, n) before a unit; out of line, once for all the roles.
+__device__ __noinline__ int4 unit_before(int4 u, int hk, int group, int plane, int n, uint32_t magic, const int* C,
+                                         const int* P) {
+    const Planes planes{n, magic};
+    if (u.z > 0) {
+        --u.z;
+        return u;
+    }
+    int nt = planes.blocks(C[u.x] * group, plane);
+    if (u.y > 0) {
+        --u.y;
+    } else {
+#pragma unroll 1
+        do {
+            --u.x;
+            nt = planes.blocks(C[u.x] * group, plane);
+        } while (nt == 0);
+        u.y = hk - 1;
+        u.w = (P[u.x] + C[u.x] + kGrain - 1) / kGrain;
+    }
+    u.z = nt - 1;
+    return u;
+}
+
+// The units of a block's range [s0, e), last to first.
 struct Walk : Unit {
-    int s0, e, hk, group;
+    int s0, e, hk, group, plane;
+    Planes planes;
     const int* C;
     const int* P;
-    __device__ __forceinline__ int g0() const { return max(s0 - U, 0); }
-    __device__ __forceinline__ int g1() const { return min(e - U, n); }
+    __device__ __forceinline__ int g0() const { return max(s0 - U - kUnitCost, 0); }
+    __device__ __forceinline__ int g1() const { return min(e - U - kUnitCost, n); }
+    __device__ __forceinline__ bool whole() const { return s0 <= U && e >= end(); }
     __device__ __forceinline__ int len() const { return P[r] + C[r]; }
-    __device__ __forceinline__ int ta() const { return g0() * kGranule; }
-    __device__ __forceinline__ int te() const { return min(g1() * kGranule, len()); }
-    __device__ __forceinline__ int flat() const { return min(kRows, C[r] * group - t * kRows); }
+    __device__ __forceinline__ int flat() const { return C[r] * group; }
+    __device__ __forceinline__ int f0() const { return (plane + planes.n * t) * kRows; }  // first flat row
+    // its tokens in the range: [ta, te)
+    __device__ __forceinline__ int ta() const { return g0() * kGrain; }
+    __device__ __forceinline__ int te() const { return min(g1() * kGrain, len()); }
+    // step to the unit before
+    __device__ __forceinline__ void back() {
+        const int4 v = unit_before(make_int4(r, k, t, n), hk, group, plane, planes.n, planes.magic, C, P);
+        r = v.x;
+        k = v.y;
+        t = v.z;
+        n = v.w;
+        U -= n + kUnitCost;
+    }
     __device__ __forceinline__ bool prev() {
         if (U <= s0) return false;
         e = U;
-        if (t > 0) {
-            --t;
-        } else {
-            if (k > 0) {
-                --k;
-            } else {
-                do --r; while (C[r] == 0);
-                k = hk - 1;
-            }
-            t = (C[r] * group + kRows - 1) / kRows - 1;
-            n = (len() + kGranule - 1) / kGranule;
-        }
-        U -= n;
+        back();
         return true;
     }
 };
@@ -192,6 +282,16 @@ struct Walk : Unit {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
     const uint32_t bytes = valid ? 16u : 0u;  // nothing is read when it is not: zeros are written
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// Columns c .. c + 15 of this warp's 32 lanes, and the wait.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr)
+        : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
@@ -206,181 +306,290 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 // Nonzero bits 15 / 31: the word's low / high half is an infinity or NaN.
 __device__ __forceinline__ uint32_t no_number(uint32_t w) { return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u; }
 
-// 64 mask bits of a node from node index j0 on (j0 > -64; bits of negative
+// The waits of tcgen05.cuh with everything but the first try out of line: the
+// roles' loops share the instruction cache, which they would not fit.
+__device__ __noinline__ bool wait1_slow(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    return mbar_wait1(bar, parity, abort);
+}
+__device__ __noinline__ bool waitw_slow(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    return mbar_waitw(bar, parity, abort);
+}
+__device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    return mbar_try_wait_sleep(bar, parity) || wait1_slow(bar, parity, abort);
+}
+__device__ __forceinline__ bool waitw(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity)) || waitw_slow(bar, parity, abort);
+}
+// Lanes 0 to 3 (and the others with lane 3) each name a barrier: one look at all
+// of them together, for the latency of one, and where that does not do, one
+// wait after the other.  (Waits that sleep take one address for the warp.)
+__device__ __noinline__ bool wait4_slow(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; ok && i < 4; ++i)
+        ok = mbar_waitw(__shfl_sync(0xffffffffu, bar, i), __shfl_sync(0xffffffffu, parity, i), abort);
+    return ok;
+}
+__device__ __forceinline__ bool wait4(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    uint32_t there;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(there)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return __all_sync(0xffffffffu, there) || wait4_slow(bar, parity, abort);
+}
+__device__ __noinline__ bool drain1(uint32_t bar, uint32_t parity) { return mbar_drain1(bar, parity); }
+
+// A ring's slot and fill parity, advanced a slot at a time.
+template <int kSlots>
+struct Ring {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == kSlots) {
+            s = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+// 32 mask bits of a node from node index j0 on (j0 > -32; bits of negative
 // nodes, cached tokens, are set).
-__device__ __forceinline__ uint64_t mask_bits(const uint32_t* row, int words, int j0) {
-    const int w = max(j0, 0) >> 5;
-    auto word = [&](int i) -> uint64_t { return i < words ? __ldg(row + i) : 0u; };
-    if (j0 < 0) return ((word(0) | word(1) << 32) << -j0) | ((uint64_t(1) << -j0) - 1);
-    const int sh = j0 & 31;
-    const uint64_t lo = word(w) | word(w + 1) << 32;
-    return sh ? (lo >> sh) | word(w + 2) << (64 - sh) : lo;
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int words, int j0) {
+    auto word = [&](int i) -> uint32_t { return i < words ? __ldg(row + i) : 0u; };
+    if (j0 < 0) return (word(0) << -j0) | ((1u << -j0) - 1);
+    return __funnelshift_r(word(j0 >> 5), word((j0 >> 5) + 1), j0 & 31);
 }
-__device__ __forceinline__ uint64_t low_bits(int n) {
-    return n <= 0 ? 0 : n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
-}
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
-// A node's V that is no number reaches the rows that see it: the odd nodes'
-// elements of dims d0 .. d0 + 63 are added to this thread's stored output
-// (`orow`, fp16) or partial (`po`, dim group g at po[g * kRows]).
+// A node's V that is no number reaches the rows that see it: such elements of
+// dims d0 .. d0 + 63 of nodes j0 .. j1 - 1 are added to this thread's stored
+// output (`orow`, fp16) or partial (`po`, dim group e at po[e * kRows]).
 template <bool kFp8>
-__device__ __noinline__ void add_odd(const Params& p, const uint32_t* odd, int r, int P, int C, int node, int g,
-                                     int kvh, int d0, __half* orow, float4* po) {
-    for (int w = 0; w < kMaxWords; ++w) {
-        for (uint32_t bits = odd[w]; bits; bits &= bits - 1) {
-            const int j = 32 * w + __ffs(bits) - 1;
-            const bool sees = p.mask ? (p.mask[(int64_t)g * p.words + w] >> (j & 31)) & 1 : j <= node;
-            if (j >= C || !sees) continue;
-            const int t = P + j, pb = p.tables[(int64_t)r * p.mbpr + t / p.bs];
-            if (pb < 0 || pb >= p.nb) continue;
-            const int64_t at = (((int64_t)pb * p.bs + t % p.bs) * p.hk + kvh) * kHeadDim + d0;
-            for (int d = 0; d < 64; ++d) {
-                __half x;
-                if (kFp8) {
-                    uint32_t lo, hi;
-                    widen4(static_cast<const uint8_t*>(p.v_pool)[at + d], lo, hi);
-                    x = __ushort_as_half((unsigned short)(lo & 0xffffu));
-                } else {
-                    x = static_cast<const __half*>(p.v_pool)[at + d];
-                }
-                const float f = __half2float(x);
-                if (isfinite(f)) continue;
-                if (orow) orow[d] = __float2half_rn(__half2float(orow[d]) + f);
-                if (po) reinterpret_cast<float*>(po + (d >> 2) * kRows)[d & 3] += f;
+__device__ __noinline__ void add_odd(const Params& p, int r, int P, int j0, int j1, int node, int g, int kvh, int d0,
+                                     __half* orow, float4* po) {
+#pragma unroll 1
+    for (int j = j0; j < j1; ++j) {
+        const bool sees = p.mask ? (p.mask[(int64_t)g * p.words + (j >> 5)] >> (j & 31)) & 1 : j <= node;
+        if (!sees) continue;
+        const int t = P + j, pb = p.tables[(int64_t)r * p.mbpr + t / p.bs];
+        if (pb < 0 || pb >= p.nb) continue;
+        const int64_t at = (((int64_t)pb * p.bs + t % p.bs) * p.hk + kvh) * kHeadDim + d0;
+#pragma unroll 1
+        for (int d = 0; d < 64; ++d) {
+            __half x;
+            if (kFp8) {
+                uint32_t lo, hi;
+                widen4(static_cast<const uint8_t*>(p.v_pool)[at + d], lo, hi);
+                x = __ushort_as_half((unsigned short)(lo & 0xffffu));
+            } else {
+                x = static_cast<const __half*>(p.v_pool)[at + d];
             }
+            const float f = __half2float(x);
+            if (isfinite(f)) continue;
+            if (orow) orow[d] = __float2half_rn(__half2float(orow[d]) + f);
+            if (po) reinterpret_cast<float*>(po + (d >> 2) * kRows)[d & 3] += f;
         }
     }
 }
 
-// Merge the P pieces of a unit that starts in block `first`: jobs of eight dims
-// by some rows, claimed by warps.
-__device__ __forceinline__ void merge_unit(const Params& p, const Unit& u, int q0, int nq, int P, int first, bool last,
-                                        float vs) {
-    const int lane = threadIdx.x & 31;
-    int* head = p.heads + (int64_t)first * kHeadInts;
-    bool ready = last;
-    if (!ready) {
-        const uint64_t t0 = now_ns();
-        for (;;) {
-            int seen = 0;
-            if (lane == 0) asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(seen) : "l"(head) : "memory");
-            seen = __shfl_sync(0xffffffffu, seen, 0);
-            if (seen >= P) {
-                ready = true;
-                break;
+// A share of merging a unit cut over P blocks, the first of them `first`: (32
+// flat rows) x (4 kND dims) a warp's turn, turn w of all blocks' warps together,
+// every 8 P-th; kNP pieces' loads are in flight together.
+template <int kND, int kNP>
+__device__ __forceinline__ void merge_share(const Params& p, int k, int f0, int q0, int nq, int P, int first,
+                                            int piece, float vs) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kCols = 32 / kND;
+    const int jobs = kCols * ((nq + 31) / 32);
+#pragma unroll 1
+    for (int job = piece * kSoftWarps + warp; job < jobs; job += P * kSoftWarps) {
+        const int cc = job % kCols, i = (job / kCols) * 32 + lane;  // dims 4 kND cc .. of flat row i of the unit
+        if (i >= nq) continue;
+        float M = -INFINITY, Lt = 0.f, acc[4 * kND];
+#pragma unroll
+        for (int e = 0; e < 4 * kND; ++e) acc[e] = 0.f;
+#pragma unroll 1
+        for (int j0 = 0; j0 < P; j0 += kNP) {
+            // (no branch between the loads: past the last piece it is read again and left out)
+            float mj[kNP], lj[kNP];
+            float4 x[kNP][kND];
+#pragma unroll
+            for (int j = 0; j < kNP; ++j) {
+                const int jj = min(j0 + j, P - 1);
+                const float* s = p.part + ((int64_t)(first + jj) * 2 + (jj == P - 1)) * kPartFloats;
+                mj[j] = __ldcg(s + i);
+                lj[j] = __ldcg(s + kRows + i);
+                const float4* o = reinterpret_cast<const float4*>(s + 2 * kRows) + kND * cc * kRows + i;
+#pragma unroll
+                for (int e = 0; e < kND; ++e) x[j][e] = __ldcg(o + e * kRows);
             }
-            if (__shfl_sync(0xffffffffu, (int)(now_ns() - t0 > kHelpNs), 0)) break;
-            __nanosleep(32);
-        }
-    }
-    if (ready) {
-        const int nrb = (nq + 31) / 32, rs = min(nrb, max(1, P / 2)), jobs = 16 * rs;
-        for (;;) {
-            int job = 0;
-            if (lane == 0) job = atomicAdd(head + 1, 1);
-            job = __shfl_sync(0xffffffffu, job, 0);
-            if (job >= jobs) break;
-            const int cc = job & 15;  // dims 8 cc ..
-            for (int rb = job >> 4; rb < nrb; rb += rs) {
-                const int i = rb * 32 + lane;
-                if (i >= nq) continue;
-                float M = -INFINITY, Lt = 0.f, acc[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-                for (int j0 = 0; j0 < P; j0 += 4) {
-                    float mj[4], lj[4];
-                    float4 x[4], y[4];
+            for (int j = 0; j < kNP; ++j) {
+                if (j0 + j >= P || mj[j] == -INFINITY) continue;
+                const float mn = fmaxf(M, mj[j]);
+                const float a = M == -INFINITY ? 0.f : fast_exp2(M - mn), w = fast_exp2(mj[j] - mn);
+                M = mn;
+                Lt = Lt * a + w * lj[j];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        mj[j] = -INFINITY;
-                        if (j0 + j < P) {
-                            const float* s = p.part + ((int64_t)(first + j0 + j) * 2 + (j0 + j == P - 1)) * kPartFloats;
-                            mj[j] = __ldcg(s + i);
-                            lj[j] = __ldcg(s + kRows + i);
-                            const float4* o = reinterpret_cast<const float4*>(s + 2 * kRows) + 2 * cc * kRows + i;
-                            x[j] = __ldcg(o);
-                            y[j] = __ldcg(o + kRows);
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j0 + j >= P || mj[j] == -INFINITY) continue;
-                        const float mn = fmaxf(M, mj[j]);
-                        const float a = M == -INFINITY ? 0.f : fast_exp2(M - mn), w = fast_exp2(mj[j] - mn);
-                        M = mn;
-                        Lt = Lt * a + w * lj[j];
-                        const float o[8] = {x[j].x, x[j].y, x[j].z, x[j].w, y[j].x, y[j].y, y[j].z, y[j].w};
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) acc[e] = acc[e] * a + w * o[e];
-                    }
+                for (int e = 0; e < kND; ++e) {
+                    acc[4 * e] = acc[4 * e] * a + w * x[j][e].x;
+                    acc[4 * e + 1] = acc[4 * e + 1] * a + w * x[j][e].y;
+                    acc[4 * e + 2] = acc[4 * e + 2] * a + w * x[j][e].z;
+                    acc[4 * e + 3] = acc[4 * e + 3] * a + w * x[j][e].w;
                 }
-                const float inv = Lt == 0.f ? 0.f : vs / Lt;
-                const int f = u.t * kRows + i;
-                uint4 o4;
-                o4.x = pack_half2(acc[0] * inv, acc[1] * inv);
-                o4.y = pack_half2(acc[2] * inv, acc[3] * inv);
-                o4.z = pack_half2(acc[4] * inv, acc[5] * inv);
-                o4.w = pack_half2(acc[6] * inv, acc[7] * inv);
-                *reinterpret_cast<uint4*>(p.out + ((int64_t)(q0 + f / p.group) * p.hq + u.k * p.group + f % p.group) *
-                                                      kHeadDim + cc * 8) = o4;
             }
         }
+        const float inv = Lt == 0.f ? 0.f : vs / Lt;
+        const int f = f0 + i, node = div_of(f, p.group);
+        __half* dst = p.out + ((int64_t)(q0 + node) * p.hq + k * p.group + (f - node * p.group)) * kHeadDim + 4 * kND * cc;
+#pragma unroll
+        for (int e = 0; e < kND; ++e)
+            *reinterpret_cast<uint2*>(dst + 4 * e) = make_uint2(pack_half2(acc[4 * e] * inv, acc[4 * e + 1] * inv),
+                                                                pack_half2(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
     }
-    // the last of the unit's warps to leave re-arms its words for the next call
-    __syncwarp();
-    if (lane == 0) {
+}
+
+// A wrapping increment: the word goes back to zero after 2 P of them.
+__device__ __forceinline__ int count_up(int* word, int P) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(word), "r"(2 * P - 1) : "memory");
+    return (int)old;
+}
+
+// One thread of each of a cut unit's blocks, after its own piece was counted as
+// the n-th: waits for the others and says whether the block merges its share.
+// `head`: the count, then a bit for each piece whose block gave up.  A block
+// that gives up sets its bit and then looks at the count once more; the last
+// one to arrive counts and then looks at the bits: one of the two sees the
+// other, and whoever takes the bit away does the share (the last block gets the
+// pieces it took in `taken`).  Every block, or the last one in its place, counts
+// a second time, which brings the word back to zero.
+__device__ __forceinline__ bool gather(int* head, int P, int piece, int n, volatile int* taken) {
+    const bool last = n == P;
+    const uint64_t t0 = now_ns();
+    while (n < P) {
+        if (now_ns() - t0 > kHelpNs) {
+            int* word = head + 1 + (piece >> 5);
+            const int bit = 1 << (piece & 31);
+            atomicOr(word, bit);
+            __threadfence();
+            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(n) : "l"(head) : "memory");
+            if (n < P || !(atomicAnd(word, ~bit) & bit)) return false;
+            break;
+        }
+        __nanosleep(20);
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(n) : "l"(head) : "memory");
+    }
+    count_up(head, P);
+    if (last) {
         __threadfence();
-        if (atomicAdd(head + 2, 1) == P * kSoftWarps - 1) {
-            head[0] = 0;
-            head[1] = 0;
-            head[2] = 0;
+        for (int i = 0; i < (P + 31) / 32; ++i) {
+            if (!*reinterpret_cast<volatile int*>(head + 1 + i)) continue;
+            const int bits = atomicExch(head + 1 + i, 0);
+            taken[i] = bits;
+            for (int k = __popc(bits); k > 0; --k) count_up(head, P);
         }
     }
+    return true;
 }
 
 template <bool kFp8>
 __global__ void __launch_bounds__(threads<kFp8>(), 1)
     tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const __grid_constant__ Params p) {
+    using S = Smem<kFp8>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
-    const uint32_t bar_kfull = sbase + Smem::bars;           // [K slots]
-    const uint32_t bar_kempty = bar_kfull + kKSlots * 8;     // [K slots]
-    const uint32_t bar_vfull = bar_kempty + kKSlots * 8;     // [V slots]
-    const uint32_t bar_vempty = bar_vfull + kVSlots * 8;     // [V slots]
-    const uint32_t bar_s = bar_vempty + kVSlots * 8;         // [3]: S buffer computed
-    const uint32_t bar_p = bar_s + 8 * kSBufs;               // [3]: P of S buffer written
-    const uint32_t bar_o = bar_p + 8 * kSBufs;               // [3]: PV product of buffer done
-    const uint32_t bar_x = bar_o + 8 * kSBufs;               // [2]: both halves' row maxima of a tile written
-    const uint32_t bar_l = bar_x + 16;                       // both halves' row sums written
-    const uint32_t bar_qfree = bar_l + 8;                    // a segment's S products are done with its queries
-    const uint32_t bar_odrained = bar_qfree + 8;             // the softmax warps have read a segment's O out
-    const uint32_t bar_sfin = bar_odrained + 8;              // the S issuer's last products are complete
-    const uint32_t bar_pfin = bar_sfin + 8;                  // the PV issuer's last products are complete
-    const uint32_t bar_pub = bar_pfin + 8;                   // the softmax warps have written a partial
-    uint32_t* sm_tmem = reinterpret_cast<uint32_t*>(smem + Smem::tmem);
-    volatile int* sm_misc = reinterpret_cast<volatile int*>(smem + Smem::misc);
-    const volatile int* abort = sm_misc + 7;
-    volatile uint32_t* sm_bad = reinterpret_cast<volatile uint32_t*>(smem + Smem::bad);
-    uint32_t* sm_odd = reinterpret_cast<uint32_t*>(smem + Smem::odd);
-    int* sm_part = reinterpret_cast<int*>(smem + Smem::part);
-    int* sm_pre = reinterpret_cast<int*>(smem + Smem::pre);
-    int* sm_C = reinterpret_cast<int*>(smem + Smem::rowc);
-    int* sm_P = reinterpret_cast<int*>(smem + Smem::rowp);
-    int* sm_qs = reinterpret_cast<int*>(smem + Smem::rowq);
+    const uint32_t bar_kfull = sbase + S::bars;                // [K slots]
+    const uint32_t bar_kempty = bar_kfull + S::kslots * 8;
+    const uint32_t bar_vfull = bar_kempty + S::kslots * 8;     // [V slots]
+    const uint32_t bar_vempty = bar_vfull + S::vslots * 8;
+    const uint32_t bar_krfull = bar_vempty + S::vslots * 8;    // [raw slots] of K codes
+    const uint32_t bar_krempty = bar_krfull + S::raws * 8;
+    const uint32_t bar_vrfull = bar_krempty + S::raws * 8;     // [raw slots] of V codes
+    const uint32_t bar_vrempty = bar_vrfull + S::raws * 8;
+    const uint32_t bar_s = bar_vrempty + S::raws * 8;          // [S buffers]: computed
+    const uint32_t bar_p = bar_s + 8 * kSBufs;                 // [S buffers]: P written
+    const uint32_t bar_o = bar_p + 8 * kSBufs;                 // [S buffers]: P's product done
+    const uint32_t bar_m = bar_o + 8 * kSBufs;                 // [8 softmax warps]: a job's references known
+    const uint32_t bar_l = bar_m + 8 * kSoftWarps;             // both groups' row sums of a segment written
+    const uint32_t bar_qfree = bar_l + 8;                      // a segment's S products are done with its queries
+    const uint32_t bar_fin = bar_qfree + 8;                    // a segment's last PV product is done
+    const uint32_t bar_odrained = bar_fin + 8;                 // the softmax warps have read a segment's O out
+    const uint32_t bar_sfin = bar_odrained + 8;                // the S issuer's last products are complete
+    const uint32_t bar_pfin = bar_sfin + 8;                    // the PV issuer's last products are complete
+    const uint32_t bar_pub = bar_pfin + 8;                     // the softmax warps have written a partial
+    const uint32_t bar_go = bar_pub + 8;                       // a cut unit's pieces are all there (or given up)
+    uint32_t* sm_tmem = reinterpret_cast<uint32_t*>(smem + S::tmem);
+    volatile int* sm_misc = reinterpret_cast<volatile int*>(smem + S::misc);
+    const volatile int* abort = sm_misc + 8;
+    volatile uint32_t* sm_bad = reinterpret_cast<volatile uint32_t*>(smem + S::bad);
+    int* sm_part = reinterpret_cast<int*>(smem + S::part);
+    int* sm_C = reinterpret_cast<int*>(smem + S::rowc);
+    int* sm_P = reinterpret_cast<int*>(smem + S::rowp);
 
-    constexpr int kThreads = threads<kFp8>();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = p.rows, group = p.group;
 
-    // ---- per row: nodes, cached tokens, granules of all its units; their prefix ----
-    const int per = (rows + kThreads - 1) / kThreads;
-    int sum = 0;
-    for (int i = 0; i < per; ++i) {
-        const int r = tid * per + i;
-        if (r < rows) {
+    // ---- barriers, tensor memory, descriptors ----
+    if (tid == kPvIssue * 32) {
+        const int fill = kFp8 ? kConvWarps : 1;
+        for (int s = 0; s < S::kslots; ++s) {
+            mbar_init(bar_kfull + 8 * s, fill);
+            mbar_init(bar_kempty + 8 * s, 1);
+        }
+        for (int s = 0; s < S::vslots; ++s) {
+            mbar_init(bar_vfull + 8 * s, fill);
+            mbar_init(bar_vempty + 8 * s, 1);
+        }
+        for (int s = 0; s < S::raws; ++s) {
+            mbar_init(bar_krfull + 8 * s, 1);
+            mbar_init(bar_krempty + 8 * s, kConvWarps);
+            mbar_init(bar_vrfull + 8 * s, 1);
+            mbar_init(bar_vrempty + 8 * s, kConvWarps);
+        }
+        for (int b = 0; b < kSBufs; ++b) {
+            mbar_init(bar_s + 8 * b, 1);
+            mbar_init(bar_p + 8 * b, kSoftWarps / 2);
+            mbar_init(bar_o + 8 * b, 1);
+        }
+        for (int b = 0; b < kSoftWarps; ++b) mbar_init(bar_m + 8 * b, 1);
+        mbar_init(bar_l, kSoftWarps);
+        mbar_init(bar_qfree, 1);
+        mbar_init(bar_fin, 1);
+        mbar_init(bar_odrained, kSoftWarps);
+        mbar_init(bar_sfin, 1);
+        mbar_init(bar_pfin, 1);
+        mbar_init(bar_pub, kSoftWarps);
+        mbar_init(bar_go, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kLoad && lane < 2)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &vmap : &kmap)) : "memory");
+    if (warp == kSIssue) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + S::tmem),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+
+    // ---- per row: nodes, cached tokens, its units' length in each plane; the planes'
+    // prefixes.  Two halves of the block do the same, six warps each: one for
+    // the range's lower cut, one for the upper.  One warp's dependent instructions
+    // take some five clocks each, so what counts here is their number ----
+    constexpr int kHalfWarps = 6;
+    const int side = warp >= kHalfWarps, hw = warp - side * kHalfWarps;  // further warps only wait
+    const int per = (rows + kHalfWarps * 32 - 1) / (kHalfWarps * 32), r0 = (hw * 32 + lane) * per;
+    const Planes planes = p.planes;
+    int sum[kPlanes] = {0, 0, 0, 0}, incl[kPlanes];
+    if (hw < kHalfWarps) {
+#pragma unroll 1
+        for (int r = r0; r < min(r0 + per, rows); ++r) {
             const int q0 = p.q_start[r], L = p.seq_lens[r];
             int C = p.q_start[r + 1] - q0;
             if (C < 0 || L < C || L > p.limit || q0 < 0 || q0 > p.total - C) {
@@ -390,133 +599,157 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                 if (blockIdx.x == 0) flag_error(p.dev_err, PKV_DEV_ERR_MASK);
                 C = 0;
             }
-            sm_C[r] = C;
-            sm_P[r] = L - C;
-            sm_qs[r] = q0;
-            // below 2^31 in total (checked by the host)
-            sm_pre[r] = C > 0 ? p.hk * ((C * group + kRows - 1) / kRows) * ((L + kGranule - 1) / kGranule) : 0;
-            sum += sm_pre[r];
-        }
-    }
-    sm_part[tid] = sum;
-    if (tid < 2 * kMaxWords) sm_odd[tid] = 0;
-    __syncthreads();
-    if (warp == 0) {
-        constexpr int kPer = (kThreads + 31) / 32;
-        int v[kPer], acc = 0;
+            if (side == 0) {
+                sm_C[r] = C;
+                sm_P[r] = L - C;
+            }
+            // a unit's length (all units' together stay below 2^31, checked by the host)
+            const int len = C > 0 ? p.hk * ((L + kGrain - 1) / kGrain + kUnitCost) : 0;
+            sum[0] += len * planes.blocks(C * group, 0);
+            if (planes.n > 1) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            v[j] = sm_part[lane * kPer + j];
-            acc += v[j];
-        }
-        int incl = acc;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
-        }
-        int run = incl - acc;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            sm_part[lane * kPer + j] = run;
-            run += v[j];
-        }
-    }
-    __syncthreads();
-    {
-        int run = sm_part[tid];
-        for (int i = 0; i < per; ++i) {
-            const int r = tid * per + i;
-            if (r < rows) {
-                const int c = sm_pre[r];
-                sm_pre[r] = run;
-                run += c;
+                for (int x = 1; x < kPlanes; ++x)
+                    if (x < planes.n) sum[x] += len * planes.blocks(C * group, x);
             }
         }
-        if (tid == kThreads - 1) sm_pre[rows] = run;
+        auto scan = [&](int x) {
+            incl[x] = sum[x];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, incl[x], o);
+                if (lane >= o) incl[x] += t;
+            }
+            if (lane == 31) sm_part[(x * 2 + side) * 8 + hw] = incl[x];
+        };
+        scan(0);
+        if (planes.n > 1) {
+#pragma unroll
+            for (int x = 1; x < kPlanes; ++x)
+                if (x < planes.n) scan(x);
+        }
     }
+    if (tid < 48) sm_misc[tid] = 0;
     __syncthreads();
 
-    // ---- this block's range ----
+    // ---- this block's plane, the plane's blocks, and its range: the thread whose
+    // row a cut falls in moves the cut ----
+    int plane = 0, base_block = 0, run = 0, mine = 0;
     Split sp;
-    sp.W = sm_pre[rows];
-    sp.G = min((int)gridDim.x, max(sp.W / kMinGranules, 1));
-    sp.slack = max(kMinGranules, sp.W / sp.G / 16);
-    const int cta = blockIdx.x;
-    if (sp.W == 0 || cta >= sp.G) return;
-    auto locate = [&](int x) -> Unit {  // the unit that holds granule x
-        int lo = 0, hi = rows - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (sm_pre[mid] <= x) lo = mid; else hi = mid - 1;
+    sp.W = 0;
+    {
+        // of this half's warps: the work before this one and the whole plane's
+        auto plane_of = [&](int x, int& before) -> int {
+            int v = lane < kHalfWarps ? sm_part[(x * 2 + side) * 8 + lane] : 0;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += t;
+            }
+            before = __shfl_sync(0xffffffffu, v, max(hw - 1, 0));
+            if (hw == 0) before = 0;
+            return __shfl_sync(0xffffffffu, v, kHalfWarps - 1);
+        };
+        int before;
+        int W = plane_of(0, before);
+        int from = 0, to = (int)gridDim.x;
+        if (planes.n > 1) {
+            // blocks in proportion to the planes' work, one at least where there is any
+            float Wf[kPlanes], all = 0.f;
+            int later = 0;  // planes with work that are still to come
+            int Wi[kPlanes], bf[kPlanes];
+            Wi[0] = W;
+            bf[0] = before;
+#pragma unroll
+            for (int x = 1; x < kPlanes; ++x) {
+                Wi[x] = bf[x] = 0;
+                if (x < planes.n) Wi[x] = plane_of(x, bf[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < kPlanes; ++x) {
+                all += Wf[x] = (float)Wi[x];
+                later += Wi[x] > 0;
+            }
+            const float share = all > 0.f ? __fdividef((float)gridDim.x, all) : 0.f;
+            float upto = 0.f;
+            int next = 0;
+            W = 0;
+#pragma unroll
+            for (int x = 0; x < kPlanes; ++x) {
+                upto += Wf[x];
+                later -= Wi[x] > 0;
+                const int end = min(max(__float2int_rn(upto * share), next + (Wi[x] > 0)), (int)gridDim.x - later);
+                if ((int)blockIdx.x >= next && (int)blockIdx.x < end) {
+                    plane = x;
+                    W = Wi[x];
+                    before = bf[x];
+                    from = next;
+                    to = end;
+                }
+                next = end;
+            }
         }
-        Unit u;
-        u.r = lo;
-        u.n = (sm_P[lo] + sm_C[lo] + kGranule - 1) / kGranule;
-        const int nt = (sm_C[lo] * group + kRows - 1) / kRows;
-        const int i = (x - sm_pre[lo]) / u.n;
-        u.k = i / nt;
-        u.t = i - u.k * nt;
-        u.U = sm_pre[lo] + i * u.n;
-        return u;
-    };
-    // warp 0: the moved cuts on both sides and the unit before the upper one
-    if (warp == 0) {
-        const int x = sp.raw(cta + (lane & 1));
-        const int cut = x < sp.W ? sp.moved(x, locate(x)) : sp.W;
-        const int c0 = __shfl_sync(0xffffffffu, cut, 0), c1 = __shfl_sync(0xffffffffu, cut, 1);
-        if (c0 < c1) {
-            const Unit u = locate(c1 - 1);
-            if (lane == 0) {
+        if (W > 0) {
+            base_block = from;
+            int i = incl[0], m = sum[0];
+            if (planes.n > 1) {
+#pragma unroll
+                for (int x = 1; x < kPlanes; ++x)
+                    if (x == plane) {
+                        i = incl[x];
+                        m = sum[x];
+                    }
+            }
+            run = before + i - m;
+            mine = hw < kHalfWarps ? m : 0;
+            sp.set(W, to - from);
+        }
+    }
+    const int cta = (int)blockIdx.x - base_block;
+    if (sp.W > 0 && cta < sp.G) {
+        // the lower cut lies in [run, run + mine) of one thread of the first half, the upper one
+        // in (run, run + mine] of one of the second
+        const int x = sp.raw(cta + side), in = x - side;
+        if (in >= run && in < run + mine) {
+            Walk u;
+            u.hk = p.hk;
+            u.group = group;
+            u.plane = plane;
+            u.planes = planes;
+            u.C = sm_C;
+            u.P = sm_P;
+            u.r = r0;
+            int at = in - run, nt;
+#pragma unroll 1
+            for (;; ++u.r) {
+                nt = planes.blocks(u.flat(), plane);
+                u.n = (u.len() + kGrain - 1) / kGrain;
+                const int here = p.hk * nt * (u.n + kUnitCost);
+                if (at < here) break;
+                at -= here;
+            }
+            const int i = div_of(at, u.n + kUnitCost);
+            u.k = div_of(i, nt);
+            u.t = i - u.k * nt;
+            u.U = in - (at - i * (u.n + kUnitCost));
+            const int cut = x < u.end() ? sp.moved(x, u) : x;
+            if (side == 0) {
+                sm_misc[6] = cut;
+            } else {
+                if (cut == u.U && cut > 0) u.back();  // the unit before the cut
                 sm_misc[0] = u.r;
                 sm_misc[1] = u.k;
                 sm_misc[2] = u.t;
                 sm_misc[3] = u.U;
                 sm_misc[4] = u.n;
+                sm_misc[7] = cut;
             }
         }
-        if (lane == 0) {
-            sm_misc[5] = c0;
-            sm_misc[6] = c1;
-            sm_misc[7] = 0;  // abort
-        }
-    }
-
-    // ---- barriers and tensor memory ----
-    if (tid == 32) {
-        const int fill = kFp8 ? kConvWarps : 1;
-        for (int s = 0; s < kKSlots; ++s) {
-            mbar_init(bar_kfull + 8 * s, fill);
-            mbar_init(bar_kempty + 8 * s, 1);
-        }
-        for (int s = 0; s < kVSlots; ++s) {
-            mbar_init(bar_vfull + 8 * s, fill);
-            mbar_init(bar_vempty + 8 * s, 1);
-        }
-        mbar_init(bar_l, kSoftWarps);
-        for (int b = 0; b < 2; ++b) mbar_init(bar_x + 8 * b, kSoftWarps);
-        for (int b = 0; b < kSBufs; ++b) {
-            mbar_init(bar_s + 8 * b, 1);
-            mbar_init(bar_p + 8 * b, kSoftWarps);
-            mbar_init(bar_o + 8 * b, 1);
-        }
-        mbar_init(bar_qfree, 1);
-        mbar_init(bar_odrained, kSoftWarps);
-        mbar_init(bar_sfin, 1);
-        mbar_init(bar_pfin, 1);
-        mbar_init(bar_pub, kSoftWarps);
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + Smem::tmem),
-                     "r"(kTmemCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *sm_tmem;
-    auto raise_abort = [&]() { sm_misc[7] = 1; };
+    auto raise_abort = [&]() { sm_misc[8] = 1; };
 
     Walk w;
     w.r = sm_misc[0];
@@ -524,45 +757,65 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
     w.t = sm_misc[2];
     w.U = sm_misc[3];
     w.n = sm_misc[4];
-    w.s0 = sm_misc[5];
-    w.e = sm_misc[6];
+    w.s0 = sm_misc[6];
+    w.e = sm_misc[7];
     w.hk = p.hk;
     w.group = group;
+    w.plane = plane;
+    w.planes = planes;
     w.C = sm_C;
     w.P = sm_P;
-    const bool any = w.s0 < w.e;  // both cuts may have moved to one border
 
-    if (!any) {
-        // nothing to do but to free the tensor memory below
-    } else if (!kFp8 && warp >= kLoad) {
+    // A unit's flat rows (256 bytes a row, swizzled; rows past the last are zeros), by one warp.
+    auto load_queries = [&](const Walk& u) {
+        const int F = u.flat(), q0 = __ldg(p.q_start + u.r), ch = lane & 15;
+        const uint32_t dst0 = sbase + S::q + (ch >> 3) * kHalfQ;
+#pragma unroll 1
+        for (int j = 0; j < kRows; j += 32) {
+            // of flat row j + lane: (node, head) index, or -1
+            const int f = u.f0() + j + lane, node = div_of(f, group);
+            const int at = f < F ? (q0 + node) * p.hq + u.k * group + (f - node * group) : -1;
+#pragma unroll 4
+            for (int x = 0; x < 16; ++x) {
+                const int rr = 2 * x + (lane >> 4);
+                const int a = __shfl_sync(0xffffffffu, at, rr);
+                cp_async16(dst0 + (j + rr) * 128 + (((ch & 7) ^ (rr & 7)) << 4),
+                           p.q + (int64_t)max(a, 0) * kHeadDim + ch * 8, a >= 0);
+            }
+        }
+    };
+
+    if (w.s0 >= w.e) {
+        // no work, or both cuts moved to one border: nothing but to free the tensor memory below
+    } else if (warp == kLoad || warp == kLoad + 1) {
         // ============================== TMA ==============================
-        // Warp kLoad streams K tiles, the next one V halves.  Table entries are
+        // K tiles or V granules (FP8: granules of codes).  Table entries are
         // fetched a batch ahead: lane l handles box l % gpu of copy unit l / gpu
         // of a batch, so the table's latency is paid once a batch.
         const bool is_v = warp == kLoad + 1;
-        const int nslots = is_v ? kVSlots : kKSlots;
-        const int unit_tok = is_v ? 64 : kTile;
-        const uint32_t full0 = is_v ? bar_vfull : bar_kfull;
-        const uint32_t empty0 = is_v ? bar_vempty : bar_kempty;
-        const uint32_t ring = sbase + (is_v ? Smem::vring : Smem::kring);
-        const uint32_t slot_bytes = is_v ? kVSlot : kKSlot;
-        const uint32_t half_bytes = is_v ? kVHalf : kKHalf;
+        const int nslots = kFp8 ? S::raws : is_v ? S::vslots : S::kslots;
+        const int unit_tok = kFp8 || is_v ? kGrain : kTile;
+        const uint32_t full0 = kFp8 ? (is_v ? bar_vrfull : bar_krfull) : (is_v ? bar_vfull : bar_kfull);
+        const uint32_t empty0 = kFp8 ? (is_v ? bar_vrempty : bar_krempty) : (is_v ? bar_vempty : bar_kempty);
+        const uint32_t ring = sbase + (kFp8 ? (is_v ? S::vraw : S::kraw) : (is_v ? S::vring : S::kring));
+        const uint32_t slot_bytes = kFp8 ? kRaw : is_v ? kVSlot : kKSlot;
+        const uint32_t half_bytes = slot_bytes / 2;
         const CUtensorMap* map = is_v ? &vmap : &kmap;
         const int box = p.box;
         const int gpu = unit_tok / box, upb = 32 / gpu;
         const int my_j = lane / gpu, my_g = lane % gpu;
         const uint32_t box_bytes = (uint32_t)box * 128;
         const int nowhere = p.nb * p.bs;  // a row past the pool: a copy of zeros
-        int s = 0, armed = 0;
+        int s = 0, armed = 0, grain = 0;
         uint32_t ph = 0, fb = full0, eb = empty0, slot = ring;
         bool ok = true;
         do {
             const int ta = w.ta(), te = w.te();
             const int units = (te - ta + unit_tok - 1) / unit_tok;
             const int32_t* trow = p.tables + (int64_t)w.r * p.mbpr;
-            auto fetch = [&](int ub) -> int {  // raw block id of this lane's box in the batch at unit ub
+            auto fetch = [&](int ub) -> int {  // raw block id of this lane's box in the batch at copy unit ub
                 const int tok = ta + (ub + my_j) * unit_tok + my_g * box;
-                return tok < te ? __ldg(trow + tok / p.bs) : 0;
+                return tok < te ? __ldg(trow + (unsigned)tok / (unsigned)p.bs) : 0;
             };
             auto to_row = [&](int ub, int pb) -> int {  // its pool row, or -1 for no copy
                 const int tok = ta + (ub + my_j) * unit_tok + my_g * box;
@@ -571,14 +824,16 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     if (!is_v) flag_error(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
                     return nowhere;
                 }
-                return pb * p.bs + tok % p.bs;
+                return pb * p.bs + (int)((unsigned)tok % (unsigned)p.bs);
             };
-            int pb_next = fetch(0);
-            int row = to_row(0, pb_next);
-            pb_next = fetch(upb);
-            int j = 0;
+            int pb = fetch(0), row = -1, j = 0;
+#pragma unroll 1
             for (int u = 0; u < units; ++u) {
-                if (!mbar_waitw(eb, ph ^ 1, abort)) {
+                if (j == 0) {
+                    row = to_row(u, pb);
+                    pb = fetch(u + upb);
+                }
+                if (!waitw(eb, ph ^ 1, abort)) {
                     ok = false;
                     break;
                 }
@@ -586,24 +841,23 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                 const uint32_t nissue = __popc(__ballot_sync(0xffffffffu, issue));
                 if (!is_v) {
                     // groups of 16 tokens whose table entry is out of range: read by the softmax
-                    // warps at this tile, long before the word's next use eight tiles on
+                    // warps at this tile, before the word's next use 32 granules on (the rings
+                    // and S buffers hold fewer between the two)
                     const uint32_t mine = issue && row == nowhere ? ((1u << (box / 16)) - 1) << (my_g * (box / 16)) : 0;
                     const uint32_t all = __reduce_or_sync(0xffffffffu, mine);
-                    if (lane == 0) sm_bad[armed & 7] = all;
+                    const bool two = !kFp8 && te - ta - u * kTile > kGrain;
+                    if (lane < 1 + two) sm_bad[(grain + lane) & 31] = all >> (4 * lane);
+                    grain += 1 + two;
                 }
-                if (lane == 0) mbar_arrive_expect_tx(fb, nissue * 2 * box_bytes);
+                if (lane == 0) mbar_arrive_expect_tx(fb, nissue * (kFp8 ? 1 : 2) * box_bytes);
                 __syncwarp();
                 if (issue) {
                     const uint32_t st = slot + my_g * box_bytes;
                     tma_load_3d(st, map, 0, w.k, row, fb);
-                    tma_load_3d(st + half_bytes, map, 64, w.k, row, fb);
+                    if (!kFp8) tma_load_3d(st + half_bytes, map, 64, w.k, row, fb);
                 }
                 ++armed;
-                if (++j == upb) {
-                    j = 0;
-                    row = to_row(u + 1, pb_next);
-                    pb_next = fetch(u + 1 + upb);
-                }
+                if (++j == upb) j = 0;
                 if (++s == nslots) {
                     s = 0;
                     ph ^= 1;
@@ -622,117 +876,70 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
         }
         // every armed slot's copies have landed before the block exits
+#pragma unroll 1
         for (int u = max(0, armed - nslots); u < armed; ++u)
-            if (!mbar_drain1(full0 + 8 * (u % nslots), (uint32_t)(u / nslots) & 1) && lane == 0)
+            if (!drain1(full0 + 8 * (u % nslots), (uint32_t)(u / nslots) & 1) && lane == 0)
                 flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
         __syncwarp();
-    } else if (kFp8 && warp >= kLoad) {
-        // ======================= FP8: load and widen =======================
-        // Per tile, thread (warp c, lane l) takes 16 codes (l % 8) of token 4 c +
-        // l / 8 of each of the tile's eight 16-token groups, K then V.  A tile's
-        // V is loaded before its K is stored and the next tile's K before its V
-        // is, and its table entries a tile earlier still.
-        const int c = warp - kLoad, tok_in = 4 * c + (lane >> 3), col = lane & 7;
-        const int tok_bytes = p.hk * kHeadDim;
-        Walk nx = w;  // the walk, one tile ahead
-        int nt0 = nx.ta();
-        bool more = true;
-        auto fetch = [&]() -> int {  // raw block id of group `lane` of the next tile
-            const int tok = nt0 + 16 * lane;
-            return more && lane < 8 && tok < nx.te() ? __ldg(p.tables + (int64_t)nx.r * p.mbpr + tok / p.bs) : 0;
-        };
-        int pb = fetch();
-        int row = -1, te = 0, t0 = 0, kvh = 0;
-        auto step = [&]() -> bool {  // the next tile becomes the present one
-            if (!more) return false;
-            t0 = nt0;
-            te = nx.te();
-            kvh = nx.k;
-            const int tok = t0 + 16 * lane;
-            row = -1;
-            if (lane < 8 && tok < te) {
-                if (pb < 0 || pb >= p.nb) {
-                    row = -2;  // not to be seen
-                    if (c == 0) flag_error(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
-                } else {
-                    row = pb * p.bs + tok % p.bs;
-                }
-            }
-            nt0 += kTile;
-            if (nt0 >= te) {
-                more = nx.prev();
-                nt0 = nx.ta();
-            }
-            pb = fetch();
-            return true;
-        };
-        auto load = [&](const void* pool, uint4 (&x)[8]) {
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const int base = __shfl_sync(0xffffffffu, row, g);
-                const bool have = base >= 0 && t0 + 16 * g + tok_in < te;
-                x[g] = have ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) +
-                                                                   (int64_t)(base + tok_in) * tok_bytes +
-                                                                   kvh * kHeadDim + col * 16))
-                            : make_uint4(0, 0, 0, 0);
-            }
-        };
-        auto store = [&](uint32_t lo, uint32_t half_bytes, int r0, const uint4& x) {
-            // chunks 2 col and 2 col + 1 of 8 dims; the lanes of the upper dims store theirs the
-            // other way round, so that eight lanes meet eight bank groups
-            const uint4 a = widen8(make_uint2(x.x, x.y)), b = widen8(make_uint2(x.z, x.w));
-            const int sw = col >> 2;
-            const uint32_t at = lo + sw * half_bytes + r0 * 128;
-            const int c0 = 2 * (col & 3) + sw, c1 = 2 * (col & 3) + 1 - sw;
-            sts16(at + ((c0 ^ (r0 & 7)) << 4), sw ? b : a);
-            sts16(at + ((c1 ^ (r0 & 7)) << 4), sw ? a : b);
-        };
-        int ks = 0, vs = 0, tile = 0;
-        uint32_t kph = 0, vph = 0;
+    } else if (kFp8 && warp >= kConv) {
+        // ========================= FP8: widening =========================
+        // Thread (warp c, lane l) widens 16 codes (chunk l % 8) of tokens 16 c +
+        // l / 8 + 4 i of a granule: 32 bytes in two stores, the lanes of the upper
+        // dims the other way round, so that eight lanes meet eight bank groups.
+        // Rows past the last token hold whatever the slot held: never seen.
+        const int c = warp - kConv, col = lane & 7, sw = col >> 2;
+        const int ch0 = 2 * (col & 3) + sw, ch1 = 2 * (col & 3) + 1 - sw;
+        Ring<S::raws ? S::raws : 1> rk, rv;
+        Ring<S::kslots> k;
+        Ring<S::vslots> v;
         bool ok = true;
-        uint4 xk[8], xv[8];
-        bool have = step();
-        load(p.k_pool, xk);
-        while (have) {
-            load(p.v_pool, xv);
-            const int n = te - t0;  // tokens of this tile that are this segment's (may exceed 128)
-            const uint32_t gone = __ballot_sync(0xffffffffu, row == -2);
-            // K
-            if (!(ok = mbar_waitw(bar_kempty + 8 * ks, kph ^ 1, abort))) break;
-            if (c == 0 && lane == 0) sm_bad[tile & 7] = gone;
-            ++tile;
+        auto widen = [&](uint32_t raw, uint32_t dst, uint32_t half_bytes) {
+            uint4 x[4];
 #pragma unroll
-            for (int g = 0; g < 8; ++g)
-                if (16 * g < n) store(sbase + Smem::kring + ks * kKSlot, kKHalf, 16 * g + tok_in, xk[g]);
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * c + (lane >> 3) + 4 * i;
+                x[i] = lds16(raw + r * 128 + ((col ^ (r & 7)) << 4));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * c + (lane >> 3) + 4 * i;
+                const uint4 a = widen8(make_uint2(x[i].x, x[i].y)), b = widen8(make_uint2(x[i].z, x[i].w));
+                const uint32_t at = dst + sw * half_bytes + r * 128;
+                sts16(at + ((ch0 ^ (r & 7)) << 4), sw ? b : a);
+                sts16(at + ((ch1 ^ (r & 7)) << 4), sw ? a : b);
+            }
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar_kfull + 8 * ks);
-            if (++ks == kKSlots) {
-                ks = 0;
-                kph ^= 1;
-            }
-            have = step();
-            if (have) load(p.k_pool, xk);
-            // V, in halves
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (64 * h < n) {
-                    if (!(ok = mbar_waitw(bar_vempty + 8 * vs, vph ^ 1, abort))) break;
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        if (64 * h + 16 * g < n)
-                            store(sbase + Smem::vring + vs * kVSlot, kVHalf, 16 * g + tok_in, xv[4 * h + g]);
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_vfull + 8 * vs);
-                    if (++vs == kVSlots) {
-                        vs = 0;
-                        vph ^= 1;
+        };
+        do {
+#pragma unroll 1
+            for (int g = w.g0(); ok && g < w.g1(); g += 2) {
+                const int n = min(2, w.g1() - g);  // granules of the tile
+                if (!(ok = waitw(bar_kempty + 8 * k.s, k.ph ^ 1, abort))) break;
+#pragma unroll 1
+                for (int h = 0; h < n; ++h) {
+                    if (!(ok = waitw(bar_krfull + 8 * rk.s, rk.ph, abort))) break;
+                    widen(sbase + S::kraw + rk.s * kRaw, sbase + S::kring + k.s * kKSlot + h * (kGrain * 128), kKHalf);
+                    if (lane == 0) mbar_arrive(bar_krempty + 8 * rk.s);
+                    rk.next();
+                }
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(bar_kfull + 8 * k.s);
+                k.next();
+#pragma unroll 1
+                for (int h = 0; h < n; ++h) {
+                    if (!(ok = waitw(bar_vrfull + 8 * rv.s, rv.ph, abort))) break;
+                    if (!(ok = waitw(bar_vempty + 8 * v.s, v.ph ^ 1, abort))) break;
+                    widen(sbase + S::vraw + rv.s * kRaw, sbase + S::vring + v.s * kVSlot, kVHalf);
+                    if (lane == 0) {
+                        mbar_arrive(bar_vfull + 8 * v.s);
+                        mbar_arrive(bar_vrempty + 8 * rv.s);
                     }
+                    rv.next();
+                    v.next();
                 }
             }
-            if (!ok) break;
-        }
+        } while (ok && w.prev());
         if (!ok && lane == 0) {
             raise_abort();
             flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
@@ -740,76 +947,48 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         __syncwarp();
     } else if (warp == kSIssue) {
         // ====================== queries and S issue ======================
-        // Per segment the warp brings the unit's 128 flat rows in (256 bytes a
-        // row, swizzled; rows past the unit's are zeros) once the previous
-        // segment's products no longer read the buffer.  Then its first lane
-        // issues S_t = Q . K_t^T into S buffer t % 3, once K_t has landed and
-        // PV_{t-3} has read P_{t-3} out of that buffer.
+        // Per segment the warp brings the unit's flat rows in once the previous
+        // segment's products no longer read the buffer.  Then job after job: S = Q . K^T
+        // into the next S buffer, once the tile has landed and the P that the
+        // buffer held has been used.  The warp stays together and one lane
+        // issues: with the loop in one lane's branch the warp ran split from the
+        // second segment on, and its query loads took 11 us instead of 1.6.
         const uint32_t id_s = idesc(kRows, kTile, 0);
-        const uint64_t kd0 = sdesc(sbase + Smem::kring, 16, 1024);
-        uint64_t kd = kd0;
-        const uint64_t qd = sdesc(sbase + Smem::q, 16, 1024);
-        uint32_t kf = bar_kfull, ke = bar_kempty, ph = 0;
-        int s = 0, sb = 0, gt = 0, seg = 0;
-        uint32_t sph = 0;  // use parity of S buffer sb
+        const uint64_t kd0 = sdesc(sbase + S::kring, 16, 1024);
+        const uint64_t qd0 = sdesc(sbase + S::q, 16, 1024);
+        Ring<S::kslots> k;
+        Ring<kSBufs> b;
+        int seg = 0;
         bool ok = true;
         do {
-            const int nq = w.flat(), q0 = sm_qs[w.r];
-            int at[4];  // of rows lane, lane + 32, ..: (node, head) index, or -1
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = 32 * j + lane, f = w.t * kRows + i, node = f / group;
-                at[j] = i < nq ? (q0 + node) * p.hq + w.k * group + (f - node * group) : -1;
-            }
-            if (seg > 0 && !(ok = mbar_waitw(bar_qfree, (uint32_t)(seg - 1) & 1, abort))) break;
-            const int ch = lane & 15;
-            const uint32_t dst0 = sbase + Smem::q + (ch >> 3) * kHalfQ;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-#pragma unroll 4
-                for (int x = 0; x < 16; ++x) {
-                    const int rr = 2 * x + (lane >> 4), i = 32 * j + rr;
-                    const int a = __shfl_sync(0xffffffffu, at[j], rr);
-                    cp_async16(dst0 + i * 128 + (((ch & 7) ^ (i & 7)) << 4), p.q + (int64_t)max(a, 0) * kHeadDim + ch * 8,
-                               a >= 0);
-                }
-            }
+            // (parities of a phase before the first: such a wait passes at once)
+            if (!(ok = waitw(bar_qfree, (uint32_t)(seg + 1) & 1, abort))) break;
+            load_queries(w);
             asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                const int te = w.te();
-                for (int t0 = w.ta(); t0 < te; t0 += kTile, ++gt) {
-                    if (!(ok = mbar_wait1(kf, ph, abort))) break;
-                    if (gt >= kSBufs && !(ok = mbar_wait1(bar_o + 8 * sb, sph ^ 1, abort))) break;
-                    tc_fence_after();
-                    const uint32_t d = tmem + kColS + sb * kTile;
+            const int te = w.te();
+#pragma unroll 1
+            for (int t0 = w.ta(); ok && t0 < te; t0 += kTile) {
+                if (!(ok = wait4(lane ? bar_o + 8 * b.s : bar_kfull + 8 * k.s, lane ? b.ph ^ 1 : k.ph, abort))) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t kd = kd0 + (uint64_t)(k.s * (kKSlot >> 4));
+                    const uint32_t d = tmem + kColS + b.s * 128;
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t off = (uint32_t)((((ks >> 2) * kHalfQ) + (ks & 3) * 32) >> 4);
-                        umma_ss(d, qd + off, kd + off, id_s, ks > 0);
+                        const uint64_t off = (uint64_t)(((ks >> 2) * kHalfQ + (ks & 3) * 32) >> 4);
+                        umma_ss(d, qd0 + off, kd + off, id_s, ks > 0);
                     }
-                    umma_commit(bar_s + 8 * sb);
-                    umma_commit(ke);  // K_t is no longer read
-                    if (++sb == kSBufs) {
-                        sb = 0;
-                        sph ^= 1;
-                    }
-                    if (++s == kKSlots) {
-                        s = 0;
-                        ph ^= 1;
-                        kd = kd0;
-                        kf = bar_kfull;
-                        ke = bar_kempty;
-                    } else {
-                        kd += kKSlot >> 4;
-                        kf += 8;
-                        ke += 8;
-                    }
+                    umma_commit(bar_s + 8 * b.s);
+                    umma_commit(bar_kempty + 8 * k.s);  // the tile is no longer read
                 }
-                if (ok) umma_commit(bar_qfree);
+                __syncwarp();
+                b.next();
+                k.next();
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            if (ok && lane == 0) umma_commit(bar_qfree);
+            __syncwarp();
             ++seg;
         } while (ok && w.prev());
         if (lane == 0) {
@@ -818,364 +997,450 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                 flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
             }
             umma_commit(bar_sfin);
-            if (!mbar_drain1(bar_sfin, 0)) flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+            if (!drain1(bar_sfin, 0)) flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
         }
         __syncwarp();
     } else if (warp == kPvIssue) {
         // ============================ PV issue ===========================
-        // O += P_t . V_t once both V halves have landed and the softmax warps
-        // have stored P_t (and seen to V's rows that need it); a segment's first
-        // product starts O afresh, after the previous segment's O was read.
-        // K-steps past the last token are skipped.
-        if (lane == 0) {
-            const uint32_t id_o = idesc(kRows, 128, 1);
-            const uint64_t vd0 = sdesc(sbase + Smem::vring, kVHalf, 1024);
-            int va = 0;        // V slot of a tile's first half
-            uint32_t vph = 0;  // its fill parity
-            int pb = 0;        // S buffer holding P_t
-            uint32_t pph = 0;  // its use parity
-            int seg = 0;
-            bool ok = true;
-            do {
-                const int ta = w.ta(), te = w.te();
-                for (int t0 = ta; t0 < te; t0 += kTile) {
-                    int vb = va + 1;
-                    uint32_t vphb = vph;
-                    if (vb == kVSlots) {
-                        vb = 0;
-                        vphb ^= 1;
-                    }
-                    const bool two = te - t0 > 64;
-                    const int nsteps = (min(kTile, te - t0) + 15) / 16;
-                    if (!(ok = mbar_wait1(bar_vfull + 8 * va, vph, abort))) break;
-                    if (two && !(ok = mbar_wait1(bar_vfull + 8 * vb, vphb, abort))) break;
-                    if (!(ok = mbar_wait1(bar_p + 8 * pb, pph, abort))) break;
-                    if (t0 == ta && seg > 0 && !(ok = mbar_wait1(bar_odrained, (uint32_t)(seg - 1) & 1, abort))) break;
-                    tc_fence_after();
-                    const uint32_t pa = tmem + kColS + pb * kTile;
-                    const uint64_t da = vd0 + (uint64_t)(va * (kVSlot >> 4));
-                    const uint64_t db = vd0 + (uint64_t)(vb * (kVSlot >> 4));
+        // Job after job: O of its stream += P . V once V's tile has landed and
+        // the softmax warps have stored P (and seen to V's rows that need it); a
+        // segment's first products start the accumulators afresh, after the
+        // previous segment's were read out.  K-steps past the last token are
+        // skipped.
+        const uint32_t id_o = idesc(kRows, 128, 1);
+        const uint64_t vd0 = sdesc(sbase + S::vring, kVHalf, 1024);
+        Ring<S::vslots> v;
+        Ring<kSBufs> b;
+        int seg = 0;
+        bool ok = true;
+        do {
+            const int ta = w.ta(), te = w.te();
+#pragma unroll 1
+            for (int t0 = ta; ok && t0 < te; t0 += kTile) {
+                const int nsteps = (min(kTile, te - t0) + 15) / 16;
+                const bool two = te - t0 > kGrain;
+                // lane 0: V's first half; lane 1: its second; lane 2: the accumulator read out (a
+                // segment's first product); the others: P
+                uint32_t wbar = bar_p + 8 * b.s, wph = b.ph;
+                const int va = v.s;
+                if (lane == 0) wbar = bar_vfull + 8 * v.s, wph = v.ph;
+                v.next();
+                const int vb = v.s;
+                if (two) {
+                    if (lane == 1) wbar = bar_vfull + 8 * v.s, wph = v.ph;
+                    v.next();
+                }
+                if (lane == 2 && t0 == ta) wbar = bar_odrained, wph = (uint32_t)(seg + 1) & 1;
+                if (!(ok = wait4(wbar, wph, abort))) break;
+                const uint64_t da = vd0 + (uint64_t)(va * (kVSlot >> 4)), db = vd0 + (uint64_t)(vb * (kVSlot >> 4));
+                tc_fence_after();
+                if (lane == 0) {
                     // tokens 64 e .. 64 e + 63 sit in columns 64 e .. 64 e + 31
+                    const uint32_t pa = tmem + kColS + b.s * 128;
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
+                    for (int kk = 0; kk < 8; ++kk)
                         if (kk < nsteps)
-                            umma_ts(tmem + kColO, pa + (kk >> 2) * 64 + (kk & 3) * 8,
-                                    (kk < 4 ? da : db) + (uint64_t)((kk & 3) * 128), id_o,
-                                    (t0 > ta || kk > 0) ? 1u : 0u);
-                    }
-                    umma_commit(bar_o + 8 * pb);
+                            umma_ts(tmem, pa + (kk >> 2) * 64 + (kk & 3) * 8, (kk < 4 ? da : db) + (uint64_t)((kk & 3) * 128),
+                                    id_o, (t0 > ta || kk > 0) ? 1u : 0u);
+                    umma_commit(bar_o + 8 * b.s);
                     umma_commit(bar_vempty + 8 * va);
                     if (two) umma_commit(bar_vempty + 8 * vb);
-                    va = two ? vb + 1 : vb;
-                    vph = vphb;
-                    if (va == kVSlots) {
-                        va = 0;
-                        vph ^= 1;
-                    }
-                    if (++pb == kSBufs) {
-                        pb = 0;
-                        pph ^= 1;
-                    }
+                    if (t0 + kTile >= te) umma_commit(bar_fin);
                 }
-                ++seg;
-            } while (ok && w.prev());
+                __syncwarp();
+                b.next();
+            }
+            ++seg;
+        } while (ok && w.prev());
+        if (lane == 0) {
             if (!ok) {
                 raise_abort();
                 flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
             }
             umma_commit(bar_pfin);
-            if (!mbar_drain1(bar_pfin, 0)) flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+            if (!drain1(bar_pfin, 0)) flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
         }
         __syncwarp();
-    } else {
+    } else if (warp < kSoftWarps) {
         // ============================ softmax =============================
-        const int quarter = warp & 3, hf = warp >> 2;
-        const int i = quarter * 32 + lane;  // flat row of the unit, TMEM lane
+        const int quarter = warp & 3, wg = warp >> 2;
+        const int i = quarter * 32 + lane;  // flat row of the M block, TMEM lane
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-        float* xmax = reinterpret_cast<float*>(smem + Smem::xch);  // [2][2][128]
-        float* xsum = xmax + 4 * kRows;                            // [2][128]
+        float* sm_ref = reinterpret_cast<float*>(smem + S::ref);  // [2][128]: of even and odd jobs
+        float* sm_sum = reinterpret_cast<float*>(smem + S::sum);  // [2 groups][last reference, sum][128]
         bool ok = true;
-        int sb = 0, psb = 0;          // S buffer of this tile and of the previous one
-        uint32_t sph = 0, psph = 0;   // their use parities
-        int gt = 0, seg = 0;          // tiles and segments done by this block
-        int va = 0;                   // V slot of the tile's first half
-        uint32_t vph = 0;             // its fill parity
-        // the cut units to merge in the end: the one that goes on behind this
-        // block's range (stored first), the one that began before it
-        Unit cut[2];
-        int cutP[2] = {0, 0}, cutF[2] = {0, 0};
-        bool cutL[2] = {false, false};
-        uint32_t pubs = 0;
+        int job = 0, seg = 0;          // jobs and segments done by this block
+        int grain = 0;                 // granules
+        Ring<S::vslots> v;
+        Ring<kSBufs> b;
+        // The cut units' pieces that this block stores: the one that goes on behind its range
+        // (stored first), the one that began before it.
+        auto record = [&](int x) { return sm_misc + 16 + 16 * x; };
+        int stored = 0, counted = 0, gos = 0;  // pieces, and uses of bar_go
+        // Count the piece stored last.  Not at once: the release waits for its stores, and warp 0
+        // with it, so it comes at the end of the next segment, when they are long done (before
+        // a fold, lest blocks wait for each other in a row), or in the end.
+        auto count_piece = [&]() -> bool {
+            if (counted == stored) return true;
+            ++counted;
+            if (warp != 0) return true;
+            if (!waitw(bar_pub, counted - 1, abort)) return false;
+            if (lane == 0) {
+                volatile int* c = record(counted - 1);
+                int* word = p.heads + (int64_t)c[8] * kHeadInts;
+                if (c[7] == 2)
+                    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(word) : "memory");
+                else
+                    c[9] = count_up(word, c[7]) + 1;
+            }
+            return true;
+        };
         do {
-            const int r = w.r, C = sm_C[r], P = sm_P[r], nq = w.flat();
-            const int f = w.t * kRows + min(i, nq - 1);  // rows past the unit's shadow its last one
-            const int node = f / group, h = w.k * group + (f - node * group), g = sm_qs[r] + node;
-            const uint32_t* mrow = p.mask ? p.mask + (int64_t)g * p.words : nullptr;
+            const int r = w.r, P = sm_P[r], F = w.flat(), q0 = __ldg(p.q_start + r);
             const int ta = w.ta(), te = w.te();
             const float sc = p.scale * (kFp8 ? p.k_scale[w.k] : 1.f);
             // weights are powers of two: a scale of zero stands for the smallest one, so that
             // a masked score of -inf stays one
             const float scale_log2 = fmaxf(fabsf(sc) * kLog2e, 1e-37f);
             const bool flip = sc < 0.f;
-            uint32_t* odd = sm_odd + (seg & 1) * kMaxWords;
-            bool scanned = false;
-            float m = -INFINITY, l = 0.f;
-            for (int t0 = ta; t0 < te; t0 += kTile, ++gt) {
-                // ---- what this thread's row sees of its 64 tokens ----
-                const int base = t0 + hf * 64;
-                const bool nodes = t0 + kTile > P;  // the tile holds nodes
-                uint64_t vis = ~uint64_t(0);
-                if (base + 63 >= P) {
-                    const int rel = base - P;
-                    vis = mrow ? mask_bits(mrow, p.words, rel) : low_bits(node - rel + 1);
-                }
-                vis &= low_bits(te - base);
-                if (!(ok = mbar_waitw(bar_s + 8 * sb, sph, abort))) break;
-                tc_fence_after();
-                float s[64];
-                {
-                    uint32_t v0[32], v1[32];
-                    tmem_ld64(tmem + lane_base + kColS + sb * kTile + hf * 64, v0, v1);
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        s[c] = __uint_as_float(v0[c]);
-                        s[32 + c] = __uint_as_float(v1[c]);
-                    }
-                }
-                const uint32_t gone = (sm_bad[gt & 7] >> (4 * hf)) & 15u;
-                if (flip) {
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) s[c] = -s[c];
-                }
-                if (gone) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if ((gone >> e) & 1) vis &= ~(uint64_t(0xffff) << (16 * e));
-                }
-                if (__any_sync(0xffffffffu, vis != ~uint64_t(0))) {
-                    const uint32_t lo = (uint32_t)vis, hi = (uint32_t)(vis >> 32);
-#pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        s[c] = ((c < 32 ? lo : hi) >> (c & 31)) & 1 ? s[c] : -INFINITY;
-                }
-                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int c = 0; c < 64; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
-                const float pm = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                xmax[((gt & 1) * 2 + hf) * kRows + i] = pm;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_x + 8 * (gt & 1));
-                if (!(ok = mbar_waitw(bar_x + 8 * (gt & 1), ((uint32_t)gt >> 1) & 1, abort))) break;
-                // every softmax warp is past the previous segment: its odd nodes' words are free
-                if (t0 == ta && tid < kMaxWords) sm_odd[((seg + 1) & 1) * kMaxWords + tid] = 0;
-                const float mx = fmaxf(pm, xmax[((gt & 1) * 2 + (hf ^ 1)) * kRows + i]) * scale_log2;
-                // Lazy rescaling: the reference maximum m only moves when a score
-                // exceeds it by more than 2^8 (weights stay <= 256, exact enough in
-                // fp16).  A row that sees nothing yet stays at m = -inf with zero weights.
-                float alpha = 1.f;
-                bool moved = false;
-                if (mx > m + 8.f) {
-                    alpha = fast_exp2(m - mx);  // 0 while m is -inf
-                    m = mx;
-                    moved = t0 > ta;
-                }
-                const float mneg = m == -INFINITY ? 0.f : -m;
-                uint32_t pk[32];
-                // scores in pairs: one packed FMA for the exponents, one packed add
-                // for the row sums; P is rounded to fp16 for the product (2^-11 a weight)
-                const uint64_t sc2 = f32x2(scale_log2, scale_log2), mn2 = f32x2(mneg, mneg);
-                uint64_t rs2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    float x0, x1;
-                    f32x2_split(fma_f32x2(f32x2(s[2 * c], s[2 * c + 1]), sc2, mn2), x0, x1);
-                    const float e0 = fast_exp2(x0);
-                    const float e1 = fast_exp2(x1);
-                    pk[c] = pack_half2(e0, e1);
-                    rs2[c & 1] = add_f32x2(rs2[c & 1], f32x2(e0, e1));
-                }
-                float r0, r1, r2, r3;
-                f32x2_split(rs2[0], r0, r1);
-                f32x2_split(rs2[1], r2, r3);
-                l = l * alpha + ((r0 + r1) + (r2 + r3));
-                // O is rescaled only after the previous PV product is complete.
-                if (__any_sync(0xffffffffu, moved)) {
-                    if (!(ok = mbar_waitw(bar_o + 8 * psb, psph, abort))) break;
-                    tc_fence_after();
+            const bool whole = w.whole();
+            int first = 0;
+            const int np = whole ? 1 : sp.pieces(w, first);
+            first += base_block;
+            // this group's last reference and its sum of the row's weights
+            float ref = -INFINITY, l = 0.f;
 #pragma unroll 1
-                    for (int c0 = 0; c0 < 64; c0 += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(tmem + lane_base + kColO + hf * 64 + c0, v);
+            for (int t0 = ta; ok && t0 < te; t0 += kTile) {
+                const bool nodes = t0 + kTile > P;  // the tile holds nodes
+                const bool two = te - t0 > kGrain;
+                const int va = v.s;
+                const uint32_t va_ph = v.ph;
+                v.next();
+                const int vb = v.s;
+                const uint32_t vb_ph = v.ph;
+                if (two) v.next();
+                if ((job & 1) == wg) {
+                    // what this thread's flat row sees of a tile that holds nodes, 32 tokens a word
+                    uint32_t vis[4];
+                    if (nodes) {
+                        const int node = div_of(min(w.f0() + i, F - 1), group);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * alpha);
-                        tmem_st32(tmem + lane_base + kColO + hf * 64 + c0, v);
-                    }
-                }
-                // P over the first 32 of this half's own 64 S columns (already read)
-                tmem_st32(tmem + lane_base + kColS + sb * kTile + hf * 64, pk);
-                // ---- V of a tile that holds nodes: zero what is no number (and rows
-                // past the last token, up to the last k-step's end) ----
-                int vb = va + 1;
-                uint32_t vphb = vph;
-                if (vb == kVSlots) {
-                    vb = 0;
-                    vphb ^= 1;
-                }
-                const bool two = te - t0 > 64;
-                if (nodes) {
-                    scanned = true;
-                    if (!(ok = mbar_waitw(bar_vfull + 8 * va, vph, abort))) break;
-                    if (two && !(ok = mbar_waitw(bar_vfull + 8 * vb, vphb, abort))) break;
-                    const int vrows = min(kTile, te - t0), row = tid & 127, up = tid >> 7;  // up: dims 64 ..
-                    const uint32_t at = sbase + Smem::vring + (row >= 64 ? vb : va) * kVSlot + up * kVHalf + (row & 63) * 128;
-                    if (row < vrows && t0 + row >= P) {
-                        uint32_t any_odd = 0;
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const uint4 x = lds16(at + (((c + row) & 7) << 4));
-                            any_odd |= no_number(x.x) | no_number(x.y) | no_number(x.z) | no_number(x.w);
+                        for (int e = 0; e < 4; ++e) {
+                            const int rel = t0 + 32 * e - P;
+                            vis[e] = rel <= -32 ? ~0u
+                                     : p.mask   ? mask_bits(p.mask + (int64_t)(q0 + node) * p.words, p.words, rel)
+                                                : low_bits(node - rel + 1);
                         }
-                        if (any_odd) {
-                            for (int c = 0; c < 8; ++c) {
-                                uint4 x = lds16(at + (c << 4));
-                                uint32_t* e = reinterpret_cast<uint32_t*>(&x);
-                                for (int d = 0; d < 4; ++d) {
-                                    const uint32_t o = no_number(e[d]);
-                                    if (o & 0x8000u) e[d] &= 0xffff0000u;
-                                    if (o & 0x80000000u) e[d] &= 0x0000ffffu;
-                                }
-                                sts16(at + (c << 4), x);
+                    }
+                    if (!(ok = waitw(bar_s + 8 * b.s, b.ph, abort))) break;
+                    tc_fence_after();
+                    const uint32_t scol = tmem + lane_base + kColS + b.s * 128;
+                    const uint32_t gone = sm_bad[grain & 31] | (two ? sm_bad[(grain + 1) & 31] << 4 : 0u);
+                    if (nodes || !two || gone || flip) {
+                        // ---- tokens that this thread's flat row does not see: their scores become
+                        // -inf (and all are negated where the scale is negative) ----
+                        const uint32_t sign = flip ? 0x80000000u : 0u;
+#pragma unroll 1
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t see = low_bits(te - t0 - 32 * e);
+                            if (nodes) {
+                                see &= vis[0];
+                                vis[0] = vis[1];
+                                vis[1] = vis[2];
+                                vis[2] = vis[3];
                             }
-                            const int j = t0 + row - P;
-                            atomicOr(&odd[j >> 5], 1u << (j & 31));
-                        }
-                    } else if (row >= vrows && row < (vrows + 15) / 16 * 16) {
+                            if ((gone >> (2 * e)) & 1) see &= 0xffff0000u;
+                            if ((gone >> (2 * e)) & 2) see &= 0x0000ffffu;
+                            uint32_t x[32];
+                            tmem_ld32(scol + 32 * e, x);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) sts16(at + (((c + row) & 7) << 4), make_uint4(0, 0, 0, 0));
+                            for (int c = 0; c < 32; ++c) x[c] = (see >> c) & 1 ? x[c] ^ sign : 0xff800000u;
+                            tmem_st32(scol + 32 * e, x);
+                        }
+                        tmem_st_wait();
                     }
-                    fence_async_smem();
+                    float s[64];
+                    auto load = [&](int e) {
+                        uint32_t v0[32], v1[32];
+                        tmem_ld64(scol + e * 64, v0, v1);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            s[c] = __uint_as_float(v0[c]);
+                            s[32 + c] = __uint_as_float(v1[c]);
+                        }
+                    };
+                    // the row's maximum: half 0, then half 1, which stays in registers
+                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int e = 0; e < 2; ++e) {
+                        load(e);
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
+                    }
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
+                    // The reference so far comes from the job before, the other group's.  Lazy
+                    // rescaling: it only moves when a score exceeds it by more than 2^8 (weights
+                    // stay <= 256, exact enough in fp16).  A row that sees nothing yet stays at
+                    // -inf with zero weights.
+                    float now = -INFINITY, alpha = 1.f;
+                    bool moved = false;
+                    if (t0 > ta) {
+                        if (!(ok = waitw(bar_m + 8 * ((wg ^ 1) * 4 + quarter), ((uint32_t)(job - 1) >> 1) & 1, abort))) break;
+                        now = sm_ref[((job - 1) & 1) * kRows + i];
+                    }
+                    if (mx > now + 8.f) {
+                        alpha = fast_exp2(now - mx);  // 0 while it is -inf
+                        now = mx;
+                        moved = t0 > ta;
+                    }
+                    sm_ref[(job & 1) * kRows + i] = now;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_m + 8 * (wg * 4 + quarter));
+                    l *= ref == now ? 1.f : fast_exp2(ref - now);  // 0 while ref is -inf
+                    ref = now;
+                    const float mneg = now == -INFINITY ? 0.f : -now;
+                    // scores in pairs: one packed FMA for the exponents, one packed add for the
+                    // row sums; P is rounded to fp16 for the product (2^-11 a weight) and goes
+                    // over the first 32 of the half's own 64 S columns, already read
+                    const uint64_t sc2 = f32x2(scale_log2, scale_log2), mn2 = f32x2(mneg, mneg);
+                    uint64_t rs2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+#pragma unroll 1
+                    for (int e = 1; e >= 0; --e) {
+                        if (e == 0) load(0);
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            float x0, x1;
+                            f32x2_split(fma_f32x2(f32x2(s[2 * c], s[2 * c + 1]), sc2, mn2), x0, x1);
+                            const float e0 = fast_exp2(x0);
+                            const float e1 = fast_exp2(x1);
+                            pk[c] = pack_half2(e0, e1);
+                            rs2[c & 1] = add_f32x2(rs2[c & 1], f32x2(e0, e1));
+                        }
+                        tmem_st32(scol + e * 64, pk);
+                    }
+                    float r0, r1, r2, r3;
+                    f32x2_split(rs2[0], r0, r1);
+                    f32x2_split(rs2[1], r2, r3);
+                    l += (r0 + r1) + (r2 + r3);
+                    // O is rescaled only after the product before is complete
+                    if (__any_sync(0xffffffffu, moved)) {
+                        if (!(ok = waitw(bar_o + 8 * ((job - 1) % kSBufs), (uint32_t)((job - 1) / kSBufs) & 1, abort))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < 128; c0 += 32) {
+                            uint32_t x[32];
+                            tmem_ld32(tmem + lane_base + c0, x);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) x[c] = __float_as_uint(__uint_as_float(x[c]) * alpha);
+                            tmem_st32(tmem + lane_base + c0, x);
+                        }
+                    }
+                    // ---- V of a tile that holds nodes: zero what is no number (and rows past
+                    // the last token, up to the last k-step's end) ----
+                    if (nodes) {
+                        // the product two jobs before first: then the slots' fills before are used, and a
+                        // wait for this fill's parity means this fill (vslots >= 4)
+                        if (!(ok = waitw(bar_o + 8 * ((job + 1) % kSBufs), (uint32_t)((job + 1) / kSBufs + 1) & 1, abort)))
+                            break;
+                        if (!(ok = waitw(bar_vfull + 8 * va, va_ph, abort))) break;
+                        if (two && !(ok = waitw(bar_vfull + 8 * vb, vb_ph, abort))) break;
+                        const int vrows = min(kTile, te - t0);
+                        const uint32_t at = sbase + S::vring + (i >= kGrain ? vb : va) * kVSlot + (i & 63) * 128;
+                        if (i < vrows && t0 + i >= P) {
+                            uint32_t any_odd = 0;
+#pragma unroll 4
+                            for (int c = 0; c < 16; ++c) {
+                                const uint4 x = lds16(at + (c >> 3) * kVHalf + (((c + i) & 7) << 4));
+                                any_odd |= no_number(x.x) | no_number(x.y) | no_number(x.z) | no_number(x.w);
+                            }
+                            if (any_odd) {
+#pragma unroll 1
+                                for (int c = 0; c < 16; ++c) {
+                                    const uint32_t a = at + (c >> 3) * kVHalf + ((c & 7) << 4);
+                                    uint4 x = lds16(a);
+                                    uint32_t* e = reinterpret_cast<uint32_t*>(&x);
+                                    for (int d = 0; d < 4; ++d) {
+                                        const uint32_t o = no_number(e[d]);
+                                        if (o & 0x8000u) e[d] &= 0xffff0000u;
+                                        if (o & 0x80000000u) e[d] &= 0x0000ffffu;
+                                    }
+                                    sts16(a, x);
+                                }
+                                sm_misc[9] = 1;
+                            }
+                        } else if (i >= vrows && i < (vrows + 15) / 16 * 16) {
+#pragma unroll 4
+                            for (int c = 0; c < 16; ++c)
+                                sts16(at + (c >> 3) * kVHalf + (((c + i) & 7) << 4), make_uint4(0, 0, 0, 0));
+                        }
+                        fence_async_smem();
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_p + 8 * b.s);
                 }
-                va = two ? vb + 1 : vb;
-                vph = vphb;
-                if (va == kVSlots) {
-                    va = 0;
-                    vph ^= 1;
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_p + 8 * sb);
-                psb = sb;
-                psph = sph;
-                if (++sb == kSBufs) {
-                    sb = 0;
-                    sph ^= 1;
-                }
+                ++job;
+                b.next();
+                grain += 1 + two;
             }
             if (!ok) break;
-            // ---- end of the segment: wait for its last PV product, add the two
-            // halves' row sums ----
-            if (!(ok = mbar_waitw(bar_o + 8 * psb, psph, abort))) break;
-            xsum[hf * kRows + i] = l;
+            // ---- end of the segment: its last PV product (which every job's P came
+            // before), the two groups' sums ----
+            sm_sum[wg * 2 * kRows + i] = ref;
+            sm_sum[(wg * 2 + 1) * kRows + i] = l;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_l);
-            if (!(ok = mbar_waitw(bar_l, (uint32_t)seg & 1, abort))) break;
+            if (!(ok = waitw(bar_l, (uint32_t)seg & 1, abort))) break;
+            if (!(ok = waitw(bar_fin, (uint32_t)seg & 1, abort))) break;
             tc_fence_after();
-            const float L = l + xsum[(hf ^ 1) * kRows + i];
-            bool any_odd = false;
-            if (scanned) any_odd = __any_sync(0xffffffffu, odd[lane] != 0);
-            uint32_t v[32], v2[32];
-            tmem_ld64(tmem + lane_base + kColO + hf * 64, v, v2);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_odrained);  // O is free for the next segment
-            const bool mine = i < nq;
-            if (w.g0() == 0 && w.g1() == w.n) {
-                // ---- a whole unit: normalise and store ----
-                const float vsc = kFp8 ? p.v_scale[w.k] : 1.f;
-                const float inv = L == 0.f ? 0.f : __fdividef(vsc, L);
-                __half* orow = p.out + ((int64_t)g * p.hq + h) * kHeadDim + hf * 64;
-                if (mine && p.out_v8) {
-#pragma unroll
-                    for (int c = 0; c < 64; c += 16) {
-                        const uint32_t* u = c < 32 ? v + c : v2 + (c - 32);
-                        uint32_t w8[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            w8[e] = pack_half2(__uint_as_float(u[2 * e]) * inv, __uint_as_float(u[2 * e + 1]) * inv);
-                        st_v8(orow + c, w8);
+            const bool ends = w.g1() == w.n;
+            // the second of two pieces: wait for the first's partial, which its block stores
+            // before anything else
+            const bool fold = np == 2 && ends;
+            if (!(ok = count_piece())) break;
+            if (fold) {
+                // this is the block's last segment and its products are done: the K and V rings are
+                // idle and take the partial
+                if (tid == 0) {
+                    int* word = p.heads + (int64_t)first * kHeadInts;
+                    const uint64_t from = now_ns();
+                    int there;
+                    for (;;) {
+                        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(there) : "l"(word) : "memory");
+                        if (there || now_ns() - from > kWaitLimitNs || *abort) break;
+                        __nanosleep(20);
                     }
-                } else if (mine) {
-#pragma unroll
-                    for (int c = 0; c < 64; c += 8) {
-                        const uint32_t* u = c < 32 ? v + c : v2 + (c - 32);
-                        uint4 q4;
-                        q4.x = pack_half2(__uint_as_float(u[0]) * inv, __uint_as_float(u[1]) * inv);
-                        q4.y = pack_half2(__uint_as_float(u[2]) * inv, __uint_as_float(u[3]) * inv);
-                        q4.z = pack_half2(__uint_as_float(u[4]) * inv, __uint_as_float(u[5]) * inv);
-                        q4.w = pack_half2(__uint_as_float(u[6]) * inv, __uint_as_float(u[7]) * inv);
-                        *reinterpret_cast<uint4*>(orow + c) = q4;
+                    sm_misc[10] = there;
+                    if (there) {
+                        *word = 0;
+                        asm volatile("fence.proxy.async.global;" ::: "memory");
+                        mbar_arrive_expect_tx(bar_go, (uint32_t)kPartFloats * 4u);
+                        bulk_load(sbase + S::kring, p.part + (int64_t)first * 2 * kPartFloats, (uint32_t)kPartFloats * 4u, bar_go);
+                    } else {
+                        mbar_arrive(bar_go);
                     }
                 }
-                if (mine && any_odd) add_odd<kFp8>(p, odd, r, P, C, node, g, w.k, hf * 64, orow, nullptr);
-            } else {
-                // ---- a piece: store the partial and count it ----
-                const bool ends = w.g1() == w.n;
-                float* slot = p.part + ((int64_t)cta * 2 + ends) * kPartFloats;
-                if (hf == 0) {
-                    __stcg(slot + i, m);
-                    __stcg(slot + kRows + i, L);
+                if (!(ok = waitw(bar_go, gos & 1, abort) && sm_misc[10])) break;
+                ++gos;
+            }
+            // some node's V, of this segment or another, was no number
+            const bool any_odd = sm_misc[9] != 0;
+            const int j0 = max(ta - P, 0), j1 = te - P;  // the segment's nodes
+            const float vsc = kFp8 ? p.v_scale[w.k] : 1.f;
+            // this group's half of the dims
+            {
+                const int f = min(w.f0() + i, F - 1), node = div_of(f, group), h = w.k * group + (f - node * group);
+                const bool mine = w.f0() + i < F;
+                const float M0 = sm_sum[i], M1 = sm_sum[2 * kRows + i];
+                float M = fmaxf(M0, M1), a0 = 1.f, a2 = 0.f;
+                float Lr = (M0 == M ? sm_sum[kRows + i] : sm_sum[kRows + i] * fast_exp2(M0 - M)) +
+                           (M1 == M ? sm_sum[3 * kRows + i] : sm_sum[3 * kRows + i] * fast_exp2(M1 - M));
+                const float* before = reinterpret_cast<const float*>(smem + S::kring);  // fold: the first piece's
+                if (fold) {
+                    const float Ma = M, Mb = before[i], lb = before[kRows + i];
+                    M = fmaxf(Ma, Mb);
+                    a0 = Ma == -INFINITY ? 0.f : fast_exp2(Ma - M);
+                    a2 = Mb == -INFINITY ? 0.f : fast_exp2(Mb - M);
+                    Lr = Lr * a0 + lb * a2;
                 }
-                float4* po = reinterpret_cast<float4*>(slot + 2 * kRows) + hf * 16 * kRows + i;
-                if (mine) {
+                const bool out = whole || fold;
+                const float inv = !out ? 1.f : Lr == 0.f ? 0.f : __fdividef(vsc, Lr);
+                a0 *= inv;
+                a2 *= inv;
+                __half* orow = p.out + ((int64_t)(q0 + node) * p.hq + h) * kHeadDim + wg * 64;
+                float* slot = p.part + ((int64_t)blockIdx.x * 2 + ends) * kPartFloats;
+                if (!out && wg == 0) {
+                    __stcg(slot + i, M);
+                    __stcg(slot + kRows + i, Lr);
+                }
+                float4* po = reinterpret_cast<float4*>(slot + 2 * kRows) + wg * 16 * kRows + i;
+                const float4* pb = reinterpret_cast<const float4*>(before + 2 * kRows) + wg * 16 * kRows + i;
+                // sixteen dims at a time, rolled: this code runs once a segment, and fetching
+                // it costs more than running it
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 16) {
+                    uint32_t x[16];
+                    tmem_ld16(tmem + lane_base + wg * 64 + c, x);
+                    float o[16];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const uint32_t* u = e < 8 ? v + 4 * e : v2 + 4 * (e - 8);
-                        __stcg(po + e * kRows, make_float4(__uint_as_float(u[0]), __uint_as_float(u[1]),
-                                                           __uint_as_float(u[2]), __uint_as_float(u[3])));
+                    for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(x[e]) * a0;
+                    if (fold) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 y = pb[(c / 4 + e) * kRows];
+                            o[4 * e] += y.x * a2;
+                            o[4 * e + 1] += y.y * a2;
+                            o[4 * e + 2] += y.z * a2;
+                            o[4 * e + 3] += y.w * a2;
+                        }
                     }
-                    if (any_odd) add_odd<kFp8>(p, odd, r, P, C, node, g, w.k, hf * 64, nullptr, po);
+                    if (out && mine) {
+                        uint32_t u8[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) u8[e] = pack_half2(o[2 * e], o[2 * e + 1]);
+                        *reinterpret_cast<uint4*>(orow + c) = make_uint4(u8[0], u8[1], u8[2], u8[3]);
+                        *reinterpret_cast<uint4*>(orow + c + 8) = make_uint4(u8[4], u8[5], u8[6], u8[7]);
+                    } else if (mine) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            __stcg(po + (c / 4 + e) * kRows, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+                    }
                 }
-                __threadfence();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_odrained);  // O is free for the next segment
+                if (mine && any_odd)
+                    add_odd<kFp8>(p, r, P, j0, j1, node, q0 + node, w.k, wg * 64, out ? orow : nullptr, out ? nullptr : po);
+            }
+            if (!whole && !fold) {
+                if (tid == 0) {
+                    volatile int* c = record(stored);
+                    c[7] = np;
+                    c[8] = first;
+                    c[10] = w.r;
+                    c[11] = w.k;
+                    c[12] = w.t;
+                }
+                ++stored;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_pub);
-                const int x = cutP[0] ? 1 : 0;
-                cut[x] = w;
-                cutP[x] = sp.pieces(w, cutF[x]);
-                if (warp == 0) {
-                    // every softmax warp's stores are ordered before this count
-                    if (!(ok = mbar_waitw(bar_pub, pubs & 1, abort))) break;
-                    int old = 0;
-                    if (lane == 0) {
-                        __threadfence();
-                        old = atomicAdd(p.heads + (int64_t)cutF[x] * kHeadInts, 1);
-                        __threadfence();
-                    }
-                    cutL[x] = __shfl_sync(0xffffffffu, old, 0) == cutP[x] - 1;
-                }
-                ++pubs;
             }
             ++seg;
         } while (w.prev());
+        if (ok) ok = count_piece();
+        // ---- the cut units ----
+#pragma unroll 1
+        for (int x = 0; ok && x < stored; ++x) {
+            // (thread 0 wrote the record; the others read it after the wait)
+            volatile int* c = record(x);
+            if (tid == 0) {
+                c[6] = c[7] == 2 ? 0 : gather(p.heads + (int64_t)c[8] * kHeadInts, c[7], (int)blockIdx.x - c[8], c[9], c);
+                mbar_arrive(bar_go);
+            }
+            if (!(ok = waitw(bar_go, gos & 1, abort))) break;
+            ++gos;
+            const int np = c[7], first = c[8], r = c[10], k = c[11], t = c[12];
+            if (np == 2) continue;
+            const float vsc = kFp8 ? p.v_scale[k] : 1.f;
+            const int f0 = (plane + planes.n * t) * kRows, nq = min(kRows, sm_C[r] * group - f0);
+#pragma unroll 1
+            for (int y = -1; y < np; ++y) {
+                if (y < 0 ? !c[6] : !((c[y >> 5] >> (y & 31)) & 1)) continue;
+                merge_share<1, 8>(p, k, f0, __ldg(p.q_start + r), nq, np, first, y < 0 ? (int)blockIdx.x - first : y, vsc);
+            }
+        }
         if (!ok && lane == 0) {
             raise_abort();
             flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
-        }
-        if (ok) {
-#pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
-                if (!cutP[x]) break;
-                const Unit& u = cut[x];
-                const int nq = min(kRows, sm_C[u.r] * group - u.t * kRows);
-                merge_unit(p, u, sm_qs[u.r], nq, cutP[x], cutF[x], cutL[x], kFp8 ? p.v_scale[u.k] : 1.f);
-            }
         }
     }
 
     // ---- release tensor memory ----
     tc_fence_before();
     __syncthreads();
-    if (warp == 2) {
+    if (warp == kSIssue) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
     }
@@ -1183,6 +1448,12 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
 
 size_t head_bytes() { return align_up((size_t)kMaxGrid * kHeadInts * sizeof(int), 256); }
 size_t workspace_bytes() { return head_bytes() + (size_t)kMaxGrid * 2 * kPartFloats * sizeof(float); }
+
+template <bool kFp8>
+bool prepare_kernel() {
+    return cudaFuncSetAttribute(tree_kernel<kFp8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Smem<kFp8>::total) == cudaSuccess;
+}
 
 // Once per device: the SM count, and the kernels' shared-memory size.
 struct Device {
@@ -1199,10 +1470,7 @@ int device_blocks(int* blocks) {
     std::call_once(d.once, [&] {
         int sms = 0;
         if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0 ||
-            cudaFuncSetAttribute(tree_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::total()) !=
-                cudaSuccess ||
-            cudaFuncSetAttribute(tree_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::total()) !=
-                cudaSuccess) {
+            !prepare_kernel<false>() || !prepare_kernel<true>()) {
             d.status = PKV_ERR_CUDA;
             return;
         }
@@ -1214,7 +1482,7 @@ int device_blocks(int* blocks) {
 
 template <bool kFp8>
 int launch(const Params& prm, const CUtensorMap& km, const CUtensorMap& vm, int blocks, cudaStream_t stream) {
-    tree_kernel<kFp8><<<blocks, threads<kFp8>(), Smem::total(), stream>>>(km, vm, prm);
+    tree_kernel<kFp8><<<blocks, threads<kFp8>(), Smem<kFp8>::total, stream>>>(km, vm, prm);
     return launch_status();
 }
 
@@ -1248,17 +1516,18 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
         (mask && mask_words > kMaxWords))
         return PKV_ERR_UNSUPPORTED;
     const int group = q_heads / kv_heads;
-    // all units' granules, every (token, head) index and every pool row stay below 2^31
-    const int64_t granules = (int64_t)kv_heads * (((int64_t)total_q * group) / kRows + rows) *
-                             (((int64_t)max_seq_len + kGranule - 1) / kGranule);
+    // the units' sequence, every (token, head) index and every pool row stay below 2^31
+    const int64_t tiles = (int64_t)kv_heads * (((int64_t)total_q * group) / kRows + rows) *
+                          (((int64_t)max_seq_len + kGrain - 1) / kGrain + kUnitCost);
     const int64_t pool_rows = (int64_t)num_blocks * block_size;
-    if (granules >= (int64_t(1) << 31) || pool_rows >= (int64_t(1) << 31) - kTile ||
+    if (tiles >= (int64_t(1) << 31) || pool_rows >= (int64_t(1) << 31) - kTile ||
         (int64_t)total_q * q_heads >= (int64_t(1) << 31))
         return PKV_ERR_UNSUPPORTED;
     if (rows == 0 || total_q == 0) return PKV_OK;
     if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens || !q_start) return PKV_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool)) return PKV_ERR_INVALID_ARG;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < tree::workspace_bytes())
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
+        workspace_bytes < tree::workspace_bytes())
         return PKV_ERR_WORKSPACE;
 
     int blocks = 0, st = device_blocks(&blocks);
@@ -1266,7 +1535,6 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     Params prm{};
     prm.q = static_cast<const __half*>(q);
     prm.out = static_cast<__half*>(out);
-    prm.k_pool = k_pool;
     prm.v_pool = v_pool;
     prm.k_scale = k_scale;
     prm.v_scale = v_scale;
@@ -1285,18 +1553,24 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     prm.nb = num_blocks;
     prm.limit = max_seq_len;
     prm.scale = scale;
-    prm.out_v8 = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
     prm.heads = static_cast<int*>(workspace);
     prm.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + head_bytes());
     prm.dev_err = dev_err;
     prm.box = 16;  // the largest power of two that divides a page, at most a granule
-    while (prm.box < kGranule && block_size % (2 * prm.box) == 0) prm.box *= 2;
-    CUtensorMap km{}, vm{};
-    if (k_scale) return launch<true>(prm, km, vm, blocks, stream);
+    while (prm.box < kGrain && block_size % (2 * prm.box) == 0) prm.box *= 2;
+    const bool fp8 = k_scale != nullptr;
+    const int elt = fp8 ? 1 : 2;
     const int64_t dims[3] = {kHeadDim, kv_heads, pool_rows};
-    const int64_t strides[2] = {kHeadDim * 2, (int64_t)kv_heads * kHeadDim * 2};
-    const int box[3] = {64, 1, prm.box};
-    if ((st = encode_map_3d(k_pool, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, strides, box, &km)) != PKV_OK) return st;
-    if ((st = encode_map_3d(v_pool, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims, strides, box, &vm)) != PKV_OK) return st;
-    return launch<false>(prm, km, vm, blocks, stream);
+    const int64_t strides[2] = {kHeadDim * elt, (int64_t)kv_heads * kHeadDim * elt};
+    const int box[3] = {fp8 ? kHeadDim : 64, 1, prm.box};
+    const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap km, vm;
+    if ((st = encode_map_3d(k_pool, type, dims, strides, box, &km)) != PKV_OK) return st;
+    if ((st = encode_map_3d(v_pool, type, dims, strides, box, &vm)) != PKV_OK) return st;
+    int64_t nodes = total_q < max_seq_len ? total_q : max_seq_len;  // the most a row can have
+    if (mask && nodes > 32 * (int64_t)mask_words) nodes = 32 * (int64_t)mask_words;
+    const int64_t m = (nodes * group + kRows - 1) / kRows;
+    prm.planes.n = m < 1 ? 1 : m > kPlanes ? kPlanes : (int)m;
+    prm.planes.magic = prm.planes.n > 1 ? (uint32_t)((0x100000000ull + prm.planes.n - 1) / prm.planes.n) : 0u;
+    return fp8 ? launch<true>(prm, km, vm, blocks, stream) : launch<false>(prm, km, vm, blocks, stream);
 }
