@@ -16,9 +16,11 @@
 // of a unit's border moves to it, which spares a partial result of 64 KB for a
 // little imbalance.  Rows of several M blocks: M block m belongs to plane
 // m % planes, the blocks are shared out over the planes by their work, and each
-// plane is a sequence of its own.  Planes of equal work are walked in step, so
-// the M blocks of a row read its cache at the same time, from DRAM once: in one
-// sequence, 64 rows of 4096 tokens and 64 nodes took three times the traffic.
+// plane is a sequence of its own.  Planes of equal work get as many blocks each and
+// are walked in step, so the M blocks of a row read its cache at the same time,
+// from DRAM once: in one sequence, 64 rows of 4096 tokens and 64 nodes (three M
+// blocks) took three times the traffic, and with 51, 51 and 50 blocks, which drift
+// apart, 110 us instead of 104.
 //
 // Units cut over P blocks.  A block walks its range from the last unit to the
 // first, so a piece that others continue comes first.  It stores its partial
@@ -298,6 +300,11 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                  : "memory");
 }
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
@@ -539,7 +546,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
 
     // ---- barriers, tensor memory, descriptors ----
     if (tid == kPvIssue * 32) {
-        const int fill = kFp8 ? kConvWarps : 1;
+        const int fill = kFp8 ? kConvWarps / 2 : 1;
         for (int s = 0; s < S::kslots; ++s) {
             mbar_init(bar_kfull + 8 * s, fill);
             mbar_init(bar_kempty + 8 * s, 1);
@@ -550,9 +557,9 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         }
         for (int s = 0; s < S::raws; ++s) {
             mbar_init(bar_krfull + 8 * s, 1);
-            mbar_init(bar_krempty + 8 * s, kConvWarps);
+            mbar_init(bar_krempty + 8 * s, kConvWarps / 2);
             mbar_init(bar_vrfull + 8 * s, 1);
-            mbar_init(bar_vrempty + 8 * s, kConvWarps);
+            mbar_init(bar_vrempty + 8 * s, kConvWarps / 2);
         }
         for (int b = 0; b < kSBufs; ++b) {
             mbar_init(bar_s + 8 * b, 1);
@@ -670,6 +677,11 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                 later += Wi[x] > 0;
             }
             const float share = all > 0.f ? __fdividef((float)gridDim.x, all) : 0.f;
+            // planes of equal work get as many blocks each, so that they stay in step
+            bool even = true;
+#pragma unroll
+            for (int x = 1; x < kPlanes; ++x) even = even && (x >= planes.n || Wi[x] == Wi[0]);
+            const int each = (int)((uint64_t)gridDim.x * planes.magic >> 32);
             float upto = 0.f;
             int next = 0;
             W = 0;
@@ -677,7 +689,8 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             for (int x = 0; x < kPlanes; ++x) {
                 upto += Wf[x];
                 later -= Wi[x] > 0;
-                const int end = min(max(__float2int_rn(upto * share), next + (Wi[x] > 0)), (int)gridDim.x - later);
+                const int end = even ? next + (x < planes.n ? each : 0)
+                                     : min(max(__float2int_rn(upto * share), next + (Wi[x] > 0)), (int)gridDim.x - later);
                 if ((int)blockIdx.x >= next && (int)blockIdx.x < end) {
                     plane = x;
                     W = Wi[x];
@@ -883,60 +896,57 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         __syncwarp();
     } else if (kFp8 && warp >= kConv) {
         // ========================= FP8: widening =========================
-        // Thread (warp c, lane l) widens 16 codes (chunk l % 8) of tokens 16 c +
-        // l / 8 + 4 i of a granule: 32 bytes in two stores, the lanes of the upper
-        // dims the other way round, so that eight lanes meet eight bank groups.
-        // Rows past the last token hold whatever the slot held: never seen.
-        const int c = warp - kConv, col = lane & 7, sw = col >> 2;
-        const int ch0 = 2 * (col & 3) + sw, ch1 = 2 * (col & 3) + 1 - sw;
-        Ring<S::raws ? S::raws : 1> rk, rv;
-        Ring<S::kslots> k;
-        Ring<S::vslots> v;
+        // Two warps for K and two for V, so that neither waits for the other's slots (in one
+        // sequence the next tile's K came after this tile's V, whose slots are free only after
+        // the product two tiles before).  Thread (warp c, lane l) widens 8 codes (chunk l % 16) of
+        // tokens 32 c + l / 16 + 2 i of a granule: eight lanes write one row's 128 bytes of one
+        // half, so all banks at once.  Rows past the last token hold whatever the slot held:
+        // never seen.
+        const int c = (warp - kConv) & 1, col = lane & 15;
+        const bool is_v = warp - kConv >= 2;
+        uint32_t from[4], to[4];  // rows i and i + 4 have the same swizzle
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 32 * c + (lane >> 4) + 2 * i;
+            from[i] = sbase + (is_v ? S::vraw : S::kraw) + r * 128 + (((col >> 1) ^ (r & 7)) << 4) + (col & 1) * 8;
+            to[i] = sbase + (is_v ? S::vring + (col >> 3) * kVHalf : S::kring + (col >> 3) * kKHalf) + r * 128 +
+                    (((col & 7) ^ (r & 7)) << 4);
+        }
+        const uint32_t rfull0 = is_v ? bar_vrfull : bar_krfull, rempty0 = is_v ? bar_vrempty : bar_krempty;
+        const uint32_t full0 = is_v ? bar_vfull : bar_kfull, empty0 = is_v ? bar_vempty : bar_kempty;
+        Ring<S::raws ? S::raws : 1> raw;
+        int slot = 0;  // of the operand ring
+        uint32_t slot_ph = 0;
         bool ok = true;
-        auto widen = [&](uint32_t raw, uint32_t dst, uint32_t half_bytes) {
-            uint4 x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 16 * c + (lane >> 3) + 4 * i;
-                x[i] = lds16(raw + r * 128 + ((col ^ (r & 7)) << 4));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 16 * c + (lane >> 3) + 4 * i;
-                const uint4 a = widen8(make_uint2(x[i].x, x[i].y)), b = widen8(make_uint2(x[i].z, x[i].w));
-                const uint32_t at = dst + sw * half_bytes + r * 128;
-                sts16(at + ((ch0 ^ (r & 7)) << 4), sw ? b : a);
-                sts16(at + ((ch1 ^ (r & 7)) << 4), sw ? a : b);
-            }
-            fence_async_smem();
-            __syncwarp();
-        };
         do {
+            const int g1 = w.g1();
 #pragma unroll 1
-            for (int g = w.g0(); ok && g < w.g1(); g += 2) {
-                const int n = min(2, w.g1() - g);  // granules of the tile
-                if (!(ok = waitw(bar_kempty + 8 * k.s, k.ph ^ 1, abort))) break;
+            for (int g = w.g0(), h = 0; g < g1; ++g) {
+                // h: the granule of its tile; a tile's K is one slot, its V a slot a granule
+                if (!(ok = wait4(lane == 0 ? empty0 + 8 * slot : rfull0 + 8 * raw.s, lane == 0 ? slot_ph ^ 1 : raw.ph,
+                                 abort)))
+                    break;
+                const uint32_t src = raw.s * kRaw, dst = is_v ? slot * kVSlot : slot * kKSlot + h * (kGrain * 128);
 #pragma unroll 1
-                for (int h = 0; h < n; ++h) {
-                    if (!(ok = waitw(bar_krfull + 8 * rk.s, rk.ph, abort))) break;
-                    widen(sbase + S::kraw + rk.s * kRaw, sbase + S::kring + k.s * kKSlot + h * (kGrain * 128), kKHalf);
-                    if (lane == 0) mbar_arrive(bar_krempty + 8 * rk.s);
-                    rk.next();
+                for (int b = 0; b < 4096; b += 2048) {
+                    uint2 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = lds8(src + b + from[i & 3] + (i >> 2) * 1024);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sts16(dst + b + to[i & 3] + (i >> 2) * 1024, widen8(x[i]));
                 }
-                if (!ok) break;
-                if (lane == 0) mbar_arrive(bar_kfull + 8 * k.s);
-                k.next();
-#pragma unroll 1
-                for (int h = 0; h < n; ++h) {
-                    if (!(ok = waitw(bar_vrfull + 8 * rv.s, rv.ph, abort))) break;
-                    if (!(ok = waitw(bar_vempty + 8 * v.s, v.ph ^ 1, abort))) break;
-                    widen(sbase + S::vraw + rv.s * kRaw, sbase + S::vring + v.s * kVSlot, kVHalf);
-                    if (lane == 0) {
-                        mbar_arrive(bar_vfull + 8 * v.s);
-                        mbar_arrive(bar_vrempty + 8 * rv.s);
-                    }
-                    rv.next();
-                    v.next();
+                fence_async_smem();
+                __syncwarp();
+                const bool full = is_v || h || g + 1 == g1;
+                if (lane == 0) {
+                    mbar_arrive(rempty0 + 8 * raw.s);
+                    if (full) mbar_arrive(full0 + 8 * slot);
+                }
+                raw.next();
+                h = is_v ? 0 : h ^ 1;
+                if (full && ++slot == (is_v ? S::vslots : S::kslots)) {
+                    slot = 0;
+                    slot_ph ^= 1;
                 }
             }
         } while (ok && w.prev());
@@ -1098,15 +1108,9 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         do {
             const int r = w.r, P = sm_P[r], F = w.flat(), q0 = __ldg(p.q_start + r);
             const int ta = w.ta(), te = w.te();
-            const float sc = p.scale * (kFp8 ? p.k_scale[w.k] : 1.f);
-            // weights are powers of two: a scale of zero stands for the smallest one, so that
-            // a masked score of -inf stays one
-            const float scale_log2 = fmaxf(fabsf(sc) * kLog2e, 1e-37f);
-            const bool flip = sc < 0.f;
+            // (loaded here, first used when scores are there)
+            const float k_sc = kFp8 ? __ldg(p.k_scale + w.k) : 1.f, v_sc = kFp8 ? __ldg(p.v_scale + w.k) : 1.f;
             const bool whole = w.whole();
-            int first = 0;
-            const int np = whole ? 1 : sp.pieces(w, first);
-            first += base_block;
             // this group's last reference and its sum of the row's weights
             float ref = -INFINITY, l = 0.f;
 #pragma unroll 1
@@ -1134,6 +1138,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     }
                     if (!(ok = waitw(bar_s + 8 * b.s, b.ph, abort))) break;
                     tc_fence_after();
+                    // weights are powers of two: a scale of zero stands for the smallest one, so that
+                    // a masked score of -inf stays one
+                    const float sc = p.scale * k_sc, scale_log2 = fmaxf(fabsf(sc) * kLog2e, 1e-37f);
+                    const bool flip = sc < 0.f;
                     const uint32_t scol = tmem + lane_base + kColS + b.s * 128;
                     const uint32_t gone = sm_bad[grain & 31] | (two ? sm_bad[(grain + 1) & 31] << 4 : 0u);
                     if (nodes || !two || gone || flip) {
@@ -1292,6 +1300,9 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             sm_sum[(wg * 2 + 1) * kRows + i] = l;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar_l);
+            int first = 0;
+            const int np = whole ? 1 : sp.pieces(w, first);
+            first += base_block;
             if (!(ok = waitw(bar_l, (uint32_t)seg & 1, abort))) break;
             if (!(ok = waitw(bar_fin, (uint32_t)seg & 1, abort))) break;
             tc_fence_after();
@@ -1328,7 +1339,6 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             // some node's V, of this segment or another, was no number
             const bool any_odd = sm_misc[9] != 0;
             const int j0 = max(ta - P, 0), j1 = te - P;  // the segment's nodes
-            const float vsc = kFp8 ? p.v_scale[w.k] : 1.f;
             // this group's half of the dims
             {
                 const int f = min(w.f0() + i, F - 1), node = div_of(f, group), h = w.k * group + (f - node * group);
@@ -1346,7 +1356,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     Lr = Lr * a0 + lb * a2;
                 }
                 const bool out = whole || fold;
-                const float inv = !out ? 1.f : Lr == 0.f ? 0.f : __fdividef(vsc, Lr);
+                const float inv = !out ? 1.f : Lr == 0.f ? 0.f : __fdividef(v_sc, Lr);
                 a0 *= inv;
                 a2 *= inv;
                 __half* orow = p.out + ((int64_t)(q0 + node) * p.hq + h) * kHeadDim + wg * 64;

@@ -27,6 +27,9 @@ def units_of(lens, nodes, group, hk, plane, planes):
 
 def blocks_of(work, grid):
     """[(first, one past the last) block] of each plane."""
+    if len(set(work)) == 1 and work[0]:  # equal work: as many blocks each, in step
+        each = grid // len(work)
+        return [(x * each, (x + 1) * each) for x in range(len(work))]
     f = np.float32
     total = f(0)
     for w in work:
