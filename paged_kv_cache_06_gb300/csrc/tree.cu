@@ -83,9 +83,18 @@ constexpr int kMaxRows = 1024;
 constexpr int kMaxGrid = 192;  // blocks: one per SM, at most this many
 constexpr int kMaxWords = 32;  // mask words: up to 1024 nodes a row
 constexpr int kHeadInts = 32;  // ints between two units' words: count, then given-up blocks' bits
-constexpr int kUnitCost = 4;   // granules that a unit's queries, first scores and output cost in time
-constexpr int kMinSlack = 4;   // granules: a cut this near a unit's border moves to it
-static_assert(kMinSlack >= kUnitCost, "a cut that stays lies past the unit's fixed cost");
+// Granules that a unit's queries, first scores and output cost in time, and how near a
+// unit's border a cut moves to it (farther than the cost, so that a cut that stays lies
+// past it): a piece more costs its block a start, a partial and a merge, which is worth
+// some imbalance.  Over FP8 pools a segment starts later and its products come slower.
+// Measured, cost and slack: fp16, 32 rows of 16..512 and one of 4096, 8..24
+// nodes: 2, 5: 19.0 us; 4, 4: 21.0; 3, 6: 20.6; 6, 12: 23.4; 90 drawn batches'
+// geometric mean 15.3, 15.5, 15.1, 15.8.  FP8, 32 rows of 1024 and 25 nodes: 8, 12: 23.3;
+// 8, 8: 28.8; 4, 4: 30.7; 96 rows of 16..8192, chains of 3..7: 38.6; 41.2; 46.6.
+template <bool kFp8>
+__host__ __device__ constexpr int unit_cost() { return kFp8 ? 8 : 2; }
+template <bool kFp8>
+__host__ __device__ constexpr int unit_slack() { return kFp8 ? 12 : 5; }
 constexpr uint32_t kHalfQ = kRows * 128;   // 128 flat rows x 64 dims
 constexpr uint32_t kQBlock = 2 * kHalfQ;
 constexpr uint32_t kKHalf = kTile * 128;   // 128 tokens x 64 dims
@@ -180,6 +189,7 @@ __device__ __forceinline__ int div_of(int a, int b) {
 
 // A unit: M block plane + planes t of KV head k of row r, its place U in the
 // plane's sequence and its n granules; there it takes n + kUnitCost.
+template <int kUnitCost>
 struct Unit {
     int r, k, t, U, n;
     __device__ __forceinline__ int end() const { return U + n + kUnitCost; }
@@ -189,23 +199,25 @@ __device__ __noinline__ int cut_at(int x, int W, int G, int quo, int rem);
 
 // How a plane's sequence of units, W long, is cut over its G blocks: raw cut c lies at
 // floor(W c / G); one within `slack` of a border of its unit moves there.
+template <int kUnitCost>
 struct Split {
+    using Of = Unit<kUnitCost>;
     int W, G, slack, quo, rem;
-    __device__ __forceinline__ void set(int w, int blocks) {
+    __device__ __forceinline__ void set(int w, int blocks, int least) {
         W = w;
         G = min(blocks, max(w, 1));
         quo = W / G;
         rem = W - quo * G;
-        slack = max(kMinSlack, quo / 16);
+        slack = max(least, quo / 16);
     }
     __device__ __forceinline__ int raw(int c) const { return quo * c + div_of(rem * c, G); }
-    __device__ __forceinline__ int moved(int x, const Unit& u) const {
+    __device__ __forceinline__ int moved(int x, const Of& u) const {
         const int d0 = x - u.U, d1 = u.end() - x;
         if (min(d0, d1) > slack) return x;
         return d0 <= d1 ? u.U : u.end();
     }
     // The pieces of unit u (1: whole) and the plane's block that holds the first one.
-    __device__ __forceinline__ int pieces(const Unit& u, int& first) const {
+    __device__ __forceinline__ int pieces(const Of& u, int& first) const {
         const int a = u.U + slack + 1, b = u.end() - slack;  // cuts that stay lie in [a, b)
         if (a >= b) return 1;
         const int lo = cut_at(a, W, G, quo, rem), hi = cut_at(b, W, G, quo, rem);
@@ -250,7 +262,14 @@ __device__ __noinline__ int4 unit_before(int4 u, int hk, int group, int plane, i
 }
 
 // The units of a block's range [s0, e), last to first.
-struct Walk : Unit {
+template <int kUnitCost>
+struct Walk : Unit<kUnitCost> {
+    using Unit<kUnitCost>::r;
+    using Unit<kUnitCost>::k;
+    using Unit<kUnitCost>::t;
+    using Unit<kUnitCost>::U;
+    using Unit<kUnitCost>::n;
+    using Unit<kUnitCost>::end;
     int s0, e, hk, group, plane;
     Planes planes;
     const int* C;
@@ -509,6 +528,8 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
     tree_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const __grid_constant__ Params p) {
     using S = Smem<kFp8>;
+    constexpr int kUnitCost = unit_cost<kFp8>();
+    using Walk = tree::Walk<kUnitCost>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -641,7 +662,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
     // ---- this block's plane, the plane's blocks, and its range: the thread whose
     // row a cut falls in moves the cut ----
     int plane = 0, base_block = 0, run = 0, mine = 0;
-    Split sp;
+    Split<kUnitCost> sp;
     sp.W = 0;
     {
         // of this half's warps: the work before this one and the whole plane's
@@ -714,7 +735,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             }
             run = before + i - m;
             mine = hw < kHalfWarps ? m : 0;
-            sp.set(W, to - from);
+            sp.set(W, to - from, unit_slack<kFp8>());
         }
     }
     const int cta = (int)blockIdx.x - base_block;
@@ -1528,7 +1549,7 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     const int group = q_heads / kv_heads;
     // the units' sequence, every (token, head) index and every pool row stay below 2^31
     const int64_t tiles = (int64_t)kv_heads * (((int64_t)total_q * group) / kRows + rows) *
-                          (((int64_t)max_seq_len + kGrain - 1) / kGrain + kUnitCost);
+                          (((int64_t)max_seq_len + kGrain - 1) / kGrain + unit_cost<true>());
     const int64_t pool_rows = (int64_t)num_blocks * block_size;
     if (tiles >= (int64_t(1) << 31) || pool_rows >= (int64_t(1) << 31) - kTile ||
         (int64_t)total_q * q_heads >= (int64_t(1) << 31))

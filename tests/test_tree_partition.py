@@ -5,11 +5,19 @@ them, and at most one piece a block of either kind (one that goes on behind its
 range, one that began before it); and the counting by which the blocks of a cut
 unit find each other, under every kind of interleaving."""
 import random
+import sys
 
 import numpy as np
 import pytest
 
-MIN_SLACK, UNIT_COST, GRAIN, ROWS = 4, 4, 64, 128
+UNIT_COST, MIN_SLACK, GRAIN, ROWS = 2, 5, 64, 128
+
+
+@pytest.fixture(params=[(2, 5), (8, 12)], autouse=True)
+def costs(request, monkeypatch):
+    """A unit's fixed cost in granules, and how near its border a cut moves: fp16 pools, FP8 pools."""
+    monkeypatch.setattr(sys.modules[__name__], "UNIT_COST", request.param[0])
+    monkeypatch.setattr(sys.modules[__name__], "MIN_SLACK", request.param[1])
 
 
 def units_of(lens, nodes, group, hk, plane, planes):
