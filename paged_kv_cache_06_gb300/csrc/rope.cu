@@ -12,10 +12,9 @@
 // rounded once: to fp16, or for E4M3 pools straight from the 32-bit value
 // (no fp16 rounding in between).
 //
-// Work.  A thread block takes kTokens tokens (or one, for small batches).  Warp
-// t finds token t's row and pool slot while the other threads make the block's
-// table of factors, one pair a thread, shared by all heads; then each item is
-// sixteen rotated dims of one head (two 16-byte vectors), eight passed-through
+// Work.  A thread block takes some tokens.  A thread a token finds its row and pool
+// slot; all make the block's table of factors, one pair a thread, shared by all heads;
+// then each item is sixteen rotated dims of one head (two 16-byte vectors), eight passed-through
 // dims, or eight dims of a value.  A thread's first item is loaded before the
 // table is made, so the two latencies overlap.
 #include <math.h>
@@ -27,7 +26,8 @@ namespace pkv {
 namespace rope {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 4;  // tokens per block of a large batch
+constexpr int kBlocks = 5;   // resident per SM
+constexpr int kTokens = 32;  // tokens per block, at most
 
 // n / d for n < 2^16 and 1 <= d < 2^16, by one multiplication.
 struct Div {
@@ -57,18 +57,17 @@ struct Params {
     Div per_head, pass_head, val_head, per_token;
 };
 
-// The row r whose chunk holds token g (q_start[r] <= g < q_start[r + 1]), found
-// by the whole warp, 32 entries a round; -1 for a token behind the last row.
+// The row r whose chunk holds token g (q_start[r] <= g < q_start[r + 1]); -1 for a
+// token behind the last row.
 __device__ __forceinline__ int row_of(const int32_t* q_start, int rows, int g) {
-    const int lane = threadIdx.x & 31;
     int lo = 0, n = rows + 1;  // entries lo .. lo + n - 1; q_start[lo] <= g
     while (n > 1) {
-        const int step = (n + 31) / 32;
-        const int i = lane * step;
-        const unsigned below = __ballot_sync(0xffffffffu, i < n && q_start[lo + i] <= g);
-        const int top = below ? 31 - __clz(below) : 0;
-        lo += top * step;
-        n = min(step, n - top * step);
+        const int m = (n + 3) >> 2;  // three entries at once
+        int c = 0;
+#pragma unroll
+        for (int e = 1; e < 4; ++e) c += e * m < n && __ldg(q_start + lo + e * m) <= g;
+        lo += c * m;
+        n = min(m, n - c * m);
     }
     return lo < rows ? lo : -1;
 }
@@ -113,10 +112,10 @@ struct Item {
 };
 
 template <bool kFp8, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ Params p, int tokens) {
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const __grid_constant__ Params p, int tokens) {
     extern __shared__ float2 factors[];  // [tokens][4][rot / 16][2]
     __shared__ int sm_slot[kTokens], sm_pos[kTokens];
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const int g0 = blockIdx.x * tokens;
     const int nt = min(tokens, p.total - g0);
     const int half = p.rot / 2, chunks = p.rot / 16;
@@ -157,31 +156,29 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
     Item it = load(tid);
 
     // ---- each token's row, slot and position ----
-    for (int t = warp; t < nt; t += kThreads / 32) {
+    if (tid < nt) {
+        const int t = tid;
         const int g = g0 + t;
         const int r = row_of(p.q_start, p.rows, g);
         int slot = -2, pos = 0;  // -2: the token is left alone; -1: only its keys and values are
         if (r >= 0) {
             const int q0 = p.q_start[r], C = p.q_start[r + 1] - q0, L = p.seq_lens[r];
             if (C < 0 || L < C || L > p.limit || q0 < 0 || q0 > p.total - C) {
-                if ((tid & 31) == 0) flag_error(p.dev_err, PKV_DEV_ERR_SEQ_LEN);
+                flag_error(p.dev_err, PKV_DEV_ERR_SEQ_LEN);
             } else if (g >= q0 && g - q0 < C) {
                 pos = L - C + (g - q0);
                 const int lb = pos / p.bs;
                 const int pb = lb < p.mbpr ? p.tables[(int64_t)r * p.mbpr + lb] : -1;
                 slot = -1;
                 if (pb < 0 || pb >= p.nb) {
-                    if ((tid & 31) == 0)
-                        flag_error(p.dev_err, lb < p.mbpr ? PKV_DEV_ERR_BLOCK_ID : PKV_DEV_ERR_POSITION);
+                    flag_error(p.dev_err, lb < p.mbpr ? PKV_DEV_ERR_BLOCK_ID : PKV_DEV_ERR_POSITION);
                 } else {
                     slot = pb * p.bs + pos % p.bs;  // below 2^31 (checked by the host)
                 }
             }
         }
-        if ((tid & 31) == 0) {
-            sm_slot[t] = slot;
-            sm_pos[t] = p.rope_positions ? p.rope_positions[g] : pos;
-        }
+        sm_slot[t] = slot;
+        sm_pos[t] = p.rope_positions ? p.rope_positions[g] : pos;
     }
     __syncthreads();
 
@@ -319,7 +316,7 @@ extern "C" int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, con
     if ((k_scale == nullptr) != (v_scale == nullptr)) return PKV_ERR_INVALID_ARG;
     if (head_dim % 8 || rot_dim % 16) return PKV_ERR_UNSUPPORTED;
     // the item index of a block stays below 2^16 and a slot below 2^31
-    if (((int64_t)q_heads + 2 * kv_heads) * (head_dim / 8) * kTokens >= 65536 || rot_dim > 1024 ||
+    if (((int64_t)q_heads + 2 * kv_heads) * (head_dim / 8) * 4 >= 65536 || rot_dim > 1024 ||
         (int64_t)num_blocks * block_size >= (int64_t(1) << 31))
         return PKV_ERR_UNSUPPORTED;
     if (rows == 0 || total_q == 0) return PKV_OK;
@@ -373,7 +370,16 @@ extern "C" int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, con
     p.pass_head = make_div(pass > 0 ? pass : 1);
     p.val_head = make_div(head_dim / 8);
     p.per_token = make_div(p.n_pair + p.n_pass + p.n_val);
-    const int tokens = total_q < 4 * 152 ? 1 : kTokens;
+    // As many tokens a block as fill the SMs once: small batches take a block a token, the
+    // shortest path; large ones pay for the look-up and the table of factors once a block,
+    // all blocks are resident together, and no last wave runs alone.  Measured: 32 tokens:
+    // 3.1 us (a token a block); 640 tokens, half of each head rotated, E4M3: a token a
+    // block 4.3 us, four 5.4; 15,000 tokens: 20 a block 24.8 us, 4 a block 26.7, 8 a block
+    // 26.4, 16 a block 27.3 (one and a half waves).
+    const int items = p.n_pair + p.n_pass + p.n_val, wave = 152 * kBlocks;
+    int tokens = total_q < wave ? 1 : (total_q + wave - 1) / wave;
+    if (tokens > kTokens) tokens = kTokens;
+    if (tokens > 65535 / items) tokens = 65535 / items;
     const int grid = (total_q + tokens - 1) / tokens;
     const size_t smem = (size_t)tokens * (rot_dim / 2) * sizeof(float2);
     const bool il = layout == PKV_ROPE_INTERLEAVED;
