@@ -492,7 +492,8 @@ int pkv_rope_rates(uint64_t* rates, const double* freqs, int n);
  * q: fp16, token g's heads at q + g * q_stride (elements; a multiple of 8, at
  * least q_heads * head_dim), so q, k_new and v_new may be views of one
  * projection's output; q_out: fp16 [total_q][q_heads][head_dim], contiguous.
- * q_out == q is allowed when q_stride == q_heads * head_dim.  q_heads == 0
+ * q_out == q is allowed when q_stride == q_heads * head_dim; any other overlap
+ * of q_out with q, k_new or v_new is PKV_ERR_INVALID_ARG.  q_heads == 0
  * (q, q_out unused) writes keys and values only.  k_new, v_new: fp16, strides
  * likewise, at least kv_heads * head_dim.
  * Pools: fp16 when k_scale == v_scale == null (values copied bit-exactly),
@@ -534,7 +535,7 @@ int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, const float* k
  * over the tokens it sees, head h reading KV head h / (q_heads / kv_heads).  A
  * node that sees nothing gives zeros.  Tokens that a node does not see do not
  * reach its output whatever they hold (infinities and NaN included).
- * q, out: fp16 [total_q][q_heads][head_dim].  mask: device uint32
+ * q, out: fp16 [total_q][q_heads][head_dim], not overlapping.  mask: device uint32
  * [total_q][mask_words]; a row of more than 32 * mask_words nodes is skipped
  * and flagged PKV_DEV_ERR_MASK.  Pools: fp16 when k_scale == v_scale == null,
  * else E4M3 codes with one scale per KV head (as in
@@ -574,7 +575,7 @@ size_t paged_attention_tree_workspace_size(int rows, int total_q, int q_heads, i
  * accepted nodes of row r, strictly increasing node indices below C_r.  For
  * each j < path_lens[r], each layer and both pools, the slot of position
  * P_r + j becomes a bit-exact copy of what the slot of P_r + path[r][j] held
- * before the call.  new_seq_lens (may be null; must not overlap seq_lens):
+ * before the call.  new_seq_lens (may be null; must not overlap an input):
  * device int32 [rows], new_seq_lens[r] = P_r + path_lens[r].  A path that is
  * no such list, or path_lens[r] outside [0, min(max_path, C_r)], skips the row
  * (its new length too) and sets PKV_DEV_ERR_POSITION; a table entry out of
@@ -653,7 +654,7 @@ int pkv_debug_set_decode_hooks(unsigned poll_limit, const void* stuck_word);
  * *host_err and clear it on the device.  Returns PKV_ERR_CUDA if the stream
  * reported an error.  The only library call that blocks.  If the word holds
  * PKV_DEV_ERR_TIMEOUT, the outputs of the calls that reported into it are
- * invalid, and every decode or prefill workspace those calls used must be
+ * invalid, and every decode, prefill or tree workspace those calls used must be
  * zero-filled again before its next use (the library's own scratch is
  * cleared by its next call).
  */

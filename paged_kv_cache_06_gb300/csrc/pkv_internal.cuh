@@ -29,6 +29,11 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
+// Whether `a_bytes` at a and `b_bytes` at b have a byte in common.
+inline bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 inline int launch_status() {

@@ -328,7 +328,14 @@ extern "C" int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, con
         v_stride % 8)
         return PKV_ERR_INVALID_ARG;
     // in place only where each output lies exactly over its input
-    if (q_heads > 0 && q_out == q && q_stride != qd) return PKV_ERR_INVALID_ARG;
+    if (q_heads > 0) {
+        const size_t out = (size_t)total_q * qd * 2;
+        auto over = [&](const void* x, int64_t stride, int64_t width) {
+            return overlap(q_out, out, x, ((size_t)(total_q - 1) * stride + width) * 2);
+        };
+        if (q_out == q ? q_stride != qd : over(q, q_stride, qd)) return PKV_ERR_INVALID_ARG;
+        if (over(k_new, k_stride, kd) || over(v_new, v_stride, kd)) return PKV_ERR_INVALID_ARG;
+    }
     if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool) ||
         (q_heads > 0 && (!aligned16(q) || !aligned16(q_out))) || (reinterpret_cast<uintptr_t>(rates) & 7))
         return PKV_ERR_INVALID_ARG;
@@ -380,8 +387,10 @@ extern "C" int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, con
     int tokens = total_q < wave ? 1 : (total_q + wave - 1) / wave;
     if (tokens > kTokens) tokens = kTokens;
     if (tokens > 65535 / items) tokens = 65535 / items;
+    const int table = rot_dim / 2 * (int)sizeof(float2);  // at most 40 KB of factors a block
+    if (tokens > 40960 / table) tokens = 40960 / table;
     const int grid = (total_q + tokens - 1) / tokens;
-    const size_t smem = (size_t)tokens * (rot_dim / 2) * sizeof(float2);
+    const size_t smem = (size_t)tokens * table;
     const bool il = layout == PKV_ROPE_INTERLEAVED;
     if (k_scale) {
         if (il)

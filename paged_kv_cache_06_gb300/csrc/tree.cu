@@ -1567,6 +1567,8 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     if (rows == 0 || total_q == 0) return PKV_OK;
     if (!out || !q || !k_pool || !v_pool || !block_tables || !seq_lens || !q_start) return PKV_ERR_INVALID_ARG;
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool)) return PKV_ERR_INVALID_ARG;
+    const size_t bytes = (size_t)total_q * q_heads * head_dim * 2;
+    if (overlap(out, bytes, q, bytes)) return PKV_ERR_INVALID_ARG;  // other blocks still read the queries
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) ||
         workspace_bytes < tree::workspace_bytes())
         return PKV_ERR_WORKSPACE;

@@ -109,10 +109,13 @@ extern "C" int paged_kv_tree_commit(void* k_pool, void* v_pool, const int32_t* b
     if (!k_pool || !v_pool || !block_tables || !seq_lens || !q_start || !path_lens || (max_path > 0 && !path))
         return PKV_ERR_INVALID_ARG;
     if (!aligned16(k_pool) || !aligned16(v_pool)) return PKV_ERR_INVALID_ARG;
+    // every layer's warps read these, so the new lengths lie elsewhere
     if (new_seq_lens) {
-        // every layer's warps read the old lengths, so the new ones lie elsewhere
-        const uintptr_t a = reinterpret_cast<uintptr_t>(new_seq_lens), b = reinterpret_cast<uintptr_t>(seq_lens);
-        if (a < b + (size_t)rows * 4 && b < a + (size_t)rows * 4) return PKV_ERR_INVALID_ARG;
+        const size_t n = (size_t)rows * 4;
+        if (overlap(new_seq_lens, n, seq_lens, n) || overlap(new_seq_lens, n, q_start, n + 4) ||
+            overlap(new_seq_lens, n, path_lens, n) || overlap(new_seq_lens, n, path, n * max_path) ||
+            overlap(new_seq_lens, n, block_tables, n * max_blocks_per_row))
+            return PKV_ERR_INVALID_ARG;
     }
     const int64_t warps = (int64_t)layers * 2 * rows;
     const int64_t blocks = (warps + kWarps - 1) / kWarps;

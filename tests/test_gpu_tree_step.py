@@ -483,6 +483,9 @@ ROPES = [
     ([11, 900], [700, 301], 64, 7, 1, 80, 16, "interleaved"),
     ([3, 1], [400, 600], 16, 3, 1, 256, 256, "half"),
     ([3] * 1100, [1] * 1100, 16, 2, 1, 64, 64, "interleaved"),   # more rows than a block has threads
+    ([7, 300, 0], [1500, 0, 907], 64, 12, 2, 128, 128, "half"),  # four tokens a block, the last one part full
+    ([1], [25000], 128, 1, 1, 64, 32, "half"),                   # the most tokens a block
+    ([9], [9200], 16, 1, 1, 1024, 1024, "interleaved"),          # a table of factors of the most pairs
 ]
 
 

@@ -151,6 +151,11 @@ def test_rope_append_refusals():
     assert rope(sq=1528) == INVALID and rope(sq=1540) == INVALID       # too short; not a multiple of 8
     assert rope(sk=128) == INVALID and rope(sv=260) == INVALID
     assert rope(q_out=FAKE, sq=1544) == INVALID                        # in place needs equal layouts
+    size = 9 * 12 * 128 * 2
+    for off in (256, size - 16, -256, 16 - size):                      # over part of an input
+        assert rope(q=OTHER + off) == INVALID, off
+    for n, s in (("kn", "sk"), ("vn", "sv")):
+        assert rope(**{n: OTHER}) == INVALID and rope(**{n: OTHER - 8 * 512 - 256, s: 256}) == INVALID
     assert rope(msl=257) == INVALID and rope(bs=0) == INVALID and rope(hk=0) == INVALID
     assert rope(nb=1 << 27, bs=16) == UNSUPPORTED
     assert rope(rows=0, k=0) == 0 and rope(total=0, q=0) == 0          # nothing to do
@@ -177,6 +182,8 @@ def test_tree_attention_refusals():
     assert tree(words=0) == INVALID and tree(words=33) == UNSUPPORTED
     assert tree(d=64) == UNSUPPORTED and tree(bs=24) == UNSUPPORTED and tree(rows=1025) == UNSUPPORTED
     assert tree(hq=12, hk=5) == INVALID and tree(scale=float("inf")) == INVALID
+    for off in (0, 256, 9 * 12 * 256 - 16, 16 - 9 * 12 * 256):              # the output over the queries
+        assert tree(q=OTHER + off) == INVALID, off
     assert tree(msl=257) == INVALID and tree(nb=0) == INVALID
     assert tree(ws=0) == WORKSPACE and tree(wsb=8) == WORKSPACE and tree(ws=0x100010) == WORKSPACE
     assert tree(rows=0, out=0) == 0 and tree(total=0, q=0) == 0
@@ -203,6 +210,8 @@ def test_tree_commit_refusals():
         assert commit(**{n: 0}) == INVALID, n
     assert commit(k=ODD) == INVALID and commit(v=ODD) == INVALID
     assert commit(new=FAKE) == INVALID and commit(new=FAKE + 12) == INVALID   # overlaps seq_lens
+    for n, size in (("sl", 16), ("qs", 20), ("path", 128), ("pl", 16)):       # what every layer reads
+        assert commit(**{n: OTHER - size + 4}) == INVALID and commit(**{n: OTHER + 12}) == INVALID, n
     assert commit(eb=4) == INVALID and commit(d=12) == UNSUPPORTED and commit(d=8, eb=1) == UNSUPPORTED
     assert commit(rows=-1) == INVALID and commit(mp=-1) == INVALID and commit(msl=257) == INVALID
     assert commit(nb=1 << 27) == UNSUPPORTED
