@@ -75,7 +75,7 @@ using namespace tc;
 
 constexpr int kRows = 128;     // flat rows of an M block: TMEM lanes
 constexpr int kTile = 128;     // tokens of a tile
-constexpr int kGrain = 64;     // tokens of a granule: the grain of the work split, and of V's slots
+constexpr int kGrainLog = 6, kGrain = 1 << kGrainLog;  // tokens of a granule: the grain of the work split, and of V's slots
 constexpr int kSoftWarps = 8;
 constexpr int kSIssue = 8, kPvIssue = 9, kLoad = 10, kConv = 12;  // warp roles
 constexpr int kConvWarps = 4;
@@ -126,6 +126,20 @@ struct Planes {
     }
 };
 
+// n / d for 0 <= n < 2^31 and d >= 2: with 2^(l - 1) < d <= 2^l and m = ceil(2^(31 + l) / d),
+// n m / 2^(31 + l) is above n / d by less than 1 / d.
+struct By {
+    uint32_t m;
+    int shift;
+    void set(int d) {
+        int l = 1;
+        while ((1ll << l) < d) ++l;
+        m = (uint32_t)(((1ull << (31 + l)) + d - 1) / d);
+        shift = l - 1;
+    }
+    __device__ __forceinline__ int operator()(int n) const { return (int)(__umulhi((uint32_t)n, m) >> shift); }
+};
+
 struct Params {
     const __half* q;
     __half* out;
@@ -139,7 +153,8 @@ struct Params {
     int words;
     int rows, total, hq, hk, group, bs, mbpr, nb, limit;
     Planes planes;
-    int box;       // tokens per copy
+    int box;       // log2 of the tokens per copy
+    By by_bs;      // block_size
     float scale;
     float* part;   // [grid][2][kPartFloats]
     int* heads;    // [grid][kHeadInts], zero between calls: of the cut unit that starts in a block
@@ -206,7 +221,7 @@ struct Split {
     __device__ __forceinline__ void set(int w, int blocks, int least) {
         W = w;
         G = min(blocks, max(w, 1));
-        quo = W / G;
+        quo = div_of(W, G);
         rem = W - quo * G;
         slack = max(least, quo / 16);
     }
@@ -838,9 +853,9 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         const uint32_t slot_bytes = kFp8 ? kRaw : is_v ? kVSlot : kKSlot;
         const uint32_t half_bytes = slot_bytes / 2;
         const CUtensorMap* map = is_v ? &vmap : &kmap;
-        const int box = p.box;
-        const int gpu = unit_tok / box, upb = 32 / gpu;
-        const int my_j = lane / gpu, my_g = lane % gpu;
+        const int box = 1 << p.box;
+        const int per_unit = (kFp8 || is_v ? kGrainLog : kGrainLog + 1) - p.box, upb = 32 >> per_unit;  // log2 boxes a unit
+        const int my_j = lane >> per_unit, my_g = lane & ((1 << per_unit) - 1);
         const uint32_t box_bytes = (uint32_t)box * 128;
         const int nowhere = p.nb * p.bs;  // a row past the pool: a copy of zeros
         int s = 0, armed = 0, grain = 0;
@@ -852,7 +867,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             const int32_t* trow = p.tables + (int64_t)w.r * p.mbpr;
             auto fetch = [&](int ub) -> int {  // raw block id of this lane's box in the batch at copy unit ub
                 const int tok = ta + (ub + my_j) * unit_tok + my_g * box;
-                return tok < te ? __ldg(trow + (unsigned)tok / (unsigned)p.bs) : 0;
+                return tok < te ? __ldg(trow + p.by_bs(tok)) : 0;
             };
             auto to_row = [&](int ub, int pb) -> int {  // its pool row, or -1 for no copy
                 const int tok = ta + (ub + my_j) * unit_tok + my_g * box;
@@ -861,7 +876,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     if (!is_v) flag_error(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
                     return nowhere;
                 }
-                return pb * p.bs + (int)((unsigned)tok % (unsigned)p.bs);
+                return pb * p.bs + tok - p.by_bs(tok) * p.bs;
             };
             int pb = fetch(0), row = -1, j = 0;
 #pragma unroll 1
@@ -1599,13 +1614,14 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     prm.heads = static_cast<int*>(workspace);
     prm.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + head_bytes());
     prm.dev_err = dev_err;
-    prm.box = 16;  // the largest power of two that divides a page, at most a granule
-    while (prm.box < kGrain && block_size % (2 * prm.box) == 0) prm.box *= 2;
+    prm.box = 4;  // the largest power of two that divides a page, at most a granule
+    while ((1 << prm.box) < kGrain && block_size % (2 << prm.box) == 0) ++prm.box;
+    prm.by_bs.set(block_size);
     const bool fp8 = k_scale != nullptr;
     const int elt = fp8 ? 1 : 2;
     const int64_t dims[3] = {kHeadDim, kv_heads, pool_rows};
     const int64_t strides[2] = {kHeadDim * elt, (int64_t)kv_heads * kHeadDim * elt};
-    const int box[3] = {fp8 ? kHeadDim : 64, 1, prm.box};
+    const int box[3] = {fp8 ? kHeadDim : 64, 1, 1 << prm.box};
     const CUtensorMapDataType type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap km, vm;
     if ((st = encode_map_3d(k_pool, type, dims, strides, box, &km)) != PKV_OK) return st;
