@@ -11,7 +11,9 @@
 // time (two table entries a step) and then move the tokens' columns.  Steps
 // already in place (path[j] == j) move nothing.  The bytes are few (a thousand a
 // token and layer at 2 KV heads), so the chain lengths -> path -> table ->
-// load -> store bounds it, and all layers go in one launch.
+// load -> store bounds it, and all layers go in one launch: 32 rows, one layer,
+// fp16: 3.2 us; 64 rows, 28 layers, E4M3: 4.2 us (3 MB moved, 0.7 TB/s).  Eight
+// loads in flight a lane cover a path of eight steps in one round.
 #include "pkv_internal.cuh"
 
 namespace pkv {
