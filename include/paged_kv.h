@@ -476,6 +476,13 @@ int pkv_rope_frequencies(double* freqs, int rot_dim, double base, int scaling, d
                          double original_len, double low, double high);
 int pkv_rope_rates(uint64_t* rates, const double* freqs, int n);
 
+/* The next three calls use programmatic stream serialization without a flag:
+ * their blocks may be set up while the kernel before them runs, but touch no
+ * memory until it and all earlier work in `stream` are complete, so the order
+ * of calls is the stream's.  (A PKV_FLAG_PDL call may directly follow
+ * paged_attention_tree; the other two write pools, which that flag excludes.)
+ */
+
 /*
  * paged_kv_rope_append -- rotary positions on the step's queries and keys,
  * and its keys and values written to their slots; one launch.

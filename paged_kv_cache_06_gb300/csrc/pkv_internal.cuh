@@ -40,6 +40,30 @@ inline int launch_status() {
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+// Launch a kernel whose blocks may be set up while the kernel before it in the stream
+// still runs: it touches no memory before its griddep_wait(), which returns when all
+// that came before is complete, so the order is the stream's.  Back to back in a graph
+// this takes 0.4 to 0.5 us off a launch (path commit of 32 rows: 3.0 -> 2.55 us).
+template <class... P, class... A>
+inline int launch_early(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                        A&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+    }
+    return launch_status();
+}
+
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Bytes at the start of a decode workspace that must be zero before a call.

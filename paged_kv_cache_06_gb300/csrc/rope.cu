@@ -28,6 +28,7 @@
 
 #include "fp8_codec.cuh"
 #include "pkv_internal.cuh"
+#include "ptx.cuh"
 
 namespace pkv {
 namespace rope {
@@ -160,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const __
         }
         return it;
     };
+    ptx::griddep_wait();
     Item it = load(tid);
 
     // ---- each token's row, slot and position ----
@@ -399,16 +401,7 @@ extern "C" int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, con
     const int grid = (total_q + tokens - 1) / tokens;
     const size_t smem = (size_t)tokens * table;
     const bool il = layout == PKV_ROPE_INTERLEAVED;
-    if (k_scale) {
-        if (il)
-            rope_append_kernel<true, true><<<grid, kThreads, smem, stream>>>(p, tokens);
-        else
-            rope_append_kernel<true, false><<<grid, kThreads, smem, stream>>>(p, tokens);
-    } else {
-        if (il)
-            rope_append_kernel<false, true><<<grid, kThreads, smem, stream>>>(p, tokens);
-        else
-            rope_append_kernel<false, false><<<grid, kThreads, smem, stream>>>(p, tokens);
-    }
-    return launch_status();
+    auto* kernel = k_scale ? (il ? rope_append_kernel<true, true> : rope_append_kernel<true, false>)
+                           : (il ? rope_append_kernel<false, true> : rope_append_kernel<false, false>);
+    return launch_early(kernel, grid, kThreads, smem, stream, p, tokens);
 }

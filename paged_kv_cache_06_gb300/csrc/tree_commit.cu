@@ -15,6 +15,7 @@
 // fp16: 3.2 us; 64 rows, 28 layers, E4M3: 4.2 us (3 MB moved, 0.7 TB/s).  Eight
 // loads in flight a lane cover a path of eight steps in one round.
 #include "pkv_internal.cuh"
+#include "ptx.cuh"
 
 namespace pkv {
 namespace commit {
@@ -30,6 +31,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_commit_kernel(
     const int lane = threadIdx.x & 31;
     const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (w >= (int64_t)layers * 2 * rows) return;
+    ptx::griddep_wait();
     const int r = (int)(w % rows), lp = (int)(w / rows);
     const bool first = lp == 0;  // reports for its row
     const int n = path_lens[r], L = seq_lens[r], C = q_start[r + 1] - q_start[r];
@@ -122,9 +124,8 @@ extern "C" int paged_kv_tree_commit(void* k_pool, void* v_pool, const int32_t* b
     const int64_t warps = (int64_t)layers * 2 * rows;
     const int64_t blocks = (warps + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
-    tree_commit_kernel<<<(unsigned)blocks, kWarps * 32, 0, stream>>>(
-        static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), block_tables, seq_lens, q_start, path,
-        path_lens, new_seq_lens, layers, rows, max_path, (int)vecs, block_size, max_blocks_per_row, num_blocks,
-        max_seq_len, dev_err);
-    return launch_status();
+    return launch_early(tree_commit_kernel, (unsigned)blocks, kWarps * 32, 0, stream, static_cast<uint4*>(k_pool),
+                        static_cast<uint4*>(v_pool), block_tables, seq_lens, q_start, path, path_lens, new_seq_lens,
+                        layers, rows, max_path, (int)vecs, block_size, max_blocks_per_row, num_blocks, max_seq_len,
+                        dev_err);
 }

@@ -727,6 +727,76 @@ def test_commit_flags_what_is_no_path(cuda_device):
 # ---- the step as a whole ----
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_calls_back_to_back_keep_the_streams_order(cuda_device, fp8):
+    """Every call reads what the one before wrote (queries and keys from the
+    last output, committed slots, lengths): with a wait after each, without,
+    and captured, the same bits.  A decode that starts early follows each tree
+    (fp16 pools)."""
+    hq, hk, d, rounds = 12, 2, 128, 8
+    step = Step([300, 17, 2000, 60], [9, 4, 13, 1], 16, fp8=fp8, seed=77, fill=False)
+    T = step.total
+    x0 = torch.randn(T, hq, d, generator=step.gen).half().cuda()
+    mask = ops.tree_mask(random_parents(step.nodes, 4), step.starts).cuda()
+    rates = ops.rope_rates(ops.rope_frequencies(d))
+    paths = [[0, 2, 3, 8], [1, 3], [4, 5, 6, 12], [0]]
+    path = i32([p + [-1] * (4 - len(p)) for p in paths])
+    lens = i32([len(p) for p in paths])
+    at = i32([n - 1 for n in step.lens])
+    new = x0[:step.rows, :hk].contiguous()
+
+    def run(how):
+        a = step.gpu()
+        x, y, out = x0.clone(), torch.empty_like(x0), torch.empty_like(x0)
+        nl = torch.zeros(step.rows, dtype=torch.int32, device="cuda")
+        z = torch.zeros(step.rows, hq, d, dtype=torch.float16, device="cuda")
+        ws = ops.alloc_tree_workspace(step.rows, T, hq, hk, d, 16)
+        dws = ops.alloc_workspace(step.rows, hq, hk, d, step.max_len, 16)
+        err = err_word()
+        rows = (a["block_tables"], a["seq_lens"], a["q_start"])
+        scales = dict(k_scale=a["k_scale"], v_scale=a["v_scale"])
+        wait = torch.cuda.synchronize if how == "waits" else lambda: None
+
+        def go():
+            for _ in range(rounds):
+                ops.rope_append(a["k_pool"], a["v_pool"], *rows, x[:, :hk], x[:, hk:2 * hk], rates, step.max_len,
+                                q=x, q_out=y, dev_err=err, **scales)
+                wait()
+                ops.tree_attention(out, y, a["k_pool"], a["v_pool"], *rows, 0.09, step.max_len, ws, mask=mask,
+                                   dev_err=err, **scales)
+                wait()
+                if not fp8:
+                    ops.append_decode(z, out[:step.rows], a["k_pool"], a["v_pool"], *rows[:2], at, new, new, 0.09,
+                                      step.max_len, dws, pdl=True, dev_err=err)
+                    wait()
+                    ops.tree_attention(x, out, a["k_pool"], a["v_pool"], *rows, 0.09, step.max_len, ws, mask=mask,
+                                       dev_err=err)
+                    wait()
+                ops.tree_commit(a["k_pool"], a["v_pool"], *rows, path, lens, step.max_len, new_seq_lens=nl, dev_err=err)
+                wait()
+                ops.tree_attention(x, out, a["k_pool"], a["v_pool"], *rows, 0.09, step.max_len, ws, mask=mask,
+                                   dev_err=err, **scales)
+                wait()
+
+        if how == "graph":
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                go()
+            g.replay()
+        else:
+            go()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        return [t.cpu() for t in (x, y, out, z, nl, a["k_pool"].view(torch.uint8), a["v_pool"].view(torch.uint8))]
+
+    want = run("waits")
+    assert bool(torch.isfinite(want[0]).all()) and want[4].tolist() == [p + len(q) for p, q in zip(step.prefix, paths)]
+    for how in ("stream", "stream", "graph"):
+        for name, w, g in zip(("x", "y", "out", "z", "lens", "k", "v"), want, run(how)):
+            assert torch.equal(w.view(torch.uint8) if w.dtype == torch.float16 else w,
+                               g.view(torch.uint8) if g.dtype == torch.float16 else g), (how, name)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_a_drafted_step_end_to_end(cuda_device, fp8):
     """Block manager, rotary append of a tree, tree attention, commit of an
     accepted path, truncation, and a second step of one token over what was
