@@ -327,6 +327,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool v
     const uint32_t bytes = valid ? 16u : 0u;  // nothing is read when it is not: zeros are written
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 // Columns c .. c + 15 of this warp's 32 lanes, and the wait.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&v)[16]) {
     asm volatile(
@@ -1222,23 +1229,29 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                         }
                         tmem_st_wait();
                     }
-                    float s[64];
+                    // (FP8: 128 registers a thread, so half as many scores at once)
+                    constexpr int kAtOnce = kFp8 ? 32 : 64, kParts = 128 / kAtOnce;
+                    float s[kAtOnce];
                     auto load = [&](int e) {
-                        uint32_t v0[32], v1[32];
-                        tmem_ld64(scol + e * 64, v0, v1);
+                        uint32_t v0[32];
+                        if constexpr (kAtOnce == 64) {
+                            uint32_t v1[32];
+                            tmem_ld64(scol + e * 64, v0, v1);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            s[c] = __uint_as_float(v0[c]);
-                            s[32 + c] = __uint_as_float(v1[c]);
+                            for (int c = 0; c < 32; ++c) s[32 + c] = __uint_as_float(v1[c]);
+                        } else {
+                            tmem_ld32(scol + e * 32, v0);
                         }
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) s[c] = __uint_as_float(v0[c]);
                     };
-                    // the row's maximum: half 0, then half 1, which stays in registers
+                    // the row's maximum, part by part; part 0, the last, stays in registers
                     float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = kParts - 1; e >= 0; --e) {
                         load(e);
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
+                        for (int c = 0; c < kAtOnce; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
                     }
                     const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
                     // The reference so far comes from the job before, the other group's.  Lazy
@@ -1263,16 +1276,16 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     ref = now;
                     const float mneg = now == -INFINITY ? 0.f : -now;
                     // scores in pairs: one packed FMA for the exponents, one packed add for the
-                    // row sums; P is rounded to fp16 for the product (2^-11 a weight) and goes
-                    // over the first 32 of the half's own 64 S columns, already read
+                    // row sums; P is rounded to fp16 for the product (2^-11 a weight) and goes over the
+                    // first 32 of each half's own 64 S columns, of parts already read
                     const uint64_t sc2 = f32x2(scale_log2, scale_log2), mn2 = f32x2(mneg, mneg);
                     uint64_t rs2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
 #pragma unroll 1
-                    for (int e = 1; e >= 0; --e) {
-                        if (e == 0) load(0);
-                        uint32_t pk[32];
+                    for (int e = 0; e < kParts; ++e) {
+                        if (e > 0) load(e);
+                        uint32_t pk[kAtOnce / 2];
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
+                        for (int c = 0; c < kAtOnce / 2; ++c) {
                             float x0, x1;
                             f32x2_split(fma_f32x2(f32x2(s[2 * c], s[2 * c + 1]), sc2, mn2), x0, x1);
                             const float e0 = fast_exp2(x0);
@@ -1280,7 +1293,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                             pk[c] = pack_half2(e0, e1);
                             rs2[c & 1] = add_f32x2(rs2[c & 1], f32x2(e0, e1));
                         }
-                        tmem_st32(scol + e * 64, pk);
+                        if constexpr (kAtOnce == 64)
+                            tmem_st32(scol + e * 64, pk);
+                        else
+                            tmem_st16(scol + (e >> 1) * 64 + (e & 1) * 16, pk);
                     }
                     float r0, r1, r2, r3;
                     f32x2_split(rs2[0], r0, r1);
