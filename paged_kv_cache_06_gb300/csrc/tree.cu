@@ -97,12 +97,13 @@ constexpr int kHeadInts = 32;  // ints between two units' words: count, then giv
 // some imbalance.  Over FP8 pools a segment starts later and its products come slower.
 // Measured, cost and slack: fp16, 32 rows of 16..512 and one of 4096, 8..24
 // nodes: 2, 5: 19.0 us; 4, 4: 21.0; 3, 6: 20.6; 6, 12: 23.4; 90 drawn batches'
-// geometric mean 15.3, 15.5, 15.1, 15.8.  FP8, 32 rows of 1024 and 25 nodes: 8, 12: 23.3;
-// 8, 8: 28.8; 4, 4: 30.7; 96 rows of 16..8192, chains of 3..7: 38.6; 41.2; 46.6.
+// geometric mean 15.3, 15.5, 15.1, 15.8.  FP8, 32 rows of 1024 and 25 nodes; 96 rows of
+// 16..8192, chains of 3..7; 28 drawn batches: 6, 10: 20.7, 35.2, 15.8; 8, 12: 20.7, 35.4,
+// 16.0; 8, 9: 23.4, 37.1, 15.7; 4, 6: 24.7, 35.9, 15.8.
 template <bool kFp8>
-__host__ __device__ constexpr int unit_cost() { return kFp8 ? 8 : 2; }
+__host__ __device__ constexpr int unit_cost() { return kFp8 ? 6 : 2; }
 template <bool kFp8>
-__host__ __device__ constexpr int unit_slack() { return kFp8 ? 12 : 5; }
+__host__ __device__ constexpr int unit_slack() { return kFp8 ? 10 : 5; }
 constexpr uint32_t kHalfQ = kRows * 128;   // 128 flat rows x 64 dims
 constexpr uint32_t kQBlock = 2 * kHalfQ;
 constexpr uint32_t kKHalf = kTile * 128;   // 128 tokens x 64 dims

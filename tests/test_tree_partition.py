@@ -13,7 +13,7 @@ import pytest
 UNIT_COST, MIN_SLACK, GRAIN, ROWS = 2, 5, 64, 128
 
 
-@pytest.fixture(params=[(2, 5), (8, 12)], autouse=True)
+@pytest.fixture(params=[(2, 5), (6, 10)], autouse=True)
 def costs(request, monkeypatch):
     """A unit's fixed cost in granules, and how near its border a cut moves: fp16 pools, FP8 pools."""
     monkeypatch.setattr(sys.modules[__name__], "UNIT_COST", request.param[0])
