@@ -19,7 +19,7 @@
 // table is made, so the two latencies overlap.
 //
 // What bounds it: a small step is a launch and the chain q_start -> length -> table
-// -> factors -> store (32 tokens, 12 + 2 heads of 128: 3.1 us); a large one the copy
+// -> factors -> store (32 tokens, 12 + 2 heads of 128: 2.9 us); a large one the copy
 // bandwidth, less the first 3 to 4 us in which every block looks up and makes its
 // table (15,000 tokens: 24.8 us, 4.8 TB/s read and written, 71% of a plain copy's
 // rate).  48 registers and five blocks an SM: with four, 25.3 us; with six, which
@@ -389,8 +389,8 @@ extern "C" int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, con
     // As many tokens a block as fill the SMs once: small batches take a block a token, the
     // shortest path; large ones pay for the look-up and the table of factors once a block,
     // all blocks are resident together, and no last wave runs alone.  Measured: 32 tokens:
-    // 3.1 us (a token a block); 640 tokens, half of each head rotated, E4M3: a token a
-    // block 4.3 us, four 5.4; 15,000 tokens: 20 a block 24.8 us, 4 a block 26.7, 8 a block
+    // 2.9 us (a token a block); 640 tokens, half of each head rotated, E4M3: a token a
+    // block 4.2 us, four 5.4; 15,000 tokens: 20 a block 24.8 us, 4 a block 26.7, 8 a block
     // 26.4, 16 a block 27.3 (one and a half waves).
     const int items = p.n_pair + p.n_pass + p.n_val, wave = 152 * kBlocks;
     int tokens = total_q < wave ? 1 : (total_q + wave - 1) / wave;

@@ -54,12 +54,13 @@
 // clocks that nothing hides, so tiles of 64 tokens ran at half the rate.
 //
 // What bounds it (12 query heads over 2 unless said).  64 rows of 4096, 64 nodes:
-// 103.6 us, 990 TFLOP/s, 51% of cuBLAS's rate; each tile is copied to an SM once for
+// 101.9 us, 1003 TFLOP/s, 52% of cuBLAS's rate; each tile is copied to an SM once for
 // 128 flat rows, and those 64 KB every 0.95 us are 10.3 TB/s, which is what L2 gives
-// the SMs here.  4 rows of 32768, 5 to 16 nodes: 35.0 us; the copies run at DRAM's
+// the SMs here.  4 rows of 32768, 5 to 16 nodes: 34.9 us; the copies run at DRAM's
 // rate for 22 of them, 6 are the start and 5 the merge of 19 pieces.  32 rows of 1024,
-// 25 nodes, E4M3: 23.7 us, nine tiles a block at 1.2 us, paced by widening and softmax.
-// 4 rows of 0 to 200: 9.0 us, one dependent chain.
+// 25 nodes, E4M3: 21.0 us, nine tiles a block at 1.1 us, paced by the widening (0.55 us
+// a granule for a pool's two warps) with 224 KB a tile through shared memory (0.9 us).
+// 4 rows of 0 to 200: 8.3 us, one dependent chain.
 // Every wait is bounded: a block that gives up flags the error, tells its other
 // warps to stop, and lets its copies and products in flight finish before it
 // frees tensor memory.
