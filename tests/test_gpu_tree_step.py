@@ -218,6 +218,47 @@ def test_chain_matches_the_formula(cuda_device, case, fp8):
     check(tree_run(step, q, None, 0.0883), ref, tol, f"chain {case}")
 
 
+@pytest.mark.parametrize("prefix,nodes,hq,hk", [
+    ([300, 17, 2000, 64], [22] * 4, 12, 2),      # two M blocks a row, the second nearly empty
+    ([300, 17, 2000, 64], [43, 64, 50, 60], 12, 2),              # three, of unequal nodes
+    ([0] * 40, [86] * 40, 6, 1),                 # four and a part: not even
+    ([900, 31, 700] * 6, [85] * 18, 12, 2),      # four
+    ([20000], [64], 12, 2),                      # one row over all blocks
+    ([1], [33], 4, 1),                           # less work than blocks
+    ([100, 5000, 3], [64, 0, 64], 8, 2),         # and a row without nodes
+])
+def test_rows_of_equally_many_query_tiles(cuda_device, prefix, nodes, hq, hk):
+    """Blocks that read the same tokens for different query tiles load them
+    together: against 64 bits, with numbers that are none in unseen and seen
+    values, a bad table entry, and the same bits every time."""
+    step = Step(prefix, nodes, 16, hk=hk, seed=sum(nodes))
+    q = torch.randn(step.total, hq, 128, generator=step.gen).half()
+    mask = ops.tree_mask(random_parents(nodes, 5), step.starts)
+    ref, tol = tree_ref(step, q, seen_of(step, mask), 0.0883)
+    err = err_word()
+    got = tree_run(step, q, mask, 0.0883, err)
+    assert int(err.item()) == 0
+    check(got, ref, tol)
+    for _ in range(3):
+        assert torch.equal(tree_run(step, q, mask, 0.0883), got)
+    # a cached token's block out of range: nobody sees its sixteen tokens
+    r = int(np.argmax([p if n else -1 for p, n in zip(step.prefix, step.nodes)]))
+    if step.prefix[r] >= 32:
+        t = step.tables.copy()
+        t[r, 1] = step.nb
+        ref, tol = tree_ref(step, q, seen_of(step, mask), 0.0883, skip={r: list(range(16, 32))})
+        check(tree_run(step, q, mask, 0.0883, err, block_tables=i32(t)), ref, tol)
+        assert ops.check_error(err) == ERR_BLOCK
+    # the first row's last node holds an infinity in V: it reaches those who see it alone
+    a, n = int(step.starts[0]), step.nodes[0]
+    step.v_pool.view(-1, hk, 128)[step.slots(0, step.prefix[0] + n - 1)] = float("inf")
+    got2 = tree_run(step, q, mask, 0.0883)
+    sees = torch.zeros(step.total, dtype=torch.bool)
+    sees[a:a + n] = seen_of(step, mask)[0][:, n - 1]
+    assert torch.equal(got2[~sees.cuda()], got[~sees.cuda()])
+    assert bool(torch.isinf(got2[sees.cuda()]).all())
+
+
 def test_large_scores_and_scale(cuda_device):
     """Scores far apart: the running maximum moves late and often."""
     step = Step([1500, 700], [20, 9], 64, seed=7)
