@@ -368,14 +368,8 @@ __device__ __forceinline__ uint32_t no_number(uint32_t w) { return ((w & 0x7c007
 
 // The waits of tcgen05.cuh with everything but the first try out of line: the
 // roles' loops share the instruction cache, which they would not fit.
-__device__ __noinline__ bool wait1_slow(uint32_t bar, uint32_t parity, const volatile int* abort) {
-    return mbar_wait1(bar, parity, abort);
-}
 __device__ __noinline__ bool waitw_slow(uint32_t bar, uint32_t parity, const volatile int* abort) {
     return mbar_waitw(bar, parity, abort);
-}
-__device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity, const volatile int* abort) {
-    return mbar_try_wait_sleep(bar, parity) || wait1_slow(bar, parity, abort);
 }
 __device__ __forceinline__ bool waitw(uint32_t bar, uint32_t parity, const volatile int* abort) {
     return __all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity)) || waitw_slow(bar, parity, abort);
@@ -457,61 +451,52 @@ __device__ __noinline__ void add_odd(const Params& p, int r, int P, int j0, int 
 }
 
 // A share of merging a unit cut over P blocks, the first of them `first`: (32
-// flat rows) x (4 kND dims) a warp's turn, turn w of all blocks' warps together,
-// every 8 P-th; kNP pieces' loads are in flight together.
-// `dry`: one turn without its store (see its call).
-template <int kND, int kNP>
+// flat rows) x (4 dims) a warp's turn, turn w of all blocks' warps together, every
+// 8 P-th; eight pieces' loads are in flight together (ten: 2% slower for a unit of 16
+// pieces, 1% faster for one of 19; sixteen spill).  `dry`: one turn without its store (see its
+// call).
+constexpr int kMergeAtOnce = 8;
 __device__ __noinline__ void merge_share(const Params& p, int k, int f0, int q0, int nq, int P, int first, int piece,
                                          float vs, bool dry) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kCols = 32 / kND;
-    const int jobs = kCols * ((nq + 31) / 32);
+    const int jobs = (nq + 31) / 32 * 32;
 #pragma unroll 1
     for (int job = piece * kSoftWarps + warp; job < jobs; job += P * kSoftWarps) {
-        const int cc = job % kCols, i = (job / kCols) * 32 + lane;  // dims 4 kND cc .. of flat row i of the unit
+        const int cc = job & 31, i = (job & ~31) + lane;  // dims 4 cc .. of flat row i of the unit
         if (i >= nq) continue;
-        float M = -INFINITY, Lt = 0.f, acc[4 * kND];
-#pragma unroll
-        for (int e = 0; e < 4 * kND; ++e) acc[e] = 0.f;
+        float M = -INFINITY, Lt = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-        for (int j0 = 0; j0 < P; j0 += kNP) {
+        for (int j0 = 0; j0 < P; j0 += kMergeAtOnce) {
             // (no branch between the loads: past the last piece it is read again and left out)
-            float mj[kNP], lj[kNP];
-            float4 x[kNP][kND];
+            float mj[kMergeAtOnce], lj[kMergeAtOnce];
+            float4 x[kMergeAtOnce];
 #pragma unroll
-            for (int j = 0; j < kNP; ++j) {
+            for (int j = 0; j < kMergeAtOnce; ++j) {
                 const int jj = min(j0 + j, P - 1);
                 const float* s = p.part + ((int64_t)(first + jj) * 2 + (jj == P - 1)) * kPartFloats;
                 mj[j] = __ldcg(s + i);
                 lj[j] = __ldcg(s + kRows + i);
-                const float4* o = reinterpret_cast<const float4*>(s + 2 * kRows) + kND * cc * kRows + i;
-#pragma unroll
-                for (int e = 0; e < kND; ++e) x[j][e] = __ldcg(o + e * kRows);
+                x[j] = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows) + cc * kRows + i);
             }
 #pragma unroll
-            for (int j = 0; j < kNP; ++j) {
+            for (int j = 0; j < kMergeAtOnce; ++j) {
                 if (j0 + j >= P || mj[j] == -INFINITY) continue;
                 const float mn = fmaxf(M, mj[j]);
                 const float a = M == -INFINITY ? 0.f : fast_exp2(M - mn), w = fast_exp2(mj[j] - mn);
                 M = mn;
                 Lt = Lt * a + w * lj[j];
-#pragma unroll
-                for (int e = 0; e < kND; ++e) {
-                    acc[4 * e] = acc[4 * e] * a + w * x[j][e].x;
-                    acc[4 * e + 1] = acc[4 * e + 1] * a + w * x[j][e].y;
-                    acc[4 * e + 2] = acc[4 * e + 2] * a + w * x[j][e].z;
-                    acc[4 * e + 3] = acc[4 * e + 3] * a + w * x[j][e].w;
-                }
+                acc.x = acc.x * a + w * x[j].x;
+                acc.y = acc.y * a + w * x[j].y;
+                acc.z = acc.z * a + w * x[j].z;
+                acc.w = acc.w * a + w * x[j].w;
             }
         }
         if (dry) return;
         const float inv = Lt == 0.f ? 0.f : __fdividef(vs, Lt);
         const int f = f0 + i, node = div_of(f, p.group);
-        __half* dst = p.out + ((int64_t)(q0 + node) * p.hq + k * p.group + (f - node * p.group)) * kHeadDim + 4 * kND * cc;
-#pragma unroll
-        for (int e = 0; e < kND; ++e)
-            *reinterpret_cast<uint2*>(dst + 4 * e) = make_uint2(pack_half2(acc[4 * e] * inv, acc[4 * e + 1] * inv),
-                                                                pack_half2(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv));
+        *reinterpret_cast<uint2*>(p.out + ((int64_t)(q0 + node) * p.hq + k * p.group + (f - node * p.group)) * kHeadDim + 4 * cc) =
+            make_uint2(pack_half2(acc.x * inv, acc.y * inv), pack_half2(acc.z * inv, acc.w * inv));
     }
 }
 
@@ -1082,7 +1067,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         // This warp has nothing to do before the first P, so it runs a turn of it now, which
         // leaves the code in the SM's cache: 1.0 us of 19 over ragged rows, 1.3 of 36 over four
         // rows of 32768.
-        if (lane == 0) merge_share<1, 8>(p, 0, 0, 0, 1, 1, (int)blockIdx.x, 0, 1.f, true);
+        if (lane == 0) merge_share(p, 0, 0, 0, 1, 1, (int)blockIdx.x, 0, 1.f, true);
         __syncwarp();
         const uint64_t vd0 = sdesc(sbase + S::vring, kVHalf, 1024);
         Ring<S::vslots> v;
@@ -1516,7 +1501,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
 #pragma unroll 1
             for (int y = -1; y < (c[13] ? np : 0); ++y) {
                 if (y < 0 ? !c[6] : !((c[y >> 5] >> (y & 31)) & 1)) continue;
-                merge_share<1, 8>(p, k, f0, __ldg(p.q_start + r), nq, np, first, y < 0 ? (int)blockIdx.x - first : y,
+                merge_share(p, k, f0, __ldg(p.q_start + r), nq, np, first, y < 0 ? (int)blockIdx.x - first : y,
                                   vsc, false);
             }
         }
