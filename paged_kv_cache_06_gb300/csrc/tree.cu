@@ -481,7 +481,9 @@ __device__ __noinline__ void merge_share(const Params& p, int k, int f0, int q0,
             }
 #pragma unroll
             for (int j = 0; j < kMergeAtOnce; ++j) {
-                if (j0 + j >= P || mj[j] == -INFINITY) continue;
+                // (a piece that the row sees nothing of; one of NaN scores alone has that reference
+                // too, and a sum that is NaN)
+                if (j0 + j >= P || (mj[j] == -INFINITY && lj[j] == 0.f)) continue;
                 const float mn = fmaxf(M, mj[j]);
                 const float a = M == -INFINITY ? 0.f : fast_exp2(M - mn), w = fast_exp2(mj[j] - mn);
                 M = mn;
