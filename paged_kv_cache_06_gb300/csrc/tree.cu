@@ -1192,8 +1192,9 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     if (!(ok = waitw(bar_s + 8 * b.s, b.ph, abort))) break;
                     tc_fence_after();
                     // weights are powers of two: a scale of zero stands for the smallest one, so that
-                    // a masked score of -inf stays one
-                    const float sc = p.scale * k_sc, scale_log2 = fmaxf(fabsf(sc) * kLog2e, 1e-37f);
+                    // a masked score of -inf stays one (and one that is NaN stays NaN)
+                    const float sc = p.scale * k_sc, sc_log2 = fabsf(sc) * kLog2e;
+                    const float scale_log2 = sc_log2 < 1e-37f ? 1e-37f : sc_log2;
                     const bool flip = sc < 0.f;
                     const uint32_t scol = tmem + lane_base + kColS + b.s * 128;
                     const uint32_t gone = sm_bad[grain & 31] | (two ? sm_bad[(grain + 1) & 31] << 4 : 0u);

@@ -46,3 +46,19 @@ def test_cached_keys_that_are_no_numbers_reach_every_node(cuda_device, prefix, n
     n = nodes[0]
     assert bool(torch.isnan(got[:n, 6:]).all())
     assert torch.equal(got[:n, :6], want[:n, :6]) and torch.equal(got[n:], want[n:])
+
+
+@pytest.mark.parametrize("prefix,nodes", CUTS)
+def test_scales_that_are_no_numbers(cuda_device, prefix, nodes):
+    """A KV head whose key or value scale is NaN has no numbers for answers; the other
+    head keeps its bits."""
+    step = Step(prefix, nodes, 64, fp8=True, seed=43)
+    q = torch.randn(step.total, 12, 128, generator=step.gen).half()
+    mask = ops.tree_mask(random_parents(nodes, 2), step.starts)
+    want = tree_run(step, q, mask, 0.1)
+    for name in ("k_scale", "v_scale"):
+        sc = getattr(step, name).clone()
+        sc[0] = float("nan")
+        got = tree_run(step, q, mask, 0.1, **{name: sc.cuda()})
+        assert bool(torch.isnan(got[:, :6]).all()), name
+        assert torch.equal(got[:, 6:], want[:, 6:]), name
