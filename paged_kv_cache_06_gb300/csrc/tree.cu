@@ -119,6 +119,11 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kPartFloats = 2 * kRows + kRows * kHeadDim;
 constexpr uint64_t kHelpNs = 100000;  // how long a block waits for a unit's other pieces
 constexpr float kLog2e = 1.4426950408889634f;
+// A weight of the reference maximum is 2^7, so that one of 2^8 times it, the most there
+// is, stays below fp16's largest value, and the smallest normal one is 2^-21 of it (without the
+// 2^7: 2^-14, and weights below 2^-25 were lost to the output while the row's sum kept
+// them).  O and the sums carry the same factor in every piece.
+constexpr float kWeightLog2 = 7.f;
 constexpr int kSBufs = 3;        // S buffers of 128 columns
 constexpr uint32_t kColS = 128;  // above the accumulator's 128 columns
 
@@ -1248,8 +1253,8 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
                     // The reference so far comes from the job before, the other group's.  Lazy
                     // rescaling: it only moves when a score exceeds it by more than 2^8 (weights
-                    // stay <= 256, exact enough in fp16).  A row that sees nothing yet stays at
-                    // -inf with zero weights.
+                    // stay <= 2^8 of it).  A row that sees nothing yet stays at -inf with zero
+                    // weights.
                     float now = -INFINITY, alpha = 1.f;
                     bool moved = false;
                     if (t0 > ta) {
@@ -1266,10 +1271,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     if (lane == 0) mbar_arrive(bar_m + 8 * (wg * 4 + quarter));
                     l *= ref == now ? 1.f : fast_exp2(ref - now);  // 0 while ref is -inf
                     ref = now;
-                    const float mneg = now == -INFINITY ? 0.f : -now;
+                    const float mneg = now == -INFINITY ? 0.f : kWeightLog2 - now;
                     // scores in pairs: one packed FMA for the exponents, one packed add for the
-                    // row sums; P is rounded to fp16 for the product (2^-11 a weight) and goes over the
-                    // first 32 of each half's own 64 S columns, of parts already read
+                    // row sums; P is rounded to fp16 for the product (2^-11 a weight; see kWeightLog2)
+                    // and goes over the first 32 of each half's own 64 S columns, of parts already read
                     const uint64_t sc2 = f32x2(scale_log2, scale_log2), mn2 = f32x2(mneg, mneg);
                     uint64_t rs2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
 #pragma unroll 1

@@ -1,11 +1,12 @@
 """GPU tests of the drafted step's edges: numbers that are none, weights far
 below a row's largest, bad rows, calls that start early, units cut between
 blocks."""
+import numpy as np
 import pytest
 import torch
 
 from paged_kv_cache_06_gb300 import ops
-from test_gpu_tree_step import Step, random_parents, tree_run
+from test_gpu_tree_step import Step, check, random_parents, seen_of, tree_ref, tree_run
 
 pytestmark = pytest.mark.gpu
 
@@ -62,3 +63,40 @@ def test_scales_that_are_no_numbers(cuda_device, prefix, nodes):
         got = tree_run(step, q, mask, 0.1, **{name: sc.cuda()})
         assert bool(torch.isnan(got[:, :6]).all()), name
         assert torch.equal(got[:, 6:], want[:, 6:]), name
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("cached,nodes", [(1000, 3), (4090, 6), (30000, 2)])
+def test_weights_far_below_the_largest_count(cuda_device, cached, nodes, fp8):
+    """One token in 128 has a weight of 1 and a value of 0, all others a weight of 2^-26
+    and a large value: what they add up to is the answer.
+
+    Weights are stored for their product as fp16 numbers 2^7 above the row's reference,
+    so one below 2^-21 of it is off by 2^-32 of it at most; the rest as in tree_ref,
+    whose bound for small weights is 2^-25."""
+    bits = 26
+    step = Step([cached], [nodes], 64, hk=1, fp8=fp8, seed=44)
+    L = step.lens[0]
+    big = torch.arange(L) % 128 == 40
+    k = torch.zeros(L, 1, 128)
+    k[big, 0, 0] = 1.0
+    v = torch.where(big, 0.0, 448.0 if fp8 else 60000.0)[:, None, None].expand(L, 1, 128)
+    for pool, x in ((step.k_pool, k), (step.v_pool, v)):
+        x = x.to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else x.half()
+        pool.view(-1, 1, 128)[step.slots(0)] = x
+    if fp8:
+        step.k_scale, step.v_scale = torch.ones(1), torch.full((1,), 134.0)
+    q = torch.zeros(step.total, 4, 128, dtype=torch.float16)
+    q[:, :, 0] = 1.0
+    scale = bits * float(np.log(2.0))
+    ref, tol = tree_ref(step, q, seen_of(step, None), scale)
+    low = 2.0 ** -25 - 2.0 ** -32
+    val = 60032.0 if fp8 else 60000.0
+    n = L - int(big.sum())
+    # tree_ref's bound for the small weights' roundings, less what 2^7 more leaves of it; every
+    # node sees at least n - nodes of those tokens
+    tol = tol - low * val * (n - nodes)
+    # p|v| of a row is the row's answer, so its other terms stay
+    got = tree_run(step, q, None, scale)
+    assert float(ref.min()) > 0.05
+    check(got, ref, tol)
