@@ -1408,6 +1408,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (p.plan) {
         if (bp->G != G) {  // made for another grid: nothing is read or written
             if (tid == 0) flag_error(p.dev_err, PKV_DEV_ERR_PLAN);
+            // A launch that starts early waits for this grid alone, so this grid must not be
+            // complete before the one it follows.
+            griddep_wait();
             return;
         }
         W = bp->W;

@@ -6,9 +6,11 @@ import pytest
 import torch
 
 from paged_kv_cache_06_gb300 import ops
-from test_gpu_tree_step import Step, check, random_parents, seen_of, tree_ref, tree_run
+from test_gpu_tree_step import Step, check, err_word, i32, random_parents, seen_of, tree_ref, tree_run
 
 pytestmark = pytest.mark.gpu
+
+ERR_PLAN = 0x10
 
 # prefix, nodes: whole units; units of two pieces (76 units of 64 granules over 152
 # blocks); units of many pieces
@@ -100,3 +102,40 @@ def test_weights_far_below_the_largest_count(cuda_device, cached, nodes, fp8):
     got = tree_run(step, q, None, scale)
     assert float(ref.min()) > 0.05
     check(got, ref, tol)
+
+
+def test_a_refused_plan_keeps_the_streams_order(cuda_device):
+    """Tree attention, a planned decode that starts early and refuses its plan, and a
+    rotary append in place on the tree's output: the append waits for the tree."""
+    step = Step([30000, 9000, 50], [9, 12, 3], 64, seed=46, fill=False)
+    T, d = step.total, 128
+    q = torch.randn(T, 12, d, generator=step.gen).half().cuda()
+    k, v = (torch.randn(T, 2, d, generator=step.gen).half().cuda() for _ in range(2))
+    rates = ops.rope_rates(ops.rope_frequencies(d))
+    a = step.gpu()
+    rows = (a["block_tables"], a["seq_lens"], a["q_start"])
+    ws = ops.alloc_tree_workspace(3, T, 12, 2, d, 64)
+    dws = ops.alloc_workspace(3, 12, 2, d, step.max_len, 64)
+    plan = ops.alloc_plan(3, 12, 2, d, step.max_len, 64)
+    ops.plan(plan, a["block_tables"], i32([16, 16, 16]), None, 12, 2, d, 64, step.nb, 16)
+    z = torch.empty(3, 12, d, dtype=torch.float16, device="cuda")
+    err = err_word()
+
+    def go(wait):
+        out = torch.full_like(q, float("nan"))
+        torch.cuda.synchronize()
+        for _ in range(4):
+            ops.tree_attention(out, q, a["k_pool"], a["v_pool"], *rows, 0.1, step.max_len, ws)
+            wait()
+            ops.decode_planned(z, q[:3], a["k_pool"], a["v_pool"], *rows[:2], 0.1, step.max_len, plan, dws, pdl=True,
+                               dev_err=err)
+            wait()
+            ops.rope_append(a["k_pool"], a["v_pool"], *rows, k, v, rates, step.max_len, q=out, q_out=out)
+            wait()
+        torch.cuda.synchronize()
+        assert ops.check_error(err) == ERR_PLAN
+        return out
+
+    want = go(torch.cuda.synchronize)
+    for _ in range(5):
+        assert torch.equal(go(lambda: None), want)
