@@ -73,7 +73,7 @@ __device__ __forceinline__ int row_of(const int32_t* q_start, int rows, int g) {
         const int m = (n + 3) >> 2;  // three entries at once
         int c = 0;
 #pragma unroll
-        for (int e = 1; e < 4; ++e) c += e * m < n && __ldg(q_start + lo + e * m) <= g;
+        for (int e = 1; e < 4; ++e) c += e * m < n && q_start[lo + e * m] <= g;
         lo += c * m;
         n = min(m, n - c * m);
     }

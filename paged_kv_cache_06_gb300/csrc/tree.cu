@@ -418,7 +418,7 @@ struct Ring {
 // 32 mask bits of a node from node index j0 on (j0 > -32; bits of negative
 // nodes, cached tokens, are set).
 __device__ __forceinline__ uint32_t mask_bits(const uint32_t* row, int words, int j0) {
-    auto word = [&](int i) -> uint32_t { return i < words ? __ldg(row + i) : 0u; };
+    auto word = [&](int i) -> uint32_t { return i < words ? row[i] : 0u; };
     if (j0 < 0) return (word(0) << -j0) | ((1u << -j0) - 1);
     return __funnelshift_r(word(j0 >> 5), word((j0 >> 5) + 1), j0 & 31);
 }
@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
 
     // A unit's flat rows (256 bytes a row, swizzled; rows past the last are zeros), by one warp.
     auto load_queries = [&](const Walk& u) {
-        const int F = u.flat(), q0 = __ldg(p.q_start + u.r), ch = lane & 15;
+        const int F = u.flat(), q0 = p.q_start[u.r], ch = lane & 15;
         const uint32_t dst0 = sbase + S::q + (ch >> 3) * kHalfQ;
 #pragma unroll 1
         for (int j = 0; j < kRows; j += 32) {
@@ -880,7 +880,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             const int32_t* trow = p.tables + (int64_t)w.r * p.mbpr;
             auto fetch = [&](int ub) -> int {  // raw block id of this lane's box in the batch at copy unit ub
                 const int tok = ta + (ub + my_j) * unit_tok + my_g * box;
-                return tok < te ? __ldg(trow + p.by_bs(tok)) : 0;
+                return tok < te ? trow[p.by_bs(tok)] : 0;
             };
             auto to_row = [&](int ub, int pb) -> int {  // its pool row, or -1 for no copy
                 const int tok = ta + (ub + my_j) * unit_tok + my_g * box;
@@ -1164,10 +1164,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             return true;
         };
         do {
-            const int r = w.r, P = sm_P[r], F = w.flat(), q0 = __ldg(p.q_start + r);
+            const int r = w.r, P = sm_P[r], F = w.flat(), q0 = p.q_start[r];
             const int ta = w.ta(), te = w.te();
             // (loaded here, first used when scores are there)
-            const float k_sc = kFp8 ? __ldg(p.k_scale + w.k) : 1.f, v_sc = kFp8 ? __ldg(p.v_scale + w.k) : 1.f;
+            const float k_sc = kFp8 ? p.k_scale[w.k] : 1.f, v_sc = kFp8 ? p.v_scale[w.k] : 1.f;
             const bool whole = w.whole();
             // this group's last reference and its sum of the row's weights
             float ref = -INFINITY, l = 0.f;
@@ -1509,7 +1509,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
 #pragma unroll 1
             for (int y = -1; y < (c[13] ? np : 0); ++y) {
                 if (y < 0 ? !c[6] : !((c[y >> 5] >> (y & 31)) & 1)) continue;
-                merge_share(p, k, f0, __ldg(p.q_start + r), nq, np, first, y < 0 ? (int)blockIdx.x - first : y,
+                merge_share(p, k, f0, p.q_start[r], nq, np, first, y < 0 ? (int)blockIdx.x - first : y,
                                   vsc, false);
             }
         }

@@ -24,9 +24,8 @@ constexpr int kWarps = 4;   // per block
 constexpr int kBatch = 8;   // steps loaded before the first is stored
 
 __global__ void __launch_bounds__(kWarps * 32) tree_commit_kernel(
-    uint4* __restrict__ k_pool, uint4* __restrict__ v_pool, const int32_t* __restrict__ tables,
-    const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ q_start,
-    const int32_t* __restrict__ path, const int32_t* __restrict__ path_lens, int32_t* __restrict__ new_lens,
+    uint4* k_pool, uint4* v_pool, const int32_t* tables, const int32_t* seq_lens, const int32_t* q_start,
+    const int32_t* path, const int32_t* path_lens, int32_t* new_lens,
     int layers, int rows, int max_path, int vecs, int bs, int mbpr, int nb, int limit, int32_t* dev_err) {
     const int lane = threadIdx.x & 31;
     const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);

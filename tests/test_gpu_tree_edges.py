@@ -139,3 +139,80 @@ def test_a_refused_plan_keeps_the_streams_order(cuda_device):
     want = go(torch.cuda.synchronize)
     for _ in range(5):
         assert torch.equal(go(lambda: None), want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_what_a_call_reads_may_come_from_the_kernel_before_it(cuda_device, fp8):
+    """Lengths from the commit, then starts, paths, tables, positions, rates and mask words
+    that kernels of the same stream have just written: with a wait after each, without, and
+    captured, the same bits."""
+    hq, hk, d, rounds = 12, 2, 128, 6
+    step = Step([300, 17, 2000, 60], [9, 4, 13, 6], 16, fp8=fp8, seed=47, fill=False)
+    T, rows = step.total, step.rows
+    x0 = torch.randn(T, hq, d, generator=step.gen).half().cuda()
+    masks = [ops.tree_mask(random_parents(step.nodes, s), step.starts).cuda() for s in range(rounds)]
+    rates = [ops.rope_rates(ops.rope_frequencies(d, base=10000.0 + 500 * s)) for s in range(rounds)]
+    paths = [i32([[0, 2, 3 + s % 3, 8], [1, 3, -1, -1], [4, 5, 6 + s, 12], [s % 6, -1, -1, -1]]) for s in range(rounds)]
+    counts = i32([4, 2, 4, 1])
+    # the rows change places from round to round: starts, tables and lengths with them
+    order = [torch.roll(torch.arange(rows), s).cuda() for s in range(rounds)]
+    nodes = i32(step.nodes)
+
+    def run(how):
+        a = step.gpu()
+        x, out = x0.clone(), torch.empty_like(x0)
+        lens, nl = a["seq_lens"].clone(), torch.zeros(rows, dtype=torch.int32, device="cuda")
+        tables, starts = torch.full_like(a["block_tables"], -1), torch.full_like(a["q_start"], -1)
+        mask, rate, path, pos = (torch.full_like(t, -1) for t in (masks[0], rates[0], paths[0], x0[:, 0, 0].int()))
+        plen = torch.full_like(counts, -1)
+        ws = ops.alloc_tree_workspace(rows, T, hq, hk, d, 16)
+        err = err_word()
+        args = (tables, lens, starts)
+        sc = dict(k_scale=a["k_scale"], v_scale=a["v_scale"])
+        wait = torch.cuda.synchronize if how == "waits" else lambda: None
+
+        def go():
+            for s in range(rounds):
+                o = order[s]
+                starts.copy_(a["q_start"])
+                starts[1:].copy_(torch.cumsum(nodes[o], 0))
+                torch.index_select(a["block_tables"], 0, o, out=tables)
+                torch.index_select(a["seq_lens"], 0, o, out=lens)
+                mask.copy_(masks[s] if s % rows == 0 else mask)
+                rate.copy_(rates[s])
+                pos.fill_(100 * s)
+                wait()
+                ops.rope_append(a["k_pool"], a["v_pool"], *args, x[:, :hk], x[:, hk:2 * hk], rate, step.max_len,
+                                q=x, q_out=out, rope_positions=pos, dev_err=err, **sc)
+                wait()
+                ops.tree_attention(x, out, a["k_pool"], a["v_pool"], *args, 0.09, step.max_len, ws,
+                                   mask=mask if s % rows == 0 else None, dev_err=err, **sc)
+                torch.index_select(paths[s], 0, o, out=path)
+                torch.index_select(counts, 0, o, out=plen)
+                wait()
+                ops.tree_commit(a["k_pool"], a["v_pool"], *args, path, plen, step.max_len, new_seq_lens=nl, dev_err=err)
+                # the committed tokens alone, as the next step's lengths and no new nodes but the last
+                lens.copy_(nl)
+                starts.copy_(torch.arange(rows + 1, device="cuda"))
+                wait()
+                ops.tree_attention(out[:rows], x[:rows], a["k_pool"], a["v_pool"], *args, 0.09, step.max_len, ws,
+                                   dev_err=err, **sc)
+                x[:rows].copy_(out[:rows])
+                wait()
+
+        if how == "graph":
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                go()
+            g.replay()
+        else:
+            go()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        return [t.cpu().view(torch.uint8) for t in (x, out, nl, a["k_pool"], a["v_pool"])], x
+
+    want, x = run("waits")
+    assert bool(torch.isfinite(x).all())
+    for how in ("stream", "stream", "graph"):
+        for w, g in zip(want, run(how)[0]):
+            assert torch.equal(w, g), how
