@@ -657,6 +657,16 @@ int paged_attention_decode_noalloc(void* out, const void* q, const void* k_pool,
 int pkv_debug_set_decode_hooks(unsigned poll_limit, const void* stuck_word);
 
 /*
+ * pkv_debug_set_tree_hooks -- test hook of paged_attention_tree's split units.
+ * A block waits for a unit's other pieces for help_ns nanoseconds (0 = the
+ * default, 100,000) and then leaves its share of the merge to the last block to
+ * arrive; the result is the same, bit for bit.  Applies to launches made (and
+ * captured) after the call, from any thread, until changed.  For tests; not for
+ * production use.
+ */
+int pkv_debug_set_tree_hooks(unsigned help_ns);
+
+/*
  * pkv_check_error -- synchronise `stream`, copy the device error word to
  * *host_err and clear it on the device.  Returns PKV_ERR_CUDA if the stream
  * reported an error.  The only library call that blocks.  If the word holds

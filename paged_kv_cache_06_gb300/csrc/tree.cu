@@ -74,6 +74,7 @@
 // the last token); a node that does see such an element gets it added to its
 // output afterwards.  Cached tokens are seen by every node of the row and need
 // no such care.
+#include <atomic>
 #include <mutex>
 
 #include "fp8_codec.cuh"
@@ -117,7 +118,7 @@ constexpr uint32_t kRaw = kGrain * 128;    // a granule of codes
 constexpr uint32_t kTmemCols = 512;
 // A partial of one M block: m[128], l[128], then O as [32 groups of 4 dims][128 rows][4].
 constexpr int kPartFloats = 2 * kRows + kRows * kHeadDim;
-constexpr uint64_t kHelpNs = 100000;  // how long a block waits for a unit's other pieces
+constexpr uint32_t kHelpNs = 100000;  // how long a block waits for a unit's other pieces
 constexpr float kLog2e = 1.4426950408889634f;
 // A weight of the reference maximum is 2^7, so that one of 2^8 times it, the most there
 // is, stays below fp16's largest value, and the smallest normal one is 2^-21 of it (without the
@@ -175,6 +176,7 @@ struct Params {
     float scale;
     float* part;   // [grid][2][kPartFloats]
     int* heads;    // [grid][kHeadInts], zero between calls: of the cut unit that starts in a block
+    uint32_t help_ns;  // kHelpNs, but for tests
     int32_t* dev_err;
 };
 
@@ -522,11 +524,11 @@ __device__ __forceinline__ int count_up(int* word, int P) {
 // other, and whoever takes the bit away does the share (the last block gets the
 // pieces it took in `taken`).  Every block, or the last one in its place, counts
 // a second time, which brings the word back to zero.
-__device__ __forceinline__ bool gather(int* head, int P, int piece, int n, volatile int* taken) {
+__device__ __forceinline__ bool gather(int* head, int P, int piece, int n, uint32_t help_ns, volatile int* taken) {
     const bool last = n == P;
     const uint64_t t0 = now_ns();
     while (n < P) {
-        if (now_ns() - t0 > kHelpNs) {
+        if (now_ns() - t0 > help_ns) {
             int* word = head + 1 + (piece >> 5);
             const int bit = 1 << (piece & 31);
             atomicOr(word, bit);
@@ -1497,7 +1499,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             // (thread 0 wrote the record; the others read it after the wait)
             volatile int* c = record(x);
             if (tid == 0) {
-                c[6] = c[7] == 2 ? 0 : gather(p.heads + (int64_t)c[8] * kHeadInts, c[7], (int)blockIdx.x - c[8], c[9], c);
+                c[6] = c[7] == 2 ? 0 : gather(p.heads + (int64_t)c[8] * kHeadInts, c[7], (int)blockIdx.x - c[8], c[9], p.help_ns, c);
                 mbar_arrive(bar_go);
             }
             if (!(ok = waitw(bar_go, gos & 1, abort))) break;
@@ -1561,6 +1563,9 @@ int device_blocks(int* blocks) {
     *blocks = d.blocks;
     return d.status;
 }
+
+// For tests (pkv_debug_set_tree_hooks); 0 in normal use.
+std::atomic<uint32_t> g_hook_help_ns{0};
 
 template <bool kFp8>
 int launch(const Params& prm, const CUtensorMap& km, const CUtensorMap& vm, int blocks, cudaStream_t stream) {
@@ -1639,6 +1644,8 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     prm.heads = static_cast<int*>(workspace);
     prm.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + head_bytes());
     prm.dev_err = dev_err;
+    const uint32_t help_ns = g_hook_help_ns.load(std::memory_order_relaxed);
+    prm.help_ns = help_ns ? help_ns : kHelpNs;
     prm.box = 4;  // the largest power of two that divides a page, at most a granule
     while ((1 << prm.box) < kGrain && block_size % (2 << prm.box) == 0) ++prm.box;
     prm.by_bs.set(block_size);
@@ -1657,4 +1664,9 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     prm.planes.n = m < 1 ? 1 : m > kPlanes ? kPlanes : (int)m;
     prm.planes.magic = prm.planes.n > 1 ? (uint32_t)((0x100000000ull + prm.planes.n - 1) / prm.planes.n) : 0u;
     return fp8 ? launch<true>(prm, km, vm, blocks, stream) : launch<false>(prm, km, vm, blocks, stream);
+}
+
+extern "C" int pkv_debug_set_tree_hooks(unsigned help_ns) {
+    pkv::tree::g_hook_help_ns.store(help_ns, std::memory_order_relaxed);
+    return PKV_OK;
 }

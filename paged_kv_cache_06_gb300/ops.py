@@ -130,6 +130,8 @@ def _declare(L: ctypes.CDLL) -> None:
     L.paged_kv_tree_commit.restype = I
     L.pkv_debug_set_decode_hooks.argtypes = [ctypes.c_uint, P]
     L.pkv_debug_set_decode_hooks.restype = I
+    L.pkv_debug_set_tree_hooks.argtypes = [ctypes.c_uint]
+    L.pkv_debug_set_tree_hooks.restype = I
 
 
 def status_string(status: int) -> str:
@@ -618,6 +620,13 @@ def check_error(dev_err: torch.Tensor, stream=None) -> int:
     st = lib().pkv_check_error(_ptr(dev_err), _stream(stream), ctypes.byref(host))
     _check("pkv_check_error", st)
     return int(host.value)
+
+
+def debug_set_tree_hooks(help_ns: int = 0) -> None:
+    """pkv_debug_set_tree_hooks: how long a block of tree_attention waits for a
+    split unit's other pieces before it leaves its share of the merge to
+    another block (0 restores the default).  Test hook."""
+    _check("pkv_debug_set_tree_hooks", lib().pkv_debug_set_tree_hooks(int(help_ns)))
 
 
 def debug_set_decode_hooks(poll_limit: int = 0, stuck_word: Optional[torch.Tensor] = None) -> None:

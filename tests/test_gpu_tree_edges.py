@@ -104,6 +104,30 @@ def test_weights_far_below_the_largest_count(cuda_device, cached, nodes, fp8):
     check(got, ref, tol)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_shares_given_up_are_merged_by_the_last_block(cuda_device, fp8):
+    """Units of three pieces and more whose blocks wait for each other for next to no
+    time: whoever arrives last does the others' shares, with the same bits, and the
+    workspace is ready for the next call."""
+    for prefix, nodes, heads in (([20000, 50], [9, 3], (12, 2)), ([9000, 7000, 8000], [6, 4, 5], (4, 4)),
+                                 ([30000], [64], (12, 2))):
+        step = Step(prefix, nodes, 64, hk=heads[1], fp8=fp8, seed=48)
+        q = torch.randn(step.total, heads[0], 128, generator=step.gen).half()
+        ws = ops.alloc_tree_workspace(step.rows, step.total, *heads, 128, 64)
+        err = err_word()
+        want = tree_run(step, q, None, 0.1, err, workspace=ws)
+        try:
+            for help_ns in (1, 1, 1, 500, 2000, 1, 3000):
+                ops.debug_set_tree_hooks(help_ns)
+                assert torch.equal(tree_run(step, q, None, 0.1, err, workspace=ws), want), help_ns
+        finally:
+            ops.debug_set_tree_hooks()
+        assert torch.equal(tree_run(step, q, None, 0.1, err, workspace=ws), want)
+        assert ops.check_error(err) == 0
+        # the words by which blocks find each other are back at zero (they come before the partials)
+        assert int(ws[:192 * 32 * 4].count_nonzero()) == 0
+
+
 def test_a_refused_plan_keeps_the_streams_order(cuda_device):
     """Tree attention, a planned decode that starts early and refuses its plan, and a
     rotary append in place on the tree's output: the append waits for the tree."""
