@@ -657,14 +657,16 @@ int paged_attention_decode_noalloc(void* out, const void* q, const void* k_pool,
 int pkv_debug_set_decode_hooks(unsigned poll_limit, const void* stuck_word);
 
 /*
- * pkv_debug_set_tree_hooks -- test hook of paged_attention_tree's split units.
+ * pkv_debug_set_tree_hooks -- test hooks of paged_attention_tree's split units.
  * A block waits for a unit's other pieces for help_ns nanoseconds (0 = the
  * default, 100,000) and then leaves its share of the merge to the last block to
- * arrive; the result is the same, bit for bit.  Applies to launches made (and
- * captured) after the call, from any thread, until changed.  For tests; not for
- * production use.
+ * arrive; the result is the same, bit for bit.  With stop_folds != 0 a block
+ * that has fetched the other half of a unit cut in two gives up there and flags
+ * PKV_DEV_ERR_TIMEOUT (zero-fill the workspace afterwards).  (0, 0) restores
+ * normal operation.  Both apply to launches made (and captured) after the call,
+ * from any thread, until changed.  For tests; not for production use.
  */
-int pkv_debug_set_tree_hooks(unsigned help_ns);
+int pkv_debug_set_tree_hooks(unsigned help_ns, int stop_folds);
 
 /*
  * pkv_check_error -- synchronise `stream`, copy the device error word to

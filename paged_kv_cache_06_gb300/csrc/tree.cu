@@ -177,6 +177,7 @@ struct Params {
     float* part;   // [grid][2][kPartFloats]
     int* heads;    // [grid][kHeadInts], zero between calls: of the cut unit that starts in a block
     uint32_t help_ns;  // kHelpNs, but for tests
+    uint32_t stop;     // for tests: blocks that fold give up once the copy is issued
     int32_t* dev_err;
 };
 
@@ -1403,7 +1404,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                         mbar_arrive(bar_go);
                     }
                 }
-                if (!(ok = waitw(bar_go, gos & 1, abort) && sm_misc[10])) break;
+                ok = waitw(bar_go, gos & 1, abort) && !p.stop;
+                // the copy that this warp has issued lands before the block may exit
+                if (!ok && warp == 0 && sm_misc[10]) drain1(bar_go, gos & 1);
+                if (!(ok = ok && sm_misc[10])) break;
                 ++gos;
             }
             // some node's V, of this segment or another, was no number
@@ -1565,7 +1569,7 @@ int device_blocks(int* blocks) {
 }
 
 // For tests (pkv_debug_set_tree_hooks); 0 in normal use.
-std::atomic<uint32_t> g_hook_help_ns{0};
+std::atomic<uint32_t> g_hook_help_ns{0}, g_hook_stop{0};
 
 template <bool kFp8>
 int launch(const Params& prm, const CUtensorMap& km, const CUtensorMap& vm, int blocks, cudaStream_t stream) {
@@ -1646,6 +1650,7 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     prm.dev_err = dev_err;
     const uint32_t help_ns = g_hook_help_ns.load(std::memory_order_relaxed);
     prm.help_ns = help_ns ? help_ns : kHelpNs;
+    prm.stop = g_hook_stop.load(std::memory_order_relaxed);
     prm.box = 4;  // the largest power of two that divides a page, at most a granule
     while ((1 << prm.box) < kGrain && block_size % (2 << prm.box) == 0) ++prm.box;
     prm.by_bs.set(block_size);
@@ -1666,7 +1671,8 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     return fp8 ? launch<true>(prm, km, vm, blocks, stream) : launch<false>(prm, km, vm, blocks, stream);
 }
 
-extern "C" int pkv_debug_set_tree_hooks(unsigned help_ns) {
+extern "C" int pkv_debug_set_tree_hooks(unsigned help_ns, int stop_folds) {
     pkv::tree::g_hook_help_ns.store(help_ns, std::memory_order_relaxed);
+    pkv::tree::g_hook_stop.store(stop_folds != 0, std::memory_order_relaxed);
     return PKV_OK;
 }

@@ -1,12 +1,14 @@
 """GPU tests of the drafted step's edges: numbers that are none, weights far
 below a row's largest, bad rows, calls that start early, units cut between
 blocks."""
+import time
+
 import numpy as np
 import pytest
 import torch
 
 from paged_kv_cache_06_gb300 import ops
-from test_gpu_tree_step import Step, check, err_word, i32, random_parents, seen_of, tree_ref, tree_run
+from test_gpu_tree_step import ERR_TIMEOUT, Step, check, err_word, i32, random_parents, seen_of, tree_ref, tree_run
 
 pytestmark = pytest.mark.gpu
 
@@ -126,6 +128,33 @@ def test_shares_given_up_are_merged_by_the_last_block(cuda_device, fp8):
         assert ops.check_error(err) == 0
         # the words by which blocks find each other are back at zero (they come before the partials)
         assert int(ws[:192 * 32 * 4].count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_block_that_gives_up_its_fold_waits_for_the_copy(cuda_device, fp8):
+    """A block that gives up between issuing the copy of the other half and using it:
+    the call ends soon, flags the error, and the next one on a zero-filled workspace
+    is right."""
+    prefix, nodes = CUTS[1]
+    step = Step(prefix, nodes, 64, fp8=fp8, seed=49)
+    q = torch.randn(step.total, 12, 128, generator=step.gen).half()
+    ws = ops.alloc_tree_workspace(step.rows, step.total, 12, 2, 128, 64)
+    err = err_word()
+    want = tree_run(step, q, None, 0.1, err, workspace=ws)
+    assert ops.check_error(err) == 0
+    for _ in range(3):
+        try:
+            ops.debug_set_tree_hooks(0, True)
+            t0 = time.perf_counter()
+            got = tree_run(step, q, None, 0.1, err, workspace=ws)
+            assert time.perf_counter() - t0 < 2.0
+        finally:
+            ops.debug_set_tree_hooks()
+        assert ops.check_error(err) == ERR_TIMEOUT
+        assert bool(torch.isnan(got).any())           # what the blocks left out
+        ws.zero_()
+        assert torch.equal(tree_run(step, q, None, 0.1, err, workspace=ws), want)
+        assert ops.check_error(err) == 0
 
 
 def test_a_refused_plan_keeps_the_streams_order(cuda_device):
