@@ -26,15 +26,16 @@
 // first, so a piece that others continue comes first.  It stores its partial
 // result (reference maxima, row sums, unnormalised output in 32 bits).  Of two
 // pieces the second folds the first's partial into its own result when it is
-// done: the block before, which started earlier, stored it long ago.  Of more
+// done: the block before, which as a rule started earlier, stored it long ago.  Of more
 // pieces each stores its partial and counts itself, and in the end each block
 // waits for its cut units' other pieces and merges its share of each (some rows
 // by some dims), over the pieces in order, so the result does not depend on
-// time.  A block that has waited
-// kHelpNs gives its share up, and the block that arrives last, which waits for
-// nobody, does what was given up: so no block's progress depends on another
-// one running, and two calls can share the GPU.  The counts return to zero by
-// themselves (a wrapping increment on arrival and one on departure).
+// time.  A block that has waited kHelpNs goes on: it gives its share up, and the block that
+// arrives last, which waits for nobody, does what was given up; or, the second of two, it
+// stores its piece, and whichever of the two stores last merges both, by the same
+// operations.  So no block's progress depends on another one running, and two
+// calls can share the GPU.  The counts return to zero by themselves (a wrapping
+// increment on arrival and one on departure; a pair's by the block that uses both pieces).
 //
 // Warp roles (each walks the same segments, a unit's part in the block's range):
 //   warps 0-7   softmax, in two groups of four that take alternate jobs: one
@@ -510,11 +511,54 @@ __device__ __noinline__ void merge_share(const Params& p, int k, int f0, int q0,
     }
 }
 
+// The weights of the two pieces of a unit, `a` the first's, and the normalisation in them:
+// one order of operations for the fold and for the merge of a pair, so that the
+// result is the same whichever was done.
+__device__ __forceinline__ void pair_weights(float ma, float la, float mb, float lb, float vs, float& a, float& b) {
+    const float M = fmaxf(ma, mb);
+    a = ma == -INFINITY ? 0.f : fast_exp2(ma - M);
+    b = mb == -INFINITY ? 0.f : fast_exp2(mb - M);
+    const float L = __fmaf_rn(lb, b, __fmul_rn(la, a));
+    const float inv = L == 0.f ? 0.f : __fdividef(vs, L);
+    a *= inv;
+    b *= inv;
+}
+__device__ __forceinline__ float pair_sum(float x, float a, float y, float b) { return __fmaf_rn(x, a, __fmul_rn(y, b)); }
+
+// The merge of a unit cut in two, whose second block did not wait for the first: all of it,
+// by the eight softmax warps of whichever block stored its piece last.
+__device__ __noinline__ void merge_pair(const Params& p, int k, int f0, int q0, int nq, int first, float vs) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float* s = p.part + (int64_t)first * 2 * kPartFloats;  // the second piece: of the next block, its slot 1
+    const float* z = s + 3 * kPartFloats;
+#pragma unroll 1
+    for (int job = warp; job < (nq + 31) / 32 * 32; job += kSoftWarps) {
+        const int cc = job & 31, i = (job & ~31) + lane;
+        if (i >= nq) continue;
+        float a, b;
+        pair_weights(__ldcg(s + i), __ldcg(s + kRows + i), __ldcg(z + i), __ldcg(z + kRows + i), vs, a, b);
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(s + 2 * kRows) + cc * kRows + i);
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(z + 2 * kRows) + cc * kRows + i);
+        const int f = f0 + i, node = div_of(f, p.group);
+        *reinterpret_cast<uint2*>(p.out + ((int64_t)(q0 + node) * p.hq + k * p.group + (f - node * p.group)) * kHeadDim + 4 * cc) =
+            make_uint2(pack_half2(pair_sum(x.x, a, y.x, b), pair_sum(x.y, a, y.y, b)),
+                       pack_half2(pair_sum(x.z, a, y.z, b), pair_sum(x.w, a, y.w, b)));
+    }
+}
+
 // A wrapping increment: the word goes back to zero after 2 P of them.
 __device__ __forceinline__ int count_up(int* word, int P) {
     unsigned old;
     asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(word), "r"(2 * P - 1) : "memory");
     return (int)old;
+}
+
+// Of two pieces, the first (0) or the second (1), whose block did not wait, is stored: nonzero
+// when the other one was stored before, and its block leaves the merge to this one.
+__device__ __forceinline__ int count_pair(int* word, int piece) {
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(word), "r"(1 + piece) : "memory");
+    return old;
 }
 
 // One thread of each of a cut unit's blocks, after its own piece was counted as
@@ -1159,10 +1203,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             if (lane == 0) {
                 volatile int* c = record(counted - 1);
                 int* word = p.heads + (int64_t)c[8] * kHeadInts;
-                if (c[7] == 2)
-                    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(word) : "memory");
-                else
-                    c[9] = count_up(word, c[7]) + 1;
+                c[9] = c[7] == 2 ? count_pair(word, (int)blockIdx.x - c[8]) : count_up(word, c[7]) + 1;
             }
             return true;
         };
@@ -1380,7 +1421,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             const bool ends = w.g1() == w.n;
             // the second of two pieces: wait for the first's partial, which its block stores
             // before anything else
-            const bool fold = np == 2 && ends;
+            bool fold = np == 2 && ends;
             if (!(ok = count_piece())) break;
             if (fold) {
                 // this is the block's last segment and its products are done: the K and V rings are
@@ -1391,7 +1432,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     int there;
                     for (;;) {
                         asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(there) : "l"(word) : "memory");
-                        if (there || now_ns() - from > kWaitLimitNs || *abort) break;
+                        if (there || now_ns() - from > p.help_ns) break;
                         __nanosleep(20);
                     }
                     sm_misc[10] = there;
@@ -1404,10 +1445,12 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                         mbar_arrive(bar_go);
                     }
                 }
-                ok = waitw(bar_go, gos & 1, abort) && !p.stop;
+                ok = waitw(bar_go, gos & 1, abort);
+                fold = sm_misc[10] != 0;  // or else this piece is stored, and whichever block stores last merges
+                if (p.stop && fold) ok = false;
                 // the copy that this warp has issued lands before the block may exit
-                if (!ok && warp == 0 && sm_misc[10]) drain1(bar_go, gos & 1);
-                if (!(ok = ok && sm_misc[10])) break;
+                if (!ok && warp == 0 && fold) drain1(bar_go, gos & 1);
+                if (!ok) break;
                 ++gos;
             }
             // some node's V, of this segment or another, was no number
@@ -1418,21 +1461,16 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                 const int f = min(w.f0() + i, F - 1), node = div_of(f, group), h = w.k * group + (f - node * group);
                 const bool mine = w.f0() + i < F;
                 const float M0 = sm_sum[i], M1 = sm_sum[2 * kRows + i];
-                float M = fmaxf(M0, M1), a0 = 1.f, a2 = 0.f;
-                float Lr = (M0 == M ? sm_sum[kRows + i] : sm_sum[kRows + i] * fast_exp2(M0 - M)) +
+                const float M = fmaxf(M0, M1);
+                float a0 = 1.f, a2 = 0.f;
+                const float Lr = (M0 == M ? sm_sum[kRows + i] : sm_sum[kRows + i] * fast_exp2(M0 - M)) +
                            (M1 == M ? sm_sum[3 * kRows + i] : sm_sum[3 * kRows + i] * fast_exp2(M1 - M));
                 const float* before = reinterpret_cast<const float*>(smem + S::kring);  // fold: the first piece's
-                if (fold) {
-                    const float Ma = M, Mb = before[i], lb = before[kRows + i];
-                    M = fmaxf(Ma, Mb);
-                    a0 = Ma == -INFINITY ? 0.f : fast_exp2(Ma - M);
-                    a2 = Mb == -INFINITY ? 0.f : fast_exp2(Mb - M);
-                    Lr = Lr * a0 + lb * a2;
-                }
                 const bool out = whole || fold;
-                const float inv = !out ? 1.f : Lr == 0.f ? 0.f : __fdividef(v_sc, Lr);
-                a0 *= inv;
-                a2 *= inv;
+                if (fold)
+                    pair_weights(before[i], before[kRows + i], M, Lr, v_sc, a2, a0);
+                else if (whole)
+                    a0 = Lr == 0.f ? 0.f : __fdividef(v_sc, Lr);
                 __half* orow = p.out + ((int64_t)(q0 + node) * p.hq + h) * kHeadDim + wg * 64;
                 float* slot = p.part + ((int64_t)blockIdx.x * 2 + ends) * kPartFloats;
                 if (!out && wg == 0) {
@@ -1454,10 +1492,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float4 y = pb[(c / 4 + e) * kRows];
-                            o[4 * e] += y.x * a2;
-                            o[4 * e + 1] += y.y * a2;
-                            o[4 * e + 2] += y.z * a2;
-                            o[4 * e + 3] += y.w * a2;
+                            o[4 * e] = __fmaf_rn(y.x, a2, o[4 * e]);
+                            o[4 * e + 1] = __fmaf_rn(y.y, a2, o[4 * e + 1]);
+                            o[4 * e + 2] = __fmaf_rn(y.z, a2, o[4 * e + 2]);
+                            o[4 * e + 3] = __fmaf_rn(y.w, a2, o[4 * e + 3]);
                         }
                     }
                     if (out && mine) {
@@ -1503,15 +1541,25 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             // (thread 0 wrote the record; the others read it after the wait)
             volatile int* c = record(x);
             if (tid == 0) {
-                c[6] = c[7] == 2 ? 0 : gather(p.heads + (int64_t)c[8] * kHeadInts, c[7], (int)blockIdx.x - c[8], c[9], p.help_ns, c);
+                if (c[7] == 2) {
+                    c[6] = c[9];  // the pair's other piece came first: the merge is this block's
+                    if (c[9]) p.heads[(int64_t)c[8] * kHeadInts] = 0;
+                } else {
+                    c[6] = gather(p.heads + (int64_t)c[8] * kHeadInts, c[7], (int)blockIdx.x - c[8], c[9],
+                                  p.help_ns, c);
+                }
                 mbar_arrive(bar_go);
             }
             if (!(ok = waitw(bar_go, gos & 1, abort))) break;
             ++gos;
             const int np = c[7], first = c[8], r = c[10], k = c[11], t = c[12];
-            if (np == 2) continue;
+            if (np == 2 && !c[6]) continue;
             const float vsc = kFp8 ? p.v_scale[k] : 1.f;
             const int f0 = (plane + planes.n * t) * kRows, nq = min(kRows, sm_C[r] * group - f0);
+            if (np == 2) {
+                merge_pair(p, k, f0, p.q_start[r], nq, first, vsc);
+                continue;
+            }
 #pragma unroll 1
             for (int y = -1; y < (c[13] ? np : 0); ++y) {
                 if (y < 0 ? !c[6] : !((c[y >> 5] >> (y & 31)) & 1)) continue;

@@ -111,23 +111,48 @@ def test_shares_given_up_are_merged_by_the_last_block(cuda_device, fp8):
     """Units of three pieces and more whose blocks wait for each other for next to no
     time: whoever arrives last does the others' shares, with the same bits, and the
     workspace is ready for the next call."""
-    for prefix, nodes, heads in (([20000, 50], [9, 3], (12, 2)), ([9000, 7000, 8000], [6, 4, 5], (4, 4)),
-                                 ([30000], [64], (12, 2))):
+    patience(fp8, (([20000, 50], [9, 3], (12, 2)), ([9000, 7000, 8000], [6, 4, 5], (4, 4)),
+                   ([30000], [64], (12, 2))))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_the_second_of_two_pieces_does_not_wait_for_the_first(cuda_device, fp8):
+    """Units of two pieces whose second block hardly waits: whichever block stores last
+    merges the two, with the fold's bits."""
+    # 76 units over 152 blocks: every one in two halves
+    folded, handed_over = patience(fp8, (([4090] * 38, [6] * 38, (12, 2)),))
+    assert folded == 0 and (handed_over > 0 or fp8)  # over FP8 pools the second half is the longer one
+    patience(fp8, (([2000] * 38, [40] * 38, (12, 2)), ([4000] * 19, [30] * 19, (32, 4)),
+                   ([1500, 900, 3000] * 13, [12, 3, 22] * 13, (12, 2))))
+
+
+def patience(fp8, batches):
+    """The same bits however long blocks wait; how many blocks stored a last piece with the
+    usual patience and with none (a partial is 2 x 128 + 128 x 128 floats, two a block)."""
+    counts = [0, 0]
+
+    def last_pieces(ws):
+        return int((ws[192 * 32 * 4:].view(torch.float32).view(192, 2, -1)[:, 1] != 0).any(-1).sum())
+
+    for prefix, nodes, heads in batches:
         step = Step(prefix, nodes, 64, hk=heads[1], fp8=fp8, seed=48)
         q = torch.randn(step.total, heads[0], 128, generator=step.gen).half()
         ws = ops.alloc_tree_workspace(step.rows, step.total, *heads, 128, 64)
         err = err_word()
         want = tree_run(step, q, None, 0.1, err, workspace=ws)
+        counts[0] += last_pieces(ws)
         try:
             for help_ns in (1, 1, 1, 500, 2000, 1, 3000):
                 ops.debug_set_tree_hooks(help_ns)
                 assert torch.equal(tree_run(step, q, None, 0.1, err, workspace=ws), want), help_ns
         finally:
             ops.debug_set_tree_hooks()
+        counts[1] += last_pieces(ws)
         assert torch.equal(tree_run(step, q, None, 0.1, err, workspace=ws), want)
         assert ops.check_error(err) == 0
         # the words by which blocks find each other are back at zero (they come before the partials)
         assert int(ws[:192 * 32 * 4].count_nonzero()) == 0
+    return counts
 
 
 @pytest.mark.parametrize("fp8", [False, True])
