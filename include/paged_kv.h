@@ -442,7 +442,10 @@ int paged_attention_decode_planned(void* out, const void* q, void* k_pool, void*
  *                            to positions P_r, P_r + 1, ...
  * A row with C_r < 0, C_r > seq_lens[r] or seq_lens[r] > max_seq_len (or, in
  * the first two, nodes past total_q) is skipped by each of them (nothing of it
- * is written) and flagged PKV_DEV_ERR_SEQ_LEN.
+ * is written) and flagged PKV_DEV_ERR_SEQ_LEN.  Where starts fall, rows name the same
+ * nodes, and which row's answer a node gets is not defined; paged_attention_tree
+ * writes nothing and flags PKV_DEV_ERR_SEQ_LEN when such rows' work passes 2^31
+ * tile steps.
  */
 
 /* Rotary frequencies and their fixed-point form (host functions, no GPU).
@@ -659,8 +662,8 @@ int pkv_debug_set_decode_hooks(unsigned poll_limit, const void* stuck_word);
 /*
  * pkv_debug_set_tree_hooks -- test hooks of paged_attention_tree's split units.
  * A block waits for a unit's other pieces for help_ns nanoseconds (0 = the
- * default, 100,000) and then leaves its share of the merge to the last block to
- * arrive; the result is the same, bit for bit.  With stop_folds != 0 a block
+ * default, 100,000) and then leaves the merge, or its share of it, to another
+ * block; the result is the same, bit for bit.  With stop_folds != 0 a block
  * that has fetched the other half of a unit cut in two gives up there and flags
  * PKV_DEV_ERR_TIMEOUT (zero-fill the workspace afterwards).  (0, 0) restores
  * normal operation.  Both apply to launches made (and captured) after the call,

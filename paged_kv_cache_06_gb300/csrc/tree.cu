@@ -297,6 +297,11 @@ __device__ __noinline__ int4 unit_before(int4 u, int hk, int group, int plane, i
     return u;
 }
 
+// a + b, kept at 2^31 - 1: the work of rows whose starts fall, so that they overlap, may
+// pass what the host has allowed for.
+constexpr int kTooMuch = 0x7fffffff;
+__device__ __forceinline__ int add_work(int a, int b) { return (int)min((unsigned)a + (unsigned)b, (unsigned)kTooMuch); }
+
 // The units of a block's range [s0, e), last to first.
 template <int kUnitCost>
 struct Walk : Unit<kUnitCost> {
@@ -709,13 +714,14 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                 sm_C[r] = C;
                 sm_P[r] = L - C;
             }
-            // a unit's length (all units' together stay below 2^31, checked by the host)
+            // a unit's length (all units' together stay below kTooMuch, checked by the host for starts
+            // that rise)
             const int len = C > 0 ? p.hk * ((L + kGrain - 1) / kGrain + kUnitCost) : 0;
-            sum[0] += len * planes.blocks(C * group, 0);
+            sum[0] = add_work(sum[0], len * planes.blocks(C * group, 0));
             if (planes.n > 1) {
 #pragma unroll
                 for (int x = 1; x < kPlanes; ++x)
-                    if (x < planes.n) sum[x] += len * planes.blocks(C * group, x);
+                    if (x < planes.n) sum[x] = add_work(sum[x], len * planes.blocks(C * group, x));
             }
         }
         auto scan = [&](int x) {
@@ -723,7 +729,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int t = __shfl_up_sync(0xffffffffu, incl[x], o);
-                if (lane >= o) incl[x] += t;
+                if (lane >= o) incl[x] = add_work(incl[x], t);
             }
             if (lane == 31) sm_part[(x * 2 + side) * 8 + hw] = incl[x];
         };
@@ -749,7 +755,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) {
                 const int t = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += t;
+                if (lane >= o) v = add_work(v, t);
             }
             before = __shfl_sync(0xffffffffu, v, max(hw - 1, 0));
             if (hw == 0) before = 0;
@@ -765,10 +771,17 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             int Wi[kPlanes], bf[kPlanes];
             Wi[0] = W;
             bf[0] = before;
+            bool fits = W < kTooMuch;
 #pragma unroll
             for (int x = 1; x < kPlanes; ++x) {
                 Wi[x] = bf[x] = 0;
                 if (x < planes.n) Wi[x] = plane_of(x, bf[x]);
+                fits = fits && Wi[x] < kTooMuch;
+            }
+            if (!fits) {  // (rows of one M block each always fit)
+                if (blockIdx.x == 0 && tid == 0) flag_error(p.dev_err, PKV_DEV_ERR_SEQ_LEN);
+#pragma unroll
+                for (int x = 0; x < kPlanes; ++x) Wi[x] = 0;
             }
 #pragma unroll
             for (int x = 0; x < kPlanes; ++x) {
@@ -1658,7 +1671,7 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     const int64_t tiles = (int64_t)kv_heads * (((int64_t)total_q * group) / kRows + rows) *
                           (((int64_t)max_seq_len + kGrain - 1) / kGrain + unit_cost<true>());
     const int64_t pool_rows = (int64_t)num_blocks * block_size;
-    if (tiles >= (int64_t(1) << 31) || pool_rows >= (int64_t(1) << 31) - kTile ||
+    if (tiles >= kTooMuch || pool_rows >= (int64_t(1) << 31) - kTile ||
         (int64_t)total_q * q_heads >= (int64_t(1) << 31))
         return PKV_ERR_UNSUPPORTED;
     if (rows == 0 || total_q == 0) return PKV_OK;

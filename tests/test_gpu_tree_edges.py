@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from paged_kv_cache_06_gb300 import ops
-from test_gpu_tree_step import ERR_TIMEOUT, Step, check, err_word, i32, random_parents, seen_of, tree_ref, tree_run
+from test_gpu_tree_step import ERR_LEN, ERR_TIMEOUT, Step, check, err_word, i32, random_parents, seen_of, tree_ref, tree_run
 
 pytestmark = pytest.mark.gpu
 
@@ -294,3 +294,33 @@ def test_what_a_call_reads_may_come_from_the_kernel_before_it(cuda_device, fp8):
     for how in ("stream", "stream", "graph"):
         for w, g in zip(want, run(how)[0]):
             assert torch.equal(w, g), how
+
+
+def test_rows_that_overlap_beyond_all_bounds_are_refused(cuda_device):
+    """Starts that rise and fall: every other row names all the nodes, and their work
+    together passes 2^31 tile steps (512 rows x 8 KV heads x 256 M blocks of each of four
+    planes x 3,125 granules).  Nothing is written; smaller ones are answered."""
+    hq, hk, T, rows, L = 64, 8, 16384, 1024, 200000
+    pool = torch.randn(1, 64, hk, 128, device="cuda").half()
+    q = torch.zeros(T, hq, 128, dtype=torch.float16, device="cuda")
+    q[:64] = torch.randn(64, hq, 128, device="cuda").half()
+    ws = ops.alloc_tree_workspace(rows, T, hq, hk, 128, 64)
+    tables = torch.zeros(rows, L // 64, dtype=torch.int32, device="cuda")
+    err = err_word()
+
+    def go(nodes, length, total):
+        starts = torch.zeros(rows + 1, dtype=torch.int32)
+        starts[1::2] = nodes
+        out = torch.full((total, hq, 128), float("nan"), dtype=torch.float16, device="cuda")
+        ops.tree_attention(out, q[:total], pool, pool, tables, torch.full((rows,), length, dtype=torch.int32).cuda(),
+                           starts.cuda(), 0.1, L, ws, dev_err=err)
+        assert ops.check_error(err) == ERR_LEN        # the rows between have fewer than no nodes
+        return out
+
+    assert bool(torch.isnan(go(T, L, T)).all())
+    got = go(64, 300, 64)                             # every other row gives the same answers, but for roundings
+    want = torch.empty_like(got)
+    ops.tree_attention(want, q[:64], pool, pool, tables[:1], i32([300]), i32([0, 64]), 0.1, L, ws, dev_err=err)
+    torch.cuda.synchronize()
+    assert ops.check_error(err) == 0
+    assert bool(((got - want).float().abs() <= 2e-3 + 2e-3 * want.float().abs()).all())
