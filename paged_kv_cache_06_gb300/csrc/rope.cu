@@ -98,6 +98,11 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return v;
 }
 
+// Whether a row of C nodes from q0 on and L tokens is skipped (and flagged).
+__device__ __forceinline__ bool bad_row(int q0, int C, int L, int limit, int total) {
+    return C < 0 || L < C || L > limit || q0 < 0 || q0 > total - C;
+}
+
 // Eight values to the pool: fp16, or E4M3 codes of the quotient by the scale.
 template <bool kFp8>
 __device__ __forceinline__ void store8(void* pool, int64_t at, const float (&x)[8], float scale) {
@@ -172,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const __
         int slot = -2, pos = 0;  // -2: the token is left alone; -1: only its keys and values are
         if (r >= 0) {
             const int q0 = p.q_start[r], C = p.q_start[r + 1] - q0, L = p.seq_lens[r];
-            if (C < 0 || L < C || L > p.limit || q0 < 0 || q0 > p.total - C) {
+            if (bad_row(q0, C, L, p.limit, p.total)) {
                 flag_error(p.dev_err, PKV_DEV_ERR_SEQ_LEN);
             } else if (g >= q0 && g - q0 < C) {
                 pos = L - C + (g - q0);
@@ -188,6 +193,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_append_kernel(const __
         }
         sm_slot[t] = slot;
         sm_pos[t] = p.rope_positions ? p.rope_positions[g] : pos;
+    } else if (blockIdx.x == 0 && p.dev_err) {
+        // rows that no token leads to (without nodes, or past total) are looked at by the first
+        // block's other threads meanwhile
+        for (int r = tid - nt; r < p.rows; r += kThreads - nt)
+            if (bad_row(p.q_start[r], p.q_start[r + 1] - p.q_start[r], p.seq_lens[r], p.limit, p.total))
+                flag_error(p.dev_err, PKV_DEV_ERR_SEQ_LEN);
     }
     __syncthreads();
 

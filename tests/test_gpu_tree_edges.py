@@ -324,3 +324,38 @@ def test_rows_that_overlap_beyond_all_bounds_are_refused(cuda_device):
     torch.cuda.synchronize()
     assert ops.check_error(err) == 0
     assert bool(((got - want).float().abs() <= 2e-3 + 2e-3 * want.float().abs()).all())
+
+
+def test_rope_append_flags_rows_that_no_token_leads_to(cuda_device):
+    """Rows without nodes, of falling starts, and behind total_q are looked at too."""
+    step = Step([20, 9, 40], [6, 3, 2], 16, seed=45, fill=False)
+    k, v = (torch.randn(11, 2, 128, generator=step.gen).half().cuda() for _ in range(2))
+    rates = ops.rope_rates(ops.rope_frequencies(128))
+
+    def go(lens, starts, total=11):
+        a = step.gpu(seq_lens=i32(lens), q_start=i32(starts))
+        err = err_word()
+        ops.rope_append(a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], a["q_start"], k[:total], v[:total],
+                        rates, step.max_len, dev_err=err)
+        return ops.check_error(err)
+
+    assert go([26, 12, 42], [0, 6, 9, 11]) == 0
+    assert go([26, 12, 42], [0, 6, 6, 8]) == 0
+    assert go([26, 1000, 42], [0, 6, 6, 8]) == ERR_LEN      # above the bound, without nodes
+    assert go([26, -1, 42], [0, 6, 6, 8]) == ERR_LEN
+    assert go([26, 12, 42], [0, 6, 2, 2]) == ERR_LEN        # fewer than no nodes
+    assert go([26, 12, 42], [0, 6, 9, 11], total=6) == ERR_LEN   # nodes past total_q
+    rows = 700                                               # more rows than the block has threads
+    t = torch.zeros(rows, 1, dtype=torch.int32)
+    for bad in (0, 255, 699):
+        lens = torch.full((rows,), 1, dtype=torch.int32)
+        lens[bad] = 17
+        st = torch.zeros(rows + 1, dtype=torch.int32)
+        st[-1] = 1
+        if bad == rows - 1:
+            st[1:] = 1
+        a = step.gpu(block_tables=t.cuda(), seq_lens=lens.cuda(), q_start=st.cuda())
+        err = err_word()
+        ops.rope_append(a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], a["q_start"], k[:1], v[:1], rates,
+                        16, dev_err=err)
+        assert ops.check_error(err) == ERR_LEN, bad
