@@ -758,7 +758,11 @@ int pkv_bm_append_slot(pkv_block_manager* bm, int64_t seq_id, int32_t* position_
 /*
  * pkv_bm_truncate -- set the sequence's length back to new_len <= its length
  * (PKV_ERR_INVALID_ARG otherwise): the host's side of paged_kv_tree_commit.  Its blocks stay
- * with it, so the next pkv_bm_append_slot calls reuse them.
+ * with it, and the next pkv_bm_append_slot calls reuse those that it does not
+ * share; a shared one is copied on the first write into it, as ever.  A sequence
+ * admitted with a reservation keeps its promise: the private blocks that
+ * such copies will need are taken now, or the call returns PKV_ERR_NO_BLOCKS and
+ * changes nothing.
  */
 int pkv_bm_truncate(pkv_block_manager* bm, int64_t seq_id, int new_len);
 

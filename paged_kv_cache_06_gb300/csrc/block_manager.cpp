@@ -28,6 +28,7 @@ struct Sequence {
     std::vector<int32_t> table;     // physical ids of logical blocks 0..n-1
     std::vector<int32_t> reserved;  // private blocks held for later (reserve on admit)
     int64_t len = 0;                // tokens written
+    int64_t promised = 0;           // blocks that the reservation covers (0 without one)
 };
 
 struct Prefix {
@@ -141,6 +142,7 @@ int pkv_bm_admit(pkv_block_manager* bm, int64_t seq_id, int prompt_len, int max_
 
     Sequence s;
     s.len = prompt_len;
+    s.promised = reserve ? total_blocks : 0;
     for (int64_t i = 0; i < shared_used; ++i) {
         const int32_t id = pre->blocks[(size_t)i];
         ++bm->refcount[id];
@@ -195,8 +197,26 @@ int pkv_bm_truncate(pkv_block_manager* bm, int64_t seq_id, int new_len) {
     if (!bm) return PKV_ERR_INVALID_ARG;
     auto it = bm->seqs.find(seq_id);
     if (it == bm->seqs.end()) return PKV_ERR_NOT_FOUND;
-    if (new_len < 0 || new_len > it->second.len) return PKV_ERR_INVALID_ARG;
-    it->second.len = new_len;
+    Sequence& s = it->second;
+    if (new_len < 0 || new_len > s.len) return PKV_ERR_INVALID_ARG;
+    if (s.promised > 0 && new_len < s.len) {
+        // What the sequence may still write up to its promised length has to be at hand: the
+        // blocks that its table lacks, and a private copy of each shared block from new_len on.
+        int64_t need = std::max<int64_t>(0, s.promised - (int64_t)s.table.size());
+        for (size_t b = (size_t)(new_len / bm->block_size); b < s.table.size(); ++b)
+            need += bm->refcount[s.table[b]] > 1;
+        const int64_t more = need - (int64_t)s.reserved.size();
+        if (more > 0) {
+            if (!bm->can_pop(more)) return PKV_ERR_NO_BLOCKS;
+            try {
+                s.reserved.reserve((size_t)need);
+            } catch (const std::bad_alloc&) {
+                return PKV_ERR_NO_BLOCKS;
+            }
+            for (int64_t i = 0; i < more; ++i) s.reserved.push_back(bm->pop());
+        }
+    }
+    s.len = new_len;
     return PKV_OK;
 }
 
