@@ -2,9 +2,11 @@
 and the Python binding of the drafted step's calls, ``_binding.so``.
 
 Translation units compile in parallel into ``_build/`` and link into
-``paged_kv_cache_06_gb300/libpagedkv.so``; ``csrc/python/`` compiles against the
-installed torch's headers into ``_binding.so`` beside it, which links to it.
-Rebuilds only when a source or header is newer than the products.  Usage: ``python -m
+``paged_kv_cache_06_gb300/libpagedkv.so``, for which nvcc and g++ are enough;
+``csrc/python/`` compiles against the installed torch's and Python's headers into
+``_binding.so`` beside it, which links to it, and is left out where there is no
+torch.  Rebuilds only when a source or header is newer than the product, and the
+binding also when torch or Python is another one.  Usage: ``python -m
 paged_kv_cache_06_gb300.build [--force]``.
 """
 from __future__ import annotations
@@ -49,24 +51,49 @@ def sources():
     return cu, cpp
 
 
-def _inputs():
-    cu, cpp = sources()
-    hdr = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+def _headers():
+    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
-    return cu + cpp + hdr + [BINDING_SRC]
+
+
+def _older(product: str, inputs) -> bool:
+    return not os.path.exists(product) or any(os.path.getmtime(p) > os.path.getmtime(product) for p in inputs)
+
+
+def library_is_stale() -> bool:
+    cu, cpp = sources()
+    return _older(LIB_PATH, cu + cpp + _headers())
+
+
+def _torch_dir() -> str | None:
+    """The installed torch's folder, without importing it (None: no torch)."""
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
+
+
+def _binding_stamp() -> str:
+    """What the binding was compiled against."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return "\n".join([sys.version, str(sysconfig.get_config_var("SOABI")), _torch_dir(), f.read()])
+
+
+def binding_is_stale() -> bool:
+    if _older(BINDING_PATH, _headers() + [BINDING_SRC]):
+        return True
+    try:
+        with open(_stamp_path()) as f:
+            return f.read() != _binding_stamp()
+    except OSError:
+        return True
+
+
+def _stamp_path() -> str:
+    return os.path.join(BUILD_DIR, "binding.stamp")
 
 
 def is_stale() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(BINDING_PATH)):
-        return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return any(os.path.getmtime(p) > t for p in _inputs())
-
-
-def _torch_dir() -> str:
-    """The installed torch's folder, without importing it."""
-    import importlib.util
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+    return library_is_stale() or (_torch_dir() is not None and binding_is_stale())
 
 
 def _binding_flags():
@@ -98,32 +125,54 @@ def _compile(src: str, verbose: bool, ptxas_info: bool) -> str:
     return obj
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every CUDA/C++ source for sm_103a and link libpagedkv.so."""
-    if not force and not ptxas_info and not is_stale():
-        return LIB_PATH
+def _compile_all(srcs, verbose: bool, ptxas_info: bool):
     os.makedirs(BUILD_DIR, exist_ok=True)
-    cu, cpp = sources()
-    srcs = [BINDING_SRC] + cu + cpp  # the slowest first
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        binding, *objs = ex.map(lambda s: _compile(s, verbose, ptxas_info), srcs)
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
+        return [ex.submit(_compile, s, verbose, ptxas_info) for s in srcs]
+
+
+def _link(cmd, path: str) -> None:
+    tmp = path + f".tmp{os.getpid()}"
+    res = subprocess.run([x if x is not None else tmp for x in cmd], capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"linking {os.path.basename(path)} failed:\n{res.stderr}")
+    os.replace(tmp, path)
+
+
+def _link_library(objs) -> None:
     lib_dir = os.path.join(_cuda_home(), "lib64")
-    cmd = [_nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
-           "-L", lib_dir, "-Xlinker", f"-rpath,{lib_dir}"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"linking libpagedkv.so failed:\n{res.stderr}")
-    os.replace(tmp, LIB_PATH)
-    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    _link([_nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", None, *objs,
+           "-L", lib_dir, "-Xlinker", f"-rpath,{lib_dir}"], LIB_PATH)
+
+
+def _link_binding(obj: str) -> None:
+    lib_dir = os.path.join(_cuda_home(), "lib64")
     torch_lib = os.path.join(_torch_dir(), "lib")
-    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, binding, "-L", HERE, "-l:libpagedkv.so",
+    _link([os.environ.get("CXX", "g++"), "-shared", "-o", None, obj, "-L", HERE, "-l:libpagedkv.so",
            "-Wl,-rpath,$ORIGIN", "-L", torch_lib, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-           "-lc10_cuda", "-L", lib_dir, "-lcudart", f"-Wl,-rpath,{torch_lib}", f"-Wl,-rpath,{lib_dir}"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"linking _binding.so failed:\n{res.stderr}")
-    os.replace(tmp, BINDING_PATH)
+           "-lc10_cuda", "-L", lib_dir, "-lcudart", f"-Wl,-rpath,{torch_lib}", f"-Wl,-rpath,{lib_dir}"],
+          BINDING_PATH)
+    with open(_stamp_path(), "w") as f:
+        f.write(_binding_stamp())
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False, library: bool = True,
+          binding: bool = True) -> str:
+    """Compile every CUDA/C++ source for sm_103a and link libpagedkv.so, then the
+    binding (where torch is installed); either may be left out.  The library does not
+    depend on the binding: it is linked before the binding's errors are raised."""
+    library = library and (force or ptxas_info or library_is_stale())
+    binding = binding and _torch_dir() is not None and (force or binding_is_stale())
+    cu, cpp = sources()
+    # the slowest first
+    srcs = ([BINDING_SRC] if binding else []) + (cu + cpp if library else [])
+    if not srcs:
+        return LIB_PATH
+    objs = _compile_all(srcs, verbose, ptxas_info)
+    if library:
+        _link_library([o.result() for o in objs[binding:]])
+    if binding:
+        _link_binding(objs[0].result())
     return LIB_PATH
 
 

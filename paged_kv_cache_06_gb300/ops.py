@@ -45,7 +45,7 @@ def lib() -> ctypes.CDLL:
     global _lib
     with _lock:
         if _lib is None:
-            path = _build.build()
+            path = _build.build(binding=False)
             if not os.path.exists(path):
                 raise RuntimeError(f"libpagedkv.so missing at {path}")
             L = ctypes.CDLL(path)
@@ -55,12 +55,13 @@ def lib() -> ctypes.CDLL:
 
 
 def binding():
-    """The C++ binding module of the drafted step's calls (loads the library
-    first, which it links against)."""
+    """The C++ binding module of the drafted step's calls (built first if it is
+    missing or stale; loads the library, which it links against)."""
     global _ext
     lib()
     with _lock:
         if _ext is None:
+            _build.build(library=False)
             path = _build.BINDING_PATH
             loader = importlib.machinery.ExtensionFileLoader(f"{__package__}._binding", path)
             spec = importlib.util.spec_from_file_location(loader.name, path, loader=loader)
