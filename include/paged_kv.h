@@ -464,7 +464,8 @@ int paged_attention_decode_planned(void* out, const void* q, void* k_pool, void*
  *                                of more than `high` turns stay, pairs of fewer
  *                                than `low` are interpolated
  * rot_dim even, base > 1, factor >= 1 (unused by NONE); original_len, low <
- * high are used by BY_PARTS alone.  PKV_ERR_INVALID_ARG otherwise.
+ * high are used by BY_PARTS alone; the scaled base and high - low finite.
+ * PKV_ERR_INVALID_ARG otherwise.
  *
  * pkv_rope_rates -- rates[i] = freqs[i] / 2 pi as a fraction of a turn in 64
  * bits (modulo a turn), the form in which paged_kv_rope_append takes the

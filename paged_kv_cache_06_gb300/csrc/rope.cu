@@ -285,9 +285,11 @@ extern "C" int pkv_rope_frequencies(double* freqs, int rot_dim, double base, int
     if (scaling == PKV_ROPE_SCALING_BASE) {
         if (rot_dim <= 2) return PKV_ERR_INVALID_ARG;
         base *= pow(factor, (double)rot_dim / (rot_dim - 2));
+        if (!isfinite(base)) return PKV_ERR_INVALID_ARG;
     }
     if (scaling == PKV_ROPE_SCALING_BY_PARTS &&
-        (!(original_len > 0.0) || !isfinite(original_len) || !isfinite(low) || !(high > low) || !isfinite(high)))
+        (!(original_len > 0.0) || !isfinite(original_len) || !isfinite(low) || !(high > low) || !isfinite(high) ||
+         !isfinite(high - low)))
         return PKV_ERR_INVALID_ARG;
     for (int i = 0; i < rot_dim / 2; ++i) {
         double f = pow(base, -2.0 * i / rot_dim);
