@@ -81,14 +81,13 @@
 #include "fp8_codec.cuh"
 #include "pkv_internal.cuh"
 #include "tcgen05.cuh"
+#include "tree_split.cuh"
 
 namespace pkv {
 namespace tree {
 using namespace tc;
 
-constexpr int kRows = 128;     // flat rows of an M block: TMEM lanes
 constexpr int kTile = 128;     // tokens of a tile
-constexpr int kGrainLog = 6, kGrain = 1 << kGrainLog;  // tokens of a granule: the grain of the work split, and of V's slots
 constexpr int kSoftWarps = 8;
 constexpr int kSIssue = 8, kPvIssue = 9, kLoad = 10, kConv = 12;  // warp roles
 constexpr int kConvWarps = 4;
@@ -96,19 +95,6 @@ constexpr int kMaxRows = 1024;
 constexpr int kMaxGrid = 192;  // blocks: one per SM, at most this many
 constexpr int kMaxWords = 32;  // mask words: up to 1024 nodes a row
 constexpr int kHeadInts = 32;  // ints between two units' words: count, then given-up blocks' bits
-// Granules that a unit's queries, first scores and output cost in time, and how near a
-// unit's border a cut moves to it (farther than the cost, so that a cut that stays lies
-// past it): a piece more costs its block a start, a partial and a merge, which is worth
-// some imbalance.  Over FP8 pools a segment starts later and its products come slower.
-// Measured, cost and slack: fp16, 32 rows of 16..512 and one of 4096, 8..24
-// nodes: 2, 5: 19.0 us; 4, 4: 21.0; 3, 6: 20.6; 6, 12: 23.4; 90 drawn batches'
-// geometric mean 15.3, 15.5, 15.1, 15.8.  FP8, 32 rows of 1024 and 25 nodes; 96 rows of
-// 16..8192, chains of 3..7; 28 drawn batches: 6, 10: 20.7, 35.2, 15.8; 8, 12: 20.7, 35.4,
-// 16.0; 8, 9: 23.4, 37.1, 15.7; 4, 6: 24.7, 35.9, 15.8.
-template <bool kFp8>
-__host__ __device__ constexpr int unit_cost() { return kFp8 ? 6 : 2; }
-template <bool kFp8>
-__host__ __device__ constexpr int unit_slack() { return kFp8 ? 10 : 5; }
 constexpr uint32_t kHalfQ = kRows * 128;   // 128 flat rows x 64 dims
 constexpr uint32_t kQBlock = 2 * kHalfQ;
 constexpr uint32_t kKHalf = kTile * 128;   // 128 tokens x 64 dims
@@ -129,21 +115,8 @@ constexpr float kWeightLog2 = 7.f;
 constexpr int kSBufs = 3;        // S buffers of 128 columns
 constexpr uint32_t kColS = 128;  // above the accumulator's 128 columns
 
-constexpr int kPlanes = 4;  // at most
-
 template <bool kFp8>
 __host__ __device__ constexpr int threads() { return (kConv + (kFp8 ? kConvWarps : 0)) * 32; }
-
-// The planes: M block m of a row belongs to plane m % n; magic = 2^32 / n, rounded up.
-struct Planes {
-    int n;
-    uint32_t magic;
-    // A row's M blocks in a plane (a row has fewer than 2^28).
-    __device__ __forceinline__ int blocks(int flat, int plane) const {
-        const int m = (flat + kRows - 1) / kRows - plane;
-        return m <= 0 ? 0 : n == 1 ? m : (int)__umulhi((uint32_t)(m + n - 1), magic);
-    }
-};
 
 // n / d for 0 <= n < 2^31 and d >= 2: with 2^(l - 1) < d <= 2^l and m = ceil(2^(31 + l) / d),
 // n m / 2^(31 + l) is above n / d by less than 1 / d.
@@ -211,134 +184,6 @@ struct Smem {
     static_assert(kslots * kKSlot + vslots * kVSlot >= kPartFloats * 4, "a partial fits the rings");
     static_assert(vslots >= 4, "two tiles before this one, a slot of it was filled for the last time");
     static_assert(2 * (kslots + vslots + 2 * raws) + 3 * kSBufs + 16 <= 64, "barriers");
-};
-
-// a / b for 0 <= a < 2^31, 0 < b: a float quotient (off by 2^-21 of it at most,
-// 1024), that of the remainder (off by one), and the last step.
-__device__ __forceinline__ int div_of(int a, int b) {
-    const float rb = __fdividef(1.f, (float)b);
-    int q = (int)((float)a * rb);
-    q += __float2int_rn((float)(a - q * b) * rb);
-    const int r = a - q * b;
-    return r < 0 ? q - 1 : r >= b ? q + 1 : q;
-}
-
-// A unit: M block plane + planes t of KV head k of row r, its place U in the
-// plane's sequence and its n granules; there it takes n + kUnitCost.
-template <int kUnitCost>
-struct Unit {
-    int r, k, t, U, n;
-    __device__ __forceinline__ int end() const { return U + n + kUnitCost; }
-};
-
-__device__ __noinline__ int cut_at(int x, int W, int G, int quo, int rem);
-
-// How a plane's sequence of units, W long, is cut over its G blocks: raw cut c lies at
-// floor(W c / G); one within `slack` of a border of its unit moves there.
-template <int kUnitCost>
-struct Split {
-    using Of = Unit<kUnitCost>;
-    int W, G, slack, quo, rem;
-    __device__ __forceinline__ void set(int w, int blocks, int least) {
-        W = w;
-        G = min(blocks, max(w, 1));
-        quo = div_of(W, G);
-        rem = W - quo * G;
-        slack = max(least, quo / 16);
-    }
-    __device__ __forceinline__ int raw(int c) const { return quo * c + div_of(rem * c, G); }
-    __device__ __forceinline__ int moved(int x, const Of& u) const {
-        const int d0 = x - u.U, d1 = u.end() - x;
-        if (min(d0, d1) > slack) return x;
-        return d0 <= d1 ? u.U : u.end();
-    }
-    // The pieces of unit u (1: whole) and the plane's block that holds the first one.
-    __device__ __forceinline__ int pieces(const Of& u, int& first) const {
-        const int a = u.U + slack + 1, b = u.end() - slack;  // cuts that stay lie in [a, b)
-        if (a >= b) return 1;
-        const int lo = cut_at(a, W, G, quo, rem), hi = cut_at(b, W, G, quo, rem);
-        first = lo - 1;
-        return hi - lo + 1;
-    }
-};
-
-// The first raw cut at x or behind it: the quotient's float estimate is off by
-// one at most (there are at most kMaxGrid cuts).
-__device__ __noinline__ int cut_at(int x, int W, int G, int quo, int rem) {
-    int c = (int)__fdividef((float)x * (float)G, (float)W);
-#pragma unroll 1
-    while (c > 0 && quo * (c - 1) + div_of(rem * (c - 1), G) >= x) --c;
-#pragma unroll 1
-    while (quo * c + div_of(rem * c, G) < x) ++c;
-    return c;
-}
-
-// The unit (r, k, t, n) before a unit; out of line, once for all the roles.
-__device__ __noinline__ int4 unit_before(int4 u, int hk, int group, int plane, int n, uint32_t magic, const int* C,
-                                         const int* P) {
-    const Planes planes{n, magic};
-    if (u.z > 0) {
-        --u.z;
-        return u;
-    }
-    int nt = planes.blocks(C[u.x] * group, plane);
-    if (u.y > 0) {
-        --u.y;
-    } else {
-#pragma unroll 1
-        do {
-            --u.x;
-            nt = planes.blocks(C[u.x] * group, plane);
-        } while (nt == 0);
-        u.y = hk - 1;
-        u.w = (P[u.x] + C[u.x] + kGrain - 1) / kGrain;
-    }
-    u.z = nt - 1;
-    return u;
-}
-
-// a + b, kept at 2^31 - 1: the work of rows whose starts fall, so that they overlap, may
-// pass what the host has allowed for.
-constexpr int kTooMuch = 0x7fffffff;
-__device__ __forceinline__ int add_work(int a, int b) { return (int)min((unsigned)a + (unsigned)b, (unsigned)kTooMuch); }
-
-// The units of a block's range [s0, e), last to first.
-template <int kUnitCost>
-struct Walk : Unit<kUnitCost> {
-    using Unit<kUnitCost>::r;
-    using Unit<kUnitCost>::k;
-    using Unit<kUnitCost>::t;
-    using Unit<kUnitCost>::U;
-    using Unit<kUnitCost>::n;
-    using Unit<kUnitCost>::end;
-    int s0, e, hk, group, plane;
-    Planes planes;
-    const int* C;
-    const int* P;
-    __device__ __forceinline__ int g0() const { return max(s0 - U - kUnitCost, 0); }
-    __device__ __forceinline__ int g1() const { return min(e - U - kUnitCost, n); }
-    __device__ __forceinline__ bool whole() const { return s0 <= U && e >= end(); }
-    __device__ __forceinline__ int len() const { return P[r] + C[r]; }
-    __device__ __forceinline__ int flat() const { return C[r] * group; }
-    __device__ __forceinline__ int f0() const { return (plane + planes.n * t) * kRows; }  // first flat row
-    // its tokens in the range: [ta, te)
-    __device__ __forceinline__ int ta() const { return g0() * kGrain; }
-    __device__ __forceinline__ int te() const { return min(g1() * kGrain, len()); }
-    // step to the unit before
-    __device__ __forceinline__ void back() {
-        const int4 v = unit_before(make_int4(r, k, t, n), hk, group, plane, planes.n, planes.magic, C, P);
-        r = v.x;
-        k = v.y;
-        t = v.z;
-        n = v.w;
-        U -= n + kUnitCost;
-    }
-    __device__ __forceinline__ bool prev() {
-        if (U <= s0) return false;
-        e = U;
-        back();
-        return true;
-    }
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -765,9 +610,6 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         int W = plane_of(0, before);
         int from = 0, to = (int)gridDim.x;
         if (planes.n > 1) {
-            // blocks in proportion to the planes' work, one at least where there is any
-            float Wf[kPlanes], all = 0.f;
-            int later = 0;  // planes with work that are still to come
             int Wi[kPlanes], bf[kPlanes];
             Wi[0] = W;
             bf[0] = before;
@@ -783,35 +625,14 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
 #pragma unroll
                 for (int x = 0; x < kPlanes; ++x) Wi[x] = 0;
             }
+            const Share s = share_of(Wi, planes, (int)gridDim.x, (int)blockIdx.x);
+            plane = s.plane;
+            W = s.W;
+            from = s.from;
+            to = s.to;
 #pragma unroll
-            for (int x = 0; x < kPlanes; ++x) {
-                all += Wf[x] = (float)Wi[x];
-                later += Wi[x] > 0;
-            }
-            const float share = all > 0.f ? __fdividef((float)gridDim.x, all) : 0.f;
-            // planes of equal work get as many blocks each, so that they stay in step
-            bool even = true;
-#pragma unroll
-            for (int x = 1; x < kPlanes; ++x) even = even && (x >= planes.n || Wi[x] == Wi[0]);
-            const int each = (int)((uint64_t)gridDim.x * planes.magic >> 32);
-            float upto = 0.f;
-            int next = 0;
-            W = 0;
-#pragma unroll
-            for (int x = 0; x < kPlanes; ++x) {
-                upto += Wf[x];
-                later -= Wi[x] > 0;
-                const int end = even ? next + (x < planes.n ? each : 0)
-                                     : min(max(__float2int_rn(upto * share), next + (Wi[x] > 0)), (int)gridDim.x - later);
-                if ((int)blockIdx.x >= next && (int)blockIdx.x < end) {
-                    plane = x;
-                    W = Wi[x];
-                    before = bf[x];
-                    from = next;
-                    to = end;
-                }
-                next = end;
-            }
+            for (int x = 0; x < kPlanes; ++x)
+                if (x == plane) before = bf[x];
         }
         if (W > 0) {
             base_block = from;
@@ -843,24 +664,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             u.C = sm_C;
             u.P = sm_P;
             u.r = r0;
-            int at = in - run, nt;
-#pragma unroll 1
-            for (;; ++u.r) {
-                nt = planes.blocks(u.flat(), plane);
-                u.n = (u.len() + kGrain - 1) / kGrain;
-                const int here = p.hk * nt * (u.n + kUnitCost);
-                if (at < here) break;
-                at -= here;
-            }
-            const int i = div_of(at, u.n + kUnitCost);
-            u.k = div_of(i, nt);
-            u.t = i - u.k * nt;
-            u.U = in - (at - i * (u.n + kUnitCost));
-            const int cut = x < u.end() ? sp.moved(x, u) : x;
+            const int cut = place_cut(u, sp, x, side, run);
             if (side == 0) {
                 sm_misc[6] = cut;
             } else {
-                if (cut == u.U && cut > 0) u.back();  // the unit before the cut
                 sm_misc[0] = u.r;
                 sm_misc[1] = u.k;
                 sm_misc[2] = u.t;
@@ -1726,9 +1533,7 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     if ((st = encode_map_3d(v_pool, type, dims, strides, box, &vm)) != PKV_OK) return st;
     int64_t nodes = total_q < max_seq_len ? total_q : max_seq_len;  // the most a row can have
     if (mask && nodes > 32 * (int64_t)mask_words) nodes = 32 * (int64_t)mask_words;
-    const int64_t m = (nodes * group + kRows - 1) / kRows;
-    prm.planes.n = m < 1 ? 1 : m > kPlanes ? kPlanes : (int)m;
-    prm.planes.magic = prm.planes.n > 1 ? (uint32_t)((0x100000000ull + prm.planes.n - 1) / prm.planes.n) : 0u;
+    prm.planes = Planes::of(nodes, group);
     return fp8 ? launch<true>(prm, km, vm, blocks, stream) : launch<false>(prm, km, vm, blocks, stream);
 }
 
