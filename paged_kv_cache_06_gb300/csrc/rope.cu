@@ -405,7 +405,9 @@ extern "C" int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, con
     // 2.9 us (a token a block); 640 tokens, half of each head rotated, E4M3: a token a
     // block 4.2 us, four 5.4; 15,000 tokens: 20 a block 24.8 us, 4 a block 26.7, 8 a block
     // 26.4, 16 a block 27.3 (one and a half waves).
-    const int items = p.n_pair + p.n_pass + p.n_val, wave = 152 * kBlocks;
+    const int sms = device_sms();
+    if (sms <= 0) return PKV_ERR_CUDA;
+    const int items = p.n_pair + p.n_pass + p.n_val, wave = sms * kBlocks;
     int tokens = total_q < wave ? 1 : (total_q + wave - 1) / wave;
     if (tokens > kTokens) tokens = kTokens;
     if (tokens > 65535 / items) tokens = 65535 / items;
