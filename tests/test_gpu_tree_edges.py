@@ -359,3 +359,53 @@ def test_rope_append_flags_rows_that_no_token_leads_to(cuda_device):
         ops.rope_append(a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], a["q_start"], k[:1], v[:1], rates,
                         16, dev_err=err)
         assert ops.check_error(err) == ERR_LEN, bad
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_slots_whose_offsets_pass_32_bits(cuda_device, fp8):
+    """The last blocks of pools of more than 2^32 bytes: the same bits as in small pools."""
+    bs, hk, d = 64, 2, 128
+    step = Step([300, 40, 129], [9, 30, 5], bs, hk=hk, fp8=fp8, seed=50, fill=False)
+    extra = (1 << 32) // (bs * hk * d * (1 if fp8 else 2)) + 3
+    q = torch.randn(step.total, 12, d, generator=step.gen).half().cuda()
+    k, v = (torch.randn(step.total, hk, d, generator=step.gen).half().cuda() for _ in range(2))
+    mask = ops.tree_mask(random_parents(step.nodes, 6), step.starts).cuda()
+    rates = ops.rope_rates(ops.rope_frequencies(d))
+    paths = i32([[0, 3, 8], [2, 17, 29], [1, 4, -1]])
+
+    def run(shift):
+        a = step.gpu()
+        kp, vp = a["k_pool"], a["v_pool"]
+        if shift:
+            kp, vp = (torch.empty((shift + step.nb, *x.shape[1:]), dtype=x.dtype, device="cuda") for x in (kp, vp))
+            kp[shift:], vp[shift:] = a["k_pool"], a["v_pool"]
+        tables = torch.where(a["block_tables"] >= 0, a["block_tables"] + shift, -1).int()
+        rows = (tables, a["seq_lens"], a["q_start"])
+        sc = dict(k_scale=a["k_scale"], v_scale=a["v_scale"])
+        err, nl = err_word(), torch.zeros(3, dtype=torch.int32, device="cuda")
+        ws = ops.alloc_tree_workspace(3, step.total, 12, hk, d, bs)
+        qo, out = torch.empty_like(q), torch.empty_like(q)
+        ops.rope_append(kp, vp, *rows, k, v, rates, step.max_len, q=q, q_out=qo, dev_err=err, **sc)
+        ops.tree_attention(out, qo, kp, vp, *rows, 0.1, step.max_len, ws, mask=mask, dev_err=err, **sc)
+        ops.tree_commit(kp, vp, *rows, paths, i32([3, 3, 2]), step.max_len, new_seq_lens=nl, dev_err=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        return [x.cpu() for x in (qo, out, kp[shift:].view(torch.uint8), vp[shift:].view(torch.uint8), nl)]
+
+    for a, b in zip(run(0), run(extra)):
+        assert torch.equal(a, b)
+
+
+def test_a_prompt_sized_chain_equals_prefill(cuda_device):
+    """Chunks of hundreds to thousands of tokens without a mask, over empty and long caches,
+    beside the prefill kernel (2e-3 + 2e-3 |ref| is its tolerance; both sides take half at most)."""
+    step = Step([0, 500, 9000, 3], [2048, 1000, 700, 1500], 64, seed=51)
+    q = torch.randn(step.total, 12, 128, generator=step.gen).half()
+    a = step.gpu()
+    out = torch.empty(step.total, 12, 128, dtype=torch.float16, device="cuda")
+    ops.prefill(out, q.cuda(), a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], a["q_start"], 0.0883,
+                step.max_len)
+    err = err_word()
+    got = tree_run(step, q, None, 0.0883, err)
+    assert int(err.item()) == 0
+    assert bool(((got - out).float().abs() <= 2e-3 + 2e-3 * out.float().abs()).all())
