@@ -44,7 +44,8 @@
  * (a table entry outside [0, num_blocks), a seq_len above the bound, an
  * append position past the row's table) never fault: the offending block,
  * row or token is skipped, and when `dev_err` is non-null a PKV_DEV_ERR_*
- * bit is OR-ed into *dev_err.  Kernels never trap and never spin-wait.
+ * bit is OR-ed into *dev_err.  Kernels never trap, and every wait in them is
+ * bounded.
  */
 #ifndef PAGED_KV_H
 #define PAGED_KV_H

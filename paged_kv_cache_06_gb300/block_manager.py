@@ -116,7 +116,9 @@ class BlockManager:
         return pos.value, ((src.value, dst.value) if src.value >= 0 else None)
 
     def truncate(self, seq_id: int, new_len: int) -> None:
-        """Set the sequence's length back to ``new_len`` (its blocks stay)."""
+        """Set the sequence's length back to ``new_len`` (its blocks stay).  A
+        reservation also covers the copies that writes into shared blocks will need:
+        PagedKVError (PKV_ERR_NO_BLOCKS), with nothing changed, when none are free."""
         _check("pkv_bm_truncate", _L().pkv_bm_truncate(self._h, seq_id, new_len))
 
     def free(self, seq_id: int) -> None:

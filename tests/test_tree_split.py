@@ -100,7 +100,7 @@ def test_known_batches(host, fp8, cached, nodes, group, hk):
 @pytest.mark.parametrize("fp8", [False, True])
 def test_random_batches(host, fp8):
     rng = random.Random(int(fp8))
-    for _ in range(400):
+    for _ in range(200):
         rows = rng.choice([1, 2, rng.randint(1, 40), rng.randint(200, 1024)])
         top = 20000 if rows < 50 else 900
         nodes = [rng.choice([0, 1, rng.randint(1, 200)]) for _ in range(rows)]
