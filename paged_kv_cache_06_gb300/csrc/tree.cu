@@ -108,11 +108,13 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kPartFloats = 2 * kRows + kRows * kHeadDim;
 constexpr uint32_t kHelpNs = 100000;  // how long a block waits for a unit's other pieces
 constexpr float kLog2e = 1.4426950408889634f;
-// A weight of the reference maximum is 2^7, so that one of 2^8 times it, the most there
-// is, stays below fp16's largest value, and the smallest normal one is 2^-21 of it (without the
-// 2^7: 2^-14, and weights below 2^-25 were lost to the output while the row's sum kept
-// them).  O and the sums carry the same factor in every piece.
-constexpr float kWeightLog2 = 7.f;
+// A row's reference lies 7 below its maximum at the time, which then weighs 2^7, and moves
+// when a score passes it by more than 15: weights up to 2^15 are fp16 numbers, and the
+// smallest normal one is 2^-21 of the first maximum's (with the reference at the
+// maximum: 2^-14, and weights below 2^-25 were lost to the output while the row's sum
+// kept them).  The reference is what every difference is taken from, so its own rounding
+// is in all of them alike.
+constexpr float kWeightLog2 = 7.f, kMoveLog2 = 15.f;
 constexpr int kSBufs = 3;        // S buffers of 128 columns
 constexpr uint32_t kColS = 128;  // above the accumulator's 128 columns
 
@@ -1115,20 +1117,21 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
 #pragma unroll
                         for (int c = 0; c < kAtOnce; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], s[c]);
                     }
-                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                     // The reference so far comes from the job before, the other group's.  Lazy
-                    // rescaling: it only moves when a score exceeds it by more than 2^8 (weights
-                    // stay <= 2^8 of it).  A row that sees nothing yet stays at -inf with zero
-                    // weights.
+                    // rescaling: it only moves when a weight would pass 2^15, by the very difference
+                    // that is the weight's exponent (a sum rounds by 8 and more where scores
+                    // pass 2^26).  A row that sees nothing yet stays at -inf with zero weights.
                     float now = -INFINITY, alpha = 1.f;
                     bool moved = false;
                     if (t0 > ta) {
                         if (!(ok = waitw(bar_m + 8 * ((wg ^ 1) * 4 + quarter), ((uint32_t)(job - 1) >> 1) & 1, abort))) break;
                         now = sm_ref[((job - 1) & 1) * kRows + i];
                     }
-                    if (mx > now + 8.f) {
-                        alpha = fast_exp2(now - mx);  // 0 while it is -inf
-                        now = mx;
+                    if (__fmaf_rn(mx, scale_log2, -now) > kMoveLog2) {
+                        const float to = __fmaf_rn(mx, scale_log2, -kWeightLog2);
+                        alpha = fast_exp2(now - to);  // 0 while it is -inf
+                        now = to;
                         moved = t0 > ta;
                     }
                     sm_ref[(job & 1) * kRows + i] = now;
@@ -1136,7 +1139,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     if (lane == 0) mbar_arrive(bar_m + 8 * (wg * 4 + quarter));
                     l *= ref == now ? 1.f : fast_exp2(ref - now);  // 0 while ref is -inf
                     ref = now;
-                    const float mneg = now == -INFINITY ? 0.f : kWeightLog2 - now;
+                    const float mneg = now == -INFINITY ? 0.f : -now;
                     // scores in pairs: one packed FMA for the exponents, one packed add for the
                     // row sums; P is rounded to fp16 for the product (2^-11 a weight; see kWeightLog2)
                     // and goes over the first 32 of each half's own 64 S columns, of parts already read

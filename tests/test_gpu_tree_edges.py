@@ -409,3 +409,32 @@ def test_a_prompt_sized_chain_equals_prefill(cuda_device):
     got = tree_run(step, q, None, 0.0883, err)
     assert int(err.item()) == 0
     assert bool(((got - out).float().abs() <= 2e-3 + 2e-3 * out.float().abs()).all())
+
+
+@pytest.mark.parametrize("rise", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("log2", [20, 23, 24, 25, 26, 27])
+def test_scores_so_large_that_their_differences_round(cuda_device, log2, rise):
+    """Finite scores of 2^20 to 2^27 (in powers of two of the weight) that grow along the
+    row by a few units in the last place.  Roundings of the products decide which token
+    counts, but every answer is a mean of the row's values: finite, and between the
+    smallest and the largest of each dim."""
+    step = Step([1700, 1000], [9, 4], 16, seed=52)
+    q = torch.zeros(step.total, 12, 128, dtype=torch.float16)
+    q[:, :, 0] = 4096.0
+    q[:, :, 1] = 1.0
+    kp = step.k_pool.view(-1, 2, 128)
+    scale = 2.0 ** (log2 - 24) * float(np.log(2.0))
+    for r in range(2):
+        s = step.slots(r)
+        kp[s] = 0
+        kp[s, :, 0] = 4096.0                   # a score of 2^24 in units of the scale, more by `rise` from tile to tile
+        kp[s, :, 1] = (rise * (torch.arange(len(s)) // 128)).half()[:, None]
+    mask = ops.tree_mask(random_parents(step.nodes, 3), step.starts)
+    got = tree_run(step, q, mask, scale).double().cpu()
+    assert bool(torch.isfinite(got).all())
+    for r in range(2):
+        v = step.values(step.v_pool, r, None).repeat_interleave(6, 1)
+        a = int(step.starts[r])
+        x = got[a:a + step.nodes[r]]
+        slack = 2.0 ** -9 * v.abs().amax(0)     # weights, sums and the output are rounded to 2^-11 each
+        assert bool((x <= v.amax(0) + slack).all()) and bool((x >= v.amin(0) - slack).all())
