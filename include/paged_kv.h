@@ -546,7 +546,9 @@ int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, const float* k
  *     out[g][h][:] = sum_t softmax_t(scale * q[g][h] . K_t) * V_t[:]
  * over the tokens it sees, head h reading KV head h / (q_heads / kv_heads).  A
  * node that sees nothing gives zeros.  Tokens that a node does not see do not
- * reach its output whatever they hold (infinities and NaN included).
+ * reach its output whatever they hold (infinities and NaN included).  Scores
+ * (scales included) are below 2^27 in absolute value; beyond, where binary32 no
+ * longer tells neighbouring ones apart, the output may be NaN.
  * q, out: fp16 [total_q][q_heads][head_dim], not overlapping.  mask: device uint32
  * [total_q][mask_words]; a row of more than 32 * mask_words nodes is skipped
  * and flagged PKV_DEV_ERR_MASK.  Pools: fp16 when k_scale == v_scale == null,
