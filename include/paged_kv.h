@@ -669,11 +669,13 @@ int pkv_debug_set_decode_hooks(unsigned poll_limit, const void* stuck_word);
  * default, 100,000) and then leaves the merge, or its share of it, to another
  * block; the result is the same, bit for bit.  With stop_folds != 0 a block
  * that has fetched the other half of a unit cut in two gives up there and flags
- * PKV_DEV_ERR_TIMEOUT (zero-fill the workspace afterwards).  (0, 0) restores
- * normal operation.  Both apply to launches made (and captured) after the call,
+ * PKV_DEV_ERR_TIMEOUT (zero-fill the workspace afterwards).  linger_ns (at most
+ * 1,000,000; PKV_ERR_INVALID_ARG beyond) keeps one warp of each block behind the
+ * others at the end of every unit; the result is the same.  (0, 0, 0) restores
+ * normal operation.  All apply to launches made (and captured) after the call,
  * from any thread, until changed.  For tests; not for production use.
  */
-int pkv_debug_set_tree_hooks(unsigned help_ns, int stop_folds);
+int pkv_debug_set_tree_hooks(unsigned help_ns, int stop_folds, unsigned linger_ns);
 
 /*
  * pkv_check_error -- synchronise `stream`, copy the device error word to

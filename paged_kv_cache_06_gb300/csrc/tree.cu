@@ -155,6 +155,7 @@ struct Params {
     int* heads;    // [grid][kHeadInts], zero between calls: of the cut unit that starts in a block
     uint32_t help_ns;  // kHelpNs, but for tests
     uint32_t stop;     // for tests: blocks that fold give up once the copy is issued
+    uint32_t linger_ns;  // for tests: how long warp 0 stays behind at each segment's end
     int32_t* dev_err;
 };
 
@@ -176,8 +177,8 @@ struct Smem {
     static constexpr uint32_t misc = tmem + 16;
     static constexpr uint32_t bad = misc + 192;                    // [32] granules: 16-token groups not to be seen
     static constexpr uint32_t ref = bad + 128;                     // [2] jobs' reference maxima [128]
-    static constexpr uint32_t sum = ref + 2 * kRows * 4;           // [2 groups] last references, row sums [128]
-    static constexpr uint32_t rowc = sum + 4 * kRows * 4;          // per row: nodes
+    static constexpr uint32_t sum = ref + 2 * kRows * 4;           // of a segment and the one before: [2 groups] last references, row sums [128]
+    static constexpr uint32_t rowc = sum + 8 * kRows * 4;          // per row: nodes
     static constexpr uint32_t rowp = rowc + kMaxRows * 4;          // per row: cached tokens
     // the scan's scratch lives in the K ring: it is read before the first copy is issued
     static constexpr uint32_t part = kring;
@@ -412,6 +413,11 @@ __device__ __forceinline__ int count_pair(int* word, int piece) {
     int old;
     asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(word), "r"(1 + piece) : "memory");
     return old;
+}
+
+__device__ __noinline__ void linger(uint32_t ns) {
+    const uint64_t from = now_ns();
+    while (now_ns() - from < ns) __nanosleep(100);
 }
 
 // One thread of each of a cut unit's blocks, after its own piece was counted as
@@ -1005,7 +1011,6 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         const int i = quarter * 32 + lane;  // flat row of the M block, TMEM lane
         const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
         float* sm_ref = reinterpret_cast<float*>(smem + S::ref);  // [2][128]: of even and odd jobs
-        float* sm_sum = reinterpret_cast<float*>(smem + S::sum);  // [2 groups][last reference, sum][128]
         bool ok = true;
         int job = 0, seg = 0;          // jobs and segments done by this block
         int grain = 0;                 // granules
@@ -1232,6 +1237,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             if (!ok) break;
             // ---- end of the segment: its last PV product (which every job's P came
             // before), the two groups' sums ----
+            // (in two buffers: one is written again only after the segment between has ended for
+            // all warps, when all have read it.  A warp without a job in the next segment is at its end
+            // at once, while warp 0 may still count a piece of this one.)
+            float* sm_sum = reinterpret_cast<float*>(smem + S::sum) + (seg & 1) * 4 * kRows;  // [2 groups][last reference, sum][128]
             sm_sum[wg * 2 * kRows + i] = ref;
             sm_sum[(wg * 2 + 1) * kRows + i] = l;
             __syncwarp();
@@ -1242,6 +1251,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             if (!(ok = waitw(bar_l, (uint32_t)seg & 1, abort))) break;
             if (!(ok = waitw(bar_fin, (uint32_t)seg & 1, abort))) break;
             tc_fence_after();
+            if (p.linger_ns && warp == 0) linger(p.linger_ns);
             const bool ends = w.g1() == w.n;
             // the second of two pieces: wait for the first's partial, which its block stores
             // before anything else
@@ -1441,7 +1451,7 @@ int device_blocks(int* blocks) {
 }
 
 // For tests (pkv_debug_set_tree_hooks); 0 in normal use.
-std::atomic<uint32_t> g_hook_help_ns{0}, g_hook_stop{0};
+std::atomic<uint32_t> g_hook_help_ns{0}, g_hook_stop{0}, g_hook_linger_ns{0};
 
 template <bool kFp8>
 int launch(const Params& prm, const CUtensorMap& km, const CUtensorMap& vm, int blocks, cudaStream_t stream) {
@@ -1523,6 +1533,7 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     const uint32_t help_ns = g_hook_help_ns.load(std::memory_order_relaxed);
     prm.help_ns = help_ns ? help_ns : kHelpNs;
     prm.stop = g_hook_stop.load(std::memory_order_relaxed);
+    prm.linger_ns = g_hook_linger_ns.load(std::memory_order_relaxed);
     prm.box = 4;  // the largest power of two that divides a page, at most a granule
     while ((1 << prm.box) < kGrain && block_size % (2 << prm.box) == 0) ++prm.box;
     prm.by_bs.set(block_size);
@@ -1541,8 +1552,10 @@ extern "C" int paged_attention_tree(void* out, const void* q, const void* k_pool
     return fp8 ? launch<true>(prm, km, vm, blocks, stream) : launch<false>(prm, km, vm, blocks, stream);
 }
 
-extern "C" int pkv_debug_set_tree_hooks(unsigned help_ns, int stop_folds) {
+extern "C" int pkv_debug_set_tree_hooks(unsigned help_ns, int stop_folds, unsigned linger_ns) {
+    if (linger_ns > 1000000) return PKV_ERR_INVALID_ARG;
     pkv::tree::g_hook_help_ns.store(help_ns, std::memory_order_relaxed);
     pkv::tree::g_hook_stop.store(stop_folds != 0, std::memory_order_relaxed);
+    pkv::tree::g_hook_linger_ns.store(linger_ns, std::memory_order_relaxed);
     return PKV_OK;
 }

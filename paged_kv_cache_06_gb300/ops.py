@@ -131,7 +131,7 @@ def _declare(L: ctypes.CDLL) -> None:
     L.paged_kv_tree_commit.restype = I
     L.pkv_debug_set_decode_hooks.argtypes = [ctypes.c_uint, P]
     L.pkv_debug_set_decode_hooks.restype = I
-    L.pkv_debug_set_tree_hooks.argtypes = [ctypes.c_uint, I]
+    L.pkv_debug_set_tree_hooks.argtypes = [ctypes.c_uint, I, ctypes.c_uint]
     L.pkv_debug_set_tree_hooks.restype = I
 
 
@@ -623,12 +623,13 @@ def check_error(dev_err: torch.Tensor, stream=None) -> int:
     return int(host.value)
 
 
-def debug_set_tree_hooks(help_ns: int = 0, stop_folds: bool = False) -> None:
+def debug_set_tree_hooks(help_ns: int = 0, stop_folds: bool = False, linger_ns: int = 0) -> None:
     """pkv_debug_set_tree_hooks: how long a block of tree_attention waits for a
     split unit's other pieces before it leaves its share of the merge to
-    another block (0 restores the default), and whether a block that has fetched
-    the other half of a unit cut in two gives up (PKV_DEV_ERR_TIMEOUT).  Test hook."""
-    _check("pkv_debug_set_tree_hooks", lib().pkv_debug_set_tree_hooks(int(help_ns), int(stop_folds)))
+    another block (0 restores the default), whether a block that has fetched the
+    other half of a unit cut in two gives up (PKV_DEV_ERR_TIMEOUT), and how long
+    one warp of each block stays behind at the end of every unit.  Test hook."""
+    _check("pkv_debug_set_tree_hooks", lib().pkv_debug_set_tree_hooks(int(help_ns), int(stop_folds), int(linger_ns)))
 
 
 def debug_set_decode_hooks(poll_limit: int = 0, stuck_word: Optional[torch.Tensor] = None) -> None:

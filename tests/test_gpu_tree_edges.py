@@ -438,3 +438,26 @@ def test_scores_so_large_that_their_differences_round(cuda_device, log2, rise):
         x = got[a:a + step.nodes[r]]
         slack = 2.0 ** -9 * v.abs().amax(0)     # weights, sums and the output are rounded to 2^-11 each
         assert bool((x <= v.amax(0) + slack).all()) and bool((x >= v.amin(0) - slack).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("prefix,nodes,heads", [
+    ([0, 354, 1856, 1777, 0, 3828], [86, 1, 72, 34, 43, 3], (32, 8)),   # a piece of three, then units of one tile
+    ([40] * 300, [3] * 300, (12, 2)),                                  # four units of one tile a block
+    ([30, 3000] * 60, [5, 2] * 60, (4, 4)),
+])
+def test_a_warp_that_stays_behind_at_a_units_end(cuda_device, prefix, nodes, heads, fp8):
+    """The other softmax group may have no tile in the next unit and be at its end at once:
+    what one warp still has to read of this unit's sums must be there."""
+    step = Step(prefix, nodes, 64, hk=heads[1], fp8=fp8, seed=53)
+    q = torch.randn(step.total, heads[0], 128, generator=step.gen).half()
+    ws = ops.alloc_tree_workspace(step.rows, step.total, *heads, 128, 64)
+    err = err_word()
+    ref, tol = tree_ref(step, q, seen_of(step, None), 0.0883)
+    try:
+        for linger_ns in (20000, 3000, 0):
+            ops.debug_set_tree_hooks(0, False, linger_ns)
+            check(tree_run(step, q, None, 0.0883, err, workspace=ws), ref, tol, f"linger {linger_ns}")
+    finally:
+        ops.debug_set_tree_hooks()
+    assert ops.check_error(err) == 0
