@@ -55,13 +55,13 @@
 // clocks that nothing hides, so tiles of 64 tokens ran at half the rate.
 //
 // What bounds it (12 query heads over 2 unless said; times in a graph of calls over four
-// sets of inputs).  64 rows of 4096, 64 nodes: 102.8 us, 995 TFLOP/s, 52% of cuBLAS's
-// rate (109 us a call on fresh inputs); a job every 0.95 us.  Tensor memory
+// sets of inputs).  64 rows of 4096, 64 nodes: 102.5 us, 998 TFLOP/s, 52% of cuBLAS's
+// rate (108 us a call on fresh inputs); a job every 0.95 us.  Tensor memory
 // holds three S buffers, and each is busy for 2.5 us: P is written 1.0 us after S is
 // there, its product issued 0.7 later and done in 0.3, the next S issued and done in
 // 0.45.  (A third fewer bytes from L2 changed nothing.)  4 rows of 32768, 5 to 16
-// nodes: 35.0 us; the copies run at DRAM's rate for 22 of them, 6 are the start and 5
-// the merge of 19 pieces.  32 rows of 1024, 25 nodes, E4M3: 21.1 us, nine tiles a block
+// nodes: 35.1 us; the copies run at DRAM's rate for 22 of them, 6 are the start and 5
+// the merge of 19 pieces.  32 rows of 1024, 25 nodes, E4M3: 21.3 us, nine tiles a block
 // at 1.1 us, paced by the widening (0.55 us a granule for a pool's two warps) with
 // 224 KB a tile through shared memory (0.9 us).  4 rows of 0 to 200: 8.4 us, one
 // dependent chain.
@@ -788,6 +788,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     const uint32_t all = __reduce_or_sync(0xffffffffu, mine);
                     const bool two = !kFp8 && te - ta - u * kTile > kGrain;
                     if (lane < 1 + two) sm_bad[(grain + lane) & 31] = all >> (4 * lane);
+                    __syncwarp();  // lane 1's word too is written before lane 0 arrives
                     grain += 1 + two;
                 }
                 if (lane == 0) mbar_arrive_expect_tx(fb, nissue * (kFp8 ? 1 : 2) * box_bytes);
