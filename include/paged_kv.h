@@ -481,11 +481,11 @@ int pkv_rope_frequencies(double* freqs, int rot_dim, double base, int scaling, d
                          double original_len, double low, double high);
 int pkv_rope_rates(uint64_t* rates, const double* freqs, int n);
 
-/* The next three calls use programmatic stream serialization without a flag:
+/* The next four calls use programmatic stream serialization without a flag:
  * their blocks may be set up while the kernel before them runs, but touch no
  * memory until it and all earlier work in `stream` are complete, so the order
  * of calls is the stream's.  (A PKV_FLAG_PDL call may directly follow
- * paged_attention_tree; the other two write pools, which that flag excludes.)
+ * paged_attention_tree; the other three write pools, which that flag excludes.)
  */
 
 /*
@@ -534,6 +534,32 @@ int paged_kv_rope_append(void* q_out, void* k_pool, void* v_pool, const float* k
                          int head_dim, int rot_dim, int layout, float mscale, int block_size,
                          int max_blocks_per_row, int num_blocks, int max_seq_len,
                          int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * paged_kv_norm_rope_append -- paged_kv_rope_append of queries and keys that are
+ * normalised first, head by head, in the same launch: with x one query or key
+ * head, all head_dim dims of it,
+ *     y[d] = x[d] / sqrt(mean_d x[d]^2 + eps) * weight[d],
+ * then y is rotated, stored and quantised as paged_kv_rope_append does with x,
+ * in binary32 from x on and rounded once at the end.  Values are not
+ * normalised.
+ *
+ * q_weight, k_weight: device fp16 [head_dim], 16-byte aligned, not overlapping
+ * q_out (q_weight is unused when q_heads == 0).  eps >= 0 and finite; a head of zeros with eps
+ * == 0 gives NaN.  The other arguments, their checks and the device's flags
+ * are paged_kv_rope_append's (q_out == q included).  head_dim a multiple of 16
+ * and at most 512 (PKV_ERR_UNSUPPORTED otherwise).
+ */
+int paged_kv_norm_rope_append(void* q_out, void* k_pool, void* v_pool, const float* k_scale,
+                              const float* v_scale, const int32_t* block_tables,
+                              const int32_t* seq_lens, const int32_t* q_start,
+                              const int32_t* rope_positions, const uint64_t* rates, const void* q,
+                              const void* k_new, const void* v_new, const void* q_weight,
+                              const void* k_weight, float eps, int64_t q_stride, int64_t k_stride,
+                              int64_t v_stride, int rows, int total_q, int q_heads, int kv_heads,
+                              int head_dim, int rot_dim, int layout, float mscale, int block_size,
+                              int max_blocks_per_row, int num_blocks, int max_seq_len,
+                              int32_t* dev_err, cudaStream_t stream);
 
 /*
  * paged_attention_tree -- attention of each row's nodes over its cached
@@ -608,6 +634,62 @@ int paged_kv_tree_commit(void* k_pool, void* v_pool, const int32_t* block_tables
                          int max_path, int kv_heads, int head_dim, int elt_bytes, int block_size,
                          int max_blocks_per_row, int num_blocks, int max_seq_len,
                          int32_t* dev_err, cudaStream_t stream);
+
+/*
+ * A cache within a budget.  Attention leaves most of its weight on few tokens;
+ * a row may keep those and drop the rest.  (The pages have no counterpart; the
+ * definitions below are this library's.)  Each token of each KV head's list has a
+ * running sum of the softmax weights that queries gave it, over all queries so
+ * far and the heads of the group:
+ *     weights  float [rows][kv_heads][weights_stride], weights_stride >=
+ *              max_seq_len: entry t belongs to the token in the row's slot t.
+ *
+ * paged_kv_evict -- in every list (layer, row, KV head) the tokens of lowest
+ * weight leave the cache, every layer at once.
+ *
+ * Of a row's L = seq_lens[r] tokens, n = min(L, budget) stay in each of its
+ * lists, each list choosing its own.  A token's position (its place in the
+ * sequence, not its slot) is
+ *     token_pos[list][t]          for slots t < tracked[r],
+ *     next_pos[r] - L + t         for the slots behind them,
+ * next_pos[r] being the position that the row's next token will have; tracked
+ * == null means 0 and next_pos == null means L, so both are null until a row
+ * has lost tokens, and tracked is the new_seq_lens of the row's last eviction
+ * after.  Tokens of position below `sinks` or at least next_pos[r] - recent stay
+ * before all others (sinks + recent <= budget); then the larger weight stays,
+ * the lower slot first where weights are equal (a NaN counts as larger than any
+ * number; the two zeros are equal).
+ *
+ * The tokens that stay and lie in slots below n keep their slots.  The others
+ * that stay move, in order, to the slots below n that became free, in order:
+ * key, value, weight and position, bit for bit.  Afterwards weights_out[list][t]
+ * and token_pos_out[list][t], t < n, hold the weight and position of the token
+ * in slot t, and new_seq_lens[r] (may be null) is n; entries from n on are not
+ * written.  The outputs may be the inputs themselves (both, or neither); any
+ * other overlap is PKV_ERR_INVALID_ARG.  The row's later tokens take slots n, n +
+ * 1, ..., at rotary positions that go on from next_pos (rope_positions of
+ * paged_kv_rope_append); attention is the same in any order of the slots.
+ *
+ * weights, token_pos (and the outputs): [layers][rows][kv_heads]
+ * [weights_stride].  Pools as in paged_kv_tree_commit: [layers][num_blocks]
+ * [block_size][kv_heads][head_dim] of elt_bytes each, one block table for all
+ * layers.  Blocks in which tokens move must not be shared between rows
+ * (copy-on-write first); pkv_bm_truncate is the block manager's side.
+ * A row with a length outside [0, max_seq_len] is skipped (its new length too)
+ * and flagged PKV_DEV_ERR_SEQ_LEN; a table entry out of range sets
+ * PKV_DEV_ERR_BLOCK_ID, and the keys and values that would move from or to it
+ * do not (weights and positions do).  budget >= 1; head_dim * elt_bytes a multiple
+ * of 16; max_seq_len at most 196,608, num_blocks * block_size below 2^31
+ * (PKV_ERR_UNSUPPORTED otherwise).  Starts early, as the drafted step's calls do.
+ */
+int paged_kv_evict(void* k_pool, void* v_pool, const int32_t* block_tables,
+                   const int32_t* seq_lens, const float* weights, const int32_t* token_pos,
+                   const int32_t* tracked, const int32_t* next_pos, float* weights_out,
+                   int32_t* token_pos_out, int32_t* new_seq_lens, int layers, int rows,
+                   int kv_heads, int head_dim, int elt_bytes, int block_size,
+                   int max_blocks_per_row, int num_blocks, int max_seq_len,
+                   int64_t weights_stride, int budget, int sinks, int recent,
+                   int32_t* dev_err, cudaStream_t stream);
 
 /* Bytes of the static device scratch behind paged_attention_decode_noalloc
  * (8 MiB, held by every GPU that loads the library until the process exits). */

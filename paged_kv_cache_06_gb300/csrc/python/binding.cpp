@@ -1,6 +1,7 @@
 // Python binding of the drafted step's calls (paged_kv_rope_append,
-// paged_attention_tree, paged_kv_tree_commit): argument checks and marshalling
-// only, as in ops.py, in C++.
+// paged_attention_tree, paged_kv_tree_commit) and of those of a cache within a
+// budget (paged_kv_norm_rope_append, paged_kv_evict): argument checks and
+// marshalling only, as in ops.py, in C++.
 //
 // Each of these calls takes a dozen tensors, and checking and unpacking them
 // from Python through ctypes took 22 to 30 us a call on the Grace cores, ten
@@ -191,44 +192,71 @@ PyObject* guarded(const char* name, Py_ssize_t got, Py_ssize_t want, F&& body) {
     }
 }
 
+// The arguments that the rotary appends share, a[0 .. 17], checked and unpacked; norms
+// (a[18 .. 20]: q_weight, k_weight, eps) where `norm`.
+int append_rotated(PyObject* const* a, bool norm) {
+    Call c;
+    const Pools p = need_pools(c, a[0], a[1], a[14], a[15]);
+    const Rows r = need_rows(c, a[2], a[3], a[4]);
+    int64_t sk = 0, sv = 0, sq = 0, hq = 0;
+    const at::Tensor& k = c.tokens(a[5], "k_new", p.hk, p.d, &sk);
+    const at::Tensor& v = c.tokens(a[6], "v_new", p.hk, p.d, &sv);
+    const int64_t total = k.size(0);
+    need_shape(v, "v_new", {total, p.hk, p.d});
+    const at::Tensor& rates = c.need(a[7], "rates", at::kLong, 1);
+    if ((a[10] == Py_None) != (a[11] == Py_None)) fail(PyExc_ValueError, "q and q_out go together");
+    void *q = nullptr, *q_out = nullptr;
+    if (a[10] != Py_None) {
+        const at::Tensor& o = c.need(a[11], "q_out", at::kHalf, 3);
+        hq = o.size(1);
+        need_shape(o, "q_out", {total, hq, p.d});
+        const at::Tensor& x = c.tokens(a[10], "q", hq, p.d, &sq);
+        need_shape(x, "q", {total, hq, p.d});
+        q = x.data_ptr();
+        q_out = o.data_ptr();
+    }
+    const int32_t* pos = nullptr;
+    if (a[12] != Py_None) {
+        const at::Tensor& x = c.need(a[12], "rope_positions", at::kInt, 1);
+        need_shape(x, "rope_positions", {total});
+        pos = static_cast<const int32_t*>(x.data_ptr());
+    }
+    const void *qw = nullptr, *kw = nullptr;
+    if (norm) {
+        if (hq && a[18] == Py_None) fail(PyExc_ValueError, "q_weight goes with q");
+        if (a[18] != Py_None) {
+            const at::Tensor& x = c.need(a[18], "q_weight", at::kHalf, 1);
+            need_shape(x, "q_weight", {p.d});
+            qw = x.data_ptr();
+        }
+        const at::Tensor& x = c.need(a[19], "k_weight", at::kHalf, 1);
+        need_shape(x, "k_weight", {p.d});
+        kw = x.data_ptr();
+    }
+    auto* err = static_cast<int32_t*>(c.optional(a[16], "dev_err", at::kInt, 1));
+    const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, c.device));
+    const auto* turns = static_cast<const uint64_t*>(rates.data_ptr());
+    const int rows = narrow(r.rows, "rows"), tokens = narrow(total, "tokens"), heads = narrow(hq, "q heads"),
+              hk = narrow(p.hk, "kv heads"), d = narrow(p.d, "head_dim"), rot = narrow(2 * rates.size(0), "rot_dim"),
+              layout = to_int(a[9]), bs = narrow(p.bs, "block_size"), mbpr = narrow(r.mbpr, "block_tables"),
+              nb = narrow(p.nb, "blocks"), most = to_int(a[8]);
+    const float mscale = to_float(a[13]);
+    const cudaStream_t stream = to_stream(a[17], c.device);
+    if (norm)
+        return paged_kv_norm_rope_append(q_out, p.k, p.v, p.ks, p.vs, r.tables, r.seq_lens, r.q_start, pos, turns, q,
+                                         k.data_ptr(), v.data_ptr(), qw, kw, to_float(a[20]), sq, sk, sv, rows,
+                                         tokens, heads, hk, d, rot, layout, mscale, bs, mbpr, nb, most, err, stream);
+    return paged_kv_rope_append(q_out, p.k, p.v, p.ks, p.vs, r.tables, r.seq_lens, r.q_start, pos, turns, q,
+                                k.data_ptr(), v.data_ptr(), sq, sk, sv, rows, tokens, heads, hk, d, rot, layout,
+                                mscale, bs, mbpr, nb, most, err, stream);
+}
+
 PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded("rope_append", n, 18, [&]() -> int {
-        Call c;
-        const Pools p = need_pools(c, a[0], a[1], a[14], a[15]);
-        const Rows r = need_rows(c, a[2], a[3], a[4]);
-        int64_t sk = 0, sv = 0, sq = 0, hq = 0;
-        const at::Tensor& k = c.tokens(a[5], "k_new", p.hk, p.d, &sk);
-        const at::Tensor& v = c.tokens(a[6], "v_new", p.hk, p.d, &sv);
-        const int64_t total = k.size(0);
-        need_shape(v, "v_new", {total, p.hk, p.d});
-        const at::Tensor& rates = c.need(a[7], "rates", at::kLong, 1);
-        if ((a[10] == Py_None) != (a[11] == Py_None)) fail(PyExc_ValueError, "q and q_out go together");
-        void *q = nullptr, *q_out = nullptr;
-        if (a[10] != Py_None) {
-            const at::Tensor& o = c.need(a[11], "q_out", at::kHalf, 3);
-            hq = o.size(1);
-            need_shape(o, "q_out", {total, hq, p.d});
-            const at::Tensor& x = c.tokens(a[10], "q", hq, p.d, &sq);
-            need_shape(x, "q", {total, hq, p.d});
-            q = x.data_ptr();
-            q_out = o.data_ptr();
-        }
-        const int32_t* pos = nullptr;
-        if (a[12] != Py_None) {
-            const at::Tensor& x = c.need(a[12], "rope_positions", at::kInt, 1);
-            need_shape(x, "rope_positions", {total});
-            pos = static_cast<const int32_t*>(x.data_ptr());
-        }
-        auto* err = static_cast<int32_t*>(c.optional(a[16], "dev_err", at::kInt, 1));
-        const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, c.device));
-        return paged_kv_rope_append(
-            q_out, p.k, p.v, p.ks, p.vs, r.tables, r.seq_lens, r.q_start, pos,
-            static_cast<const uint64_t*>(rates.data_ptr()), q, k.data_ptr(), v.data_ptr(), sq, sk, sv,
-            narrow(r.rows, "rows"), narrow(total, "tokens"), narrow(hq, "q heads"), narrow(p.hk, "kv heads"),
-            narrow(p.d, "head_dim"), narrow(2 * rates.size(0), "rot_dim"), to_int(a[9]), to_float(a[13]),
-            narrow(p.bs, "block_size"), narrow(r.mbpr, "block_tables"), narrow(p.nb, "blocks"), to_int(a[8]), err,
-            to_stream(a[17], c.device));
-    });
+    return guarded("rope_append", n, 18, [&]() -> int { return append_rotated(a, false); });
+}
+
+PyObject* norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded("norm_rope_append", n, 21, [&]() -> int { return append_rotated(a, true); });
 }
 
 PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -296,6 +324,66 @@ PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded("evict", n, 17, [&]() -> int {
+        Call c;
+        const at::Tensor& k0 = c.tensor(a[0], "k_pool");
+        const at::ScalarType dt = k0.scalar_type();
+        if (dt != at::kHalf && dt != at::kByte)
+            fail(PyExc_TypeError, std::string("k_pool must be torch.float16 or torch.uint8, got ") + dtype_name(dt));
+        const int64_t nd = k0.dim() == 5 ? 5 : 4;
+        const at::Tensor& k = c.need(a[0], "k_pool", dt, nd);
+        const at::Tensor& v = c.need(a[1], "v_pool", dt, nd);
+        if (v.sizes() != k.sizes())
+            fail(PyExc_ValueError, "v_pool must have shape " + shape_of(k.sizes()) + ", got " + shape_of(v.sizes()));
+        const at::Tensor& tables = c.need(a[2], "block_tables", at::kInt, 2);
+        const at::Tensor& lens = c.need(a[3], "seq_lens", at::kInt, 1);
+        const int64_t rows = lens.size(0), layers = nd == 5 ? k.size(0) : 1, hk = k.size(nd - 2);
+        if (tables.size(0) != rows) fail(PyExc_ValueError, "block_tables must have a row per seq_len");
+        // one layer's lists, or every layer's
+        const at::Tensor& w = c.need(a[4], "weights", at::kFloat, nd - 1);
+        const at::Tensor& pos = c.need(a[5], "token_pos", at::kInt, nd - 1);
+        const int64_t stride = w.size(nd - 2);
+        if ((nd == 5 && w.size(0) != layers) || w.size(nd - 4) != rows || w.size(nd - 3) != hk)
+            fail(PyExc_ValueError, std::string("weights must be ") + (nd == 5 ? "[layers]" : "") +
+                                       "[rows][kv_heads][stride], got " + shape_of(w.sizes()));
+        auto same = [&](const at::Tensor& t, const char* name) {
+            if (t.sizes() != w.sizes())
+                fail(PyExc_ValueError, std::string(name) + " must have shape " + shape_of(w.sizes()) + ", got " + shape_of(t.sizes()));
+        };
+        same(pos, "token_pos");
+        auto per_row = [&](PyObject* o, const char* name) -> int32_t* {
+            if (o == Py_None) return nullptr;
+            const at::Tensor& x = c.need(o, name, at::kInt, 1);
+            need_shape(x, name, {rows});
+            return static_cast<int32_t*>(x.data_ptr());
+        };
+        const int32_t* tracked = per_row(a[10], "tracked");
+        const int32_t* next = per_row(a[11], "next_pos");
+        if ((a[12] == Py_None) != (a[13] == Py_None)) fail(PyExc_ValueError, "weights_out and token_pos_out go together");
+        float* w_out = static_cast<float*>(w.data_ptr());
+        int32_t* pos_out = static_cast<int32_t*>(pos.data_ptr());
+        if (a[12] != Py_None) {
+            const at::Tensor& wo = c.need(a[12], "weights_out", at::kFloat, nd - 1);
+            const at::Tensor& po = c.need(a[13], "token_pos_out", at::kInt, nd - 1);
+            same(wo, "weights_out");
+            same(po, "token_pos_out");
+            w_out = static_cast<float*>(wo.data_ptr());
+            pos_out = static_cast<int32_t*>(po.data_ptr());
+        }
+        int32_t* fresh = per_row(a[14], "new_seq_lens");
+        auto* err = static_cast<int32_t*>(c.optional(a[15], "dev_err", at::kInt, 1));
+        const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, c.device));
+        return paged_kv_evict(
+            k.data_ptr(), v.data_ptr(), static_cast<const int32_t*>(tables.data_ptr()),
+            static_cast<const int32_t*>(lens.data_ptr()), static_cast<const float*>(w.data_ptr()),
+            static_cast<const int32_t*>(pos.data_ptr()), tracked, next, w_out, pos_out, fresh, narrow(layers, "layers"),
+            narrow(rows, "rows"), narrow(hk, "kv heads"), narrow(k.size(nd - 1), "head_dim"), dt == at::kHalf ? 2 : 1,
+            narrow(k.size(nd - 3), "block_size"), narrow(tables.size(1), "block_tables"), narrow(k.size(nd - 4), "blocks"),
+            to_int(a[7]), stride, to_int(a[6]), to_int(a[8]), to_int(a[9]), err, to_stream(a[16], c.device));
+    });
+}
+
 template <class F>
 PyCFunction as_function(F f) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f));
@@ -303,8 +391,10 @@ PyCFunction as_function(F f) {
 
 PyMethodDef methods[] = {
     {"rope_append", as_function(rope_append), METH_FASTCALL, nullptr},
+    {"norm_rope_append", as_function(norm_rope_append), METH_FASTCALL, nullptr},
     {"tree_attention", as_function(tree_attention), METH_FASTCALL, nullptr},
     {"tree_commit", as_function(tree_commit), METH_FASTCALL, nullptr},
+    {"evict", as_function(evict), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -123,6 +123,10 @@ def _declare(L: ctypes.CDLL) -> None:
     L.pkv_rope_rates.restype = I
     L.paged_kv_rope_append.argtypes = [P] * 13 + [L64, L64, L64] + [I] * 7 + [F, I, I, I, I, P, P]
     L.paged_kv_rope_append.restype = I
+    L.paged_kv_norm_rope_append.argtypes = [P] * 15 + [F, L64, L64, L64] + [I] * 7 + [F, I, I, I, I, P, P]
+    L.paged_kv_norm_rope_append.restype = I
+    L.paged_kv_evict.argtypes = [P] * 11 + [I] * 9 + [L64, I, I, I, P, P]
+    L.paged_kv_evict.restype = I
     L.paged_attention_tree.argtypes = [P] * 10 + [I] * 7 + [F, I, I, I, P, S, P, P]
     L.paged_attention_tree.restype = I
     L.paged_attention_tree_workspace_size.argtypes = [I, I, I, I, I, I]
@@ -548,6 +552,23 @@ def rope_append(k_pool, v_pool, block_tables, seq_lens, q_start, k_new, v_new, r
         _check("paged_kv_rope_append", st)
 
 
+def norm_rope_append(k_pool, v_pool, block_tables, seq_lens, q_start, k_new, v_new, rates, k_weight,
+                     max_seq_len: int, eps: float = 1e-6, layout: str = "half", q=None, q_out=None,
+                     q_weight=None, rope_positions=None, mscale: float = 1.0, k_scale=None,
+                     v_scale=None, dev_err=None, stream=None):
+    """paged_kv_norm_rope_append: rope_append of queries and keys that are first
+    normalised head by head (root mean square over head_dim, ``eps`` added to the
+    mean, times ``q_weight`` / ``k_weight``, fp16 [head_dim])."""
+    code = ROPE_LAYOUTS.get(layout)
+    if code is None:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    st = (_ext or binding()).norm_rope_append(
+        k_pool, v_pool, block_tables, seq_lens, q_start, k_new, v_new, rates, max_seq_len, code, q,
+        q_out, rope_positions, mscale, k_scale, v_scale, dev_err, stream, q_weight, k_weight, eps)
+    if st:
+        _check("paged_kv_norm_rope_append", st)
+
+
 def tree_mask(parents, q_start, words: Optional[int] = None) -> torch.Tensor:
     """The mask of drafted trees, on the CPU: node i sees itself and its
     ancestors.  parents: per node of the packed step, its parent's index within
@@ -612,6 +633,28 @@ def tree_commit(k_pool, v_pool, block_tables, seq_lens, q_start, path, path_lens
         new_seq_lens, dev_err, stream)
     if st:
         _check("paged_kv_tree_commit", st)
+
+
+# ---------------------------------------------------------------------------
+# A cache within a budget: running sums of the attention weights that each cached
+# token gets, and the tokens of lowest weight dropped.  Same binding, device and
+# stream as the drafted step's calls.
+
+def evict(k_pool, v_pool, block_tables, seq_lens, weights, token_pos, budget: int,
+          max_seq_len: int, sinks: int = 0, recent: int = 0, tracked=None, next_pos=None,
+          weights_out=None, token_pos_out=None, new_seq_lens=None, dev_err=None, stream=None):
+    """paged_kv_evict: in each KV head's list of each row ``budget`` tokens stay (the
+    first ``sinks`` and last ``recent`` positions, then those of the largest
+    weight) and move together.  Pools: one layer's, or all layers' with a leading
+    [layers]; fp16, or uint8 (E4M3).  weights, token_pos: float32 / int32
+    [rows][kv_heads][stride], with a leading [layers] as the pools have it;
+    updated in place unless ``weights_out`` and ``token_pos_out`` are given.
+    tracked, next_pos, new_seq_lens: int32 [rows] (include/paged_kv.h)."""
+    st = (_ext or binding()).evict(
+        k_pool, v_pool, block_tables, seq_lens, weights, token_pos, budget, max_seq_len, sinks,
+        recent, tracked, next_pos, weights_out, token_pos_out, new_seq_lens, dev_err, stream)
+    if st:
+        _check("paged_kv_evict", st)
 
 
 def check_error(dev_err: torch.Tensor, stream=None) -> int:

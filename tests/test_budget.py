@@ -1,0 +1,98 @@
+"""The calls that keep a cache within a budget, without a GPU: the refusals that
+are made before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+from paged_kv_cache_06_gb300 import ops
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+FAKE = 0x100000       # aligned, non-null; never dereferenced by these calls
+FAR = 0x10000000
+ODD = 0x100008        # not 16-byte aligned
+
+
+def P(x):
+    return ctypes.c_void_p(x) if x else None
+
+
+def norm(**kw):
+    a = dict(q_out=FAR, k=FAKE, v=FAKE, ks=0, vs=0, bt=FAKE, sl=FAKE, qs=FAKE, rp=0, rates=FAKE, q=FAKE, kn=FAKE,
+             vn=FAKE, qw=FAKE, kw=FAKE, eps=1e-6, sq=1536, sk=256, sv=256, rows=4, total=9, hq=12, hk=2, d=128,
+             rot=128, layout=0, m=1.0, bs=16, mbpr=16, nb=64, msl=200)
+    a.update(kw)
+    return ops.lib().paged_kv_norm_rope_append(
+        *[P(a[n]) for n in ("q_out", "k", "v", "ks", "vs", "bt", "sl", "qs", "rp", "rates", "q", "kn", "vn", "qw", "kw")],
+        a["eps"], a["sq"], a["sk"], a["sv"], a["rows"], a["total"], a["hq"], a["hk"], a["d"], a["rot"], a["layout"],
+        a["m"], a["bs"], a["mbpr"], a["nb"], a["msl"], None, None)
+
+
+def test_norm_rope_append_refusals():
+    for n in ("k", "v", "bt", "sl", "qs", "rates", "q", "kn", "vn", "q_out", "qw", "kw"):
+        assert norm(**{n: 0}) == INVALID, n
+    for n in ("k", "v", "q", "kn", "vn", "q_out", "qw", "kw"):
+        assert norm(**{n: ODD}) == INVALID, n
+    for eps in (-1e-6, float("nan"), float("inf")):
+        assert norm(eps=eps) == INVALID
+    assert norm(ks=FAKE) == INVALID and norm(layout=2) == INVALID and norm(m=float("inf")) == INVALID
+    assert norm(d=120, rot=112) == UNSUPPORTED                        # a multiple of 8, as rope_append takes
+    assert norm(d=528, rot=128, sq=1 << 20, sk=1 << 20, sv=1 << 20) == UNSUPPORTED
+    assert norm(rot=24) == UNSUPPORTED and norm(rot=144) == INVALID
+    size = 9 * 12 * 128 * 2
+    for n in ("qw", "kw"):                                            # the output over a weight
+        assert norm(**{n: FAR}) == INVALID and norm(**{n: FAR + size - 16}) == INVALID
+    assert norm(q=FAR + 256) == INVALID and norm(q_out=FAKE, sq=1544) == INVALID
+    assert norm(rows=0, k=0) == 0 and norm(total=0, q=0) == 0
+
+
+def evict(**kw):
+    a = dict(k=FAKE, v=FAKE, bt=FAKE, sl=FAKE, w=FAR, pos=2 * FAR, tr=FAKE, nx=FAKE, wo=None, po=None, new=3 * FAR,
+             layers=2, rows=4, hk=2, d=128, eb=2, bs=16, mbpr=16, nb=64, msl=200, stride=200, budget=100, sinks=4,
+             recent=20)
+    a.update(kw)
+    a["wo"], a["po"] = a["w"] if a["wo"] is None else a["wo"], a["pos"] if a["po"] is None else a["po"]
+    return ops.lib().paged_kv_evict(
+        *[P(a[n]) for n in ("k", "v", "bt", "sl", "w", "pos", "tr", "nx", "wo", "po", "new")], a["layers"], a["rows"],
+        a["hk"], a["d"], a["eb"], a["bs"], a["mbpr"], a["nb"], a["msl"], a["stride"], a["budget"], a["sinks"],
+        a["recent"], None, None)
+
+
+def test_evict_refusals():
+    for n in ("k", "v", "bt", "sl", "w", "pos"):
+        assert evict(**{n: 0}) == INVALID, n
+    assert evict(k=ODD) == INVALID and evict(v=ODD) == INVALID
+    assert evict(budget=0) == INVALID and evict(sinks=-1) == INVALID and evict(recent=-1) == INVALID
+    assert evict(sinks=50, recent=51) == INVALID and evict(sinks=2 ** 31 - 1, recent=2 ** 31 - 1) == INVALID
+    assert evict(stride=199) == INVALID and evict(msl=257, stride=300) == INVALID
+    assert evict(eb=4) == INVALID and evict(d=12) == UNSUPPORTED and evict(d=8, eb=1) == UNSUPPORTED
+    assert evict(msl=196609, stride=196609, mbpr=20000) == UNSUPPORTED and evict(nb=1 << 27) == UNSUPPORTED
+    assert evict(rows=-1) == INVALID and evict(layers=-1) == INVALID and evict(hk=0) == INVALID
+    assert evict(rows=0, k=0) == 0 and evict(layers=0, k=0) == 0
+
+
+def test_evict_outputs_lie_over_nothing_else():
+    wide = 2 * 4 * 2 * 200 * 4
+    out, pos = 4 * FAR, 5 * FAR
+    assert evict(wo=out) == INVALID and evict(po=pos) == INVALID       # in place both, or neither
+    for x in (2 * FAR, FAR + 4, FAR - wide + 4, 3 * FAR, pos):         # token_pos, part of weights, new lengths, positions
+        assert evict(wo=x, po=pos) == INVALID, x
+    for x in (FAR, 2 * FAR + 4, 2 * FAR - wide + 4, 3 * FAR, out):
+        assert evict(wo=out, po=x) == INVALID, x
+    for n, size in (("sl", 16), ("bt", 256), ("tr", 16), ("nx", 16), ("w", wide), ("pos", wide)):
+        at = {"w": FAR, "pos": 2 * FAR}.get(n, FAKE)
+        assert evict(new=at) == INVALID and evict(new=at + size - 4) == INVALID, n
+    assert evict(wo=FAKE, po=pos) == INVALID and evict(wo=out, po=FAKE + 12) == INVALID
+
+
+def test_ops_refuse_cpu_tensors_and_wrong_shapes():
+    h, i = torch.zeros(4, 12, 128, dtype=torch.float16), torch.zeros(4, dtype=torch.int32)
+    pool = torch.zeros(4, 16, 2, 128, dtype=torch.float16)
+    bt, qs = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(5, dtype=torch.int32)
+    rates, w = torch.zeros(64, dtype=torch.int64), torch.zeros(128, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        ops.norm_rope_append(pool, pool, bt, i, qs, h[:, :2], h[:, :2], rates, w, 16)
+    with pytest.raises(ValueError):
+        ops.norm_rope_append(pool, pool, bt, i, qs, h, h, rates, w, 16, layout="whole")
+    with pytest.raises(ValueError):
+        ops.evict(pool, pool, bt, i, torch.zeros(4, 2, 32), torch.zeros(4, 2, 32, dtype=torch.int32), 8, 32)

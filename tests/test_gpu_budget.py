@@ -1,0 +1,377 @@
+"""GPU parity of the calls that keep a cache within a budget: head norms with
+the rotary append, and eviction, against plain 64-bit forms.
+
+Tolerances of the norms (u = 2^-24, h = 2^-11): a head's squares add up within 16
+u (at most 16 terms a lane and five additions across lanes), the mean's factor
+and sum within 2 u, its root halves that and takes 4 u itself, the two products 2 u:
+15 u of each normalised value, 16 u with the second order; the rotation 12 u m
+(|a| + |b|) on top (derived at the rotary append's tests), in all 28 u m (|a| +
+|b|), 30 u with the second order; then h |ref| (2^-25 below the normal range), or
+half an E4M3 step of the stored quotient (2^-4 of it, 2^-10 below the normal range).
+Eviction moves bits: equality.
+"""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_06_gb300 import ops
+from test_gpu_tree_step import ERR_BLOCK, ERR_LEN, Step, check, err_word, i32
+
+pytestmark = pytest.mark.gpu
+
+U, H = 2.0 ** -24, 2.0 ** -11
+
+
+# ---- norms of queries and keys with the rotary append ----
+
+def norm_ref(x, weight, eps):
+    x = x.double()
+    return x / (x.square().mean(-1, keepdim=True) + eps).sqrt() * weight.double()
+
+
+def turned(y, pos, freqs, layout, mscale):
+    """(rotated, tolerance before the output's rounding), both float64."""
+    rot = 2 * freqs.shape[0]
+    ang = torch.as_tensor(pos, dtype=torch.float64)[:, None] * freqs[None, :]
+    c, s = (mscale * f(ang)[:, None, :] for f in (torch.cos, torch.sin))
+    out, tol = y.clone(), 16 * U * y.abs()
+    i, j = (slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half" else (slice(0, rot, 2), slice(1, rot, 2))
+    a, b = y[..., i], y[..., j]
+    out[..., i], out[..., j] = a * c - b * s, a * s + b * c
+    tol[..., i] = tol[..., j] = 30 * U * abs(mscale) * (a.abs() + b.abs())
+    return out, tol
+
+
+def rounded(ref, tol):
+    return tol + H * ref.abs() + 2.0 ** -25
+
+
+NORMS = [
+    # prefix, nodes, block, q heads, kv heads, dim, rotated
+    ([5], [1], 16, 12, 2, 128, 128),
+    ([0, 63, 64, 700], [1, 1, 1, 1], 64, 12, 2, 128, 64),
+    ([3, 0, 90], [7, 0, 40], 48, 32, 8, 128, 32),
+    ([10, 2], [33, 5], 16, 4, 4, 64, 64),
+    ([10, 2], [9, 5], 16, 8, 1, 96, 96),            # a head of six lanes
+    ([10, 2], [9, 5], 16, 8, 2, 80, 16),            # of five
+    ([1, 2, 3], [300, 1, 77], 32, 28, 4, 256, 256),
+    ([0], [3], 16, 2, 1, 512, 128),
+    ([0], [3], 16, 2, 1, 16, 16),                   # a head of one lane
+    ([11] * 50, [60] * 50, 64, 12, 2, 128, 128),    # several tokens a block
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("case", range(len(NORMS)))
+def test_norm_rope_append_matches_the_formula(cuda_device, case, layout, fp8):
+    prefix, nodes, bs, hq, hk, d, rot = NORMS[case]
+    step = Step(prefix, nodes, bs, hk=hk, d=d, fp8=fp8, seed=300 + case)
+    gen, eps, mscale = step.gen, (1e-6, 0.25)[case % 2], (1.0, 1.3)[case % 3 == 1]
+    qkv = torch.randn(step.total, hq + 2 * hk, d, generator=gen).half()
+    qkv[:, 0] *= 30                                  # a loud head, a faint one
+    qkv[:, hq] *= 0.01
+    qw, kw = ((1 + 0.3 * torch.randn(d, generator=gen)).half() for _ in range(2))
+    pos = np.concatenate([[(0, 123456)[case % 2] + p + i for i in range(n)] for p, n in zip(prefix, nodes)])
+    freqs = ops.rope_frequencies(rot)
+    a, err, x = step.gpu(), err_word(), qkv.cuda()
+    q_out = torch.full((step.total, hq, d), float("nan"), dtype=torch.float16, device="cuda")
+    ops.norm_rope_append(a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], a["q_start"],
+                         x[:, hq:hq + hk], x[:, hq + hk:], ops.rope_rates(freqs), kw.cuda(), step.max_len, eps=eps,
+                         layout=layout, q=x[:, :hq], q_out=q_out, q_weight=qw.cuda(), rope_positions=i32(pos),
+                         mscale=mscale, k_scale=a["k_scale"], v_scale=a["v_scale"], dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    ref, tol = turned(norm_ref(qkv[:, :hq], qw, eps), pos, freqs, layout, mscale)
+    check(q_out, ref, rounded(ref, tol), "queries")
+    ref, tol = turned(norm_ref(qkv[:, hq:hq + hk], kw, eps), pos, freqs, layout, mscale)
+    slots = torch.cat([step.slots(r, prefix[r]) for r in range(step.rows)])
+    rest = torch.ones(step.nb * bs, dtype=torch.bool)
+    rest[slots] = False
+    for name, pool, scale in (("k_pool", step.k_pool, step.k_scale), ("v_pool", step.v_pool, step.v_scale)):
+        was, got = pool.view(-1, hk, d), a[name].cpu().view(-1, hk, d)
+        as_bits = torch.uint8 if fp8 else torch.int16
+        assert torch.equal(got.view(as_bits)[rest], was.view(as_bits)[rest]), name   # nothing else is written
+        if name == "v_pool":
+            want = qkv[:, hq + hk:]
+            if fp8:
+                want = (want.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+            assert torch.equal(got[slots].view(as_bits), want.view(as_bits))
+        elif fp8:
+            want, off = ref / scale.double()[:, None], tol / scale.double()[:, None]
+            want = want.clamp(-448, 448)
+            check(got[slots].view(torch.float8_e4m3fn).float(), want,
+                  off + torch.maximum((want.abs() + off) * 2.0 ** -4, torch.tensor(2.0 ** -10)), "keys")
+        else:
+            check(got[slots], ref, rounded(ref, tol), "keys")
+
+
+def norm_call(step, qkv, hq, weights, **kw):
+    hk, d = step.hk, step.d
+    a, x = step.gpu(), qkv.cuda()
+    args = dict(q=x[:, :hq], q_out=torch.zeros(qkv.shape[0], hq, d, dtype=torch.float16, device="cuda"),
+                q_weight=weights[0].cuda())
+    tables, lens = kw.pop("block_tables", a["block_tables"]), kw.pop("seq_lens", a["seq_lens"])
+    starts = kw.pop("q_start", a["q_start"])
+    args.update(kw)
+    ops.norm_rope_append(a["k_pool"], a["v_pool"], tables, lens, starts, x[:, hq:hq + hk], x[:, hq + hk:],
+                         ops.rope_rates(ops.rope_frequencies(d)), weights[1].cuda(), step.max_len, **args)
+    torch.cuda.synchronize()
+    return args["q_out"], a["k_pool"], a["v_pool"]
+
+
+def norm_step(prefix, nodes, bs=16, seed=0):
+    step = Step(prefix, nodes, bs, seed=seed, fill=False)
+    qkv = torch.randn(step.total + 3, 16, 128, generator=step.gen).half()
+    return step, qkv, [(1 + 0.1 * torch.randn(128, generator=step.gen)).half() for _ in range(2)]
+
+
+def test_norm_rope_append_without_queries_in_place_and_behind_the_last_row(cuda_device):
+    step, qkv, w = norm_step([30, 5, 0], [4, 1, 20], seed=1)
+    out, k, v = norm_call(step, qkv, 12, w)
+    assert bool((out[step.total:] == 0).all())                   # tokens behind the last row are left alone
+    none = norm_call(step, qkv, 12, w, q=None, q_out=None, q_weight=None)
+    assert torch.equal(none[1], k) and torch.equal(none[2], v)   # keys and values alone
+    q = qkv[:, :12].contiguous().cuda()
+    norm_call(step, qkv, 12, w, q=q, q_out=q)                    # over its own input
+    assert torch.equal(q[:step.total], out[:step.total])
+    assert torch.equal(q[step.total:].cpu(), qkv[step.total:, :12])
+
+
+def test_norm_rope_append_skips_and_flags_bad_rows(cuda_device):
+    step, qkv, w = norm_step([30, 5, 9], [4, 1, 20], seed=2)
+    out, k, v = norm_call(step, qkv, 12, w)
+    err, lens = err_word(), list(step.lens)
+    lens[1] = step.max_len + 1
+    got = norm_call(step, qkv, 12, w, seq_lens=i32(lens), dev_err=err)
+    assert ops.check_error(err) == ERR_LEN
+    assert bool((got[0][4] == 0).all()) and torch.equal(got[0][5:], out[5:]) and torch.equal(got[0][:4], out[:4])
+    t = step.tables.copy()
+    t[2, 0] = step.nb                                            # tokens 9 .. 15 of row 2
+    got = norm_call(step, qkv, 12, w, block_tables=i32(t), dev_err=err)
+    assert ops.check_error(err) == ERR_BLOCK
+    assert torch.equal(got[0], out)                              # its queries are rotated all the same
+    lost, kept = step.slots(2, 9, 16), step.slots(2, 16)
+    for new, was, pool in ((got[1], k, step.k_pool), (got[2], v, step.v_pool)):
+        new, was = new.cpu().view(-1, 2, 128), was.cpu().view(-1, 2, 128)
+        assert torch.equal(new[lost], pool.view(-1, 2, 128)[lost]) and torch.equal(new[kept], was[kept])
+
+
+def test_norms_of_heads_that_are_zero_huge_or_no_number(cuda_device):
+    step, qkv, w = norm_step([0], [6], seed=3)
+    qkv[0, 0] = 0
+    qkv[1, 1] = 65504
+    qkv[2, 2, 5] = float("inf")
+    qkv[3, 3, 7] = float("nan")
+    qkv[4, 4] = 2.0 ** -24
+    out, _, _ = norm_call(step, qkv, 12, w, eps=1e-6)
+    assert bool((out[0, 0] == 0).all()) and bool(torch.isfinite(out[1, 1]).all())
+    assert bool(torch.isnan(out[3, 3]).all()) and bool(torch.isnan(out[2, 2, [5, 69]]).all())
+    pos, freqs = np.arange(6), ops.rope_frequencies(128)
+    clean = torch.ones(6, 12, dtype=torch.bool)
+    clean[2, 2] = clean[3, 3] = False
+    ref, tol = turned(norm_ref(qkv[:6, :12], w[0], 1e-6), pos, freqs, "half", 1.0)
+    check(out[:6][clean.cuda()], ref[clean], rounded(ref, tol)[clean])
+
+
+# ---- eviction ----
+
+class Lists:
+    """Rows of `lens` tokens in `layers` layers, with weights, recorded positions for
+    the first `tracked` slots and the outcome that the definition gives."""
+
+    def __init__(self, lens, budget, bs=16, layers=2, hk=2, d=128, fp8=False, sinks=0, recent=0, tracked=None,
+                 seed=0, stride=None, weights=None, skipped=()):
+        self.step = step = Step(lens, [0] * len(lens), bs, hk=hk, d=d, fp8=False, layers=layers, seed=seed)
+        rng = np.random.default_rng(seed)
+        self.lens, self.budget, self.sinks, self.recent, self.fp8 = list(lens), budget, sinks, recent, fp8
+        self.layers, self.hk, self.d = layers, hk, d
+        self.top = max(1, max(lens))
+        stride = stride or self.top
+        shape = (layers, len(lens), hk, stride)
+        if fp8:
+            step.k_pool, step.v_pool = (torch.randint(0, 256, step.k_pool.shape, generator=step.gen, dtype=torch.uint8)
+                                        for _ in range(2))
+        self.weights = np.exp(2 * rng.standard_normal(shape)).astype(np.float32) if weights is None else weights(rng, shape)
+        self.tracked = [0] * len(lens) if tracked is None else tracked
+        self.pos = np.full(shape, -77, dtype=np.int32)
+        self.next = []
+        for r, n in enumerate(lens):
+            had = self.tracked[r] + (5 if self.tracked[r] else 0)
+            for i in np.ndindex(layers, hk):
+                self.pos[i[0], r, i[1], :self.tracked[r]] = rng.permutation(had)[:self.tracked[r]]
+            self.next.append(had + n - self.tracked[r])
+        self.want(skipped)
+
+    def want(self, skipped=()):
+        """Slots that each list's tokens move between, and the arrays afterwards."""
+        self.w_after, self.p_after = self.weights.copy(), self.pos.copy()
+        self.new = [min(n, self.budget) for n in self.lens]
+        self.moves = []
+        for i in np.ndindex(self.layers, len(self.lens), self.hk):
+            r = i[1]
+            n, keep = self.lens[r], self.new[r]
+            if r in skipped:
+                continue
+            t = np.arange(n)
+            pos = np.where(t < self.tracked[r], self.pos[i][:n], self.next[r] - n + t)
+            w = self.weights[i][:n]
+            safe = (pos < self.sinks) | (pos >= self.next[r] - self.recent)
+            rank = np.where(safe, 2, np.isnan(w).astype(int))
+            order = np.lexsort((t, -np.where(rank > 0, 0, w), -rank))
+            stays = np.zeros(n, dtype=bool)
+            stays[order[:keep]] = True
+            to, frm = t[(t < keep) & ~stays], t[(t >= keep) & stays]
+            assert len(to) == len(frm)
+            at = t[:keep].copy()
+            at[to] = frm
+            self.w_after[i][:keep], self.p_after[i][:keep] = w[at], pos[at]
+            self.moves.append((i, to, frm))
+
+    def pools_after(self):
+        s, out = self.step, []
+        for pool in (s.k_pool, s.v_pool):
+            p = pool.clone().view(self.layers, -1, self.hk, self.d)
+            for (layer, r, h), to, frm in self.moves:
+                if len(to):
+                    slots = s.slots(r)
+                    p[layer, slots[to], h] = pool.view(self.layers, -1, self.hk, self.d)[layer, slots[frm], h]
+            out.append(p.view(pool.shape))
+        return out
+
+    def run(self, in_place=True, stream=None, err=None, bare=False, max_len=None, **kw):
+        s = self.step
+        g = dict(k_pool=s.k_pool.cuda(), v_pool=s.v_pool.cuda(), block_tables=i32(s.tables), seq_lens=i32(self.lens),
+                 weights=torch.from_numpy(self.weights).cuda(), token_pos=torch.from_numpy(self.pos).cuda())
+        g.update(kw)
+        w, p = g["weights"], g["token_pos"]
+        if not in_place:
+            w, p = torch.full_like(w, -1), torch.full_like(p, -1)
+        new = torch.full((len(self.lens),), -5, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        ops.evict(**g, budget=self.budget, max_seq_len=max_len or self.top, sinks=self.sinks, recent=self.recent,
+                  tracked=None if bare else i32(self.tracked), next_pos=None if bare else i32(self.next),
+                  weights_out=None if in_place else w, token_pos_out=None if in_place else p, new_seq_lens=new,
+                  dev_err=err, stream=stream)
+        torch.cuda.synchronize()
+        return g["k_pool"], g["v_pool"], w, p, new
+
+    def check(self, got, in_place=True, skipped=()):
+        k, v, w, p, new = (x.cpu() for x in got)
+        for name, x, y in zip("kv", (k, v), self.pools_after()):
+            bits = torch.uint8 if self.fp8 else torch.int16
+            assert torch.equal(x.view(bits), y.view(bits)), name
+        for r, n in enumerate(self.new):
+            assert int(new[r]) == (-5 if r in skipped else n)
+            live = 0 if r in skipped else n
+            for x, y, before in ((w.numpy(), self.w_after, self.weights), (p.numpy(), self.p_after, self.pos)):
+                np.testing.assert_array_equal(x[:, r, :, :live].view(np.int32), y[:, r, :, :live].view(np.int32))
+                rest = x[:, r, :, live:]
+                assert (rest.view(np.int32) == before[:, r, :, live:].view(np.int32)).all() if in_place else (rest == -1).all()
+
+
+EVICTS = [
+    dict(lens=[1], budget=1),
+    dict(lens=[2, 1, 0, 3], budget=1),
+    dict(lens=[40, 17, 16, 15, 0, 33], budget=16),                       # above, at and below the budget
+    dict(lens=[300, 257, 20], budget=256, sinks=4, recent=32, tracked=[256, 256, 0]),
+    dict(lens=[1025] * 3, budget=1024, sinks=4, recent=64, tracked=[1024] * 3, layers=3),   # one token goes
+    dict(lens=[700, 3000, 90], budget=77, bs=48, hk=4, sinks=7, recent=70),   # the protected fill the budget
+    dict(lens=[700, 300], budget=100, d=64, hk=1, recent=100),
+    dict(lens=[700, 300], budget=100, d=96),
+    dict(lens=[90, 60], budget=50, d=256, layers=1),
+    dict(lens=[90, 60], budget=50, d=640, layers=1),
+    dict(lens=[4096, 4097, 511, 513], budget=512, bs=64),                # two blocks a list
+    dict(lens=[16385, 30, 9000], budget=4100, bs=128, layers=1, sinks=3, recent=1000, tracked=[4100, 30, 4100]),
+    dict(lens=[40000, 1], budget=33000, bs=64, layers=1, hk=1, d=16, sinks=4, recent=5),    # eight; most stay
+    dict(lens=[100], budget=99, stride=130),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", range(len(EVICTS)))
+def test_evict_matches_the_definition(cuda_device, case, fp8):
+    x = Lists(**EVICTS[case], fp8=fp8, seed=400 + case)
+    for in_place in (True, False):
+        err = err_word()
+        got = x.run(in_place=in_place, err=err)
+        assert int(err.item()) == 0
+        x.check(got, in_place)
+
+
+def ties(rng, shape):
+    return rng.integers(0, 3, shape).astype(np.float32)
+
+
+def odd_numbers(rng, shape):
+    w = rng.standard_normal(shape).astype(np.float32)
+    pick = rng.integers(0, 12, shape)
+    for i, x in enumerate((np.nan, np.inf, -np.inf, 0.0, -0.0, 1e-42, -1e-42)):
+        w[pick == i] = x
+    return w
+
+
+@pytest.mark.parametrize("weights", [ties, odd_numbers, lambda rng, shape: np.zeros(shape, np.float32),
+                                     lambda rng, shape: 1 + 2.0 ** -23 * rng.integers(0, 700, shape).astype(np.float32)])
+@pytest.mark.parametrize("lens,budget", [([50, 40], 39), ([3000, 2000], 1000), ([9000, 20000], 8000)])
+def test_evict_orders_ties_zeros_and_what_is_no_number(cuda_device, weights, lens, budget):
+    x = Lists(lens, budget, layers=1, d=16, sinks=2, recent=3, weights=weights, seed=budget)
+    x.check(x.run())
+
+
+def test_evict_of_a_first_time_takes_slots_for_positions(cuda_device):
+    x = Lists([100, 60, 300], 64, sinks=4, recent=20, seed=5)
+    x.check(x.run(bare=True))
+
+
+def test_evict_a_single_layer_has_lists_without_a_layer(cuda_device):
+    x = Lists([100, 60, 300], 64, layers=1, sinks=4, recent=20, seed=6)
+    s = x.step
+    k, v, w, p, new = x.run(k_pool=s.k_pool[0].cuda(), v_pool=s.v_pool[0].cuda(),
+                            weights=torch.from_numpy(x.weights[0]).cuda(), token_pos=torch.from_numpy(x.pos[0]).cuda())
+    x.check((k[None], v[None], w[None], p[None], new))
+
+
+def test_evict_skips_and_flags_bad_rows_and_blocks(cuda_device):
+    x = Lists([100, 60, 300, 80], 64, recent=20, seed=7, skipped=(1, 2))
+    err, lens = err_word(), [100, -1, 301, 80]
+    got = x.run(seq_lens=i32(lens), err=err)
+    assert ops.check_error(err) == ERR_LEN
+    x.check(got, skipped=(1, 2))
+    # the block of row 0's slots 16 .. 31 out of range: nothing moves into it, the lists' entries do
+    x = Lists([100, 60], 64, recent=20, seed=7)
+    t = x.step.tables.copy()
+    lost = int(t[0, 1])
+    t[0, 1] = x.step.nb
+    got = x.run(block_tables=i32(t), err=err)
+    assert ops.check_error(err) == ERR_BLOCK
+    after = x.pools_after()
+    for pool, want, was in zip(got[:2], after, (x.step.k_pool, x.step.v_pool)):
+        want[:, lost] = was[:, lost]
+        assert torch.equal(pool.cpu().view(torch.int16), want.view(torch.int16))
+    np.testing.assert_array_equal(got[2].cpu().numpy(), x.w_after)
+    np.testing.assert_array_equal(got[3].cpu().numpy(), x.p_after)
+
+
+def test_evict_in_a_graph_on_another_stream(cuda_device):
+    """Captured once, replayed on new contents; the same bits as an eager call."""
+    xs = [Lists([3000, 70, 5000], 1000, sinks=4, recent=100, seed=s) for s in (8, 9)]
+    g = {}
+    s = xs[0].step
+    args = dict(k_pool=s.k_pool.cuda(), v_pool=s.v_pool.cuda(), block_tables=i32(s.tables), seq_lens=i32(s.lens),
+                weights=torch.from_numpy(xs[0].weights).cuda(), token_pos=torch.from_numpy(xs[0].pos).cuda())
+    new, nxt = torch.zeros(3, dtype=torch.int32, device="cuda"), i32(xs[0].next)
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            ops.evict(**args, budget=1000, max_seq_len=5000, sinks=4, recent=100, next_pos=nxt, new_seq_lens=new)
+    for x in xs:
+        for name, y in (("k_pool", x.step.k_pool), ("v_pool", x.step.v_pool), ("block_tables", i32(x.step.tables)),
+                        ("weights", torch.from_numpy(x.weights)), ("token_pos", torch.from_numpy(x.pos))):
+            args[name].copy_(y)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        x.check((args["k_pool"], args["v_pool"], args["weights"], args["token_pos"], new))
