@@ -679,8 +679,9 @@ int paged_kv_tree_commit(void* k_pool, void* v_pool, const int32_t* block_tables
  * and flagged PKV_DEV_ERR_SEQ_LEN; a table entry out of range sets
  * PKV_DEV_ERR_BLOCK_ID, and the keys and values that would move from or to it
  * do not (weights and positions do).  budget >= 1; head_dim * elt_bytes a multiple
- * of 16; max_seq_len at most 196,608, num_blocks * block_size below 2^31
- * (PKV_ERR_UNSUPPORTED otherwise).  Starts early, as the drafted step's calls do.
+ * of 16; max_seq_len at most 196,608, rows and layers at most 65,535, num_blocks *
+ * block_size below 2^31 (PKV_ERR_UNSUPPORTED otherwise).  Starts early, as the
+ * drafted step's calls do.
  */
 int paged_kv_evict(void* k_pool, void* v_pool, const int32_t* block_tables,
                    const int32_t* seq_lens, const float* weights, const int32_t* token_pos,
