@@ -644,6 +644,45 @@ int paged_kv_tree_commit(void* k_pool, void* v_pool, const int32_t* block_tables
  *     weights  float [rows][kv_heads][weights_stride], weights_stride >=
  *              max_seq_len: entry t belongs to the token in the row's slot t.
  *
+ * Three calls: paged_attention_decode_weights and paged_attention_prefill_weights
+ * add to the sums, paged_kv_evict drops the tokens whose sums are lowest.
+ */
+
+/*
+ * paged_attention_decode_weights -- paged_attention_decode (fp16 pools, k_scale ==
+ * v_scale == null) or paged_attention_decode_fp8 (E4M3 pools), and the weights that
+ * the step's queries give:
+ *     weights[r][kvh][t] += sum_h softmax_t(scale * q[r][h] . K_t)
+ * over the query heads h of KV head kvh, for t < L - 1; the step's own token, t =
+ * L - 1, starts from zero (its entry is written, not added to).  Entries from L on are
+ * left alone.  Computed and kept in binary32.  A score that is no number makes
+ * its head's weights NaN.  A token whose table entry is out of range gets nothing.
+ *
+ * out, errors and clamped lengths as in paged_attention_decode.  Supported for
+ * head_dim 128, q_heads / kv_heads <= 8, block_size a multiple of 16, rows <=
+ * 1024, max_seq_len <= 2^26 and, with E4M3 pools, kv_heads <= 16
+ * (PKV_ERR_UNSUPPORTED otherwise).  weights lies over neither out, q nor the
+ * workspace.
+ *
+ * workspace: paged_attention_decode_weights_workspace_size(...) bytes (0 for
+ * sizes that are not supported), 256-byte aligned: a decode workspace, and 4 bytes a
+ * query head and token of max_seq_len for the scores.  Zero-filled once after
+ * allocation; sharing, reuse and timeouts as for paged_attention_decode's.
+ */
+size_t paged_attention_decode_weights_workspace_size(int rows, int q_heads, int kv_heads,
+                                                     int head_dim, int max_seq_len,
+                                                     int block_size);
+int paged_attention_decode_weights(void* out, float* weights, const void* q, const void* k_pool,
+                                   const void* v_pool, const float* k_scale,
+                                   const float* v_scale, const int32_t* block_tables,
+                                   const int32_t* seq_lens, int rows, int q_heads, int kv_heads,
+                                   int head_dim, int block_size, float scale,
+                                   int max_blocks_per_row, int num_blocks, int max_seq_len,
+                                   int64_t weights_stride, void* workspace,
+                                   size_t workspace_bytes, int32_t* dev_err,
+                                   cudaStream_t stream);
+
+/*
  * paged_kv_evict -- in every list (layer, row, KV head) the tokens of lowest
  * weight leave the cache, every layer at once.
  *

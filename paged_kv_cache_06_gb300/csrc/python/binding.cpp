@@ -1,7 +1,7 @@
 // Python binding of the drafted step's calls (paged_kv_rope_append,
 // paged_attention_tree, paged_kv_tree_commit) and of those of a cache within a
-// budget (paged_kv_norm_rope_append, paged_kv_evict): argument checks and
-// marshalling only, as in ops.py, in C++.
+// budget (paged_kv_norm_rope_append, paged_attention_decode_weights,
+// paged_kv_evict): argument checks and marshalling only, as in ops.py, in C++.
 //
 // Each of these calls takes a dozen tensors, and checking and unpacking them
 // from Python through ctypes took 22 to 30 us a call on the Grace cores, ten
@@ -324,6 +324,42 @@ PyObject* tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// Running sums float [rows][heads][stride].
+float* need_weights(Call& c, PyObject* o, int64_t rows, int64_t heads, int64_t* stride) {
+    const at::Tensor& w = c.need(o, "weights", at::kFloat, 3);
+    *stride = w.size(2);
+    need_shape(w, "weights", {rows, heads, *stride});
+    return static_cast<float*>(w.data_ptr());
+}
+
+PyObject* decode_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded("decode_weights", n, 14, [&]() -> int {
+        Call c;
+        const at::Tensor& out = c.need(a[0], "out", at::kHalf, 3);
+        const at::Tensor& q = c.need(a[2], "q", at::kHalf, 3);
+        need_shape(out, "out", {q.size(0), q.size(1), q.size(2)});
+        const Pools p = need_pools(c, a[3], a[4], a[10], a[11]);
+        const at::Tensor& tables = c.need(a[5], "block_tables", at::kInt, 2);
+        const at::Tensor& lens = c.need(a[6], "seq_lens", at::kInt, 1);
+        const int64_t rows = q.size(0);
+        need_shape(lens, "seq_lens", {rows});
+        if (tables.size(0) != rows) fail(PyExc_ValueError, "block_tables must have a row per seq_len");
+        if (p.d != q.size(2))
+            fail(PyExc_ValueError, "q has head_dim " + std::to_string(q.size(2)) + ", the pools " + std::to_string(p.d));
+        int64_t stride = 0;
+        float* w = need_weights(c, a[1], rows, p.hk, &stride);
+        const at::Tensor& ws = c.need(a[9], "workspace", at::kByte, 1);
+        auto* err = static_cast<int32_t*>(c.optional(a[12], "dev_err", at::kInt, 1));
+        const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, c.device));
+        return paged_attention_decode_weights(
+            out.data_ptr(), w, q.data_ptr(), p.k, p.v, p.ks, p.vs, static_cast<const int32_t*>(tables.data_ptr()),
+            static_cast<const int32_t*>(lens.data_ptr()), narrow(rows, "rows"), narrow(q.size(1), "q heads"),
+            narrow(p.hk, "kv heads"), narrow(p.d, "head_dim"), narrow(p.bs, "block_size"), to_float(a[7]),
+            narrow(tables.size(1), "block_tables"), narrow(p.nb, "blocks"), to_int(a[8]), stride, ws.data_ptr(),
+            (size_t)ws.numel(), err, to_stream(a[13], c.device));
+    });
+}
+
 PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded("evict", n, 17, [&]() -> int {
         Call c;
@@ -394,6 +430,7 @@ PyMethodDef methods[] = {
     {"norm_rope_append", as_function(norm_rope_append), METH_FASTCALL, nullptr},
     {"tree_attention", as_function(tree_attention), METH_FASTCALL, nullptr},
     {"tree_commit", as_function(tree_commit), METH_FASTCALL, nullptr},
+    {"decode_weights", as_function(decode_weights), METH_FASTCALL, nullptr},
     {"evict", as_function(evict), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -125,6 +125,10 @@ def _declare(L: ctypes.CDLL) -> None:
     L.paged_kv_rope_append.restype = I
     L.paged_kv_norm_rope_append.argtypes = [P] * 15 + [F, L64, L64, L64] + [I] * 7 + [F, I, I, I, I, P, P]
     L.paged_kv_norm_rope_append.restype = I
+    L.paged_attention_decode_weights.argtypes = [P] * 9 + [I] * 5 + [F, I, I, I, L64, P, S, P, P]
+    L.paged_attention_decode_weights.restype = I
+    L.paged_attention_decode_weights_workspace_size.argtypes = [I] * 6
+    L.paged_attention_decode_weights_workspace_size.restype = S
     L.paged_kv_evict.argtypes = [P] * 11 + [I] * 9 + [L64, I, I, I, P, P]
     L.paged_kv_evict.restype = I
     L.paged_attention_tree.argtypes = [P] * 10 + [I] * 7 + [F, I, I, I, P, S, P, P]
@@ -639,6 +643,35 @@ def tree_commit(k_pool, v_pool, block_tables, seq_lens, q_start, path, path_lens
 # A cache within a budget: running sums of the attention weights that each cached
 # token gets, and the tokens of lowest weight dropped.  Same binding, device and
 # stream as the drafted step's calls.
+
+def decode_weights_workspace_size(rows: int, q_heads: int, kv_heads: int, head_dim: int,
+                                  max_seq_len: int, block_size: int) -> int:
+    return int(lib().paged_attention_decode_weights_workspace_size(rows, q_heads, kv_heads, head_dim,
+                                                                   max_seq_len, block_size))
+
+
+def alloc_decode_weights_workspace(rows, q_heads, kv_heads, head_dim, max_seq_len, block_size,
+                                   device="cuda"):
+    """A zero-filled workspace of decode_weights of the size the C ABI asks for."""
+    n = decode_weights_workspace_size(rows, q_heads, kv_heads, head_dim, max_seq_len, block_size)
+    if n == 0:
+        raise ValueError("unsupported sizes for paged_attention_decode_weights")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def decode_weights(out, weights, q, k_pool, v_pool, block_tables, seq_lens, scale: float,
+                   max_seq_len: int, workspace, k_scale=None, v_scale=None, dev_err=None,
+                   stream=None):
+    """paged_attention_decode_weights: decode, and the weight that each cached token
+    got added to ``weights`` (float32 [rows][kv_heads][stride], stride >=
+    max_seq_len; the step's own token starts from zero).  FP8 pools when the scales
+    are given."""
+    st = (_ext or binding()).decode_weights(
+        out, weights, q, k_pool, v_pool, block_tables, seq_lens, scale, max_seq_len, workspace,
+        k_scale, v_scale, dev_err, stream)
+    if st:
+        _check("paged_attention_decode_weights", st)
+
 
 def evict(k_pool, v_pool, block_tables, seq_lens, weights, token_pos, budget: int,
           max_seq_len: int, sinks: int = 0, recent: int = 0, tracked=None, next_pos=None,

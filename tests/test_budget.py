@@ -46,6 +46,42 @@ def test_norm_rope_append_refusals():
     assert norm(rows=0, k=0) == 0 and norm(total=0, q=0) == 0
 
 
+def decode(**kw):
+    a = dict(out=FAR, w=2 * FAR, q=FAKE, k=FAKE, v=FAKE, ks=0, vs=0, bt=FAKE, sl=FAKE, rows=4, hq=12, hk=2, d=128, bs=16,
+             scale=0.1, mbpr=16, nb=64, msl=200, stride=200, ws=3 * FAR, wsb=None)
+    a.update(kw)
+    if a["wsb"] is None:
+        a["wsb"] = ops.decode_weights_workspace_size(4, 12, 2, 128, 200, 16)
+    return ops.lib().paged_attention_decode_weights(
+        *[P(a[n]) for n in ("out", "w", "q", "k", "v", "ks", "vs", "bt", "sl")], a["rows"], a["hq"], a["hk"], a["d"],
+        a["bs"], a["scale"], a["mbpr"], a["nb"], a["msl"], a["stride"], P(a["ws"]), a["wsb"], None, None)
+
+
+def test_decode_weights_refusals():
+    for n in ("out", "w", "q", "k", "v", "bt", "sl"):
+        assert decode(**{n: 0}) == INVALID, n
+    for n in ("out", "q", "k", "v"):
+        assert decode(**{n: ODD}) == INVALID, n
+    assert decode(ks=FAKE) == INVALID and decode(vs=FAKE) == INVALID
+    assert decode(stride=199) == INVALID and decode(msl=257, stride=300) == INVALID
+    assert decode(scale=float("nan")) == INVALID and decode(hq=12, hk=5) == INVALID and decode(bs=0) == INVALID
+    assert decode(d=64) == UNSUPPORTED and decode(bs=24) == UNSUPPORTED and decode(rows=1025) == UNSUPPORTED
+    assert decode(hq=18, hk=2) == UNSUPPORTED and decode(hq=34, hk=17, ks=FAKE, vs=FAKE) == UNSUPPORTED
+    assert decode(ws=0) == WORKSPACE and decode(wsb=64) == WORKSPACE and decode(ws=3 * FAR + 16) == WORKSPACE
+    for n in ("out", "q", "ws"):                                      # the sums over what is read or written
+        at = {"out": FAR, "q": FAKE, "ws": 3 * FAR}[n]
+        assert decode(w=at) == INVALID and decode(w=at - 4 * 2 * 200 * 4 + 4) == INVALID, n
+    assert decode(rows=0, q=0) == 0
+
+
+def test_decode_weights_workspace_size_host_arithmetic():
+    n = ops.decode_weights_workspace_size(4, 12, 2, 128, 200, 16)
+    assert n % 256 == 0 and n >= ops.workspace_size(4, 12, 2, 128, 200, 16) + 4 * 2 * 208 * 6 * 4
+    for bad in ((0, 12, 2, 128, 200, 16), (4, 12, 5, 128, 200, 16), (4, 12, 2, 64, 200, 16), (4, 18, 2, 128, 200, 16),
+                (4, 12, 2, 128, -1, 16), (4, 12, 2, 128, 200, 24), (1025, 12, 2, 128, 200, 16)):
+        assert ops.decode_weights_workspace_size(*bad) == 0, bad
+
+
 def evict(**kw):
     a = dict(k=FAKE, v=FAKE, bt=FAKE, sl=FAKE, w=FAR, pos=2 * FAR, tr=FAKE, nx=FAKE, wo=None, po=None, new=3 * FAR,
              layers=2, rows=4, hk=2, d=128, eb=2, bs=16, mbpr=16, nb=64, msl=200, stride=200, budget=100, sinks=4,

@@ -174,6 +174,122 @@ def test_norms_of_heads_that_are_zero_huge_or_no_number(cuda_device):
     check(out[:6][clean.cuda()], ref[clean], rounded(ref, tol)[clean])
 
 
+# ---- weights ----
+
+def weights_ref(step, q, scale, queries, used, skip=()):
+    """What the last used[r] of row r's queries[r] give: (sums [rows][hk] of tensors [L], their
+    tolerance before they are added to anything), and the last query's output."""
+    hq = q.shape[1]
+    g, out = hq // step.hk, []
+    a = 0
+    for r, n in enumerate(step.lens):
+        a += queries[r]
+        u = used[r]
+        if not u or not n:
+            out.append(None)
+            continue
+        k = step.values(step.k_pool, r, step.k_scale).permute(1, 0, 2).repeat_interleave(g, 0)
+        v = step.values(step.v_pool, r, step.v_scale).permute(1, 0, 2).repeat_interleave(g, 0)
+        x = q[a - u:a].double().permute(1, 0, 2)
+        s = (x @ k.transpose(1, 2)) * scale
+        hide = torch.arange(n)[None, :] > torch.arange(n - u, n)[:, None]
+        hide[:, [t for rr, t in skip if rr == r]] = True
+        s = s.masked_fill(hide, -np.inf)
+        p = torch.softmax(s, -1)
+        e = 130 * U * abs(scale) * (x.abs() @ k.abs().transpose(1, 2)).masked_fill(hide, 0).amax(-1, keepdim=True)
+        mag = s.masked_fill(hide, 0).abs().amax(-1, keepdim=True)
+        tol = p * (2 * e + (12 + n + 4 * mag) * U)
+        shape = (step.hk, g * u, n)
+        out.append((p.reshape(shape).sum(1), (tol + g * u * U * p).reshape(shape).sum(1), (p @ v, p @ v.abs(), e)))
+    return out
+
+
+def check_weights(step, got, before, ref, own):
+    """got, before: [rows][hk][stride]; row r's last own[r] tokens start from zero."""
+    got, before = got.cpu().double(), before.cpu().double()
+    for r, n in enumerate(step.lens):
+        assert torch.equal(got[r, :, n:], before[r, :, n:])
+        if ref[r] is None:
+            assert torch.equal(got[r], before[r])
+            continue
+        w = before[r, :, :n].clone()
+        w[:, n - own[r]:] = 0
+        want = w + ref[r][0]
+        check(got[r, :, :n], want, ref[r][1] + 2 * U * want.abs() + 2.0 ** -126, f"weights of row {r}")
+
+
+DECODES = [
+    ([1], 16, 12, 2),
+    ([16, 1, 0, 33, 200], 16, 12, 2),
+    ([63, 64, 65, 4100], 64, 12, 2),
+    ([700, 3, 129], 48, 32, 8),
+    ([513, 40], 112, 28, 4),
+    ([300, 31, 2], 32, 4, 4),
+    ([257, 90], 16, 8, 1),
+    ([20000, 50], 64, 12, 2),
+    ([300 + 7 * i for i in range(70)], 16, 6, 2),       # units cut between blocks, odd groups
+    ([1024] * 40, 64, 10, 2),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", range(len(DECODES)))
+def test_decode_weights_match_the_formula(cuda_device, case, fp8):
+    """Weights: a score is off by e (a dot product of 128 terms), m U (its scaling and the
+    maximum taken from it, m the largest score) and so its weight by 2 e + 4 m U of
+    itself, exponent, reciprocal and products 12 U, the sum over L weights L U, over the
+    heads g U.  The output as the tree's."""
+    lens, bs, hq, hk = DECODES[case]
+    step = Step(lens, [0] * len(lens), bs, hk=hk, fp8=fp8, seed=500 + case)
+    q = torch.randn(len(lens), hq, 128, generator=step.gen).half()
+    before = torch.rand(len(lens), hk, step.max_len + 5, generator=step.gen)
+    a, err = step.gpu(), err_word()
+    ws = ops.alloc_decode_weights_workspace(len(lens), hq, hk, 128, step.max_len, bs)
+    ref = weights_ref(step, q, 0.0883, [1] * len(lens), [1] * len(lens))
+    outs = []
+    for _ in range(2):
+        out = torch.full(q.shape, float("nan"), dtype=torch.float16, device="cuda")
+        w = before.cuda()
+        ops.decode_weights(out, w, q.cuda(), a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], 0.0883,
+                           step.max_len, ws, k_scale=a["k_scale"], v_scale=a["v_scale"], dev_err=err)
+        torch.cuda.synchronize()
+        outs.append((out, w))
+    assert int(err.item()) == 0
+    assert all(torch.equal(x, y) for x, y in zip(*outs))              # the same bits every time
+    check_weights(step, w, before, ref, [1] * len(lens))
+    for r, n in enumerate(lens):
+        if n == 0:
+            assert bool((out[r] == 0).all())
+            continue
+        o, big, e = (x[:, 0] for x in ref[r][2])
+        low = 2.0 ** -25 * step.values(step.v_pool, r, step.v_scale).abs().sum(0).repeat_interleave(hq // hk, 0)
+        check(out[r], o, H * o.abs() + (H + 2 * e + (8 + n) * U) * big + low + 2.0 ** -25, f"output of row {r}")
+
+
+def test_decode_weights_of_bad_lengths_blocks_and_numbers(cuda_device):
+    step = Step([100, 60, 300, 40], [0] * 4, 16, seed=13)
+    q = torch.randn(4, 12, 128, generator=step.gen).half()
+    q[3, 2, 5] = float("nan")
+    before = torch.rand(4, 2, 300, generator=step.gen)
+    t, lens = step.tables.copy(), [100, -4, 301, 40]                  # row 2 is clamped to 300
+    t[0, 1] = step.nb                                                  # slots 16 .. 31 of row 0
+    a, err = step.gpu(block_tables=i32(t), seq_lens=i32(lens)), err_word()
+    ws = ops.alloc_decode_weights_workspace(4, 12, 2, 128, 300, 16)
+    out, w = torch.zeros(4, 12, 128, dtype=torch.float16, device="cuda"), before.cuda()
+    ops.decode_weights(out, w, q.cuda(), a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], 0.0883, 300, ws,
+                       dev_err=err)
+    assert ops.check_error(err) == ERR_BLOCK | ERR_LEN
+    assert torch.equal(w[1].cpu(), before[1])
+    assert bool(torch.isnan(w[3, 0, :40]).all()) and bool(torch.isfinite(w[3, 1]).all())
+    assert torch.equal(w[0, :, 16:32].cpu(), before[0, :, 16:32])      # they got nothing
+    q[3, 2, 5] = 0
+    ref = weights_ref(step, q, 0.0883, [1] * 4, [1] * 4, skip=[(0, i) for i in range(16, 32)])
+    ref[1] = None
+    w[3] = before[3].cuda()
+    ref[3] = None
+    check_weights(step, w, before, ref, [1] * 4)
+
+
 # ---- eviction ----
 
 class Lists:
