@@ -658,16 +658,18 @@ int paged_kv_tree_commit(void* k_pool, void* v_pool, const int32_t* block_tables
  * left alone.  Computed and kept in binary32.  A score that is no number makes
  * its head's weights NaN.  A token whose table entry is out of range gets nothing.
  *
- * out, errors and clamped lengths as in paged_attention_decode.  Supported for
- * head_dim 128, q_heads / kv_heads <= 8, block_size a multiple of 16, rows <=
- * 1024, max_seq_len <= 2^26 and, with E4M3 pools, kv_heads <= 16
- * (PKV_ERR_UNSUPPORTED otherwise).  weights lies over neither out, q nor the
- * workspace.
+ * out, errors and clamped lengths as in paged_attention_decode (computed by another
+ * kernel: the bits may differ).  Supported for head_dim 128, q_heads / kv_heads
+ * <= 8, block_size a multiple of 16, rows <= 1024, max_seq_len <= 2^24, num_blocks *
+ * block_size and rows * kv_heads * max_seq_len / 16 below 2^31 less 1024
+ * (PKV_ERR_UNSUPPORTED otherwise).  Of out,
+ * weights, q and the workspace none that is written overlaps another.
+ * Both of its launches start early, as the drafted step's calls do.
  *
  * workspace: paged_attention_decode_weights_workspace_size(...) bytes (0 for
- * sizes that are not supported), 256-byte aligned: a decode workspace, and 4 bytes a
- * query head and token of max_seq_len for the scores.  Zero-filled once after
- * allocation; sharing, reuse and timeouts as for paged_attention_decode's.
+ * sizes that are not supported), 256-byte aligned: 4 bytes a query head (an odd group's
+ * rounded up) and token of max_seq_len for the scores, and partial results.  It may hold
+ * anything; calls that share one must be ordered.
  */
 size_t paged_attention_decode_weights_workspace_size(int rows, int q_heads, int kv_heads,
                                                      int head_dim, int max_seq_len,

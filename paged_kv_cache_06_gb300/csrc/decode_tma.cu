@@ -137,11 +137,6 @@ struct Params {
     // FP8 pools: one scale per KV head (null for fp16 pools)
     const float* k_scale;
     const float* v_scale;
-    // weights wanted: every score in base 2, [unit][tokens][score_heads], and every
-    // unit's maxima and reciprocal sums [unit][kMaxGroup]
-    float* scores;
-    float2* maxima;
-    int score_tokens, score_heads;
 };
 
 static_assert(sizeof(Params) <= 256 && sizeof(Params) % 8 == 0, "Params fit their shared-memory copy");
@@ -257,7 +252,6 @@ __device__ __forceinline__ void patch_row(unsigned char* sp, int prow, const uin
 // gq, head 2tq; s1 = gq, 2tq+1; s2, s3 = token gq+8) with `valid` tokens:
 // updates the running max and sum, rescales O and returns the B fragments
 // of P^T (token x head) for the PV product.
-template <bool kWeights>
 __device__ __forceinline__ void softmax_step(Soft& st, float (&s)[4], int valid, float scale_log2,
                                              int lane, uint32_t& pb0, uint32_t& pb1) {
     const int gq = lane >> 2;
@@ -277,25 +271,13 @@ __device__ __forceinline__ void softmax_step(Soft& st, float (&s)[4], int valid,
     const float al0 = fast_exp2(st.m0 - mu0), al1 = fast_exp2(st.m1 - mu1);
     st.m0 = mn0;
     st.m1 = mn1;
-    uint32_t px, py;
-    if constexpr (kWeights) {
-        // the sum takes the weights in 32 bits: it is also what the weights handed out are
-        // divided by
-        const float x0 = fast_exp2(s[0] - mu0), x1 = fast_exp2(s[1] - mu1);
-        const float y0 = fast_exp2(s[2] - mu0), y1 = fast_exp2(s[3] - mu1);
-        px = pack_half2(x0, x1);
-        py = pack_half2(y0, y1);
-        st.l0 = st.l0 * al0 + (x0 + y0);
-        st.l1 = st.l1 * al1 + (x1 + y1);
-    } else {
-        px = pack_half2(fast_exp2(s[0] - mu0), fast_exp2(s[1] - mu1));
-        py = pack_half2(fast_exp2(s[2] - mu0), fast_exp2(s[3] - mu1));
-        // the sum takes the fp16 weights the MMA multiplies by
-        const float2 fx = __half22float2(*reinterpret_cast<const __half2*>(&px));
-        const float2 fy = __half22float2(*reinterpret_cast<const __half2*>(&py));
-        st.l0 = st.l0 * al0 + (fx.x + fy.x);
-        st.l1 = st.l1 * al1 + (fx.y + fy.y);
-    }
+    const uint32_t px = pack_half2(fast_exp2(s[0] - mu0), fast_exp2(s[1] - mu1));
+    const uint32_t py = pack_half2(fast_exp2(s[2] - mu0), fast_exp2(s[3] - mu1));
+    // the sum takes the fp16 weights the MMA multiplies by
+    const float2 fx = __half22float2(*reinterpret_cast<const __half2*>(&px));
+    const float2 fy = __half22float2(*reinterpret_cast<const __half2*>(&py));
+    st.l0 = st.l0 * al0 + (fx.x + fy.x);
+    st.l1 = st.l1 * al1 + (fx.y + fy.y);
     // B fragments of P^T (token x head) by transposing in registers
     pb0 = movmatrix_t(px);
     pb1 = movmatrix_t(py);
@@ -310,31 +292,11 @@ __device__ __forceinline__ void softmax_step(Soft& st, float (&s)[4], int valid,
     }
 }
 
-// Where a granule's scores go when weights are wanted: this lane's two heads of its
-// first token (null otherwise), and the distance to the token eight further on.
-struct ScoreOut {
-    float* at;
-    int eight;
-    __device__ __forceinline__ ScoreOut(const Params& p, int unit, int tok0, int lane) {
-        const int gq = lane >> 2, h = 2 * (lane & 3);
-        at = h < p.score_heads
-                 ? p.scores + ((int64_t)unit * p.score_tokens + tok0 + gq) * p.score_heads + h
-                 : nullptr;
-        eight = 8 * p.score_heads;
-    }
-    __device__ __forceinline__ void store(const float (&s)[4]) const {
-        if (!at) return;
-        *reinterpret_cast<float2*>(at) = make_float2(s[0], s[1]);
-        *reinterpret_cast<float2*>(at + eight) = make_float2(s[2], s[3]);
-    }
-};
-
 // One online-softmax step of a warp over the fp16 granule staged at `slot`
 // (K dims 0-63 at +0, K 64-127 at +2 KB, V at +4 KB / +6 KB, 128-byte
 // swizzled rows) with `valid` tokens.  Rows past `valid` hold zeros.
-template <bool kWeights>
 __device__ __forceinline__ void attend(Soft& st, const uint32_t (&qb)[16], uint32_t slot, int valid,
-                                       float scale_log2, int lane, const Params& p, int unit, int tok0) {
+                                       float scale_log2, int lane) {
     float s[4];
     {
         // S^T = K . Q^T; two independent chains (even / odd k-steps)
@@ -352,8 +314,7 @@ __device__ __forceinline__ void attend(Soft& st, const uint32_t (&qb)[16], uint3
         for (int i = 0; i < 4; ++i) s[i] = c0[i] + c1[i];
     }
     uint32_t pb0, pb1;
-    softmax_step<kWeights>(st, s, valid, scale_log2, lane, pb0, pb1);
-    if constexpr (kWeights) ScoreOut(p, unit, tok0, lane).store(s);
+    softmax_step(st, s, valid, scale_log2, lane, pb0, pb1);
     // O^T += V^T . P^T
     const int row = (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
@@ -375,10 +336,8 @@ __device__ __forceinline__ void attend(Soft& st, const uint32_t (&qb)[16], uint3
 // too: row g of m-tile i is dim 16g + 2i and row g + 8 is 16g + 2i + 1, so
 // lane (g, t) reads one 16-byte chunk of each of its four V rows
 // (store_chunk_fp8 writes the result back in natural order).
-template <bool kWeights>
 __device__ __forceinline__ void attend8(Soft& st, const uint32_t (&qb)[16], const unsigned char* slot,
-                                        int valid, float scale_log2, int lane, const Params& p, int unit,
-                                        int tok0) {
+                                        int valid, float scale_log2, int lane) {
     const int g = lane >> 2, t = lane & 3;
     float s[4];
     {
@@ -403,8 +362,7 @@ __device__ __forceinline__ void attend8(Soft& st, const uint32_t (&qb)[16], cons
         for (int i = 0; i < 4; ++i) s[i] = c0[i] + c1[i];
     }
     uint32_t pb0, pb1;
-    softmax_step<kWeights>(st, s, valid, scale_log2, lane, pb0, pb1);
-    if constexpr (kWeights) ScoreOut(p, unit, tok0, lane).store(s);
+    softmax_step(st, s, valid, scale_log2, lane, pb0, pb1);
     // O^T += V^T . P^T: chunk g (dims 16g .. 16g+15) of V rows 2t, 2t+1, 8+2t, 9+2t
     const unsigned char* vb = slot + kBoxBytes;
     const int ra = 2 * t;  // rows ra, ra + 1, ra + 8, ra + 9 share ra & 7 up to the low bit
@@ -584,7 +542,6 @@ struct PieceOut {
     unsigned char* region;  // the unit's record region
     int P, idx, K, group;
     float vs;               // FP8 V scale (1 for fp16 pools)
-    float2* maxima;         // the unit's, when weights are wanted
 };
 __device__ __forceinline__ PieceOut piece_out(const Params& p, int r, int kvh, int cs, int P, int cta,
                                               float vs) {
@@ -596,28 +553,15 @@ __device__ __forceinline__ PieceOut piece_out(const Params& p, int r, int kvh, i
     po.K = P < kMergeWays ? P : kMergeWays;
     po.group = p.group;
     po.vs = vs;
-    po.maxima = p.maxima + (int64_t)(r * p.hk + kvh) * kMaxGroup;
     return po;
-}
-
-// A finished unit's maxima and reciprocal sums, from lanes 0-3 (0 for a sum of nothing,
-// whose scores are all -inf).
-__device__ __forceinline__ void emit_maxima(float2* maxima, float M0, float M1, float L0, float L1, int lane) {
-    if (lane >= 4) return;
-    // a unit of no visible token has maxima of -inf, which no score may be taken from
-    const float4 v = make_float4(M0 == -INFINITY ? 0.f : M0, L0 == 0.f ? 0.f : __fdividef(1.f, L0),
-                                 M1 == -INFINITY ? 0.f : M1, L1 == 0.f ? 0.f : __fdividef(1.f, L1));
-    reinterpret_cast<float4*>(maxima)[lane] = v;
 }
 
 // Chunk c of a piece's combined state (unnormalised acc, sums L0 / L1): the
 // fp16 output dims 16c.. when the unit is whole, else the record words.
-template <bool kFp8, bool kWeights>
-__device__ __forceinline__ void emit_chunk(const PieceOut& po, int c, const float (&acc)[4], float M0,
-                                           float M1, float L0, float L1, int lane) {
+template <bool kFp8>
+__device__ __forceinline__ void emit_chunk(const PieceOut& po, int c, const float (&acc)[4], float L0,
+                                           float L1, int lane) {
     if (po.P == 1) {
-        if constexpr (kWeights)
-            if (c == 0) emit_maxima(po.maxima, M0, M1, L0, L1, lane);
         const float inv0 = L0 > 0.f ? __fdividef(po.vs, L0) : 0.f;
         const float inv1 = L1 > 0.f ? __fdividef(po.vs, L1) : 0.f;
         if (kFp8)  // the state is in the FP8 dim order
@@ -646,7 +590,7 @@ __device__ __forceinline__ void emit_ml(const PieceOut& po, float M0, float M1, 
 // state's offset, maximum and sum is loaded up front, the weights are
 // computed once, and each chunk's k loads are issued together, so the chains
 // overlap.
-template <bool kFp8, bool kWeights>
+template <bool kFp8>
 __device__ void combine_dumps(const PieceOut& po, const unsigned char* ring,
                               const int (&slot)[kStreamWarps], int k, int j, int lane) {
     const int tq = lane & 3;
@@ -687,7 +631,7 @@ __device__ void combine_dumps(const PieceOut& po, const unsigned char* ring,
             acc[2] += ml[s].x * v[s].z;
             acc[3] += ml[s].y * v[s].w;
         }
-        emit_chunk<kFp8, kWeights>(po, c, acc, M0, M1, L0, L1, lane);
+        emit_chunk<kFp8>(po, c, acc, L0, L1, lane);
     }
     if (j == 0) emit_ml(po, M0, M1, L0, L1, lane);
 }
@@ -720,7 +664,7 @@ __device__ __forceinline__ void absorb(float& M0, float& M1, float& L0, float& L
     M1 = N1;
 }
 
-template <bool kFp8, bool kWeights>
+template <bool kFp8>
 __device__ __forceinline__ bool merge_task(const Params& p, const Task& t, int lw, int nw,
                                            unsigned char* part, int bar_id, float vs,
                                            volatile int* fail, int lane) {
@@ -780,8 +724,6 @@ __device__ __forceinline__ bool merge_task(const Params& p, const Task& t, int l
             const float inv0 = L0 > 0.f ? __fdividef(vs, L0) : 0.f;
             const float inv1 = L1 > 0.f ? __fdividef(vs, L1) : 0.f;
             __half* ob = p.out + ((int64_t)t.r * p.hq + t.kvh * p.group) * kHeadDim;
-            if constexpr (kWeights)
-                if (t.idx + m == 0) emit_maxima(p.maxima + (int64_t)t.u * kMaxGroup, M0, M1, L0, L1, lane);
             if (kFp8)
                 store_chunk_fp8(ob, t.idx + m * K, acc, inv0, inv1, p.group, lane);
             else
@@ -816,8 +758,6 @@ __device__ __forceinline__ bool merge_task(const Params& p, const Task& t, int l
         }
         const float inv0 = L0 > 0.f ? __fdividef(vs, L0) : 0.f;
         const float inv1 = L1 > 0.f ? __fdividef(vs, L1) : 0.f;
-        if constexpr (kWeights)
-            if (t.idx + m == 0) emit_maxima(p.maxima + (int64_t)t.u * kMaxGroup, M0, M1, L0, L1, lane);
         if (kFp8)
             store_chunk_fp8(ob, t.idx + m * K, acc, inv0, inv1, p.group, lane);
         else
@@ -1177,7 +1117,7 @@ __device__ __forceinline__ void stream_share(int g0, int g1, int w, int& wa, int
     wb = g0 + (int)((int64_t)ng * (w + 1) / kSWarps);
 }
 
-template <bool kPaged, bool kFp8, bool kWeights>
+template <bool kPaged, bool kFp8>
 __device__ __noinline__ void stream_warp(const Params& p, const Ctx& cx, int cta, int warp, int lane,
                                          unsigned char* scratch) {
     constexpr int kRowBytes = kFp8 ? 128 : 256;  // one token of one KV head
@@ -1254,7 +1194,7 @@ __device__ __noinline__ void stream_warp(const Params& p, const Ctx& cx, int cta
             // the whole unit lies in this share: its output, straight from registers
             const PieceOut po = piece_out(p, cr, ckvh, 0, 1, 0, kFp8 ? cx.vs[ckvh] : 1.f);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) emit_chunk<kFp8, kWeights>(po, c, st.o[c], st.m0, st.m1, st.l0, st.l1, lane);
+            for (int c = 0; c < 8; ++c) emit_chunk<kFp8>(po, c, st.o[c], st.l0, st.l1, lane);
         } else if (!at_end) {
             dump_state_global(st, scratch, lane);  // the first unit, shared with earlier warps or blocks
             parked = true;
@@ -1306,11 +1246,10 @@ __device__ __noinline__ void stream_warp(const Params& p, const Ctx& cx, int cta
         const int prow = patch_tok >= 0 ? patch_tok - (g - cus) * kGranule : -1;
         if (prow >= 0 && prow < valid) patch_row<kFp8>(sp, prow, patch_val, lane);
         __syncwarp();
-        const int unit = cr * hk + ckvh, tok0 = (g - cus) * kGranule;  // (for the scores alone)
         if (kFp8)
-            attend8<kWeights>(st, qb, sp, valid, sl2, lane, p, unit, tok0);
+            attend8(st, qb, sp, valid, sl2, lane);
         else
-            attend<kWeights>(st, qb, slot0 + s * kSlotBytes, valid, sl2, lane, p, unit, tok0);
+            attend(st, qb, slot0 + s * kSlotBytes, valid, sl2, lane);
         __syncwarp();  // the slot is read before its next copy is issued
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -1358,7 +1297,7 @@ __device__ __noinline__ void stream_warp(const Params& p, const Ctx& cx, int cta
         const int cs = owner_of(xus, cx.W, cx.Geff);
         const int P = owner_of(xus + xn - 1, cx.W, cx.Geff) - cs + 1;
         const PieceOut po = piece_out(p, xr, xkvh, cs, P, cta, kFp8 ? cx.vs[xkvh] : 1.f);
-        combine_dumps<kFp8, kWeights>(po, smem + Smem::ring, slot, b - a + 1, warp - a, lane);
+        combine_dumps<kFp8>(po, smem + Smem::ring, slot, b - a + 1, warp - a, lane);
         if (P > 1 && warp == a && lane == 0) {
             // the block's split pieces (its first and its last) are its merge tasks
             const int k = atomicAdd(&bp->ntasks, 1);
@@ -1380,7 +1319,7 @@ __device__ __noinline__ void stream_warp(const Params& p, const Ctx& cx, int cta
 // of the piece.  Combines the states the piece's warps dumped into their
 // first slots through their log-sum-exp and emits each chunk (fp16 output of
 // a whole unit, or the piece's record); warp 0 also emits a split piece's m/l.
-template <bool kFp8, bool kWeights>
+template <bool kFp8>
 __device__ void burst_emit(const PieceOut& po, const BlockPlan* bp, const unsigned char* ring, int k,
                            int j, int lane) {
     const int n = bp->pwn[k], w0 = bp->pw0[k], g0 = bp->g0, tq = lane & 3;
@@ -1417,14 +1356,12 @@ __device__ void burst_emit(const PieceOut& po, const BlockPlan* bp, const unsign
             acc[2] += ml[s].x * v.z;
             acc[3] += ml[s].y * v.w;
         }
-        emit_chunk<kFp8, kWeights>(po, c, acc, M0, M1, L0, L1, lane);
+        emit_chunk<kFp8>(po, c, acc, L0, L1, lane);
     }
     if (j == 0) emit_ml(po, M0, M1, L0, L1, lane);
 }
 
-// kWeights: the scores and every unit's maxima and sums are written too, and the sums take
-// the weights in 32 bits.
-template <bool kPaged, bool kFp8, bool kWeights>
+template <bool kPaged, bool kFp8>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_tma_kernel(const __grid_constant__ Params prm) {
     extern __shared__ unsigned char smem_raw[];
@@ -1512,7 +1449,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // ============================== consumers ==============================
     if (mode == kModeStream) {
         if (warp >= kSWarps) return;  // stream mode runs on warps 0 .. kSWarps-1
-        stream_warp<kPaged, kFp8, kWeights>(p, cx, cta, warp, lane,
+        stream_warp<kPaged, kFp8>(p, cx, cta, warp, lane,
                                   p.records + stream_scratch_offset(p) + ((size_t)cta * kSWarps + warp) * kStateBytes);
     } else {
         // ============================ burst mode ============================
@@ -1584,12 +1521,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int prow = patch_tok >= 0 ? patch_tok - (g - us) * kGranule : -1;
                 if (prow >= 0 && prow < bp->svalid[si]) patch_row<kFp8>(sp, prow, patch_val, lane);
                 __syncwarp();
-                const int unit = r * hk + kvh, tok0 = (g - us) * kGranule;  // (for the scores alone)
                 if (kFp8)
-                    attend8<kWeights>(st, qb, sp, bp->svalid[si], sl2, lane, p, unit, tok0);
+                    attend8(st, qb, sp, bp->svalid[si], sl2, lane);
                 else
-                    attend<kWeights>(st, qb, sbase + Smem::ring + si * kSlotBytes, bp->svalid[si], sl2, lane, p, unit,
-                                     tok0);
+                    attend(st, qb, sbase + Smem::ring + si * kSlotBytes, bp->svalid[si], sl2, lane);
             }
             st.reduce_l();
             __syncwarp();
@@ -1605,10 +1540,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const PieceOut po = piece_out(p, r, kvh, bp->pcs[pi], bp->pP[pi], cta, kFp8 ? sm_vs[kvh] : 1.f);
                 if (k == 1) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) emit_chunk<kFp8, kWeights>(po, c, st.o[c], st.m0, st.m1, st.l0, st.l1, lane);
+                    for (int c = 0; c < 8; ++c) emit_chunk<kFp8>(po, c, st.o[c], st.l0, st.l1, lane);
                     emit_ml(po, st.m0, st.m1, st.l0, st.l1, lane);
                 } else {
-                    burst_emit<kFp8, kWeights>(po, bp, smem + Smem::ring, pi, warp - bp->pw0[pi], lane);
+                    burst_emit<kFp8>(po, bp, smem + Smem::ring, pi, warp - bp->pw0[pi], lane);
                 }
             }
         }
@@ -1638,7 +1573,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int lw = (ntask == 1 || warp < half) ? warp : warp - half;
     const int nw = ntask == 1 ? nc : (t == 0 ? half : nc - half);
     const Task task = bp->tasks[t];
-    merge_task<kFp8, kWeights>(p, task, lw, nw, smem + Smem::ring + t * kLandBytes, kBarMerge + t,
+    merge_task<kFp8>(p, task, lw, nw, smem + Smem::ring + t * kLandBytes, kBarMerge + t,
                kFp8 ? sm_vs[task.kvh] : 1.f, sm_flags + 4 + t, lane);
 }
 
@@ -1674,7 +1609,7 @@ static const void* g_hook_stuck = nullptr;
 
 struct DeviceInfo {
     int sms = 0;
-    bool attr_set[5] = {};
+    bool attr_set[3] = {false, false, false};
 };
 
 static int device_info(DeviceInfo** out) {
@@ -1779,8 +1714,7 @@ int tma_decode_launch(void* out, const void* q, const void* k_base, const void* 
                       int kv_heads, int block_size, float scale, int mbpr, int num_blocks,
                       int max_seq_len, int width, void* workspace, int32_t* dev_err,
                       cudaStream_t stream, const AppendArgs* append, bool pdl,
-                      const float* k_scale, const float* v_scale, const void* plan,
-                      const ScoreArgs* scores) {
+                      const float* k_scale, const float* v_scale, const void* plan) {
     using namespace tma;
     const bool paged = width == 0;
     const bool fp8 = k_scale != nullptr;
@@ -1834,19 +1768,10 @@ int tma_decode_launch(void* out, const void* q, const void* k_base, const void* 
     prm.kbase = k_base;
     prm.vbase = v_base;
 
-    if (scores) {
-        if (!paged) return PKV_ERR_UNSUPPORTED;
-        prm.scores = scores->scores;
-        prm.maxima = scores->maxima;
-        prm.score_tokens = scores->tokens;
-        prm.score_heads = scores->heads;
-    }
-
     const uint32_t smem = Smem::total(rows);
-    const int which = scores ? 3 + fp8 : fp8 ? 2 : paged ? 0 : 1;
-    auto kernel = scores ? (fp8 ? decode_tma_kernel<true, true, true> : decode_tma_kernel<true, false, true>)
-                  : fp8  ? decode_tma_kernel<true, true, false>
-                         : paged ? decode_tma_kernel<true, false, false> : decode_tma_kernel<false, false, false>;
+    const int which = fp8 ? 2 : paged ? 0 : 1;
+    auto kernel = fp8 ? decode_tma_kernel<true, true>
+                      : paged ? decode_tma_kernel<true, false> : decode_tma_kernel<false, false>;
     if (!info->attr_set[which]) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  Smem::total(kMaxRows)) != cudaSuccess)

@@ -71,6 +71,7 @@ __device__ __forceinline__ uint32_t block_rank() {
 }
 // Every thread of the cluster has arrived, and what each wrote before is seen by all.
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();  // the aligned form wants the whole warp together
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The word at shared address `addr` of block `rank` of the cluster.

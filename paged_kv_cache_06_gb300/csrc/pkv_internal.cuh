@@ -110,14 +110,6 @@ struct AppendArgs {
     const void* k_new;
     const void* v_new;
 };
-// Scores and maxima that a decode launch also writes: scores in base 2
-// [rows * kv_heads][tokens][heads] (tokens: whole 16-token granules; heads: the group
-// rounded up to even), maxima and reciprocal sums [rows * kv_heads][kMaxGroup].
-struct ScoreArgs {
-    float* scores;
-    float2* maxima;
-    int tokens, heads;
-};
 // Tiled tensor map (128-byte swizzle) over a 3-D array: dims and box innermost
 // first, strides in bytes of dims 1 and 2.
 int encode_map_3d(const void* base, CUtensorMapDataType dtype, const int64_t dims[3],
@@ -143,6 +135,6 @@ int tma_decode_launch(void* out, const void* q, const void* k_base, const void* 
                       int max_seq_len, int width, void* workspace, int32_t* dev_err,
                       cudaStream_t stream, const AppendArgs* append = nullptr, bool pdl = false,
                       const float* k_scale = nullptr, const float* v_scale = nullptr,
-                      const void* plan = nullptr, const ScoreArgs* scores = nullptr);
+                      const void* plan = nullptr);
 
 }  // namespace pkv

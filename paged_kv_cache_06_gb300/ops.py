@@ -652,11 +652,11 @@ def decode_weights_workspace_size(rows: int, q_heads: int, kv_heads: int, head_d
 
 def alloc_decode_weights_workspace(rows, q_heads, kv_heads, head_dim, max_seq_len, block_size,
                                    device="cuda"):
-    """A zero-filled workspace of decode_weights of the size the C ABI asks for."""
+    """A workspace of decode_weights of the size the C ABI asks for."""
     n = decode_weights_workspace_size(rows, q_heads, kv_heads, head_dim, max_seq_len, block_size)
     if n == 0:
         raise ValueError("unsupported sizes for paged_attention_decode_weights")
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def decode_weights(out, weights, q, k_pool, v_pool, block_tables, seq_lens, scale: float,

@@ -66,17 +66,18 @@ def test_decode_weights_refusals():
     assert decode(stride=199) == INVALID and decode(msl=257, stride=300) == INVALID
     assert decode(scale=float("nan")) == INVALID and decode(hq=12, hk=5) == INVALID and decode(bs=0) == INVALID
     assert decode(d=64) == UNSUPPORTED and decode(bs=24) == UNSUPPORTED and decode(rows=1025) == UNSUPPORTED
-    assert decode(hq=18, hk=2) == UNSUPPORTED and decode(hq=34, hk=17, ks=FAKE, vs=FAKE) == UNSUPPORTED
+    assert decode(hq=18, hk=2) == UNSUPPORTED and decode(nb=1 << 27) == UNSUPPORTED
     assert decode(ws=0) == WORKSPACE and decode(wsb=64) == WORKSPACE and decode(ws=3 * FAR + 16) == WORKSPACE
     for n in ("out", "q", "ws"):                                      # the sums over what is read or written
         at = {"out": FAR, "q": FAKE, "ws": 3 * FAR}[n]
         assert decode(w=at) == INVALID and decode(w=at - 4 * 2 * 200 * 4 + 4) == INVALID, n
+    assert decode(q=FAR) == INVALID and decode(ws=FAR) == INVALID         # the output over what is read or written
     assert decode(rows=0, q=0) == 0
 
 
 def test_decode_weights_workspace_size_host_arithmetic():
     n = ops.decode_weights_workspace_size(4, 12, 2, 128, 200, 16)
-    assert n % 256 == 0 and n >= ops.workspace_size(4, 12, 2, 128, 200, 16) + 4 * 2 * 208 * 6 * 4
+    assert n % 256 == 0 and n >= 4 * 2 * 200 * 6 * 4
     for bad in ((0, 12, 2, 128, 200, 16), (4, 12, 5, 128, 200, 16), (4, 12, 2, 64, 200, 16), (4, 18, 2, 128, 200, 16),
                 (4, 12, 2, 128, -1, 16), (4, 12, 2, 128, 200, 24), (1025, 12, 2, 128, 200, 16)):
         assert ops.decode_weights_workspace_size(*bad) == 0, bad
