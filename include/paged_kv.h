@@ -685,6 +685,50 @@ int paged_attention_decode_weights(void* out, float* weights, const void* q, con
                                    cudaStream_t stream);
 
 /*
+ * paged_attention_prefill_weights -- the weights that a chunk's queries give, or
+ * the last `window` of them (a prompt's last few already tell which of its tokens
+ * matter).  q, q_start, total_q and seq_lens are paged_attention_prefill's: with C_r queries
+ * in row r's chunk, u = min(C_r, window) and i from C_r - u to C_r - 1, query i sits at
+ * position seq_lens[r] - C_r + i and
+ *     weights[r][kvh][t] += sum_i sum_h softmax_t(scale * q[i][h] . K_t)
+ * over those queries and the heads h of KV head kvh, the softmax over the tokens up to
+ * the query's position; t < seq_lens[r] - C_r adds to what is there, the chunk's own
+ * tokens start from zero.  Rows without queries and entries from seq_lens[r] on
+ * are left alone.  The keys must be in the rows' blocks; fp16 pools (k_scale ==
+ * null) or E4M3 codes with one scale per KV head.  Computed and kept in binary32.
+ * Tokens that a query does not see do not reach its weights whatever they hold.
+ *
+ * A row with C_r < 0, C_r > seq_lens[r], seq_lens[r] > max_seq_len or queries past
+ * total_q is skipped and flagged PKV_DEV_ERR_SEQ_LEN; where rows name the same queries and
+ * have more of them than total_q, nothing is written and PKV_DEV_ERR_SEQ_LEN is flagged.  A
+ * table entry out of range sets PKV_DEV_ERR_BLOCK_ID; its tokens get nothing and are
+ * nobody's share.
+ *
+ * Supported: head_dim 128, q_heads / kv_heads <= 128, block_size a multiple of 16, rows
+ * <= 1024, max_seq_len <= 2^23, num_blocks * block_size below 2^31, and below 2^30
+ * products of a query block and a token tile of 128 each (PKV_ERR_UNSUPPORTED otherwise).
+ * window >= 1.  weights, q and the workspace do not overlap.  Its launches start
+ * early, as the drafted step's calls do.
+ *
+ * workspace: paged_attention_prefill_weights_workspace_size(...) bytes (0 for sizes
+ * that are not supported), 256-byte aligned.  It may hold anything; calls that share one
+ * must be ordered.
+ */
+size_t paged_attention_prefill_weights_workspace_size(int rows, int total_q, int q_heads,
+                                                      int kv_heads, int head_dim,
+                                                      int max_seq_len, int block_size,
+                                                      int window);
+int paged_attention_prefill_weights(float* weights, const void* q, const void* k_pool,
+                                    const float* k_scale, const int32_t* block_tables,
+                                    const int32_t* seq_lens, const int32_t* q_start, int rows,
+                                    int total_q, int q_heads, int kv_heads, int head_dim,
+                                    int block_size, float scale, int window,
+                                    int max_blocks_per_row, int num_blocks, int max_seq_len,
+                                    int64_t weights_stride, void* workspace,
+                                    size_t workspace_bytes, int32_t* dev_err,
+                                    cudaStream_t stream);
+
+/*
  * paged_kv_evict -- in every list (layer, row, KV head) the tokens of lowest
  * weight leave the cache, every layer at once.
  *

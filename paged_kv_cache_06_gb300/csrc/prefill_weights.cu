@@ -1,0 +1,910 @@
+// paged_attention_prefill_weights: the softmax weights that a chunk's queries, or its
+// last `window` ones, give to each of the row's tokens, added to the tokens' running
+// sums, on the 5th-generation tensor cores (tcgen05, scores in tensor memory).
+//
+// Mathematics.  For one KV head, flat row f of a row's used queries is query f / group and head
+// f % group of the group.  With s[f][t] the base-2 scores, a token t gets
+//   sum over f that see it of 2^(s[f][t] - e[f]),   e[f] = log2 sum_t 2^s[f][t],
+// and e[f] is known only after f's last token: the scores are computed twice, each time
+// in the orientation in which the sum runs along a thread's registers.
+//   1. S = Q K^T, a flat row a thread: its reference maximum and its sum;
+//   2. e, from the pieces that a row's keys were cut into;
+//   3. S^T = K Q^T, a token a thread: the sum over the flat rows;
+//   4. the tokens' pieces added to the running sums.
+//
+// Work of 1 and 3.  A job is a 128 x 128 product of one query block, as many whole queries of
+// a group as 128 rows hold, and one tile of 128 tokens, some of which the block sees.  A
+// unit is a query block (1) or a token tile (3) of one row and KV head and walks the jobs
+// that it takes part in; all jobs of all units in order are cut into one contiguous
+// range per block, one block an SM.  A unit inside one range is done by one block; the others
+// leave pieces, which are brought together in order.
+//
+// Warp roles (each walks the same jobs):
+//   warps 0-7   sums: warps w and w + 4 share 32 rows (TMEM lanes); each takes 64 columns;
+//   warp 8      copies: the unit's fixed tile (two buffers), the others through a ring of
+//               three, by TMA; K as one box of 16 to 128 tokens of a page each, its pool
+//               rows found through the block table;
+//   warp 9      products: one thread issues eight tcgen05.mma a job into one of four
+//               buffers of 128 columns;
+//   warps 10-13 (E4M3 pools) widen K's codes, exactly, into the operand tiles.
+// Every wait is bounded: a block that gives up flags the error, tells its other warps to stop,
+// and lets its copies and products in flight finish before it frees tensor memory.
+//
+// What is not seen (later tokens, table entries out of range, rows behind a query block's
+// queries) is left out of sums and maxima by selection, whatever its scores are.
+#include <math.h>
+
+#include "fp8_codec.cuh"
+#include "pkv_internal.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+namespace prompt {
+using namespace tc;
+
+constexpr int kTile = 128;
+constexpr int kSumWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 4;
+constexpr int kRing = 3;    // streamed tiles
+constexpr int kFixed = 2;   // a unit's fixed tiles
+constexpr int kRaw = 2;     // tiles of codes
+constexpr int kBufs = 4;    // products in tensor memory
+constexpr int kAhead = 8;   // jobs between the copies and the sums, at most (ring + products below that)
+constexpr int kMaxRows = 1024;
+constexpr uint32_t kHalf = kTile * 128;      // 128 rows x 64 dims
+constexpr uint32_t kOperand = 2 * kHalf;
+constexpr uint32_t kCodes = kTile * 128;     // 128 tokens of codes
+constexpr uint32_t kTmemCols = 512;
+constexpr int kCertain = 48;                 // columns of a half that are not asked whether a query has them
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMove = 16.f;                // a score this far above the reference moves it
+
+template <bool kFp8>
+__host__ __device__ constexpr int threads() { return (kConvWarp + (kFp8 ? kConvWarps : 0)) * 32; }
+
+struct Params {
+    float* weights;
+    const float* k_scale;
+    const int32_t* tables;
+    const int32_t* seq_lens;
+    const int32_t* q_start;
+    int64_t stride;
+    int rows, total, hk, group, bs, mbpr, nb, limit, window;
+    int nq;            // queries of a block
+    int kbox;          // tokens of a copy of K
+    int grid;
+    int most_units;    // query blocks that the workspace has room for
+    float scale_log2;
+    // workspace
+    int* head;         // [0]: query blocks, [1]: 1, or 0 where nothing may be done
+    int* tile_pre;     // [rows + 1]: token tiles of the rows before
+    int2* block_info;  // [query block]: first block that has a piece of it, pieces
+    int2* tile_info;   // [token tile]
+    float2* ml;        // [block + query block][128]: maxima and sums of the pieces
+    float* neg_lse;    // [query block][128]: -e
+    float* sums;       // [block + token tile][128]
+    int32_t* dev_err;
+};
+
+// The block whose range of the W jobs holds job j (block c's starts at c W / n).
+__device__ __forceinline__ int owner_of(int j, int W, int n) { return (int)((((int64_t)j + 1) * n - 1) / W); }
+
+// Rows as the walk needs them, in shared memory.
+struct Rows {
+    const int *len, *used, *end;  // tokens, queries that count, the index behind the last query
+    const int *jobs, *units;      // jobs and units of the rows before
+    const int* blocks;            // query blocks of the rows before
+    int nq;
+    __device__ __forceinline__ int query_blocks(int r) const { return (used[r] + nq - 1) / nq; }
+    __device__ __forceinline__ int tiles(int r) const { return used[r] ? (len[r] + kTile - 1) / kTile : 0; }
+    // Token tiles that query block m sees; the first query block that sees tile k.
+    __device__ __forceinline__ int seen(int r, int m) const {
+        return (len[r] - used[r] + min(used[r], (m + 1) * nq) - 1) / kTile + 1;
+    }
+    __device__ __forceinline__ int first(int r, int k) const {
+        const int i = k * kTile - (len[r] - used[r]);
+        return i > 0 ? i / nq : 0;
+    }
+};
+
+// A place in the jobs: the unit x (query block, or token tile where kSums) of row r and KV head
+// k, and the other tile s of [s0, n) that the unit walks.
+template <bool kSums>
+struct Walk {
+    int r, k, x, s, s0, n, left;
+    __device__ __forceinline__ void enter(const Rows& w) {
+        if (kSums) {
+            s0 = w.first(r, x);
+            n = w.query_blocks(r);
+        } else {
+            s0 = 0;
+            n = w.seen(r, x);
+        }
+        s = s0;
+    }
+    // On to the next job; true where that is another unit's.
+    __device__ __forceinline__ bool next(const Rows& w, int hk) {
+        --left;
+        if (++s < n) return false;
+        if (left <= 0) return true;
+        if (++x == (kSums ? w.tiles(r) : w.query_blocks(r))) {
+            x = 0;
+            if (++k == hk) {
+                k = 0;
+                do ++r; while (w.used[r] == 0);
+            }
+        }
+        enter(w);
+        return true;
+    }
+    __device__ __forceinline__ int block() const { return kSums ? s : x; }
+    __device__ __forceinline__ int tile() const { return kSums ? x : s; }
+    __device__ __forceinline__ int unit(const Rows& w) const {
+        return w.units[r] + k * (kSums ? w.tiles(r) : w.query_blocks(r)) + x;
+    }
+};
+
+// Shared memory, from a 1024-byte boundary on.
+template <bool kFp8>
+struct Smem {
+    static constexpr uint32_t fixed = 0;
+    static constexpr uint32_t ring = fixed + kFixed * kOperand;
+    static constexpr uint32_t raw = ring + kRing * kOperand;
+    // 1: one half's maxima and sums [kAhead][128] float2; 3: -e, and one half's sums, [kAhead][128] each
+    static constexpr uint32_t lse = raw + (kFp8 ? kRaw * kCodes : 0);
+    static constexpr uint32_t comb = lse + kAhead * kTile * 4;
+    static constexpr uint32_t bars = comb + kAhead * kTile * 4;
+    static constexpr uint32_t misc = bars + 64 * 8;                      // tmem address, start [8], stop, warp sums
+    static constexpr uint32_t bad = misc + 256;                          // [16] 16-token groups of K not to be seen
+    static constexpr uint32_t rows = bad + 64;                           // 6 x [rows + 1] ints
+    __host__ __device__ static constexpr uint32_t total(int n) { return rows + 6 * ((uint32_t)n + 1) * 4 + 1024; }
+};
+static_assert(Smem<true>::total(kMaxRows) <= 232448 && Smem<false>::total(kMaxRows) <= 232448, "shared memory per block");
+static_assert(kRing + kBufs + 1 <= kAhead, "entries of jobs that the sums still need are not overwritten");
+
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ float lane_value(const uint32_t (&a)[32], const uint32_t (&b)[32], int c) {
+    return __uint_as_float(c < 32 ? a[c] : b[c - 32]);
+}
+
+// Inclusive prefix over the warp's lanes, held at `most`.
+__device__ __forceinline__ int scan_most(int v, int most) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v = min(v, most - t) + t;  // both below most: no overflow
+    }
+    return v;
+}
+
+template <bool kFp8, bool kSums>
+__global__ void __launch_bounds__(threads<kFp8>(), 1)
+    tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
+                const __grid_constant__ Params p) {
+    using S = Smem<kFp8>;
+    constexpr int kThreads = threads<kFp8>(), kWarps = kThreads / 32, kMost = 1 << 30;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t bar_ffull = sbase + S::bars;             // [kFixed] the unit's tile is there
+    const uint32_t bar_ffree = bar_ffull + 8 * kFixed;      // [kFixed] its products are done
+    const uint32_t bar_rfull = bar_ffree + 8 * kFixed;      // [kRing]
+    const uint32_t bar_rfree = bar_rfull + 8 * kRing;       // [kRing]
+    const uint32_t bar_wfull = bar_rfree + 8 * kRing;       // [kRaw] codes are there
+    const uint32_t bar_wfree = bar_wfull + 8 * kRaw;        // [kRaw] and are widened
+    const uint32_t bar_lse = bar_wfree + 8 * kRaw;          // [kAhead] a job's -e are there
+    const uint32_t bar_done = bar_lse + 8 * kAhead;         // [kBufs] products are done
+    const uint32_t bar_read = bar_done + 8 * kBufs;         // [kBufs] and are read
+    const uint32_t bar_comb = bar_read + 8 * kBufs;         // [kAhead] one half's sums of a unit are there
+    const uint32_t bar_fin = bar_comb + 8 * kAhead;         // the last products are done
+    volatile int* misc = reinterpret_cast<volatile int*>(smem + S::misc);
+    const volatile int* stop = misc + 16;
+    volatile int* bad = reinterpret_cast<volatile int*>(smem + S::bad);
+    int* sm_rows = reinterpret_cast<int*>(smem + S::rows);
+    const int rows = p.rows, hk = p.hk, nq = p.nq;
+    int *sm_len = sm_rows, *sm_used = sm_len + rows + 1, *sm_end = sm_used + rows + 1, *sm_jobs = sm_end + rows + 1;
+    int *sm_blocks = sm_jobs + rows + 1, *sm_tiles = sm_blocks + rows + 1;
+    Rows w;
+    w.len = sm_len;
+    w.used = sm_used;
+    w.end = sm_end;
+    w.jobs = sm_jobs;
+    w.units = kSums ? sm_tiles : sm_blocks;
+    w.blocks = sm_blocks;
+    w.nq = nq;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kFixed; ++i) {
+            mbar_init(bar_ffull + 8 * i, kFp8 && kSums ? kConvWarps : 1);
+            mbar_init(bar_ffree + 8 * i, 1);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(bar_rfull + 8 * i, kFp8 && !kSums ? kConvWarps : 1);
+            mbar_init(bar_rfree + 8 * i, 1);
+        }
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(bar_wfull + 8 * i, 1);
+            mbar_init(bar_wfree + 8 * i, kConvWarps);
+        }
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(bar_lse + 8 * i, 1);
+            mbar_init(bar_comb + 8 * i, kSumWarps / 2);
+        }
+        for (int i = 0; i < kBufs; ++i) {
+            mbar_init(bar_done + 8 * i, 2);  // the products, and the thread that issued them
+            mbar_init(bar_read + 8 * i, kSumWarps);
+        }
+        mbar_init(bar_fin, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        misc[16] = 0;
+    }
+    if (warp == kCopyWarp && lane < 2)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane ? &qmap : &kmap)) : "memory");
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sbase + S::misc),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    // Rows of the query operands that no copy writes hold zeros.
+    for (int i = tid; i < (kSums ? kRing : kFixed) * 2 * (kTile - nq * p.group) * 8; i += kThreads) {
+        const int per = (kTile - nq * p.group) * 8, half = i / per, c = i - half * per;
+        sts16(sbase + (kSums ? S::ring : S::fixed) + half * kHalf + nq * p.group * 128 + c * 16, make_uint4(0, 0, 0, 0));
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    griddep_wait();
+
+    // ---- the rows: lengths, then jobs, query blocks and token tiles and their prefixes ----
+    for (int r = tid; r < rows; r += kThreads) {
+        const int q0 = p.q_start[r], q1 = p.q_start[r + 1], C = q1 - q0, L = p.seq_lens[r];
+        const bool wrong = q0 < 0 || q1 < q0 || q1 > p.total || L < C || L > p.limit;
+        if (wrong && blockIdx.x == 0 && !kSums) flag_error(p.dev_err, PKV_DEV_ERR_SEQ_LEN);
+        sm_len[r] = wrong ? 0 : L;
+        sm_used[r] = wrong ? 0 : min(C, p.window);
+        sm_end[r] = q1;
+    }
+    __syncthreads();
+    for (int r = warp; r < rows; r += kWarps) {  // a warp a row: the jobs of its query blocks
+        const int nm = w.query_blocks(r);
+        int sum = 0;
+        for (int m = lane; m < nm; m += 32) sum += w.seen(r, m);
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == 0) {
+            sm_jobs[r] = (int)min((int64_t)kMost, (int64_t)sum * hk);
+            sm_blocks[r] = (int)min((int64_t)kMost, (int64_t)nm * hk);
+            sm_tiles[r] = (int)min((int64_t)kMost, (int64_t)w.tiles(r) * hk);
+        }
+    }
+    __syncthreads();
+    if (warp < 3) {  // exclusive prefixes in place, a warp an array
+        int* a = warp == 0 ? sm_jobs : warp == 1 ? sm_blocks : sm_tiles;
+        int run = 0;
+        for (int r0 = 0; r0 < rows; r0 += 32) {
+            const int v = r0 + lane < rows ? a[r0 + lane] : 0;
+            const int incl = scan_most(v, kMost), last = __shfl_sync(0xffffffffu, incl, 31);
+            if (r0 + lane < rows) a[r0 + lane] = min(incl - v, kMost - run) + run;
+            run = min(last, kMost - run) + run;
+        }
+        if (lane == 0) a[rows] = run;
+    }
+    __syncthreads();
+    // Rows that overlap may have more blocks than there is room for: nothing is done.
+    const bool fits = sm_blocks[rows] <= p.most_units && sm_jobs[rows] < kMost && sm_tiles[rows] < kMost;
+    if (blockIdx.x == 0 && !kSums) {
+        if (tid == 0) {
+            if (!fits) flag_error(p.dev_err, PKV_DEV_ERR_SEQ_LEN);
+            p.head[0] = fits ? sm_blocks[rows] : 0;
+            p.head[1] = fits;
+        }
+        for (int r = tid; r <= rows; r += kThreads) p.tile_pre[r] = sm_tiles[r];
+    }
+    const int W = fits ? sm_jobs[rows] : 0, grid = min(W, p.grid), cta = blockIdx.x;
+    const bool idle = cta >= grid;
+    const int j0 = idle ? 0 : (int)((int64_t)W * cta / grid), j1 = idle ? 0 : (int)((int64_t)W * (cta + 1) / grid);
+    if (!idle && warp == 0) {
+        // the unit that job j0 is in
+        int lo = 0, hi = rows - 1;
+        while (lo < hi) {  // the last row whose jobs start at or before j0
+            const int mid = (lo + hi + 1) >> 1;
+            if (sm_jobs[mid] <= j0) lo = mid; else hi = mid - 1;
+        }
+        const int r = lo, per_head = (sm_jobs[r + 1] - sm_jobs[r]) / hk, k = (j0 - sm_jobs[r]) / per_head;
+        const int off = j0 - sm_jobs[r] - k * per_head, units = kSums ? w.tiles(r) : w.query_blocks(r);
+        int run = 0, x = 0, before = 0;
+        for (int x0 = 0; x0 < units; x0 += 32) {
+            const int y = x0 + lane;
+            const int v = y < units ? (kSums ? w.query_blocks(r) - w.first(r, y) : w.seen(r, y)) : 0;
+            const int incl = scan_most(v, kMost);
+            const unsigned over = __ballot_sync(0xffffffffu, run + incl > off);
+            if (over) {
+                const int l = __ffs(over) - 1;
+                x = x0 + l;
+                before = run + __shfl_sync(0xffffffffu, incl - v, l);
+                break;
+            }
+            run += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) {
+            misc[4] = r;
+            misc[5] = k;
+            misc[6] = x;
+            misc[7] = off - before;  // jobs of the unit before j0
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<uint32_t*>(smem + S::misc);
+    auto give_up = [&] {
+        misc[16] = 1;
+        flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+    };
+    Walk<kSums> at;
+    if (!idle) {
+        at.r = misc[4];
+        at.k = misc[5];
+        at.x = misc[6];
+        at.enter(w);
+        at.s += misc[7];
+    }
+    at.left = j1 - j0;
+
+    if (idle) {
+        // nothing to do but the release below
+    } else if (warp == kCopyWarp) {
+        // ============================ copies ============================
+        bool ok = true, fresh = true;
+        int units = 0, jobs = 0, codes = 0;  // fixed tiles, streamed tiles and tiles of codes so far
+        Walk<kSums> c = at, ahead = at;      // `ahead`: where K is copied for next
+        const int boxes = kTile / p.kbox;
+        auto entry = [&]() -> int {          // the table entry of this lane's box there
+            const int t = ahead.tile() * kTile + lane * p.kbox;
+            if (ahead.left <= 0 || lane >= boxes || t >= w.len[ahead.r]) return 0;
+            return p.tables[(int64_t)ahead.r * p.mbpr + t / p.bs];
+        };
+        int pb = entry();
+        // K's tile to `dst`, counted at `full`; its groups that are not to be seen to `note`.
+        auto copy_k = [&](uint32_t dst, uint32_t full, int note) {
+            const int t = c.tile() * kTile + lane * p.kbox, at_bs = t % p.bs;
+            bool there = lane < boxes && t < w.len[c.r];
+            uint32_t lost = 0;
+            if (there && (pb < 0 || pb >= p.nb)) {
+                flag_error(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
+                lost = ((1u << (p.kbox / 16)) - 1) << (lane * p.kbox / 16);
+                there = false;
+            }
+            lost = __reduce_or_sync(0xffffffffu, lost);
+            const uint32_t bytes = (uint32_t)p.kbox * 128;
+            const int n = __popc(__ballot_sync(0xffffffffu, there));
+            if (lane == 0) {
+                bad[note & 15] = (int)lost;
+                mbar_arrive_expect_tx(full, (uint32_t)n * bytes * (kFp8 ? 1 : 2));
+            }
+            __syncwarp();
+            if (there) {
+                const int row = pb * p.bs + at_bs;
+                tma_load_3d(dst + lane * bytes, &kmap, 0, c.k, row, full);
+                if (!kFp8) tma_load_3d(dst + kHalf + lane * bytes, &kmap, 64, c.k, row, full);
+            }
+            if (kSums) {  // on to the next unit
+                ahead.left -= ahead.n - ahead.s - 1;
+                ahead.s = ahead.n - 1;
+            }
+            ahead.next(w, hk);
+            pb = entry();
+        };
+        auto copy_q = [&](uint32_t dst, uint32_t full) {
+            if (lane == 0) {
+                const int q = w.end[c.r] - w.used[c.r] + c.block() * nq;
+                mbar_arrive_expect_tx(full, (uint32_t)(nq * p.group) * 256u);
+                tma_load_3d(dst, &qmap, 0, c.k * p.group, q, full);
+                tma_load_3d(dst + kHalf, &qmap, 64, c.k * p.group, q, full);
+            }
+            __syncwarp();
+        };
+        auto copy_codes = [&](int note) {
+            const int s = codes % kRaw;
+            if (codes >= kRaw && !mbar_waitw(bar_wfree + 8 * s, (uint32_t)(codes / kRaw - 1) & 1, stop)) return false;
+            copy_k(sbase + S::raw + s * kCodes, bar_wfull + 8 * s, note);
+            ++codes;
+            return true;
+        };
+        while (c.left > 0) {
+            if (fresh) {
+                const int f = units % kFixed;
+                if (kSums && kFp8) {
+                    if (!(ok = copy_codes(units))) break;
+                } else {
+                    if (units >= kFixed && !(ok = mbar_waitw(bar_ffree + 8 * f, (uint32_t)(units / kFixed - 1) & 1, stop)))
+                        break;
+                    const uint32_t dst = sbase + S::fixed + f * kOperand;
+                    if (kSums)
+                        copy_k(dst, bar_ffull + 8 * f, units);
+                    else
+                        copy_q(dst, bar_ffull + 8 * f);
+                }
+                ++units;
+            }
+            const int s = jobs % kRing;
+            if (!kSums && kFp8) {
+                if (!(ok = copy_codes(jobs))) break;
+            } else {
+                if (jobs >= kRing && !(ok = mbar_waitw(bar_rfree + 8 * s, (uint32_t)(jobs / kRing - 1) & 1, stop))) break;
+                const uint32_t dst = sbase + S::ring + s * kOperand;
+                if (kSums) {
+                    copy_q(dst, bar_rfull + 8 * s);
+                    if (lane == 0) {
+                        const int e = jobs % kAhead, b = w.blocks[c.r] + c.k * w.query_blocks(c.r) + c.s;
+                        mbar_arrive_expect_tx(bar_lse + 8 * e, kTile * 4);
+                        bulk_load(sbase + S::lse + e * kTile * 4, p.neg_lse + (int64_t)b * kTile, kTile * 4, bar_lse + 8 * e);
+                    }
+                    __syncwarp();
+                } else {
+                    copy_k(dst, bar_rfull + 8 * s, jobs);
+                }
+            }
+            ++jobs;
+            fresh = c.next(w, hk);
+        }
+        if (lane == 0) {
+            if (!ok) give_up();
+            // every copy has landed before the block exits
+            auto drain = [&](uint32_t bar, int n, int count) {
+                for (int i = max(0, n - count); i < n; ++i) mbar_drain1(bar + 8 * (i % count), (uint32_t)(i / count) & 1);
+            };
+            if (!(kSums && kFp8)) drain(bar_ffull, units, kFixed);
+            if (kSums || !kFp8) drain(bar_rfull, jobs, kRing);
+            if (kFp8) drain(bar_wfull, codes, kRaw);
+            if (kSums) drain(bar_lse, jobs, kAhead);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ============================ products ============================
+        if (lane == 0) {
+            const uint32_t id = idesc(kTile, kTile, 0);
+            const uint64_t a0 = sdesc(sbase + S::fixed, 16, 1024), b0 = sdesc(sbase + S::ring, 16, 1024);
+            bool ok = true, fresh = true;
+            int units = 0, jobs = 0;
+            Walk<kSums> c = at;
+            while (c.left > 0) {
+                if (fresh) {
+                    if (!(ok = mbar_wait1(bar_ffull + 8 * (units % kFixed), (uint32_t)(units / kFixed) & 1, stop))) break;
+                    ++units;
+                }
+                const int s = jobs % kRing, b = jobs % kBufs, f = (units - 1) % kFixed;
+                if (!(ok = mbar_wait1(bar_rfull + 8 * s, (uint32_t)(jobs / kRing) & 1, stop))) break;
+                if (jobs >= kBufs && !(ok = mbar_wait1(bar_read + 8 * b, (uint32_t)(jobs / kBufs - 1) & 1, stop))) break;
+                tc_fence_after();
+                const uint64_t da = a0 + (uint64_t)(f * (kOperand >> 4)), db = b0 + (uint64_t)(s * (kOperand >> 4));
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                    umma_ss(tmem + b * kTile, da + off, db + off, id, ks > 0);
+                }
+                mbar_arrive(bar_done + 8 * b);  // (what this thread has seen, the sums see too)
+                umma_commit(bar_done + 8 * b);
+                umma_commit(bar_rfree + 8 * s);
+                ++jobs;
+                fresh = c.next(w, hk);
+                if (fresh) umma_commit(bar_ffree + 8 * f);
+            }
+            if (!ok) give_up();
+            umma_commit(bar_fin);
+            if (!mbar_drain1(bar_fin, 0)) flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (kFp8 && warp >= kConvWarp) {
+        // ============================ widening ============================
+        bool ok = true, fresh = true;
+        int units = 0, jobs = 0, codes = 0;
+        Walk<kSums> c = at;
+        const int row = tid - kConvWarp * 32;  // a token a thread
+        while (c.left > 0 && ok) {
+            if (!kSums || fresh) {
+                const int n = kSums ? units : jobs, count = kSums ? kFixed : kRing, to = n % count, from = codes % kRaw;
+                const uint32_t full = (kSums ? bar_ffull : bar_rfull) + 8 * to;
+                const uint32_t free = (kSums ? bar_ffree : bar_rfree) + 8 * to;
+                if (!(ok = mbar_waitw(bar_wfull + 8 * from, (uint32_t)(codes / kRaw) & 1, stop))) break;
+                if (n >= count && !(ok = mbar_waitw(free, (uint32_t)(n / count - 1) & 1, stop))) break;
+                const uint32_t src = sbase + S::raw + from * kCodes + row * 128;
+                const uint32_t dst = sbase + (kSums ? S::fixed : S::ring) + to * kOperand + row * 128;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 x = lds16(src + ((i ^ (row & 7)) << 4));
+                    const uint32_t o = dst + (i >> 2) * kHalf;
+                    sts16(o + (((2 * i & 7) ^ (row & 7)) << 4), widen8(make_uint2(x.x, x.y)));
+                    sts16(o + (((2 * i + 1 & 7) ^ (row & 7)) << 4), widen8(make_uint2(x.z, x.w)));
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(full);
+                    mbar_arrive(bar_wfree + 8 * from);
+                }
+                ++codes;
+            }
+            if (fresh) ++units;
+            ++jobs;
+            fresh = c.next(w, hk);
+        }
+        if (!ok && lane == 0) give_up();
+    } else if (warp < kSumWarps) {
+        // ============================ sums ============================
+        const int i = (warp & 3) * 32 + lane, hf = warp >> 2;  // row of the product; its half of the columns
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        bool ok = true, fresh = true;
+        int units = 0, jobs = 0, from = 0;
+        Walk<kSums> c = at;
+        const int group = p.group;
+        float ref = 0.f, sl2 = 0.f, acc = 0.f;  // acc: the row's sum; ref: what exponents are taken from
+        uint32_t hidden = 0;
+        while (c.left > 0) {
+            const int b = jobs % kBufs, e = jobs % kAhead;
+            if (fresh) {
+                ref = -INFINITY;
+                acc = 0.f;
+                sl2 = kFp8 ? p.scale_log2 * p.k_scale[c.k] : p.scale_log2;
+                from = c.s;
+                ++units;
+            }
+            if (!(ok = mbar_waitw(bar_done + 8 * b, (uint32_t)(jobs / kBufs) & 1, stop))) break;
+            if (kSums && !(ok = mbar_waitw(bar_lse + 8 * e, (uint32_t)(jobs / kAhead) & 1, stop))) break;
+            tc_fence_after();
+            uint32_t v[32], u[32];
+            tmem_ld64(tmem + lanes + b * kTile + hf * 64, v, u);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_read + 8 * b);
+            hidden = (uint32_t)bad[(kSums ? units - 1 : jobs) & 15];
+            // Positions: query q of the row's used ones sees tokens up to p0 + q.
+            const int p0 = w.len[c.r] - w.used[c.r], q0 = c.block() * nq, t0 = c.tile() * kTile;
+            const int here = min(nq, w.used[c.r] - q0);  // queries of the block
+            const bool plain = t0 + kTile - 1 <= p0 + q0 && here == nq && !hidden;
+            const uint64_t sl = f32x2(sl2, sl2);
+            if (!kSums) {
+                // row i: query i / group; column: token
+                const int q = i / group, last = q < here ? p0 + q0 + q - t0 - hf * 64 : -1;  // last column it sees
+                uint64_t seen = last < 0 ? 0ull : last >= 63 ? ~0ull : (2ull << last) - 1;
+                if (hidden)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        if (hidden >> (4 * hf + g) & 1) seen &= ~(0xffffull << (16 * g));
+                float top = -INFINITY;  // the largest score, in base 2
+                if (plain) {
+                    float a = __uint_as_float(v[0]), z = a;
+                    if (sl2 >= 0.f) {
+#pragma unroll
+                        for (int x = 0; x < 64; x += 4) {
+                            a = fmaxf(fmaxf(lane_value(v, u, x), lane_value(v, u, x + 1)), a);
+                            z = fmaxf(fmaxf(lane_value(v, u, x + 2), lane_value(v, u, x + 3)), z);
+                        }
+                        top = fmaxf(a, z) * sl2;
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 64; x += 4) {
+                            a = fminf(fminf(lane_value(v, u, x), lane_value(v, u, x + 1)), a);
+                            z = fminf(fminf(lane_value(v, u, x + 2), lane_value(v, u, x + 3)), z);
+                        }
+                        top = fminf(a, z) * sl2;
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 64; ++x)
+                        if (seen >> x & 1) top = fmaxf(top, lane_value(v, u, x) * sl2);
+                }
+                if (top > ref + kMove || ref == -INFINITY) {
+                    if (top > -INFINITY) {
+                        acc *= ref == -INFINITY ? 1.f : fast_exp2(ref - top);
+                        ref = top;
+                    }
+                }
+                const float base = ref == -INFINITY ? 0.f : -ref;
+                if (plain) {
+                    const uint64_t nr = f32x2(base, base);
+                    uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
+#pragma unroll
+                    for (int x = 0; x < 64; x += 4) {
+                        float a, z;
+                        f32x2_split(fma_f32x2(f32x2(lane_value(v, u, x), lane_value(v, u, x + 1)), sl, nr), a, z);
+                        s0 = add_f32x2(s0, f32x2(fast_exp2(a), fast_exp2(z)));
+                        f32x2_split(fma_f32x2(f32x2(lane_value(v, u, x + 2), lane_value(v, u, x + 3)), sl, nr), a, z);
+                        s1 = add_f32x2(s1, f32x2(fast_exp2(a), fast_exp2(z)));
+                    }
+                    float a, z;
+                    f32x2_split(add_f32x2(s0, s1), a, z);
+                    acc += a + z;
+                } else {
+                    float s = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 64; ++x)
+                        if (seen >> x & 1) s += fast_exp2(fmaf(lane_value(v, u, x), sl2, base));
+                    acc += s;
+                }
+            } else {
+                // row i: token t0 + i; column: flat row, query column / group
+                const float4* lse = reinterpret_cast<const float4*>(smem + S::lse + e * kTile * 4) + hf * 16;
+                const int full = nq * group - hf * 64;  // columns that queries have; few blocks have no others
+                if (plain && full >= kCertain) {
+                    uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
+#pragma unroll
+                    for (int x = 0; x < 64; x += 4) {
+                        const float4 y = lse[x / 4];
+                        float a, z, c2, z2;
+                        f32x2_split(fma_f32x2(f32x2(lane_value(v, u, x), lane_value(v, u, x + 1)), sl, f32x2(y.x, y.y)), a, z);
+                        f32x2_split(fma_f32x2(f32x2(lane_value(v, u, x + 2), lane_value(v, u, x + 3)), sl, f32x2(y.z, y.w)), c2, z2);
+                        if (x >= kCertain) {  // zeros times a key that is no number
+                            a = x < full ? a : -INFINITY;
+                            z = x + 1 < full ? z : -INFINITY;
+                            c2 = x + 2 < full ? c2 : -INFINITY;
+                            z2 = x + 3 < full ? z2 : -INFINITY;
+                        }
+                        s0 = add_f32x2(s0, f32x2(fast_exp2(a), fast_exp2(z)));
+                        s1 = add_f32x2(s1, f32x2(fast_exp2(c2), fast_exp2(z2)));
+                    }
+                    float a, z;
+                    f32x2_split(add_f32x2(s0, s1), a, z);
+                    acc += a + z;
+                } else {
+                    const int q = max(0, t0 + i - p0 - q0);  // the first query of the block that sees the token
+                    const int lo = min(128, q * group) - hf * 64, hi = here * group - hf * 64;
+                    uint64_t seen = hi <= 0 ? 0ull : hi >= 64 ? ~0ull : (1ull << hi) - 1;
+                    if (lo > 0) seen &= lo >= 64 ? 0ull : ~0ull << lo;
+                    if (hidden >> (i >> 4) & 1) seen = 0;
+                    float s = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) {
+                        const float y = reinterpret_cast<const float*>(lse)[x];
+                        if (seen >> x & 1) s += fast_exp2(fmaf(lane_value(v, u, x), sl2, y));
+                    }
+                    acc += s;
+                }
+            }
+            ++jobs;
+            const Walk<kSums> was = c;
+            fresh = c.next(w, hk);
+            if (!fresh) {
+                if (c.left > 0) continue;
+            }
+            // ---- the block's piece of the unit: both halves (at most kBufs + 1 units apart) ----
+            const int u8 = (units - 1) % kAhead;
+            float* one = reinterpret_cast<float*>(smem + S::comb) + u8 * kTile;
+            float2* two = reinterpret_cast<float2*>(smem + S::lse) + u8 * kTile;
+            if (hf == 1) {
+                if (kSums)
+                    one[i] = acc;
+                else
+                    two[i] = make_float2(ref, acc);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_comb + 8 * u8);
+            } else {
+                if (!(ok = mbar_waitw(bar_comb + 8 * u8, (uint32_t)((units - 1) / kAhead) & 1, stop))) break;
+                const int unit = was.unit(w);
+                const int64_t rec = (int64_t)cta + unit;
+                if (kSums) {
+                    p.sums[rec * kTile + i] = acc + one[i];
+                } else {
+                    const float2 o = two[i];
+                    const float M = fmaxf(ref, o.x), g = M == -INFINITY ? 0.f : M;
+                    p.ml[rec * kTile + i] = make_float2(M, acc * fast_exp2(ref - g) + o.y * fast_exp2(o.x - g));
+                }
+                if (i == 0 && from == was.s0) {
+                    // this block has the unit's first job: who has its last
+                    const int first = j0 + jobs - 1 - (was.s - was.s0);
+                    (kSums ? p.tile_info : p.block_info)[unit] =
+                        make_int2(cta, owner_of(first + was.n - was.s0 - 1, W, grid) - cta + 1);
+                }
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    }
+
+    // ---- release tensor memory ----
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    }
+}
+
+// 2: a query block's -e from its pieces, in order; -inf for rows that no query has or that see nothing.
+__global__ void __launch_bounds__(kTile) lse_kernel(const __grid_constant__ Params p) {
+    const int unit = (int)blockIdx.x, i = (int)threadIdx.x;
+    griddep_wait();
+    if (unit >= p.head[0]) return;
+    const int2 at = p.block_info[unit];
+    float M = -INFINITY, L = 0.f;
+    // (a call that timed out may have left anything there)
+    if (i < p.nq * p.group && at.x >= 0 && at.x < p.grid && at.y > 0 && at.y <= p.grid - at.x) {
+        const float2* ml = p.ml + ((int64_t)at.x + unit) * kTile + i;
+#pragma unroll 4
+        for (int c = 0; c < at.y; ++c) {
+            const float2 y = ml[(int64_t)c * kTile];
+            const float N = fmaxf(M, y.x), g = N == -INFINITY ? 0.f : N;
+            L = L * fast_exp2(M - g) + y.y * fast_exp2(y.x - g);
+            M = N;
+        }
+    }
+    p.neg_lse[(int64_t)unit * kTile + i] = L == 0.f ? -INFINITY : -((M == -INFINITY ? 0.f : M) + log2f(L));
+}
+
+// 4: a token's sum over its pieces, in order, added to the running sum; the chunk's own tokens
+// start from zero.
+constexpr int kEndThreads = 256;
+__global__ void __launch_bounds__(kEndThreads) add_kernel(const __grid_constant__ Params p) {
+    const int k = (int)blockIdx.x, r = (int)blockIdx.y, t = (int)(blockIdx.z * kEndThreads + threadIdx.x);
+    griddep_wait();
+    if (!p.head[1]) return;
+    const int tiles = (p.tile_pre[r + 1] - p.tile_pre[r]) / p.hk;  // 0 for rows without queries
+    const int L = p.seq_lens[r], C = p.q_start[r + 1] - p.q_start[r], tile = t / kTile;
+    if (tile >= tiles || t >= L) return;
+    const int unit = p.tile_pre[r] + k * tiles + tile;
+    float* w = p.weights + ((int64_t)r * p.hk + k) * p.stride + t;
+    const float was = t < L - C ? *w : 0.f;
+    const int2 at = p.tile_info[unit];
+    float sum = 0.f;
+    if (at.x >= 0 && at.x < p.grid && at.y > 0 && at.y <= p.grid - at.x) {
+        const float* s = p.sums + ((int64_t)at.x + unit) * kTile + t % kTile;
+#pragma unroll 4
+        for (int c = 0; c < at.y; ++c) sum += s[(int64_t)c * kTile];
+    }
+    *w = was + sum;
+}
+
+struct Layout {
+    size_t tile_pre, block_info, tile_info, ml, neg_lse, sums, bytes;
+    int64_t blocks, tiles;
+    int nq;
+};
+// Query blocks of rows whose chunks do not overlap.
+static int64_t most_blocks(int rows, int total, int kv_heads, int nq, int window) {
+    const int64_t all = (int64_t)total / nq + rows, some = (int64_t)rows * (((int64_t)window + nq - 1) / nq);
+    return (all < some ? all : some) * kv_heads;
+}
+static Layout layout(int rows, int total, int kv_heads, int group, int max_seq_len, int window, int sms) {
+    Layout l;
+    l.nq = kTile / group;
+    l.blocks = most_blocks(rows, total, kv_heads, l.nq, window);
+    l.tiles = (int64_t)rows * kv_heads * (((int64_t)max_seq_len + kTile - 1) / kTile);
+    size_t at = 256;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += align_up(bytes, 256);
+        return here;
+    };
+    l.tile_pre = take(((size_t)rows + 1) * 4);
+    l.block_info = take((size_t)l.blocks * 8);
+    l.tile_info = take((size_t)l.tiles * 8);
+    l.ml = take((size_t)(l.blocks + sms) * kTile * 8);
+    l.neg_lse = take((size_t)l.blocks * kTile * 4);
+    l.sums = take((size_t)(l.tiles + sms) * kTile * 4);
+    l.bytes = at;
+    return l;
+}
+static bool supported(int rows, int total, int q_heads, int kv_heads, int head_dim, int max_seq_len, int block_size,
+                      int window) {
+    if (head_dim != kHeadDim || block_size % 16 || rows > kMaxRows || q_heads / kv_heads > kTile ||
+        max_seq_len > (1 << 23) || kv_heads > 65535)
+        return false;
+    const int nq = kTile / (q_heads / kv_heads);
+    const int64_t tiles = ((int64_t)max_seq_len + kTile - 1) / kTile;
+    const int64_t blocks = most_blocks(rows, total, kv_heads, nq, window);
+    return blocks < (int64_t(1) << 30) && (tiles == 0 || blocks < (int64_t(1) << 30) / tiles) &&
+           (int64_t)rows * kv_heads * tiles < (int64_t(1) << 30);
+}
+
+}  // namespace prompt
+}  // namespace pkv
+
+extern "C" size_t paged_attention_prefill_weights_workspace_size(int rows, int total_q, int q_heads, int kv_heads,
+                                                                 int head_dim, int max_seq_len, int block_size,
+                                                                 int window) {
+    using namespace pkv::prompt;
+    if (rows <= 0 || total_q < 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || q_heads % kv_heads ||
+        max_seq_len < 0 || block_size <= 0 || window < 1 ||
+        !supported(rows, total_q, q_heads, kv_heads, head_dim, max_seq_len, block_size, window))
+        return 0;
+    const int sms = pkv::device_sms();  // on a machine without a GPU, as for one of 256 SMs
+    return layout(rows, total_q, kv_heads, q_heads / kv_heads, max_seq_len, window, sms > 0 ? sms : 256).bytes;
+}
+
+extern "C" int paged_attention_prefill_weights(float* weights, const void* q, const void* k_pool, const float* k_scale,
+                                               const int32_t* block_tables, const int32_t* seq_lens,
+                                               const int32_t* q_start, int rows, int total_q, int q_heads,
+                                               int kv_heads, int head_dim, int block_size, float scale, int window,
+                                               int max_blocks_per_row, int num_blocks, int max_seq_len,
+                                               int64_t weights_stride, void* workspace, size_t workspace_bytes,
+                                               int32_t* dev_err, cudaStream_t stream) {
+    using namespace pkv;
+    using namespace pkv::prompt;
+    if (q_heads <= 0 || kv_heads <= 0 || head_dim <= 0 || q_heads % kv_heads) return PKV_ERR_INVALID_ARG;
+    if (rows < 0 || total_q < 0 || block_size <= 0 || max_blocks_per_row <= 0 || num_blocks <= 0 || max_seq_len < 0 ||
+        !isfinite(scale) || window < 1 || weights_stride < max_seq_len)
+        return PKV_ERR_INVALID_ARG;
+    if ((int64_t)max_seq_len > (int64_t)max_blocks_per_row * block_size) return PKV_ERR_INVALID_ARG;
+    if (!supported(rows, total_q, q_heads, kv_heads, head_dim, max_seq_len, block_size, window) ||
+        weights_stride > (int64_t(1) << 40) || (int64_t)num_blocks * block_size >= (int64_t(1) << 31))
+        return PKV_ERR_UNSUPPORTED;
+    if (rows == 0 || total_q == 0) return PKV_OK;
+    if (!weights || !q || !k_pool || !block_tables || !seq_lens || !q_start) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_pool)) return PKV_ERR_INVALID_ARG;
+    const int sms = device_sms();
+    if (sms <= 0) return PKV_ERR_CUDA;
+    const int group = q_heads / kv_heads;
+    const Layout l = layout(rows, total_q, kv_heads, group, max_seq_len, window, sms);
+    if (!workspace || workspace_bytes < l.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return PKV_ERR_WORKSPACE;
+    const size_t wide = (size_t)rows * kv_heads * weights_stride * 4, tall = (size_t)total_q * q_heads * head_dim * 2;
+    if (overlap(weights, wide, q, tall) || overlap(weights, wide, workspace, l.bytes) ||
+        overlap(q, tall, workspace, l.bytes))
+        return PKV_ERR_INVALID_ARG;
+
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    Params p{};
+    p.weights = weights;
+    p.k_scale = k_scale;
+    p.tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.q_start = q_start;
+    p.stride = weights_stride;
+    p.rows = rows;
+    p.total = total_q;
+    p.hk = kv_heads;
+    p.group = group;
+    p.bs = block_size;
+    p.mbpr = max_blocks_per_row;
+    p.nb = num_blocks;
+    p.limit = max_seq_len;
+    p.window = window;
+    p.nq = l.nq;
+    p.kbox = 16;
+    while (p.kbox < kTile && block_size % (2 * p.kbox) == 0) p.kbox *= 2;
+    p.grid = sms;
+    p.most_units = (int)l.blocks;
+    p.scale_log2 = scale * kLog2e;
+    p.head = reinterpret_cast<int*>(ws);
+    p.tile_pre = reinterpret_cast<int*>(ws + l.tile_pre);
+    p.block_info = reinterpret_cast<int2*>(ws + l.block_info);
+    p.tile_info = reinterpret_cast<int2*>(ws + l.tile_info);
+    p.ml = reinterpret_cast<float2*>(ws + l.ml);
+    p.neg_lse = reinterpret_cast<float*>(ws + l.neg_lse);
+    p.sums = reinterpret_cast<float*>(ws + l.sums);
+    p.dev_err = dev_err;
+    if (l.blocks == 0 || max_seq_len == 0) return PKV_OK;
+
+    CUtensorMap kmap, qmap;
+    const int elt = k_scale ? 1 : 2;
+    const int64_t kdims[3] = {head_dim, kv_heads, (int64_t)num_blocks * block_size};
+    const int64_t kstrides[2] = {(int64_t)head_dim * elt, (int64_t)kv_heads * head_dim * elt};
+    const int kb[3] = {128 / elt, 1, p.kbox};
+    int st = tiled_map_3d(k_pool, k_scale ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, kdims,
+                          kstrides, kb, &kmap);
+    if (st != PKV_OK) return st;
+    const int64_t qdims[3] = {head_dim, q_heads, total_q};
+    const int64_t qstrides[2] = {(int64_t)head_dim * 2, (int64_t)q_heads * head_dim * 2};
+    const int qb[3] = {64, group, p.nq};
+    if ((st = tiled_map_3d(q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, qdims, qstrides, qb, &qmap)) != PKV_OK) return st;
+    auto* first = k_scale ? tile_kernel<true, false> : tile_kernel<false, false>;
+    auto* second = k_scale ? tile_kernel<true, true> : tile_kernel<false, true>;
+    const int most = (int)(k_scale ? Smem<true>::total(kMaxRows) : Smem<false>::total(kMaxRows));
+    const size_t smem = k_scale ? Smem<true>::total(rows) : Smem<false>::total(rows);
+    const unsigned block = (unsigned)(k_scale ? threads<true>() : threads<false>());
+    if (cudaFuncSetAttribute(first, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+        cudaFuncSetAttribute(second, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) {
+        cudaGetLastError();
+        return PKV_ERR_CUDA;
+    }
+    if ((st = launch_early(first, (unsigned)p.grid, block, smem, stream, kmap, qmap, p)) != PKV_OK) return st;
+    if ((st = launch_early(lse_kernel, (unsigned)l.blocks, kTile, 0, stream, p)) != PKV_OK) return st;
+    if ((st = launch_early(second, (unsigned)p.grid, block, smem, stream, kmap, qmap, p)) != PKV_OK) return st;
+    const unsigned z = (unsigned)((max_seq_len + kEndThreads - 1) / kEndThreads);
+    return launch_early(add_kernel, dim3((unsigned)kv_heads, (unsigned)rows, z), kEndThreads, 0, stream, p);
+}

@@ -1,7 +1,8 @@
 // Python binding of the drafted step's calls (paged_kv_rope_append,
 // paged_attention_tree, paged_kv_tree_commit) and of those of a cache within a
 // budget (paged_kv_norm_rope_append, paged_attention_decode_weights,
-// paged_kv_evict): argument checks and marshalling only, as in ops.py, in C++.
+// paged_attention_prefill_weights, paged_kv_evict): argument checks and marshalling
+// only, as in ops.py, in C++.
 //
 // Each of these calls takes a dozen tensors, and checking and unpacking them
 // from Python through ctypes took 22 to 30 us a call on the Grace cores, ten
@@ -360,6 +361,37 @@ PyObject* decode_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+PyObject* prefill_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded("prefill_weights", n, 13, [&]() -> int {
+        Call c;
+        const at::Tensor& q = c.need(a[1], "q", at::kHalf, 3);
+        const bool fp8 = a[10] != Py_None;
+        const at::Tensor& k = c.need(a[2], "k_pool", fp8 ? at::kByte : at::kHalf, 4);
+        const int64_t hk = k.size(2), d = k.size(3);
+        if (d != q.size(2))
+            fail(PyExc_ValueError, "q has head_dim " + std::to_string(q.size(2)) + ", the pool " + std::to_string(d));
+        const float* ks = nullptr;
+        if (fp8) {
+            const at::Tensor& x = c.need(a[10], "k_scale", at::kFloat, 1);
+            need_shape(x, "k_scale", {hk});
+            ks = static_cast<const float*>(x.data_ptr());
+        }
+        const Rows r = need_rows(c, a[3], a[4], a[5]);
+        int64_t stride = 0;
+        float* w = need_weights(c, a[0], r.rows, hk, &stride);
+        const at::Tensor& ws = c.need(a[8], "workspace", at::kByte, 1);
+        const int window = a[9] == Py_None ? INT_MAX : to_int(a[9]);
+        auto* err = static_cast<int32_t*>(c.optional(a[11], "dev_err", at::kInt, 1));
+        const c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, c.device));
+        return paged_attention_prefill_weights(
+            w, q.data_ptr(), k.data_ptr(), ks, r.tables, r.seq_lens, r.q_start, narrow(r.rows, "rows"),
+            narrow(q.size(0), "tokens"), narrow(q.size(1), "q heads"), narrow(hk, "kv heads"), narrow(d, "head_dim"),
+            narrow(k.size(1), "block_size"), to_float(a[6]), window, narrow(r.mbpr, "block_tables"),
+            narrow(k.size(0), "blocks"), to_int(a[7]), stride, ws.data_ptr(), (size_t)ws.numel(), err,
+            to_stream(a[12], c.device));
+    });
+}
+
 PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded("evict", n, 17, [&]() -> int {
         Call c;
@@ -431,6 +463,7 @@ PyMethodDef methods[] = {
     {"tree_attention", as_function(tree_attention), METH_FASTCALL, nullptr},
     {"tree_commit", as_function(tree_commit), METH_FASTCALL, nullptr},
     {"decode_weights", as_function(decode_weights), METH_FASTCALL, nullptr},
+    {"prefill_weights", as_function(prefill_weights), METH_FASTCALL, nullptr},
     {"evict", as_function(evict), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

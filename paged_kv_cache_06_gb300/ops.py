@@ -129,6 +129,10 @@ def _declare(L: ctypes.CDLL) -> None:
     L.paged_attention_decode_weights.restype = I
     L.paged_attention_decode_weights_workspace_size.argtypes = [I] * 6
     L.paged_attention_decode_weights_workspace_size.restype = S
+    L.paged_attention_prefill_weights.argtypes = [P] * 7 + [I] * 6 + [F, I, I, I, I, L64, P, S, P, P]
+    L.paged_attention_prefill_weights.restype = I
+    L.paged_attention_prefill_weights_workspace_size.argtypes = [I] * 8
+    L.paged_attention_prefill_weights_workspace_size.restype = S
     L.paged_kv_evict.argtypes = [P] * 11 + [I] * 9 + [L64, I, I, I, P, P]
     L.paged_kv_evict.restype = I
     L.paged_attention_tree.argtypes = [P] * 10 + [I] * 7 + [F, I, I, I, P, S, P, P]
@@ -671,6 +675,41 @@ def decode_weights(out, weights, q, k_pool, v_pool, block_tables, seq_lens, scal
         k_scale, v_scale, dev_err, stream)
     if st:
         _check("paged_attention_decode_weights", st)
+
+
+def _window(window: Optional[int]) -> int:
+    return 2 ** 31 - 1 if window is None else int(window)
+
+
+def prefill_weights_workspace_size(rows: int, total_q: int, q_heads: int, kv_heads: int,
+                                   head_dim: int, max_seq_len: int, block_size: int,
+                                   window: Optional[int] = None) -> int:
+    return int(lib().paged_attention_prefill_weights_workspace_size(
+        rows, total_q, q_heads, kv_heads, head_dim, max_seq_len, block_size, _window(window)))
+
+
+def alloc_prefill_weights_workspace(rows, total_q, q_heads, kv_heads, head_dim, max_seq_len,
+                                    block_size, window=None, device="cuda"):
+    """A workspace of prefill_weights of the size the C ABI asks for."""
+    n = prefill_weights_workspace_size(rows, total_q, q_heads, kv_heads, head_dim, max_seq_len,
+                                       block_size, window)
+    if n == 0:
+        raise ValueError("unsupported sizes for paged_attention_prefill_weights")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def prefill_weights(weights, q, k_pool, block_tables, seq_lens, q_start, scale: float,
+                    max_seq_len: int, workspace, window: Optional[int] = None, k_scale=None,
+                    dev_err=None, stream=None):
+    """paged_attention_prefill_weights: the weights that each row's chunk of queries
+    (prefill's arguments), or its last ``window``, give to the row's tokens, added to
+    ``weights`` (float32 [rows][kv_heads][stride]; the chunk's own tokens start
+    from zero).  An FP8 pool when the scale is given."""
+    st = (_ext or binding()).prefill_weights(
+        weights, q, k_pool, block_tables, seq_lens, q_start, scale, max_seq_len, workspace, window,
+        k_scale, dev_err, stream)
+    if st:
+        _check("paged_attention_prefill_weights", st)
 
 
 def evict(k_pool, v_pool, block_tables, seq_lens, weights, token_pos, budget: int,

@@ -83,6 +83,51 @@ def test_decode_weights_workspace_size_host_arithmetic():
         assert ops.decode_weights_workspace_size(*bad) == 0, bad
 
 
+def prefill(**kw):
+    a = dict(w=2 * FAR, q=FAR, k=FAKE, ks=0, bt=FAKE, sl=FAKE, qs=FAKE, rows=4, total=90, hq=12, hk=2, d=128, bs=16,
+             scale=0.1, window=32, mbpr=16, nb=64, msl=200, stride=200, ws=3 * FAR, wsb=None)
+    a.update(kw)
+    if a["wsb"] is None:
+        a["wsb"] = ops.prefill_weights_workspace_size(4, 90, 12, 2, 128, 200, 16, window=32)
+    return ops.lib().paged_attention_prefill_weights(
+        *[P(a[n]) for n in ("w", "q", "k", "ks", "bt", "sl", "qs")], a["rows"], a["total"], a["hq"], a["hk"], a["d"],
+        a["bs"], a["scale"], a["window"], a["mbpr"], a["nb"], a["msl"], a["stride"], P(a["ws"]), a["wsb"], None, None)
+
+
+def test_prefill_weights_refusals():
+    for n in ("w", "q", "k", "bt", "sl", "qs"):
+        assert prefill(**{n: 0}) == INVALID, n
+    assert prefill(q=ODD) == INVALID and prefill(k=ODD) == INVALID
+    assert prefill(window=0) == INVALID and prefill(window=-1) == INVALID
+    assert prefill(stride=199) == INVALID and prefill(msl=257, stride=300) == INVALID
+    assert prefill(scale=float("inf")) == INVALID and prefill(hq=12, hk=5) == INVALID and prefill(nb=0) == INVALID
+    assert prefill(d=64) == UNSUPPORTED and prefill(bs=24) == UNSUPPORTED and prefill(rows=1025) == UNSUPPORTED
+    assert prefill(hq=129, hk=1) == UNSUPPORTED and prefill(nb=1 << 27) == UNSUPPORTED
+    assert prefill(total=1 << 30, msl=1 << 20, stride=1 << 20, mbpr=1 << 17, window=1 << 30) == UNSUPPORTED
+
+
+def test_prefill_weights_workspace():
+    n = ops.prefill_weights_workspace_size(4, 90, 12, 2, 128, 200, 16)
+    assert n > 0 and n % 256 == 0
+    assert ops.prefill_weights_workspace_size(4, 9000, 12, 2, 128, 200, 16, window=1) <= \
+        ops.prefill_weights_workspace_size(4, 9000, 12, 2, 128, 200, 16, window=32) < \
+        ops.prefill_weights_workspace_size(4, 9000, 12, 2, 128, 200, 16)
+    for bad in ((0, 90, 12, 2, 128, 200, 16), (4, -1, 12, 2, 128, 200, 16), (4, 90, 12, 5, 128, 200, 16),
+                (4, 90, 12, 2, 64, 200, 16), (4, 90, 12, 2, 128, 200, 24), (4, 90, 129, 1, 128, 200, 16)):
+        assert ops.prefill_weights_workspace_size(*bad) == 0, bad
+    assert ops.prefill_weights_workspace_size(4, 90, 12, 2, 128, 200, 16, window=0) == 0
+    assert prefill(rows=0, q=0) == 0 and prefill(total=0, q=0) == 0
+
+
+@pytest.mark.gpu
+def test_prefill_weights_workspace_refusals_of_a_device(cuda_device):
+    """(The size depends on the device's SMs.)"""
+    assert prefill(ws=0) == WORKSPACE and prefill(wsb=256) == WORKSPACE and prefill(ws=3 * FAR + 16) == WORKSPACE
+    for at in (FAR, 3 * FAR):                                          # the sums over what is read or written
+        assert prefill(w=at) == INVALID and prefill(w=at - 4 * 2 * 200 * 4 + 4) == INVALID
+    assert prefill(q=3 * FAR) == INVALID
+
+
 def evict(**kw):
     a = dict(k=FAKE, v=FAKE, bt=FAKE, sl=FAKE, w=FAR, pos=2 * FAR, tr=FAKE, nx=FAKE, wo=None, po=None, new=3 * FAR,
              layers=2, rows=4, hk=2, d=128, eb=2, bs=16, mbpr=16, nb=64, msl=200, stride=200, budget=100, sinks=4,

@@ -176,9 +176,10 @@ def test_norms_of_heads_that_are_zero_huge_or_no_number(cuda_device):
 
 # ---- weights ----
 
-def weights_ref(step, q, scale, queries, used, skip=()):
+def weights_ref(step, q, scale, queries, used, skip=(), extra=lambda n, mag: 0):
     """What the last used[r] of row r's queries[r] give: (sums [rows][hk] of tensors [L], their
-    tolerance before they are added to anything), and the last query's output."""
+    tolerance before they are added to anything), and the queries' outputs.  extra: further roundings
+    of an exponent, in U."""
     hq = q.shape[1]
     g, out = hq // step.hk, []
     a = 0
@@ -198,7 +199,7 @@ def weights_ref(step, q, scale, queries, used, skip=()):
         p = torch.softmax(s, -1)
         e = 130 * U * abs(scale) * (x.abs() @ k.abs().transpose(1, 2)).masked_fill(hide, 0).amax(-1, keepdim=True)
         mag = s.masked_fill(hide, 0).abs().amax(-1, keepdim=True)
-        tol = p * (2 * e + (12 + n + 4 * mag) * U)
+        tol = p * (2 * e + (12 + n + 4 * mag + extra(n, mag)) * U)
         shape = (step.hk, g * u, n)
         out.append((p.reshape(shape).sum(1), (tol + g * u * U * p).reshape(shape).sum(1), (p @ v, p @ v.abs(), e)))
     return out
@@ -288,6 +289,154 @@ def test_decode_weights_of_bad_lengths_blocks_and_numbers(cuda_device):
     w[3] = before[3].cuda()
     ref[3] = None
     check_weights(step, w, before, ref, [1] * 4)
+
+
+PROMPTS = [
+    # cached, chunk, window, block, q heads, kv heads
+    ([0], [1], None, 16, 12, 2),
+    ([0, 5, 100, 0], [3, 1, 22, 0], None, 16, 12, 2),
+    ([10, 0, 127, 128], [130, 300, 1, 64], None, 64, 12, 2),       # tiles and query blocks that end anywhere
+    ([300, 1000], [200, 77], 32, 48, 12, 2),                       # the last 32 of a chunk
+    ([300, 0, 7], [40, 500, 2], 1, 16, 12, 2),                     # the last one alone
+    ([20000, 3], [6, 4], None, 64, 12, 2),                         # few queries over a long cache
+    ([0, 64], [700, 260], None, 128, 32, 8),
+    ([500, 31], [150, 90], None, 32, 28, 4),
+    ([500, 31], [129, 250], None, 16, 4, 4),                       # a head a group
+    ([257, 0], [100, 37], None, 16, 24, 1),                        # five queries a block
+    ([9, 400], [70, 11], None, 16, 10, 2),
+    ([50], [9], None, 16, 128, 1),                                 # a query a block
+    ([60, 0], [9, 33], None, 112, 65, 1),                          # one and 63 rows of nothing
+    ([37 * i % 400 for i in range(60)], [5 + i % 9 for i in range(60)], 7, 16, 12, 2),
+    ([0, 0], [2000, 1100], None, 64, 12, 2),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", range(len(PROMPTS)))
+def test_prefill_weights_match_the_formula(cuda_device, case, fp8):
+    """As decode's, with an exponent's further roundings: the logarithm of the sum is rounded
+    twice, and so is its difference from the score: below U (2 |score| + 3 log2 L) of a
+    weight, and constants within 4 U."""
+    prefix, nodes, window, bs, hq, hk = PROMPTS[case]
+    step = Step(prefix, nodes, bs, hk=hk, fp8=fp8, seed=600 + case)
+    q = torch.randn(step.total, hq, 128, generator=step.gen).half()
+    before = torch.rand(step.rows, hk, step.max_len + 3, generator=step.gen)
+    used = [min(n, window or n) for n in nodes]
+    ref = weights_ref(step, q, 0.0883, nodes, used, extra=lambda n, mag: 4 + 2 * mag + 3 * np.log2(n + 1))
+    a, err = step.gpu(), err_word()
+    ws = ops.alloc_prefill_weights_workspace(step.rows, step.total, hq, hk, 128, step.max_len, bs, window=window)
+    outs = []
+    for fill in (0, 255):                                             # whatever the workspace holds
+        ws.fill_(fill)
+        w = before.cuda()
+        ops.prefill_weights(w, q.cuda(), a["k_pool"], a["block_tables"], a["seq_lens"], a["q_start"], 0.0883,
+                            step.max_len, ws, window=window, k_scale=a["k_scale"], dev_err=err)
+        torch.cuda.synchronize()
+        outs.append(w)
+    assert int(err.item()) == 0
+    assert torch.equal(*outs)                                         # the same bits every time
+    check_weights(step, outs[0], before, ref, nodes)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_weights_of_bad_rows_blocks_and_unseen_numbers(cuda_device, fp8):
+    """A row too long, a block out of range, queries and keys that are no numbers where
+    nobody, or somebody, sees them."""
+    step = Step([100, 60, 300, 40], [30, 9, 45, 33], 16, fp8=fp8, seed=14)
+    q = torch.randn(step.total, 12, 128, generator=step.gen).half()
+    before = torch.rand(4, 2, step.max_len, generator=step.gen)
+    ws = ops.alloc_prefill_weights_workspace(4, step.total, 12, 2, 128, step.max_len, 16)
+    err = err_word()
+
+    def run(x, **kw):
+        a, w = step.gpu(**kw), before.cuda()
+        ops.prefill_weights(w, x.cuda(), a["k_pool"], a["block_tables"], a["seq_lens"], a["q_start"], 0.0883,
+                            step.max_len, ws, k_scale=a["k_scale"], dev_err=err)
+        torch.cuda.synchronize()
+        return w
+
+    more = dict(extra=lambda n, mag: 4 + 2 * mag + 3 * np.log2(n + 1))
+    clean = run(q)
+    t, lens = step.tables.copy(), list(step.lens)
+    lens[1] = step.max_len + 1
+    t[0, 1] = -1                                                       # slots 16 .. 31 of row 0
+    t[2, 20] = step.nb + 7                                             # slots 320 .. 335 of row 2
+    got = run(q, block_tables=i32(t), seq_lens=i32(lens))
+    assert ops.check_error(err) == ERR_BLOCK | ERR_LEN
+    skip = [(0, i) for i in range(16, 32)] + [(2, i) for i in range(320, 336)]
+    ref = weights_ref(step, q, 0.0883, step.nodes, step.nodes, skip=skip, **more)
+    ref[1] = None
+    check_weights(step, got, before, ref, step.nodes)
+    assert torch.equal(got[3], clean[3])
+    # a query that is no number: its tokens' sums in its head's group; the others keep their bits
+    x = q.clone()
+    x[5, 7, 3] = float("nan")                                          # row 0, query 5, KV head 1
+    got = run(x)
+    assert bool(torch.isnan(got[0, 1, :106]).all()) and bool(torch.isfinite(got[0, 1, 106:130]).all())
+    same = torch.ones(4, 2, dtype=torch.bool)
+    same[0, 1] = False
+    assert torch.equal(got[same.cuda()], clean[same.cuda()])
+    assert torch.equal(got[0, 1, 106:], clean[0, 1, 106:])             # no such query sees them
+    # a key that is no number, seen by the last three queries of row 3 alone
+    slot = step.slots(3)[70]
+    step.k_pool.view(-1, 2, 128)[slot, 0] = 0x7F if fp8 else float("nan")
+    got = run(q)
+    assert bool(torch.isnan(got[3, 0, :73]).all())
+    same = torch.ones(4, 2, dtype=torch.bool)
+    same[3, 0] = False
+    assert torch.equal(got[same.cuda()], clean[same.cuda()])
+    assert ops.check_error(err) == 0
+
+
+@pytest.mark.parametrize("chunk,done", [(40, True), (400, False)])
+def test_prefill_weights_of_rows_that_name_the_same_queries(cuda_device, chunk, done):
+    """Two rows of all the queries and two of less than none: as they come, or, where the
+    workspace has no room for so many query blocks, nothing at all."""
+    step = Step([0] * 4, [chunk] * 4, 16, seed=15)
+    q = torch.randn(chunk, 12, 128, generator=step.gen).half().cuda()
+    w = torch.rand(4, 2, chunk, generator=step.gen).cuda()
+    before, err, a = w.clone(), err_word(), step.gpu()
+    starts = torch.tensor([0, chunk, 0, chunk, 0], dtype=torch.int32)
+    ws = ops.alloc_prefill_weights_workspace(4, chunk, 12, 2, 128, chunk, 16)
+    ws.fill_(77)
+    ops.prefill_weights(w, q, a["k_pool"], a["block_tables"], a["seq_lens"], starts.cuda(), 0.1, chunk, ws, dev_err=err)
+    assert ops.check_error(err) == ERR_LEN
+    for r in range(4):
+        assert torch.equal(w[r], before[r]) == (r % 2 == 1 or not done)
+
+
+def test_decode_and_prefill_weights_in_a_graph_on_another_stream(cuda_device):
+    """Captured together over separate workspaces, replayed twice: the eager calls' bits."""
+    step = Step([700, 30, 90], [100, 64, 1], 64, seed=16)
+    q = torch.randn(step.total, 12, 128, generator=step.gen).half().cuda()
+    last = q[[99, 163, 164]].contiguous()
+    a = step.gpu()
+    wsp = ops.alloc_prefill_weights_workspace(3, step.total, 12, 2, 128, step.max_len, 64, window=16)
+    wsd = ops.alloc_decode_weights_workspace(3, 12, 2, 128, step.max_len, 64)
+    out = torch.zeros(3, 12, 128, dtype=torch.float16, device="cuda")
+    w = torch.rand(3, 2, step.max_len, generator=step.gen).cuda()
+    first = w.clone()
+
+    def both(stream=None):
+        ops.prefill_weights(w, q, a["k_pool"], a["block_tables"], a["seq_lens"], a["q_start"], 0.09, step.max_len, wsp,
+                            window=16, stream=stream)
+        ops.decode_weights(out, w, last, a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], 0.09,
+                           step.max_len, wsd, stream=stream)
+
+    both()
+    torch.cuda.synchronize()
+    want, want_out = w.clone(), out.clone()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            both()
+    for _ in range(2):
+        w.copy_(first)
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(w, want) and torch.equal(out, want_out)
 
 
 # ---- eviction ----
