@@ -20,13 +20,16 @@
 // leave pieces, which are brought together in order.
 //
 // Warp roles (each walks the same jobs):
-//   warps 0-7   sums: warps w and w + 4 share 32 rows (TMEM lanes); each takes 64 columns;
-//   warp 8      copies: the unit's fixed tile (two buffers), the others through a ring of
-//               three, by TMA; K as one box of 16 to 128 tokens of a page each, its pool
+//   warps 0-15  sums, in four groups of four that take every fourth job, each from a buffer
+//               of 128 columns of its own: a row of the product a thread, 32 scores at a time;
+//   warp 16     copies: the unit's fixed tile (two buffers), the others through a ring of
+//               four (three), by TMA; K as one box of 16 to 128 tokens of a page each, its pool
 //               rows found through the block table;
-//   warp 9      products: one thread issues eight tcgen05.mma a job into one of four
-//               buffers of 128 columns;
-//   warps 10-13 (E4M3 pools) widen K's codes, exactly, into the operand tiles.
+//   warp 17     products: one thread issues eight tcgen05.mma a job;
+//   warps 18-21 (E4M3 pools) widen K's codes, exactly, into the operand tiles.
+// The copying and the issuing warp run alone, so what an instruction of theirs takes, some five
+// clocks, is in every job: their loops keep slots and parities as running values and find
+// pool rows a batch at a time (with divisions and a look-up a job: 0.72 us a job).
 // Every wait is bounded: a block that gives up flags the error, tells its other warps to stop,
 // and lets its copies and products in flight finish before it frees tensor memory.
 //
@@ -43,18 +46,19 @@ namespace prompt {
 using namespace tc;
 
 constexpr int kTile = 128;
-constexpr int kSumWarps = 8, kCopyWarp = 8, kMmaWarp = 9, kConvWarp = 10, kConvWarps = 4;
-constexpr int kRing = 3;    // streamed tiles
+constexpr int kGroups = 4, kSumWarps = 4 * kGroups;
+constexpr int kCopyWarp = kSumWarps, kMmaWarp = kSumWarps + 1, kConvWarp = kSumWarps + 2, kConvWarps = 4;
 constexpr int kFixed = 2;   // a unit's fixed tiles
 constexpr int kRaw = 2;     // tiles of codes
-constexpr int kBufs = 4;    // products in tensor memory
-constexpr int kAhead = 8;   // jobs between the copies and the sums, at most (ring + products below that)
+constexpr int kBufs = kGroups;  // products in tensor memory, a group's each
+constexpr int kComb = 2;    // units whose sums the groups bring together
+constexpr int kAhead = 9;   // jobs between the copies and the sums, at most (ring + products below that)
 constexpr int kMaxRows = 1024;
 constexpr uint32_t kHalf = kTile * 128;      // 128 rows x 64 dims
 constexpr uint32_t kOperand = 2 * kHalf;
 constexpr uint32_t kCodes = kTile * 128;     // 128 tokens of codes
 constexpr uint32_t kTmemCols = 512;
-constexpr int kCertain = 48;                 // columns of a half that are not asked whether a query has them
+constexpr int kCertain = 112;                // columns that are not asked whether a query has them
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMove = 16.f;                // a score this far above the reference moves it
 
@@ -146,20 +150,23 @@ struct Walk {
 // Shared memory, from a 1024-byte boundary on.
 template <bool kFp8>
 struct Smem {
+    static constexpr int kRing = kFp8 ? 3 : 4;  // streamed tiles
     static constexpr uint32_t fixed = 0;
     static constexpr uint32_t ring = fixed + kFixed * kOperand;
     static constexpr uint32_t raw = ring + kRing * kOperand;
-    // 1: one half's maxima and sums [kAhead][128] float2; 3: -e, and one half's sums, [kAhead][128] each
+    // 1: groups' maxima and sums [kComb][kGroups - 1][128] float2; 3: -e [kAhead][128], then the
+    // groups' sums
     static constexpr uint32_t lse = raw + (kFp8 ? kRaw * kCodes : 0);
     static constexpr uint32_t comb = lse + kAhead * kTile * 4;
-    static constexpr uint32_t bars = comb + kAhead * kTile * 4;
+    static constexpr uint32_t bars = comb + kComb * (kGroups - 1) * kTile * 4;
+    static_assert(kComb * (kGroups - 1) * 4 <= kAhead * 4, "the groups' sums fit");
+    static_assert(kRing + kBufs + 1 <= kAhead, "entries of jobs that the sums still need are not overwritten");
     static constexpr uint32_t misc = bars + 64 * 8;                      // tmem address, start [8], stop, warp sums
     static constexpr uint32_t bad = misc + 256;                          // [16] 16-token groups of K not to be seen
     static constexpr uint32_t rows = bad + 64;                           // 6 x [rows + 1] ints
     __host__ __device__ static constexpr uint32_t total(int n) { return rows + 6 * ((uint32_t)n + 1) * 4 + 1024; }
 };
 static_assert(Smem<true>::total(kMaxRows) <= 232448 && Smem<false>::total(kMaxRows) <= 232448, "shared memory per block");
-static_assert(kRing + kBufs + 1 <= kAhead, "entries of jobs that the sums still need are not overwritten");
 
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
@@ -170,9 +177,7 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-__device__ __forceinline__ float lane_value(const uint32_t (&a)[32], const uint32_t (&b)[32], int c) {
-    return __uint_as_float(c < 32 ? a[c] : b[c - 32]);
-}
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
 // Inclusive prefix over the warp's lanes, held at `most`.
 __device__ __forceinline__ int scan_most(int v, int most) {
@@ -190,7 +195,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
     tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ Params p) {
     using S = Smem<kFp8>;
-    constexpr int kThreads = threads<kFp8>(), kWarps = kThreads / 32, kMost = 1 << 30;
+    constexpr int kThreads = threads<kFp8>(), kWarps = kThreads / 32, kMost = 1 << 30, kRing = S::kRing;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t sbase = smem_u32(smem);
@@ -203,8 +208,9 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
     const uint32_t bar_lse = bar_wfree + 8 * kRaw;          // [kAhead] a job's -e are there
     const uint32_t bar_done = bar_lse + 8 * kAhead;         // [kBufs] products are done
     const uint32_t bar_read = bar_done + 8 * kBufs;         // [kBufs] and are read
-    const uint32_t bar_comb = bar_read + 8 * kBufs;         // [kAhead] one half's sums of a unit are there
-    const uint32_t bar_fin = bar_comb + 8 * kAhead;         // the last products are done
+    const uint32_t bar_comb = bar_read + 8 * kBufs;         // [kComb] the other groups' sums of a unit are there
+    const uint32_t bar_took = bar_comb + 8 * kComb;         // [kComb] and are taken
+    const uint32_t bar_fin = bar_took + 8 * kComb;          // the last products are done
     volatile int* misc = reinterpret_cast<volatile int*>(smem + S::misc);
     const volatile int* stop = misc + 16;
     volatile int* bad = reinterpret_cast<volatile int*>(smem + S::bad);
@@ -235,13 +241,14 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             mbar_init(bar_wfull + 8 * i, 1);
             mbar_init(bar_wfree + 8 * i, kConvWarps);
         }
-        for (int i = 0; i < kAhead; ++i) {
-            mbar_init(bar_lse + 8 * i, 1);
-            mbar_init(bar_comb + 8 * i, kSumWarps / 2);
+        for (int i = 0; i < kAhead; ++i) mbar_init(bar_lse + 8 * i, 1);
+        for (int i = 0; i < kComb; ++i) {
+            mbar_init(bar_comb + 8 * i, kSumWarps - 4);
+            mbar_init(bar_took + 8 * i, 4);
         }
         for (int i = 0; i < kBufs; ++i) {
             mbar_init(bar_done + 8 * i, 2);  // the products, and the thread that issued them
-            mbar_init(bar_read + 8 * i, kSumWarps);
+            mbar_init(bar_read + 8 * i, 4);
         }
         mbar_init(bar_fin, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -361,98 +368,123 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         // nothing to do but the release below
     } else if (warp == kCopyWarp) {
         // ============================ copies ============================
-        bool ok = true, fresh = true;
-        int units = 0, jobs = 0, codes = 0;  // fixed tiles, streamed tiles and tiles of codes so far
-        Walk<kSums> c = at, ahead = at;      // `ahead`: where K is copied for next
-        const int boxes = kTile / p.kbox;
-        auto entry = [&]() -> int {          // the table entry of this lane's box there
-            const int t = ahead.tile() * kTile + lane * p.kbox;
-            if (ahead.left <= 0 || lane >= boxes || t >= w.len[ahead.r]) return 0;
-            return p.tables[(int64_t)ahead.r * p.mbpr + t / p.bs];
-        };
-        int pb = entry();
-        // K's tile to `dst`, counted at `full`; its groups that are not to be seen to `note`.
-        auto copy_k = [&](uint32_t dst, uint32_t full, int note) {
-            const int t = c.tile() * kTile + lane * p.kbox, at_bs = t % p.bs;
-            bool there = lane < boxes && t < w.len[c.r];
-            uint32_t lost = 0;
-            if (there && (pb < 0 || pb >= p.nb)) {
-                flag_error(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
-                lost = ((1u << (p.kbox / 16)) - 1) << (lane * p.kbox / 16);
-                there = false;
+        bool ok = true;
+        Walk<kSums> c = at;
+        // A ring's next slot, the parity of the wait for it to be free (from the second lap on), fills.
+        struct Ring {
+            int s = 0, fills = 0;
+            uint32_t ph = 1;
+            __device__ __forceinline__ void next(int n) {
+                ++fills;
+                if (++s == n) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
-            lost = __reduce_or_sync(0xffffffffu, lost);
-            const uint32_t bytes = (uint32_t)p.kbox * 128;
-            const int n = __popc(__ballot_sync(0xffffffffu, there));
+        };
+        Ring fix, str, raw, neg;
+        // Lane l knows box l % boxes of tile l / boxes of a batch of 32 / boxes tiles.
+        const int boxes = kTile / p.kbox, batch = 32 / boxes, my_tile = lane / boxes, my_box = lane - my_tile * boxes;
+        const uint32_t box_bytes = (uint32_t)p.kbox * 128;
+        const int my_off = my_tile * kTile + my_box * p.kbox;
+        auto fetch = [&](int r, int tile) {  // its table entry in the batch from `tile` on
+            const int t = tile * kTile + my_off;
+            return t < w.len[r] ? p.tables[(int64_t)r * p.mbpr + t / p.bs] : 0;
+        };
+        int row = -1;        // the box's pool row (-1: none)
+        uint32_t lost = 0;   // its 16-token groups that are not to be seen
+        auto resolve = [&](int r, int tile, int pb) {
+            const int t = tile * kTile + my_off;
+            row = -1;
+            lost = 0;
+            if (t < w.len[r]) {
+                if (pb >= 0 && pb < p.nb) {
+                    row = pb * p.bs + t % p.bs;
+                } else {
+                    flag_error(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
+                    lost = ((1u << (p.kbox / 16)) - 1) << (my_box * (p.kbox / 16));
+                }
+            }
+        };
+        // Tile j of the batch to the next slot of its ring.
+        auto copy_k = [&](int j, int k, int note) {
+            Ring& ring = kFp8 ? raw : kSums ? fix : str;
+            const int n = kFp8 ? kRaw : kSums ? kFixed : kRing;
+            const uint32_t full = (kFp8 ? bar_wfull : kSums ? bar_ffull : bar_rfull) + 8 * ring.s;
+            const uint32_t free = (kFp8 ? bar_wfree : kSums ? bar_ffree : bar_rfree) + 8 * ring.s;
+            const uint32_t dst = sbase + (kFp8 ? S::raw : kSums ? S::fixed : S::ring) + ring.s * (kFp8 ? kCodes : kOperand);
+            if (ring.fills >= n && !mbar_waitw(free, ring.ph, stop)) return false;
+            const bool mine = my_tile == j;
+            const uint32_t some = __ballot_sync(0xffffffffu, mine && row >= 0);
+            const uint32_t gone = __reduce_or_sync(0xffffffffu, mine ? lost : 0u);
             if (lane == 0) {
-                bad[note & 15] = (int)lost;
-                mbar_arrive_expect_tx(full, (uint32_t)n * bytes * (kFp8 ? 1 : 2));
+                bad[note & 15] = (int)gone;
+                mbar_arrive_expect_tx(full, __popc(some) * box_bytes * (kFp8 ? 1 : 2));
             }
             __syncwarp();
-            if (there) {
-                const int row = pb * p.bs + at_bs;
-                tma_load_3d(dst + lane * bytes, &kmap, 0, c.k, row, full);
-                if (!kFp8) tma_load_3d(dst + kHalf + lane * bytes, &kmap, 64, c.k, row, full);
+            if (mine && row >= 0) {
+                tma_load_3d(dst + my_box * box_bytes, &kmap, 0, k, row, full);
+                if (!kFp8) tma_load_3d(dst + kHalf + my_box * box_bytes, &kmap, 64, k, row, full);
             }
-            if (kSums) {  // on to the next unit
-                ahead.left -= ahead.n - ahead.s - 1;
-                ahead.s = ahead.n - 1;
-            }
-            ahead.next(w, hk);
-            pb = entry();
-        };
-        auto copy_q = [&](uint32_t dst, uint32_t full) {
-            if (lane == 0) {
-                const int q = w.end[c.r] - w.used[c.r] + c.block() * nq;
-                mbar_arrive_expect_tx(full, (uint32_t)(nq * p.group) * 256u);
-                tma_load_3d(dst, &qmap, 0, c.k * p.group, q, full);
-                tma_load_3d(dst + kHalf, &qmap, 64, c.k * p.group, q, full);
-            }
-            __syncwarp();
-        };
-        auto copy_codes = [&](int note) {
-            const int s = codes % kRaw;
-            if (codes >= kRaw && !mbar_waitw(bar_wfree + 8 * s, (uint32_t)(codes / kRaw - 1) & 1, stop)) return false;
-            copy_k(sbase + S::raw + s * kCodes, bar_wfull + 8 * s, note);
-            ++codes;
+            ring.next(n);
             return true;
         };
-        while (c.left > 0) {
-            if (fresh) {
-                const int f = units % kFixed;
-                if (kSums && kFp8) {
-                    if (!(ok = copy_codes(units))) break;
-                } else {
-                    if (units >= kFixed && !(ok = mbar_waitw(bar_ffree + 8 * f, (uint32_t)(units / kFixed - 1) & 1, stop)))
-                        break;
-                    const uint32_t dst = sbase + S::fixed + f * kOperand;
-                    if (kSums)
-                        copy_k(dst, bar_ffull + 8 * f, units);
-                    else
-                        copy_q(dst, bar_ffull + 8 * f);
-                }
-                ++units;
-            }
-            const int s = jobs % kRing;
-            if (!kSums && kFp8) {
-                if (!(ok = copy_codes(jobs))) break;
-            } else {
-                if (jobs >= kRing && !(ok = mbar_waitw(bar_rfree + 8 * s, (uint32_t)(jobs / kRing - 1) & 1, stop))) break;
-                const uint32_t dst = sbase + S::ring + s * kOperand;
-                if (kSums) {
-                    copy_q(dst, bar_rfull + 8 * s);
-                    if (lane == 0) {
-                        const int e = jobs % kAhead, b = w.blocks[c.r] + c.k * w.query_blocks(c.r) + c.s;
-                        mbar_arrive_expect_tx(bar_lse + 8 * e, kTile * 4);
-                        bulk_load(sbase + S::lse + e * kTile * 4, p.neg_lse + (int64_t)b * kTile, kTile * 4, bar_lse + 8 * e);
+        const uint32_t q_bytes = (uint32_t)(nq * p.group) * 256u;
+        int units = 0, jobs = 0;
+        int pb_next = fetch(c.r, c.tile());
+        while (c.left > 0 && ok) {
+            const int end = min(c.n, c.s + c.left), pb = pb_next;
+            Walk<kSums> nx = c;  // the next piece, whose first batch is looked up meanwhile
+            nx.left -= end - c.s - 1;
+            nx.s = end - 1;
+            nx.next(w, hk);
+            if (nx.left > 0) pb_next = fetch(nx.r, nx.tile());
+            resolve(c.r, c.tile(), pb);
+            int q = w.end[c.r] - w.used[c.r] + c.block() * nq;
+            if (kSums) {
+                // the fixed token tile, then the query blocks and their -e by one lane
+                if (!(ok = copy_k(0, c.k, units))) break;
+                if (lane == 0) {
+                    const float* e = p.neg_lse + (int64_t)(w.blocks[c.r] + c.k * w.query_blocks(c.r) + c.s) * kTile;
+#pragma unroll 1
+                    for (int o = c.s; o < end; ++o) {
+                        if (str.fills >= kRing && !(ok = mbar_wait1(bar_rfree + 8 * str.s, str.ph, stop))) break;
+                        const uint32_t full = bar_rfull + 8 * str.s, dst = sbase + S::ring + str.s * kOperand;
+                        mbar_arrive_expect_tx(full, q_bytes);
+                        tma_load_3d(dst, &qmap, 0, c.k * p.group, q, full);
+                        tma_load_3d(dst + kHalf, &qmap, 64, c.k * p.group, q, full);
+                        mbar_arrive_expect_tx(bar_lse + 8 * neg.s, kTile * 4);
+                        bulk_load(sbase + S::lse + neg.s * kTile * 4, e, kTile * 4, bar_lse + 8 * neg.s);
+                        q += nq;
+                        e += kTile;
+                        str.next(kRing);
+                        neg.next(kAhead);
                     }
-                    __syncwarp();
-                } else {
-                    copy_k(dst, bar_rfull + 8 * s, jobs);
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+            } else {
+                // the fixed query block, then the token tiles, a batch's rows at a time
+                if (fix.fills >= kFixed && !(ok = mbar_waitw(bar_ffree + 8 * fix.s, fix.ph, stop))) break;
+                if (lane == 0) {
+                    const uint32_t full = bar_ffull + 8 * fix.s, dst = sbase + S::fixed + fix.s * kOperand;
+                    mbar_arrive_expect_tx(full, q_bytes);
+                    tma_load_3d(dst, &qmap, 0, c.k * p.group, q, full);
+                    tma_load_3d(dst + kHalf, &qmap, 64, c.k * p.group, q, full);
+                }
+                fix.next(kFixed);
+                int pb2 = c.s + batch < end ? fetch(c.r, c.s + batch) : 0, j = 0;
+#pragma unroll 1
+                for (int o = c.s; o < end; ++o, ++j, ++jobs) {
+                    if (j == batch) {
+                        j = 0;
+                        resolve(c.r, o, pb2);
+                        pb2 = o + batch < end ? fetch(c.r, o + batch) : 0;
+                    }
+                    if (!(ok = copy_k(j, c.k, jobs))) break;
                 }
             }
-            ++jobs;
-            fresh = c.next(w, hk);
+            ++units;
+            c = nx;
         }
         if (lane == 0) {
             if (!ok) give_up();
@@ -460,10 +492,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             auto drain = [&](uint32_t bar, int n, int count) {
                 for (int i = max(0, n - count); i < n; ++i) mbar_drain1(bar + 8 * (i % count), (uint32_t)(i / count) & 1);
             };
-            if (!(kSums && kFp8)) drain(bar_ffull, units, kFixed);
-            if (kSums || !kFp8) drain(bar_rfull, jobs, kRing);
-            if (kFp8) drain(bar_wfull, codes, kRaw);
-            if (kSums) drain(bar_lse, jobs, kAhead);
+            drain(bar_ffull, fix.fills, kFixed);
+            drain(bar_rfull, str.fills, kRing);
+            drain(bar_wfull, raw.fills, kRaw);
+            drain(bar_lse, neg.fills, kAhead);
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -471,30 +503,47 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         if (lane == 0) {
             const uint32_t id = idesc(kTile, kTile, 0);
             const uint64_t a0 = sdesc(sbase + S::fixed, 16, 1024), b0 = sdesc(sbase + S::ring, 16, 1024);
-            bool ok = true, fresh = true;
-            int units = 0, jobs = 0;
+            bool ok = true;
+            int f = 0, s = 0, b = 0;
+            uint32_t fph = 0, sph = 0, bph = 1;
             Walk<kSums> c = at;
-            while (c.left > 0) {
-                if (fresh) {
-                    if (!(ok = mbar_wait1(bar_ffull + 8 * (units % kFixed), (uint32_t)(units / kFixed) & 1, stop))) break;
-                    ++units;
-                }
-                const int s = jobs % kRing, b = jobs % kBufs, f = (units - 1) % kFixed;
-                if (!(ok = mbar_wait1(bar_rfull + 8 * s, (uint32_t)(jobs / kRing) & 1, stop))) break;
-                if (jobs >= kBufs && !(ok = mbar_wait1(bar_read + 8 * b, (uint32_t)(jobs / kBufs - 1) & 1, stop))) break;
-                tc_fence_after();
-                const uint64_t da = a0 + (uint64_t)(f * (kOperand >> 4)), db = b0 + (uint64_t)(s * (kOperand >> 4));
+            while (c.left > 0 && ok) {
+                const int end = min(c.n, c.s + c.left);
+                if (!(ok = mbar_wait1(bar_ffull + 8 * f, fph, stop))) break;
+                const uint64_t da = a0 + (uint64_t)(f * (kOperand >> 4));
+#pragma unroll 1
+                for (int o = c.s; o < end; ++o) {
+                    if (!(ok = mbar_wait1(bar_rfull + 8 * s, sph, stop))) break;
+                    // (a fresh barrier counts the phase before its first as complete)
+                    if (!(ok = mbar_wait1(bar_read + 8 * b, bph, stop))) break;
+                    tc_fence_after();
+                    const uint64_t db = b0 + (uint64_t)(s * (kOperand >> 4));
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-                    umma_ss(tmem + b * kTile, da + off, db + off, id, ks > 0);
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t off = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                        umma_ss(tmem + b * kTile, da + off, db + off, id, ks > 0);
+                    }
+                    mbar_arrive(bar_done + 8 * b);  // (what this thread has seen, the sums see too)
+                    umma_commit(bar_done + 8 * b);
+                    umma_commit(bar_rfree + 8 * s);
+                    if (++s == kRing) {
+                        s = 0;
+                        sph ^= 1;
+                    }
+                    if (++b == kBufs) {
+                        b = 0;
+                        bph ^= 1;
+                    }
                 }
-                mbar_arrive(bar_done + 8 * b);  // (what this thread has seen, the sums see too)
-                umma_commit(bar_done + 8 * b);
-                umma_commit(bar_rfree + 8 * s);
-                ++jobs;
-                fresh = c.next(w, hk);
-                if (fresh) umma_commit(bar_ffree + 8 * f);
+                if (!ok) break;
+                umma_commit(bar_ffree + 8 * f);
+                if (++f == kFixed) {
+                    f = 0;
+                    fph ^= 1;
+                }
+                c.left -= end - c.s - 1;
+                c.s = end - 1;
+                c.next(w, hk);
             }
             if (!ok) give_up();
             umma_commit(bar_fin);
@@ -538,170 +587,163 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         if (!ok && lane == 0) give_up();
     } else if (warp < kSumWarps) {
         // ============================ sums ============================
-        const int i = (warp & 3) * 32 + lane, hf = warp >> 2;  // row of the product; its half of the columns
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        bool ok = true, fresh = true;
-        int units = 0, jobs = 0, from = 0;
+        const int i = (warp & 3) * 32 + lane, grp = warp >> 2;  // row of the product; group
+        const uint32_t from_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + grp * kTile;
+        bool ok = true;
+        int units = 0, jobs = 0;
         Walk<kSums> c = at;
         const int group = p.group;
-        float ref = 0.f, sl2 = 0.f, acc = 0.f;  // acc: the row's sum; ref: what exponents are taken from
-        uint32_t hidden = 0;
-        while (c.left > 0) {
-            const int b = jobs % kBufs, e = jobs % kAhead;
-            if (fresh) {
-                ref = -INFINITY;
-                acc = 0.f;
-                sl2 = kFp8 ? p.scale_log2 * p.k_scale[c.k] : p.scale_log2;
-                from = c.s;
-                ++units;
-            }
-            if (!(ok = mbar_waitw(bar_done + 8 * b, (uint32_t)(jobs / kBufs) & 1, stop))) break;
-            if (kSums && !(ok = mbar_waitw(bar_lse + 8 * e, (uint32_t)(jobs / kAhead) & 1, stop))) break;
-            tc_fence_after();
-            uint32_t v[32], u[32];
-            tmem_ld64(tmem + lanes + b * kTile + hf * 64, v, u);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_read + 8 * b);
-            hidden = (uint32_t)bad[(kSums ? units - 1 : jobs) & 15];
-            // Positions: query q of the row's used ones sees tokens up to p0 + q.
-            const int p0 = w.len[c.r] - w.used[c.r], q0 = c.block() * nq, t0 = c.tile() * kTile;
-            const int here = min(nq, w.used[c.r] - q0);  // queries of the block
-            const bool plain = t0 + kTile - 1 <= p0 + q0 && here == nq && !hidden;
+        // jobs of this block, in units: c stands at the first one not yet walked
+        while (c.left > 0 && ok) {
+            const int from = c.s, job0 = jobs;  // the piece's first job
+            const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[c.k] : p.scale_log2;
             const uint64_t sl = f32x2(sl2, sl2);
-            if (!kSums) {
-                // row i: query i / group; column: token
-                const int q = i / group, last = q < here ? p0 + q0 + q - t0 - hf * 64 : -1;  // last column it sees
-                uint64_t seen = last < 0 ? 0ull : last >= 63 ? ~0ull : (2ull << last) - 1;
-                if (hidden)
+            // Positions: query q of the row's used ones sees tokens up to p0 + q.
+            const int p0 = w.len[c.r] - w.used[c.r], end = min(c.n, c.s + c.left);
+            float ref = -INFINITY, acc = 0.f;  // what exponents are taken from; the row's sum
+#pragma unroll 1
+            for (int o = c.s; o < end; ++o, ++jobs) {
+                if (jobs % kGroups != grp) continue;
+                const int e = jobs % kAhead, turn = jobs / kGroups;
+                if (!(ok = mbar_waitw(bar_done + 8 * grp, (uint32_t)turn & 1, stop))) break;
+                if (kSums && !(ok = mbar_waitw(bar_lse + 8 * e, (uint32_t)(jobs / kAhead) & 1, stop))) break;
+                tc_fence_after();
+                const uint32_t hidden = (uint32_t)bad[(kSums ? units : jobs) & 15];
+                const int q0 = (kSums ? o : c.x) * nq, t0 = (kSums ? c.x : o) * kTile;
+                const int here = min(nq, w.used[c.r] - q0);  // queries of the block
+                const bool plain = t0 + kTile - 1 <= p0 + q0 && here == nq && !hidden && nq * group >= kCertain;
+                // columns lo .. hi - 1 count
+                int lo = 0, hi = kTile;
+                if (!kSums) {
+                    const int q = i / group;  // row i: query; column: token
+                    hi = q < here ? p0 + q0 + q - t0 + 1 : 0;
+                } else {
+                    lo = max(0, t0 + i - p0 - q0) * group;  // row i: token; column: flat row
+                    hi = hidden >> (i >> 4) & 1 ? 0 : here * group;
+                }
+                const float4* lse = reinterpret_cast<const float4*>(smem + S::lse + e * kTile * 4);
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t v[32];
+                    tmem_ld32(from_tmem + 32 * ch, v);
+                    if (!kSums && ch == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_read + 8 * grp);
+                    }
+                    uint32_t seen = low_bits(hi - 32 * ch) & ~low_bits(lo - 32 * ch);
+                    if (!kSums && hidden) {
+                        if (hidden >> (2 * ch) & 1) seen &= 0xffff0000u;
+                        if (hidden >> (2 * ch + 1) & 1) seen &= 0x0000ffffu;
+                    }
+                    float base = 0.f;
+                    if (!kSums) {
+                        float top = -INFINITY;  // the largest score, in base 2
+                        if (!plain) {
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        if (hidden >> (4 * hf + g) & 1) seen &= ~(0xffffull << (16 * g));
-                float top = -INFINITY;  // the largest score, in base 2
-                if (plain) {
-                    float a = __uint_as_float(v[0]), z = a;
-                    if (sl2 >= 0.f) {
+                            for (int x = 0; x < 32; ++x)
+                                if (seen >> x & 1) top = fmaxf(top, __uint_as_float(v[x]) * sl2);
+                        } else if (sl2 >= 0.f) {
+                            float a = -INFINITY, z = a;
 #pragma unroll
-                        for (int x = 0; x < 64; x += 4) {
-                            a = fmaxf(fmaxf(lane_value(v, u, x), lane_value(v, u, x + 1)), a);
-                            z = fmaxf(fmaxf(lane_value(v, u, x + 2), lane_value(v, u, x + 3)), z);
+                            for (int x = 0; x < 32; x += 4) {
+                                a = fmaxf(fmaxf(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), a);
+                                z = fmaxf(fmaxf(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), z);
+                            }
+                            top = fmaxf(a, z) * sl2;
+                        } else {
+                            float a = INFINITY, z = a;
+#pragma unroll
+                            for (int x = 0; x < 32; x += 4) {
+                                a = fminf(fminf(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), a);
+                                z = fminf(fminf(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), z);
+                            }
+                            top = fminf(a, z) * sl2;
                         }
-                        top = fmaxf(a, z) * sl2;
+                        if (top > ref + kMove || (ref == -INFINITY && top > ref)) {
+                            acc *= ref == -INFINITY ? 1.f : fast_exp2(ref - top);
+                            ref = top;
+                        }
+                        base = ref == -INFINITY ? 0.f : -ref;
+                    }
+                    if (plain) {
+                        uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) {
+                            float4 y = make_float4(base, base, base, base);
+                            if (kSums) y = lse[ch * 8 + x / 4];
+                            float a, b, d, f;
+                            f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sl, f32x2(y.x, y.y)), a, b);
+                            f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), sl, f32x2(y.z, y.w)), d, f);
+                            if (kSums && x >= kCertain - 96 && ch == 3) {  // zeros times a key that is no number
+                                a = seen >> x & 1 ? a : -INFINITY;
+                                b = seen >> (x + 1) & 1 ? b : -INFINITY;
+                                d = seen >> (x + 2) & 1 ? d : -INFINITY;
+                                f = seen >> (x + 3) & 1 ? f : -INFINITY;
+                            }
+                            s0 = add_f32x2(s0, f32x2(fast_exp2(a), fast_exp2(b)));
+                            s1 = add_f32x2(s1, f32x2(fast_exp2(d), fast_exp2(f)));
+                        }
+                        float a, b;
+                        f32x2_split(add_f32x2(s0, s1), a, b);
+                        acc += a + b;
                     } else {
+                        float s = 0.f;
 #pragma unroll
-                        for (int x = 0; x < 64; x += 4) {
-                            a = fminf(fminf(lane_value(v, u, x), lane_value(v, u, x + 1)), a);
-                            z = fminf(fminf(lane_value(v, u, x + 2), lane_value(v, u, x + 3)), z);
+                        for (int x = 0; x < 32; ++x) {
+                            const float y = kSums ? reinterpret_cast<const float*>(lse)[32 * ch + x] : base;
+                            if (seen >> x & 1) s += fast_exp2(fmaf(__uint_as_float(v[x]), sl2, y));
                         }
-                        top = fminf(a, z) * sl2;
-                    }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (seen >> x & 1) top = fmaxf(top, lane_value(v, u, x) * sl2);
-                }
-                if (top > ref + kMove || ref == -INFINITY) {
-                    if (top > -INFINITY) {
-                        acc *= ref == -INFINITY ? 1.f : fast_exp2(ref - top);
-                        ref = top;
+                        acc += s;
                     }
                 }
-                const float base = ref == -INFINITY ? 0.f : -ref;
-                if (plain) {
-                    const uint64_t nr = f32x2(base, base);
-                    uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
-#pragma unroll
-                    for (int x = 0; x < 64; x += 4) {
-                        float a, z;
-                        f32x2_split(fma_f32x2(f32x2(lane_value(v, u, x), lane_value(v, u, x + 1)), sl, nr), a, z);
-                        s0 = add_f32x2(s0, f32x2(fast_exp2(a), fast_exp2(z)));
-                        f32x2_split(fma_f32x2(f32x2(lane_value(v, u, x + 2), lane_value(v, u, x + 3)), sl, nr), a, z);
-                        s1 = add_f32x2(s1, f32x2(fast_exp2(a), fast_exp2(z)));
-                    }
-                    float a, z;
-                    f32x2_split(add_f32x2(s0, s1), a, z);
-                    acc += a + z;
-                } else {
-                    float s = 0.f;
-#pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (seen >> x & 1) s += fast_exp2(fmaf(lane_value(v, u, x), sl2, base));
-                    acc += s;
-                }
-            } else {
-                // row i: token t0 + i; column: flat row, query column / group
-                const float4* lse = reinterpret_cast<const float4*>(smem + S::lse + e * kTile * 4) + hf * 16;
-                const int full = nq * group - hf * 64;  // columns that queries have; few blocks have no others
-                if (plain && full >= kCertain) {
-                    uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
-#pragma unroll
-                    for (int x = 0; x < 64; x += 4) {
-                        const float4 y = lse[x / 4];
-                        float a, z, c2, z2;
-                        f32x2_split(fma_f32x2(f32x2(lane_value(v, u, x), lane_value(v, u, x + 1)), sl, f32x2(y.x, y.y)), a, z);
-                        f32x2_split(fma_f32x2(f32x2(lane_value(v, u, x + 2), lane_value(v, u, x + 3)), sl, f32x2(y.z, y.w)), c2, z2);
-                        if (x >= kCertain) {  // zeros times a key that is no number
-                            a = x < full ? a : -INFINITY;
-                            z = x + 1 < full ? z : -INFINITY;
-                            c2 = x + 2 < full ? c2 : -INFINITY;
-                            z2 = x + 3 < full ? z2 : -INFINITY;
-                        }
-                        s0 = add_f32x2(s0, f32x2(fast_exp2(a), fast_exp2(z)));
-                        s1 = add_f32x2(s1, f32x2(fast_exp2(c2), fast_exp2(z2)));
-                    }
-                    float a, z;
-                    f32x2_split(add_f32x2(s0, s1), a, z);
-                    acc += a + z;
-                } else {
-                    const int q = max(0, t0 + i - p0 - q0);  // the first query of the block that sees the token
-                    const int lo = min(128, q * group) - hf * 64, hi = here * group - hf * 64;
-                    uint64_t seen = hi <= 0 ? 0ull : hi >= 64 ? ~0ull : (1ull << hi) - 1;
-                    if (lo > 0) seen &= lo >= 64 ? 0ull : ~0ull << lo;
-                    if (hidden >> (i >> 4) & 1) seen = 0;
-                    float s = 0.f;
-#pragma unroll
-                    for (int x = 0; x < 64; ++x) {
-                        const float y = reinterpret_cast<const float*>(lse)[x];
-                        if (seen >> x & 1) s += fast_exp2(fmaf(lane_value(v, u, x), sl2, y));
-                    }
-                    acc += s;
+                if (kSums) {  // -e is read too
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_read + 8 * grp);
                 }
             }
-            ++jobs;
-            const Walk<kSums> was = c;
-            fresh = c.next(w, hk);
-            if (!fresh) {
-                if (c.left > 0) continue;
-            }
-            // ---- the block's piece of the unit: both halves (at most kBufs + 1 units apart) ----
-            const int u8 = (units - 1) % kAhead;
-            float* one = reinterpret_cast<float*>(smem + S::comb) + u8 * kTile;
-            float2* two = reinterpret_cast<float2*>(smem + S::lse) + u8 * kTile;
-            if (hf == 1) {
+            if (!ok) break;
+            // ---- the block's piece of the unit: the groups' sums ----
+            const int slot = units % kComb, lap = units / kComb;
+            float* one = reinterpret_cast<float*>(smem + S::comb) + slot * (kGroups - 1) * kTile + i;
+            float2* two = reinterpret_cast<float2*>(smem + S::lse) + slot * (kGroups - 1) * kTile + i;
+            if (grp > 0) {
+                if (lap > 0 && !(ok = mbar_waitw(bar_took + 8 * slot, (uint32_t)(lap - 1) & 1, stop))) break;
                 if (kSums)
-                    one[i] = acc;
+                    one[(grp - 1) * kTile] = acc;
                 else
-                    two[i] = make_float2(ref, acc);
+                    two[(grp - 1) * kTile] = make_float2(ref, acc);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_comb + 8 * u8);
+                if (lane == 0) mbar_arrive(bar_comb + 8 * slot);
             } else {
-                if (!(ok = mbar_waitw(bar_comb + 8 * u8, (uint32_t)((units - 1) / kAhead) & 1, stop))) break;
-                const int unit = was.unit(w);
+                if (!(ok = mbar_waitw(bar_comb + 8 * slot, (uint32_t)lap & 1, stop))) break;
+                const int unit = c.unit(w);
                 const int64_t rec = (int64_t)cta + unit;
                 if (kSums) {
-                    p.sums[rec * kTile + i] = acc + one[i];
+#pragma unroll
+                    for (int g = 0; g < kGroups - 1; ++g) acc += one[g * kTile];
+                    p.sums[rec * kTile + i] = acc;
                 } else {
-                    const float2 o = two[i];
-                    const float M = fmaxf(ref, o.x), g = M == -INFINITY ? 0.f : M;
-                    p.ml[rec * kTile + i] = make_float2(M, acc * fast_exp2(ref - g) + o.y * fast_exp2(o.x - g));
+                    float M = ref;
+#pragma unroll
+                    for (int g = 0; g < kGroups - 1; ++g) M = fmaxf(M, two[g * kTile].x);
+                    const float z = M == -INFINITY ? 0.f : M;
+                    acc *= fast_exp2(ref - z);
+#pragma unroll
+                    for (int g = 0; g < kGroups - 1; ++g) acc += two[g * kTile].y * fast_exp2(two[g * kTile].x - z);
+                    p.ml[rec * kTile + i] = make_float2(M, acc);
                 }
-                if (i == 0 && from == was.s0) {
-                    // this block has the unit's first job: who has its last
-                    const int first = j0 + jobs - 1 - (was.s - was.s0);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_took + 8 * slot);
+                if (i == 0 && from == c.s0)  // this block has the unit's first job: who has its last
                     (kSums ? p.tile_info : p.block_info)[unit] =
-                        make_int2(cta, owner_of(first + was.n - was.s0 - 1, W, grid) - cta + 1);
-                }
+                        make_int2(cta, owner_of(j0 + job0 + c.n - c.s0 - 1, W, grid) - cta + 1);
             }
+            ++units;
+            c.left -= end - c.s - 1;  // to the piece's last job
+            c.s = end - 1;
+            c.next(w, hk);
         }
         if (!ok && lane == 0) give_up();
     }
