@@ -22,6 +22,15 @@
 // block's piece of the unit.
 // The second kernel: each block finds its unit's maxima and sums over the pieces, and
 // finishes a quarter of the unit's output or 1024 tokens' weights, in the same order every time.
+// Few short rows take one launch instead: a cluster of up to eight blocks a unit, each with
+// a contiguous share of its granules; the scores stay in shared memory, the blocks tell
+// each other their maxima and sums and the parts of the output that another of them finishes
+// through distributed shared memory, and each turns its own scores into weights.
+//
+// What bounds it.  Few rows: one dependent chain (32 rows of 1024, E4M3, 9.0 us: 1.7 for the launch
+// and the length, 1.9 for the copies, 1.7 for four granules a warp, 1.3 and 2.3 for bringing the
+// block's and the cluster's parts together).  Long rows: 4 of 32768, 31.4 us; the first kernel
+// takes 25 of them, 5.3 TB/s, and the second, with its launch, 6.
 #include <math.h>
 
 #include "fp8_codec.cuh"
@@ -40,6 +49,8 @@ constexpr int kBlocks = 3;           // resident per SM
 constexpr int kRing = 16 << 10;      // bytes of a warp's ring
 constexpr int kMaxRows = 1024;
 constexpr float kMove = 8.f;
+constexpr int kClusterBlocks = 8;    // of a cluster, at most (the portable limit)
+constexpr int kClusterTokens = 4096; // of a row that a cluster takes, at most
 constexpr int kEndThreads = 256;     // of the second kernel: a warp a head
 constexpr int kEndTokens = 4;        // a thread
 constexpr int kTile = kEndThreads * kEndTokens;
@@ -62,6 +73,8 @@ struct Params {
     int tokens;        // of a row, at most: whole granules
     int pairs;         // of heads whose scores are kept
     int grid;          // blocks of the first kernel
+    int blocks;        // of a cluster
+    int slots;         // of a cluster's warps' rings
     float scale_log2;
     int* pre;          // [rows + 1]: granules of the rows before
     float* part;       // [block + unit][group][128]: the block's piece of the unit, unnormalised
@@ -182,6 +195,68 @@ __device__ __forceinline__ void add_values(float (&o)[8][4], const unsigned char
         }
     }
 }
+// A warp's running state: heads 2 t, 2 t + 1 of lane (g, t); the sums are a lane's own until reduced.
+struct State {
+    float m0, m1, l0, l1, o[8][4];
+    __device__ __forceinline__ void reset() {
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    }
+    __device__ __forceinline__ void reduce() {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+        }
+    }
+};
+// One granule of `valid` tokens; its scores to `to` (this lane's heads of token g, `pairs` a token).
+template <bool kFp8>
+__device__ __forceinline__ void attend(State& st, const unsigned char* data, uint32_t at, int valid,
+                                       const uint32_t (&qb)[16], float sl2, float2* to, int pairs, int lane) {
+    const int gq = lane >> 2;
+    float s[4];
+    scores_of<kFp8>(s, data, at, qb, lane);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = gq + 8 * (j >> 1) < valid ? s[j] * sl2 : -INFINITY;
+    if ((lane & 3) < pairs) {
+        to[0] = make_float2(s[0], s[1]);
+        to[8 * pairs] = make_float2(s[2], s[3]);
+    }
+    const float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
+    if (__any_sync(0xffffffffu, x0 > st.m0 + kMove || x1 > st.m1 + kMove)) {
+        float n0 = fmaxf(st.m0, x0), n1 = fmaxf(st.m1, x1);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
+            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
+        }
+        // (a head that has seen nothing stays at -inf, with a state of zeros)
+        const float f0 = n0 == -INFINITY ? 1.f : fast_exp2(st.m0 - n0);
+        const float f1 = n1 == -INFINITY ? 1.f : fast_exp2(st.m1 - n1);
+        st.m0 = n0;
+        st.m1 = n1;
+        st.l0 *= f0;
+        st.l1 *= f1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            st.o[i][0] *= f0;
+            st.o[i][1] *= f1;
+            st.o[i][2] *= f0;
+            st.o[i][3] *= f1;
+        }
+    }
+    const float u0 = st.m0 == -INFINITY ? 0.f : st.m0, u1 = st.m1 == -INFINITY ? 0.f : st.m1;
+    const float p0 = fast_exp2(s[0] - u0), p1 = fast_exp2(s[1] - u1);
+    const float p2 = fast_exp2(s[2] - u0), p3 = fast_exp2(s[3] - u1);
+    // the sums take the weights in 32 bits: the weights handed out are divided by them too
+    st.l0 += p0 + p2;
+    st.l1 += p1 + p3;
+    add_values<kFp8>(st.o, data, at, movmatrix_t(pack_half2(p0, p1)), movmatrix_t(pack_half2(p2, p3)), valid, lane);
+}
+
 // Place d of a half's 64 dims of head h in a warp's state; pairs of heads lie on other banks.
 __device__ __forceinline__ int state_at(int h, int d) { return h * 64 + (d ^ (((h >> 1) & 3) << 3)); }
 
@@ -310,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     for (int i = 0; i < kSlots; ++i) ask();
 
     // ============================ attention ============================
-    float m0, m1, l0, l1, o[8][4];
+    State st;
     uint32_t qb[16];
     int slot = 0;
     uint32_t parity = 0;
@@ -322,10 +397,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         const int r = row_of(g0 + from), count = (pre[r + 1] - pre[r]) / p.hk, row0 = pre[r] - g0;
         const int kvh = (from - row0) / count, unit = r * p.hk + kvh;
         const int end = min(all, row0 + (kvh + 1) * count);
-        m0 = m1 = -INFINITY;
-        l0 = l1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        st.reset();
         const bool some = x < end;
         if (some) load_q<kFp8>(qb, p.q + ((int64_t)r * p.hq + kvh * p.group) * kHeadDim, p.group, lane);
         const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[kvh] : p.scale_log2;
@@ -349,46 +421,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
             const unsigned char* data = ring + slot * kBytes;
             const uint32_t at = ring_at + slot * kBytes;
             const int2 what = asked[warp][slot];
-            float s[4];
-            scores_of<kFp8>(s, data, at, qb, lane);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[j] = gq + 8 * (j >> 1) < what.y ? s[j] * sl2 : -INFINITY;
-            if (tq < p.pairs) {
-                float2* to = reinterpret_cast<float2*>(p.scores) +
-                             ((int64_t)unit * p.tokens + what.x + gq) * p.pairs + tq;
-                to[0] = make_float2(s[0], s[1]);
-                to[8 * p.pairs] = make_float2(s[2], s[3]);
-            }
-            const float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
-            if (__any_sync(0xffffffffu, x0 > m0 + kMove || x1 > m1 + kMove)) {
-                float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) {
-                    n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));
-                    n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, off));
-                }
-                // (a head that has seen nothing stays at -inf, with a state of zeros)
-                const float f0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
-                const float f1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
-                m0 = n0;
-                m1 = n1;
-                l0 *= f0;
-                l1 *= f1;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    o[i][0] *= f0;
-                    o[i][1] *= f1;
-                    o[i][2] *= f0;
-                    o[i][3] *= f1;
-                }
-            }
-            const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-            const float p0 = fast_exp2(s[0] - u0), p1 = fast_exp2(s[1] - u1);
-            const float p2 = fast_exp2(s[2] - u0), p3 = fast_exp2(s[3] - u1);
-            // the sums take the weights in 32 bits: the weights handed out are divided by them too
-            l0 += p0 + p2;
-            l1 += p1 + p3;
-            add_values<kFp8>(o, data, at, movmatrix_t(pack_half2(p0, p1)), movmatrix_t(pack_half2(p2, p3)), what.y, lane);
+            float2* to = reinterpret_cast<float2*>(p.scores) +
+                         ((int64_t)unit * p.tokens + what.x + gq) * p.pairs + tq;
+            attend<kFp8>(st, data, at, what.y, qb, sl2, to, p.pairs, lane);
             __syncwarp();  // the slot is read before its next copy is asked for
             if (++slot == kSlots) {
                 slot = 0;
@@ -397,14 +432,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
             ask();
         }
         // ---- the block's piece: the warps' states brought together ----
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-            l0 += __shfl_xor_sync(0xffffffffu, l0, off);
-            l1 += __shfl_xor_sync(0xffffffffu, l1, off);
-        }
+        st.reduce();
         if (lane < 4) {
-            part_ml[warp][2 * lane] = make_float2(m0, l0);
-            part_ml[warp][2 * lane + 1] = make_float2(m1, l1);
+            part_ml[warp][2 * lane] = make_float2(st.m0, st.l0);
+            part_ml[warp][2 * lane + 1] = make_float2(st.m1, st.l1);
         }
         // half of the dims at a time: tiles 4 half .. 4 half + 3
         const int64_t rec = (int64_t)blockIdx.x + unit;
@@ -414,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
             float* to = part + warp * p.group * 64;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                const float (&v)[4] = o[4 * half + mt];
+                const float (&v)[4] = st.o[4 * half + mt];
                 const int d = kFp8 ? 8 * gq + 2 * mt : 16 * mt + gq, e = kFp8 ? d + 1 : d + 8;
                 if (2 * tq < p.group) {
                     to[state_at(2 * tq, d)] = v[0];
@@ -596,6 +627,273 @@ __global__ void __launch_bounds__(kEndThreads) merge_kernel(const __grid_constan
     }
 }
 
+// ---------------------------------------------------------------------------
+// Short rows: a cluster of blocks a unit, one launch.
+
+__device__ __forceinline__ uint32_t block_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();  // the aligned form wants the whole warp together
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer(uint32_t addr, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void tell(uint32_t addr, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void tell(uint32_t addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kThreads, 4)
+    cluster_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ Params p) {
+    constexpr int kBytes = granule_bytes<kFp8>, kMostSlots = kRing / kBytes, kDims = kHeadDim / 4;
+    const int slots = p.slots, ring_bytes = slots * kBytes;
+    // from 1024-byte alignment on: rings, then the block's scores [granules][16][2 * pairs]
+    extern __shared__ unsigned char raw[];
+    unsigned char* smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    float2* scores = reinterpret_cast<float2*>(smem + kWarps * ring_bytes);
+    __shared__ __align__(8) uint64_t bars[kWarps][kMostSlots];  // granule there
+    __shared__ int asked[kWarps][kMostSlots];                    // its tokens (0: none is seen)
+    __shared__ float2 part_ml[kWarps][kMaxGroup];
+    // What the blocks tell each other: this block's share of the output, group of four dims i = rank +
+    // active * j from block c at [j * active + c]; every block's maxima and sums.
+    __shared__ __align__(16) float4 told[kMaxGroup * kDims + kClusterBlocks];
+    __shared__ float2 all_ml[kClusterBlocks][kMaxGroup];
+    __shared__ float2 end_ml[kMaxGroup];                      // the unit's maxima and reciprocal sums
+    __shared__ int stop;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int gq = lane >> 2, tq = lane & 3;
+    const int rank = (int)block_rank(), kvh = (int)blockIdx.x / p.blocks, r = (int)blockIdx.y;
+    if (tid < kWarps * kMostSlots) {
+        mbar_init(smem_u32(&bars[0][0] + tid), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (tid == 0) {
+        stop = 0;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&kmap)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
+    }
+    griddep_wait();
+    int L = p.seq_lens[r];
+    if (L < 0 || L > p.limit) {
+        if (rank == 0 && kvh == 0 && tid == 0) flag_error(p.dev_err, PKV_DEV_ERR_SEQ_LEN);
+        L = L < 0 ? 0 : p.limit;
+    }
+    const int n = (L + kGranule - 1) / kGranule;
+    const int share = max(kWarps, (n + p.blocks - 1) / p.blocks);  // granules of a block
+    const int g0 = rank * share, all = min(n, g0 + share) - g0;
+    __half* ob = p.out + ((int64_t)r * p.hq + kvh * p.group) * kHeadDim;
+    if (all <= 0) {  // nothing to do: the others neither wait for this block nor read its memory
+        if (rank == 0)
+            for (int i = tid; i < p.group * kHeadDim / 8; i += kThreads)
+                reinterpret_cast<uint4*>(ob)[i] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+    const int active = (n + share - 1) / share;  // blocks that have something to do
+    if (active > 1) cluster_arrive();            // this block may be told things
+    __syncthreads();
+    const volatile int* stopped = &stop;
+    unsigned char* ring = smem + warp * ring_bytes;
+    const uint32_t ring_at = smem_u32(ring);
+
+    // ---- copies: this warp's granules warp, warp + kWarps, ... of the share ----
+    const int32_t* row = p.tables + (int64_t)r * p.mbpr;
+    int batch = warp, row_j = -1, valid_j = 0;  // lane j: granule batch + j * kWarps
+    auto look_up = [&] {
+        const int x = batch + lane * kWarps;
+        row_j = -1;
+        valid_j = 0;
+        if (x >= all) return;
+        const int t = (g0 + x) * kGranule, lb = t / p.bs, pb = row[lb];
+        if (pb < 0 || pb >= p.nb) {
+            flag_error(p.dev_err, PKV_DEV_ERR_BLOCK_ID);
+        } else {
+            row_j = pb * p.bs + (t - lb * p.bs);
+            valid_j = min(kGranule, L - t);
+        }
+    };
+    look_up();
+    int ask_x = warp, ask_slot = 0;
+    auto ask = [&] {  // the next granule into the next slot, which has been read
+        if (ask_x >= all) return;
+        if (ask_x >= batch + 32 * kWarps) {
+            batch += 32 * kWarps;
+            look_up();
+        }
+        if (lane == (ask_x - batch) / kWarps) {
+            const uint32_t to = ring_at + ask_slot * kBytes, full = smem_u32(&bars[warp][ask_slot]);
+            asked[warp][ask_slot] = valid_j;
+            mbar_arrive_expect_tx(full, row_j < 0 ? 0u : (uint32_t)kBytes);
+            if (row_j >= 0) {
+                tma_load_3d(to, &kmap, 0, kvh, row_j, full);
+                if (!kFp8) tma_load_3d(to + kBox, &kmap, 64, kvh, row_j, full);
+                tma_load_3d(to + kBytes / 2, &vmap, 0, kvh, row_j, full);
+                if (!kFp8) tma_load_3d(to + kBytes / 2 + kBox, &vmap, 64, kvh, row_j, full);
+            }
+        }
+        __syncwarp();
+        ask_x += kWarps;
+        if (++ask_slot == slots) ask_slot = 0;
+    };
+#pragma unroll 1
+    for (int i = 0; i < slots; ++i) ask();
+
+    State st;
+    st.reset();
+    uint32_t qb[16];
+    load_q<kFp8>(qb, p.q + ((int64_t)r * p.hq + kvh * p.group) * kHeadDim, p.group, lane);
+    const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[kvh] : p.scale_log2;
+    const float vs = kFp8 ? p.v_scale[kvh] : 1.f;
+    int slot = 0;
+    uint32_t parity = 0;
+#pragma unroll 1
+    for (int x = warp; x < all; x += kWarps) {
+        if (!mbar_waitw(smem_u32(&bars[warp][slot]), parity, stopped)) {
+            // gives up: what it has asked for lands before the block exits; the barriers below are
+            // for all
+            if (lane == 0) {
+                stop = 1;
+                flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
+                for (int y = x; y < ask_x; y += kWarps) {
+                    const int turn = y / kWarps;
+                    mbar_drain1(smem_u32(&bars[warp][turn % slots]), (uint32_t)(turn / slots) & 1);
+                }
+            }
+            __syncwarp();
+            break;
+        }
+        attend<kFp8>(st, ring + slot * kBytes, ring_at + slot * kBytes, asked[warp][slot], qb, sl2,
+                     scores + (x * kGranule + gq) * p.pairs + tq, p.pairs, lane);
+        __syncwarp();  // the slot is read before its next copy is asked for
+        if (++slot == slots) {
+            slot = 0;
+            parity ^= 1;
+        }
+        ask();
+    }
+
+    // ---- the block's state: the warps' states over their rings, then brought together ----
+    st.reduce();
+    if (lane < 4) {
+        part_ml[warp][2 * lane] = make_float2(st.m0, st.l0);
+        part_ml[warp][2 * lane + 1] = make_float2(st.m1, st.l1);
+    }
+    auto place = [](int h, int d) { return h * kHeadDim + (d ^ (((h >> 1) & 3) << 3)); };
+    float* mine = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+        const int d = kFp8 ? 16 * gq + 2 * mt : 16 * mt + gq, e = kFp8 ? d + 1 : d + 8;
+        mine[place(2 * tq, d)] = st.o[mt][0];
+        mine[place(2 * tq, e)] = st.o[mt][2];
+        mine[place(2 * tq + 1, d)] = st.o[mt][1];
+        mine[place(2 * tq + 1, e)] = st.o[mt][3];
+    }
+    if (active > 1) cluster_wait();
+    __syncthreads();
+    const uint32_t told_at = smem_u32(told), ml_at = smem_u32(all_ml[rank]);
+#pragma unroll 1
+    for (int i = tid; i < p.group * kDims; i += kThreads) {
+        const int h = i / kDims, d = i % kDims * 4;
+        float M = -INFINITY, Lt = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, part_ml[w][h].x);
+        const float u = M == -INFINITY ? 0.f : M;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = fast_exp2(part_ml[w][h].x - u);
+            const float4 z = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * ring_bytes) + place(h, d));
+            Lt += f * part_ml[w][h].y;
+            y.x += f * z.x;
+            y.y += f * z.y;
+            y.z += f * z.z;
+            y.w += f * z.w;
+        }
+        const int j = i / active, c = i - j * active;
+        if (active > 1)
+            tell(peer(told_at + (j * active + rank) * 16, c), y);
+        else
+            told[i] = y;
+        if (d == 0) {
+            const float2 v = make_float2(M, Lt);
+            if (active > 1)
+                for (int x = 0; x < active; ++x) tell(peer(ml_at + h * 8, x), v);
+            else
+                all_ml[0][h] = v;
+        }
+    }
+    if (active > 1) cluster_arrive();
+    // the running sum that this thread adds to first is on its way meanwhile
+    float* wts = p.weights + ((int64_t)r * p.hk + kvh) * p.stride;
+    const int t0 = g0 * kGranule, t1 = min(L, t0 + all * kGranule);
+    const float was = t0 + tid < min(t1, L - 1) ? wts[t0 + tid] : 0.f;
+    if (active > 1)
+        cluster_wait();  // nobody reads or writes another block's memory from here on
+    else
+        __syncthreads();
+
+    // ---- the unit's maxima and sums ----
+    if (tid < p.group) {
+        float M = -INFINITY, Lt = 0.f;
+        for (int c = 0; c < active; ++c) M = fmaxf(M, all_ml[c][tid].x);
+        const float u = M == -INFINITY ? 0.f : M;
+        for (int c = 0; c < active; ++c) Lt += fast_exp2(all_ml[c][tid].x - u) * all_ml[c][tid].y;
+        end_ml[tid] = make_float2(u, Lt == 0.f ? 0.f : __fdividef(1.f, Lt));  // nothing visible: zeros
+    }
+    __syncthreads();
+
+    // ---- this block's share of the output ----
+#pragma unroll 1
+    for (int j = tid; rank + active * j < p.group * kDims; j += kThreads) {
+        const int i = rank + active * j, h = i / kDims, d = i % kDims * 4;
+        const float u = end_ml[h].x, inv = end_ml[h].y * vs;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < active; ++c) {
+            const float f = fast_exp2(all_ml[c][h].x - u);
+            const float4 z = told[j * active + c];
+            y.x += f * z.x;
+            y.y += f * z.y;
+            y.z += f * z.z;
+            y.w += f * z.w;
+        }
+        *reinterpret_cast<uint2*>(ob + h * kHeadDim + d) =
+            make_uint2(pack_half2(y.x * inv, y.y * inv), pack_half2(y.z * inv, y.w * inv));
+    }
+
+    // ---- its tokens' weights ----
+#pragma unroll 1
+    for (int t = t0 + tid; t < t1; t += kThreads) {
+        const float2* s = scores + (t - t0) * p.pairs;
+        const float before = t - t0 < kThreads ? was : t < L - 1 ? wts[t] : 0.f;  // the step's own token: zero
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxGroup / 2; ++k) {
+            if (k >= p.pairs) break;
+            const float2 x = s[k];
+            sum += fast_exp2(x.x - end_ml[2 * k].x) * end_ml[2 * k].y;
+            if (2 * k + 1 < p.group) sum += fast_exp2(x.y - end_ml[2 * k + 1].x) * end_ml[2 * k + 1].y;
+        }
+        wts[t] = before + sum;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
 struct Layout {
     size_t ml, pre, scores, bytes;
     int tokens, pairs;
@@ -704,6 +1002,30 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     int st = tiled_map_3d(k_pool, type, dims, strides, box, &kmap);
     if (st == PKV_OK) st = tiled_map_3d(v_pool, type, dims, strides, box, &vmap);
     if (st != PKV_OK) return st;
+    // Clusters of up to eight blocks, four granules a warp of the longest row while a cluster may
+    // grow, where they are few enough to be resident at once, four an SM: one launch instead
+    // of two.  Clusters against the even cut, 2 KV heads: 4 rows of 100 tokens 4.7 us and 6.6,
+    // one of 4096 9.6 and 14.3, 32 of 1024 (E4M3) 9.0 and 11.7, 32 of 16 to 512 and one of 4096
+    // 10.9 and 12.1; but 32 of 4096 33.9 and 31.0, and, past four an SM, 96 of 16 to 600 and
+    // one of 4000 29.4 and 18.1, 128 of 2048 75.6 and 55.6.
+    const int n = l.tokens / kGranule;
+    p.blocks = 1;
+    while (p.blocks < kClusterBlocks && p.blocks * 4 * kWarps < n) p.blocks *= 2;
+    if (max_seq_len <= kClusterTokens && (int64_t)rows * kv_heads * p.blocks <= 4 * (int64_t)sms) {
+        int share = (n + p.blocks - 1) / p.blocks;
+        if (share < kWarps) share = kWarps;
+        const int bytes = k_scale ? granule_bytes<true> : granule_bytes<false>, most_slots = kRing / bytes;
+        p.slots = (share + kWarps - 1) / kWarps < most_slots ? (share + kWarps - 1) / kWarps : most_slots;
+        const size_t smem = 1024 + (size_t)kWarps * p.slots * bytes + (size_t)share * kGranule * p.pairs * sizeof(float2);
+        auto* kernel = k_scale ? cluster_kernel<true> : cluster_kernel<false>;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 1024 + kWarps * kRing + kClusterTokens * kMaxGroup * (int)sizeof(float)) != cudaSuccess) {
+            cudaGetLastError();
+            return PKV_ERR_CUDA;
+        }
+        return launch_early_clusters(kernel, dim3((unsigned)(kv_heads * p.blocks), (unsigned)rows), kThreads, smem,
+                                     (unsigned)p.blocks, stream, kmap, vmap, p);
+    }
     auto* attend = k_scale ? attend_kernel<true> : attend_kernel<false>;
     const int state = 64 * (int)sizeof(float);  // of a head
     const size_t smem = 1024 + (size_t)kWarps * (kRing + p.group * state) + ((size_t)rows + 1) * sizeof(int);

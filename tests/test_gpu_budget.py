@@ -230,6 +230,8 @@ DECODES = [
     ([20000, 50], 64, 12, 2),
     ([300 + 7 * i for i in range(70)], 16, 6, 2),       # units cut between blocks, odd groups
     ([1024] * 40, 64, 10, 2),
+    ([i * 37 % 500 for i in range(300)], 16, 12, 2),    # many short rows, some of nothing
+    ([5000, 70, 0], 16, 8, 1),
 ]
 
 
