@@ -52,7 +52,7 @@ constexpr int kFixed = 2;   // a unit's fixed tiles
 constexpr int kRaw = 2;     // tiles of codes
 constexpr int kBufs = kGroups;  // products in tensor memory, a group's each
 constexpr int kComb = 2;    // units whose sums the groups bring together
-constexpr int kAhead = 9;   // jobs between the copies and the sums, at most (ring + products below that)
+constexpr int kAhead = 12;  // jobs whose -e are kept: see the assertion
 constexpr int kMaxRows = 1024;
 constexpr uint32_t kHalf = kTile * 128;      // 128 rows x 64 dims
 constexpr uint32_t kOperand = 2 * kHalf;
@@ -160,7 +160,9 @@ struct Smem {
     static constexpr uint32_t comb = lse + kAhead * kTile * 4;
     static constexpr uint32_t bars = comb + kComb * (kGroups - 1) * kTile * 4;
     static_assert(kComb * (kGroups - 1) * 4 <= kAhead * 4, "the groups' sums fit");
-    static_assert(kRing + kBufs + 1 <= kAhead, "entries of jobs that the sums still need are not overwritten");
+    // -e of job j + kAhead are copied once the products of job j + kAhead - kRing are done, which were
+    // issued after the group of job j had read job j + kBufs, and so was done with job j.
+    static_assert(kAhead - kRing >= 2 * kBufs, "what the sums still need is not overwritten");
     static constexpr uint32_t misc = bars + 64 * 8;                      // tmem address, start [8], stop, warp sums
     static constexpr uint32_t bad = misc + 256;                          // [16] 16-token groups of K not to be seen
     static constexpr uint32_t rows = bad + 64;                           // 6 x [rows + 1] ints
@@ -593,115 +595,135 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         int units = 0, jobs = 0;
         Walk<kSums> c = at;
         const int group = p.group;
+        const int my_q = i / group, columns = nq * group;
+        // The 32 columns of chunk ch, all of which count but, of flat rows, those that no query has.
+        auto add_plain = [&](int ch, float& ref, float& acc, float sl2, uint64_t sl, const float4* lse) {
+            uint32_t v[32];
+            tmem_ld32(from_tmem + 32 * ch, v);
+            float base = 0.f;
+            if (!kSums) {
+                float a, z, top;  // the largest score, in base 2
+                if (sl2 >= 0.f) {
+                    a = z = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        a = fmaxf(fmaxf(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), a);
+                        z = fmaxf(fmaxf(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), z);
+                    }
+                    top = fmaxf(a, z) * sl2;
+                } else {
+                    a = z = INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 32; x += 4) {
+                        a = fminf(fminf(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), a);
+                        z = fminf(fminf(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), z);
+                    }
+                    top = fminf(a, z) * sl2;
+                }
+                if (top > ref + kMove) {  // (from -inf any score is)
+                    acc *= ref == -INFINITY ? 1.f : fast_exp2(ref - top);
+                    ref = top;
+                }
+                base = ref == -INFINITY ? 0.f : -ref;
+            }
+            uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+                float4 y = make_float4(base, base, base, base);
+                if (kSums) y = lse[ch * 8 + x / 4];
+                float a, b, d, f;
+                f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sl, f32x2(y.x, y.y)), a, b);
+                f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), sl, f32x2(y.z, y.w)), d, f);
+                if (kSums && x >= kCertain - 96) {  // zeros times a key that is no number
+                    const int from = 32 * ch + x;
+                    a = from < columns ? a : -INFINITY;
+                    b = from + 1 < columns ? b : -INFINITY;
+                    d = from + 2 < columns ? d : -INFINITY;
+                    f = from + 3 < columns ? f : -INFINITY;
+                }
+                s0 = add_f32x2(s0, f32x2(fast_exp2(a), fast_exp2(b)));
+                s1 = add_f32x2(s1, f32x2(fast_exp2(d), fast_exp2(f)));
+            }
+            float a, b;
+            f32x2_split(add_f32x2(s0, s1), a, b);
+            acc += a + b;
+        };
+        // The same of the columns in `seen`.
+        auto add_seen = [&](int ch, uint32_t seen, float& ref, float& acc, float sl2, const float4* lse) {
+            uint32_t v[32];
+            tmem_ld32(from_tmem + 32 * ch, v);
+            if (!__any_sync(0xffffffffu, seen != 0)) return;
+            float base = 0.f;
+            if (!kSums) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    if (seen >> x & 1) top = fmaxf(top, __uint_as_float(v[x]) * sl2);
+                if (top > ref + kMove) {
+                    acc *= ref == -INFINITY ? 1.f : fast_exp2(ref - top);
+                    ref = top;
+                }
+                base = ref == -INFINITY ? 0.f : -ref;
+            }
+            float s = 0.f;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+                const float y = kSums ? reinterpret_cast<const float*>(lse)[32 * ch + x] : base;
+                if (seen >> x & 1) s += fast_exp2(fmaf(__uint_as_float(v[x]), sl2, y));
+            }
+            acc += s;
+        };
+        auto let_go = [&] {  // the scores are read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_read + 8 * grp);
+        };
+        uint32_t turn = 0;  // parity of this group's next buffer
         // jobs of this block, in units: c stands at the first one not yet walked
         while (c.left > 0 && ok) {
             const int from = c.s, job0 = jobs;  // the piece's first job
             const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[c.k] : p.scale_log2;
             const uint64_t sl = f32x2(sl2, sl2);
             // Positions: query q of the row's used ones sees tokens up to p0 + q.
-            const int p0 = w.len[c.r] - w.used[c.r], end = min(c.n, c.s + c.left);
+            const int used = w.used[c.r], p0 = w.len[c.r] - used, end = min(c.n, c.s + c.left);
             float ref = -INFINITY, acc = 0.f;  // what exponents are taken from; the row's sum
+            const int skip = (grp - job0) & (kGroups - 1);
+            jobs += end - c.s;
 #pragma unroll 1
-            for (int o = c.s; o < end; ++o, ++jobs) {
-                if (jobs % kGroups != grp) continue;
-                const int e = jobs % kAhead, turn = jobs / kGroups;
-                if (!(ok = mbar_waitw(bar_done + 8 * grp, (uint32_t)turn & 1, stop))) break;
-                if (kSums && !(ok = mbar_waitw(bar_lse + 8 * e, (uint32_t)(jobs / kAhead) & 1, stop))) break;
+            for (int o = c.s + skip, job = job0 + skip; o < end; o += kGroups, job += kGroups, turn ^= 1) {
+                const int e = kSums ? job % kAhead : 0;
+                if (!(ok = mbar_waitw(bar_done + 8 * grp, turn, stop))) break;
+                if (kSums && !(ok = mbar_waitw(bar_lse + 8 * e, (uint32_t)(job / kAhead) & 1, stop))) break;
                 tc_fence_after();
-                const uint32_t hidden = (uint32_t)bad[(kSums ? units : jobs) & 15];
+                const uint32_t hidden = (uint32_t)bad[(kSums ? units : job) & 15];
                 const int q0 = (kSums ? o : c.x) * nq, t0 = (kSums ? c.x : o) * kTile;
-                const int here = min(nq, w.used[c.r] - q0);  // queries of the block
-                const bool plain = t0 + kTile - 1 <= p0 + q0 && here == nq && !hidden && nq * group >= kCertain;
-                // columns lo .. hi - 1 count
-                int lo = 0, hi = kTile;
-                if (!kSums) {
-                    const int q = i / group;  // row i: query; column: token
-                    hi = q < here ? p0 + q0 + q - t0 + 1 : 0;
-                } else {
-                    lo = max(0, t0 + i - p0 - q0) * group;  // row i: token; column: flat row
-                    hi = hidden >> (i >> 4) & 1 ? 0 : here * group;
-                }
+                const int here = min(nq, used - q0);  // queries of the block
                 const float4* lse = reinterpret_cast<const float4*>(smem + S::lse + e * kTile * 4);
+                if (t0 + kTile - 1 <= p0 + q0 && here == nq && !hidden && columns >= kCertain) {
 #pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t v[32];
-                    tmem_ld32(from_tmem + 32 * ch, v);
-                    if (!kSums && ch == 3) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar_read + 8 * grp);
+                    for (int ch = 0; ch < 4; ++ch) {
+                        add_plain(ch, ref, acc, sl2, sl, lse);
                     }
-                    uint32_t seen = low_bits(hi - 32 * ch) & ~low_bits(lo - 32 * ch);
-                    if (!kSums && hidden) {
-                        if (hidden >> (2 * ch) & 1) seen &= 0xffff0000u;
-                        if (hidden >> (2 * ch + 1) & 1) seen &= 0x0000ffffu;
-                    }
-                    float base = 0.f;
+                } else {
+                    // columns lo .. hi - 1 count
+                    int lo = 0, hi = kTile;
                     if (!kSums) {
-                        float top = -INFINITY;  // the largest score, in base 2
-                        if (!plain) {
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (seen >> x & 1) top = fmaxf(top, __uint_as_float(v[x]) * sl2);
-                        } else if (sl2 >= 0.f) {
-                            float a = -INFINITY, z = a;
-#pragma unroll
-                            for (int x = 0; x < 32; x += 4) {
-                                a = fmaxf(fmaxf(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), a);
-                                z = fmaxf(fmaxf(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), z);
-                            }
-                            top = fmaxf(a, z) * sl2;
-                        } else {
-                            float a = INFINITY, z = a;
-#pragma unroll
-                            for (int x = 0; x < 32; x += 4) {
-                                a = fminf(fminf(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), a);
-                                z = fminf(fminf(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), z);
-                            }
-                            top = fminf(a, z) * sl2;
-                        }
-                        if (top > ref + kMove || (ref == -INFINITY && top > ref)) {
-                            acc *= ref == -INFINITY ? 1.f : fast_exp2(ref - top);
-                            ref = top;
-                        }
-                        base = ref == -INFINITY ? 0.f : -ref;
-                    }
-                    if (plain) {
-                        uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
-#pragma unroll
-                        for (int x = 0; x < 32; x += 4) {
-                            float4 y = make_float4(base, base, base, base);
-                            if (kSums) y = lse[ch * 8 + x / 4];
-                            float a, b, d, f;
-                            f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), sl, f32x2(y.x, y.y)), a, b);
-                            f32x2_split(fma_f32x2(f32x2(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), sl, f32x2(y.z, y.w)), d, f);
-                            if (kSums && x >= kCertain - 96 && ch == 3) {  // zeros times a key that is no number
-                                a = seen >> x & 1 ? a : -INFINITY;
-                                b = seen >> (x + 1) & 1 ? b : -INFINITY;
-                                d = seen >> (x + 2) & 1 ? d : -INFINITY;
-                                f = seen >> (x + 3) & 1 ? f : -INFINITY;
-                            }
-                            s0 = add_f32x2(s0, f32x2(fast_exp2(a), fast_exp2(b)));
-                            s1 = add_f32x2(s1, f32x2(fast_exp2(d), fast_exp2(f)));
-                        }
-                        float a, b;
-                        f32x2_split(add_f32x2(s0, s1), a, b);
-                        acc += a + b;
+                        hi = my_q < here ? p0 + q0 + my_q - t0 + 1 : 0;  // row i: query; column: token
                     } else {
-                        float s = 0.f;
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            const float y = kSums ? reinterpret_cast<const float*>(lse)[32 * ch + x] : base;
-                            if (seen >> x & 1) s += fast_exp2(fmaf(__uint_as_float(v[x]), sl2, y));
+                        lo = max(0, t0 + i - p0 - q0) * group;  // row i: token; column: flat row
+                        hi = hidden >> (i >> 4) & 1 ? 0 : here * group;
+                    }
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        uint32_t seen = low_bits(hi - 32 * ch) & ~low_bits(lo - 32 * ch);
+                        if (!kSums && hidden) {
+                            if (hidden >> (2 * ch) & 1) seen &= 0xffff0000u;
+                            if (hidden >> (2 * ch + 1) & 1) seen &= 0x0000ffffu;
                         }
-                        acc += s;
+                        add_seen(ch, seen, ref, acc, sl2, lse);
                     }
                 }
-                if (kSums) {  // -e is read too
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_read + 8 * grp);
-                }
+                let_go();
             }
             if (!ok) break;
             // ---- the block's piece of the unit: the groups' sums ----

@@ -37,7 +37,7 @@ namespace rope {
 
 constexpr int kThreads = 256;
 constexpr int kBlocks = 5;   // resident per SM
-constexpr int kNormBlocks = 4;  // of the kernel with norms
+constexpr int kNormBlocks = 3;  // of the kernel with norms
 constexpr int kTokens = 32;  // tokens per block, at most
 
 // n / d for n < 2^16 and 1 <= d < 2^16, by one multiplication.
