@@ -642,3 +642,110 @@ def test_evict_in_a_graph_on_another_stream(cuda_device):
         graph.replay()
         torch.cuda.synchronize()
         x.check((args["k_pool"], args["v_pool"], args["weights"], args["token_pos"], new))
+
+
+# ---- the calls together ----
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_kept_within_a_budget(cuda_device, fp8):
+    """Two layers: prompts written, attended to and weighed by their last queries, cut to a
+    budget; then steps of one token each, cut again every few.  Every slot holds the key and
+    value of the position that its list records, bit for bit, each list is the definition's, and each
+    step's output and weights are those of the tokens that are left."""
+    prompt, budget, sinks, recent, bs, hq, hk, layers = [150, 40, 77], 64, 4, 16, 16, 12, 2, 2
+    rows, steps, scale, window = 3, 9, 0.0883, 16
+    top = max(prompt)
+    cap = top + steps
+    step = Step([0] * rows, [n + steps for n in prompt], bs, fp8=fp8, layers=layers, seed=700)
+    gen = step.gen
+    k_pool, v_pool = step.k_pool.cuda(), step.v_pool.cuda()
+    tables = i32(step.tables)
+    ks, vs = (None, None) if not fp8 else (step.k_scale.cuda(), step.v_scale.cuda())
+    qw, kw = ((1 + 0.1 * torch.randn(128, generator=gen)).half().cuda() for _ in range(2))
+    rates, err = ops.rope_rates(ops.rope_frequencies(128)), err_word()
+    weights = torch.zeros(layers, rows, hk, cap, device="cuda")
+    pos = torch.zeros(layers, rows, hk, cap, dtype=torch.int32, device="cuda")
+    kept = {}                                   # (layer, row, head, position): key and value as stored
+
+    def slots(r, t):
+        t = np.asarray(t)
+        return torch.from_numpy(step.tables[r, t // bs].astype(np.int64) * bs + t % bs).cuda()
+
+    def stored(layer, r, h, t):
+        s = slots(r, t)
+        return k_pool[layer].view(-1, hk, 128)[s, h], v_pool[layer].view(-1, hk, 128)[s, h]
+
+    def widened(x, scale_, h):
+        return (x.view(torch.float8_e4m3fn).double() * scale_[h].double() if fp8 else x.double()).cpu()
+
+    def append(layer, lens, counts, at):
+        starts = np.concatenate([[0], np.cumsum(counts)])
+        x = torch.randn(int(starts[-1]), hq + 2 * hk, 128, generator=gen).half().cuda()
+        q = torch.empty(int(starts[-1]), hq, 128, dtype=torch.float16, device="cuda")
+        ops.norm_rope_append(k_pool[layer], v_pool[layer], tables, i32(lens), i32(starts), x[:, hq:hq + hk],
+                             x[:, hq + hk:], rates, kw, cap, q=x[:, :hq], q_out=q, q_weight=qw,
+                             rope_positions=i32(at), k_scale=ks, v_scale=vs, dev_err=err)
+        for r in range(rows):
+            for h in range(hk):
+                t = np.arange(lens[r] - counts[r], lens[r])
+                for p, kk, vv in zip(at[starts[r]:], *stored(layer, r, h, t)):
+                    kept[layer, r, h, int(p)] = (kk.clone(), vv.clone())
+        return q, i32(starts)
+
+    def evict(lens, tracked, nxt):
+        want = []
+        for i in np.ndindex(layers, rows, hk):
+            r, n = i[1], lens[i[1]]
+            t = np.arange(n)
+            p = np.where(t < tracked[r], pos[i][:n].cpu().numpy(), nxt[r] - n + t)
+            w = weights[i][:n].cpu().numpy()
+            safe = (p < sinks) | (p >= nxt[r] - recent)
+            stays = np.zeros(n, dtype=bool)
+            stays[np.lexsort((t, -w, -safe.astype(int)))[:budget]] = True
+            want.append((i, dict(zip(p[stays].tolist(), w[stays].tolist()))))
+        new = torch.empty(rows, dtype=torch.int32, device="cuda")
+        ops.evict(k_pool, v_pool, tables, i32(lens), weights, pos, budget, cap, sinks=sinks, recent=recent,
+                  tracked=i32(tracked), next_pos=i32(nxt), new_seq_lens=new, dev_err=err)
+        left = new.tolist()
+        assert left == [min(n, budget) for n in lens]
+        for i, keep in want:
+            n = left[i[1]]
+            p = pos[i][:n].tolist()
+            assert dict(zip(p, weights[i][:n].tolist())) == keep
+            for at, kk, vv in zip(p, *stored(*i, np.arange(n))):
+                assert torch.equal(kk, kept[(*i, at)][0]) and torch.equal(vv, kept[(*i, at)][1])
+        return left
+
+    lens, nxt = list(prompt), list(prompt)
+    total = sum(prompt)
+    at = np.concatenate([np.arange(n) for n in prompt])
+    ws = ops.alloc_prefill_weights_workspace(rows, total, hq, hk, 128, cap, bs, window=window)
+    for layer in range(layers):
+        q, starts = append(layer, lens, prompt, at)
+        ops.prefill_weights(weights[layer], q, k_pool[layer], tables, i32(lens), starts, scale, cap, ws, window=window,
+                            k_scale=ks, dev_err=err)
+        given = weights[layer].sum(-1).cpu()     # every query gives each head's whole weight
+        for r, n in enumerate(prompt):
+            assert torch.allclose(given[r], torch.full((hk,), float(min(n, window) * hq // hk)), rtol=1e-4, atol=0)
+    tracked = [0] * rows
+    lens = tracked = evict(lens, tracked, nxt)
+    ws = ops.alloc_decode_weights_workspace(rows, hq, hk, 128, cap, bs)
+    for i in range(steps):
+        lens, nxt = [n + 1 for n in lens], [n + 1 for n in nxt]
+        for layer in range(layers):
+            q, _ = append(layer, lens, [1] * rows, np.array(nxt) - 1)
+            before, out = weights[layer].cpu().double(), torch.empty_like(q)
+            ops.decode_weights(out, weights[layer], q, k_pool[layer], v_pool[layer], tables, i32(lens), scale, cap, ws,
+                               k_scale=ks, v_scale=vs, dev_err=err)
+            for r in range(rows):
+                for h in range(hk):
+                    kk, vv = stored(layer, r, h, np.arange(lens[r]))
+                    kk, vv = widened(kk, ks, h), widened(vv, vs, h)
+                    p = torch.softmax(q[r, 6 * h:6 * h + 6].double().cpu() @ kk.T * scale, -1)
+                    w = before[r, h, :lens[r]]
+                    w[-1] = 0
+                    assert torch.allclose(weights[layer, r, h, :lens[r]].cpu().double(), w + p.sum(0), rtol=1e-4, atol=1e-6)
+                    assert torch.allclose(out[r, 6 * h:6 * h + 6].double().cpu(), p @ vv, rtol=4e-3, atol=4e-3)
+        if i % 4 == 3:
+            lens = tracked = evict(lens, tracked, nxt)
+    assert int(err.item()) == 0 and nxt == [n + steps for n in prompt]
