@@ -26,8 +26,10 @@
 namespace pkv {
 namespace evict {
 
-constexpr int kShortThreads = 128, kLongThreads = 512;  // of a short and a long list's blocks
-constexpr int kShort = 4096;       // tokens of a short list, at most
+// Threads of a list's blocks, and blocks an SM: of lists of up to kSmall tokens, up to kShort, and long ones.
+constexpr int kSmallThreads = 128, kSmallBlocks = 12, kSmall = 2048;
+constexpr int kShortThreads = 256, kShortBlocks = 5, kShort = 4096;
+constexpr int kLongThreads = 512, kLongBlocks = 2;
 constexpr int kChunk = 4096;       // tokens of a long list's block, while its cluster may still grow
 constexpr int kMostBlocks = 8;     // of a cluster (the portable limit)
 constexpr int kMostChunk = 24576;  // tokens of a block, at most: 6 bytes of shared memory each
@@ -232,9 +234,9 @@ __device__ __forceinline__ void move_tokens(const Params& p, const List& l, int 
     }
 }
 
-// kThreads a block; kCluster: p.blocks blocks a list.
-template <int kThreads, bool kCluster>
-__global__ void __launch_bounds__(kThreads, kCluster ? 2 : 10) evict_kernel(const __grid_constant__ Params p) {
+// kThreads a block, kBlocks blocks an SM; kCluster: p.blocks blocks a list.
+template <int kThreads, int kBlocks, bool kCluster>
+__global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const __grid_constant__ Params p) {
     constexpr int kWarps = kThreads / 32, kPer = kBins / kThreads;
     constexpr int kRounds = (kCluster ? kMostChunk : kShort) / (4 * kThreads);  // of 128 tokens a warp, at most
     extern __shared__ uint4 dyn[];
@@ -298,12 +300,14 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : 10) evict_kernel(cons
             mine[2] = safe;
         }
         cluster_sync();
-        safe = 0;
-        for (int c = 0; c < blocks; ++c) {
-            any |= peer_word(ptx::smem_u32(mine), c);
-            every &= peer_word(ptx::smem_u32(mine + 1), c);
-            safe += peer_word(ptx::smem_u32(mine + 2), c);
-        }
+        // lane c asks block c
+        const bool there = lane < blocks;
+        const uint32_t a = there ? peer_word(ptx::smem_u32(mine), lane) : 0u;
+        const uint32_t b = there ? peer_word(ptx::smem_u32(mine + 1), lane) : ~0u;
+        const uint32_t c = there ? peer_word(ptx::smem_u32(mine + 2), lane) : 0u;
+        any = __reduce_or_sync(0xffffffffu, a);
+        every = __reduce_and_sync(0xffffffffu, b);
+        safe = __reduce_add_sync(0xffffffffu, c);
     }
 
     // ---- the last key that stays: its digits from bit `shift` on are `prefix`, and of the
@@ -343,13 +347,24 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : 10) evict_kernel(cons
             const int slice = kBins / blocks;
             for (int i = tid; i < slice; i += kThreads) {
                 const int b = rank * slice + i;
-                uint32_t t = 0;
-                for (int c = 0; c < blocks; ++c) t += peer_word(ptx::smem_u32(hist + b), c);
+                uint32_t x[kMostBlocks], t = 0;  // (asked for together)
+#pragma unroll
+                for (int c = 0; c < kMostBlocks; ++c) x[c] = c < blocks ? peer_word(ptx::smem_u32(hist + b), c) : 0u;
+#pragma unroll
+                for (int c = 0; c < kMostBlocks; ++c) t += x[c];
                 all[b] = t;
             }
             cluster_sync();
-            for (int b = tid; b < kBins; b += kThreads) {
-                if (b / slice != rank) all[b] = peer_word(ptx::smem_u32(all + b), b / slice);
+            uint32_t x[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int b = tid + j * kThreads;
+                x[j] = peer_word(ptx::smem_u32(all + b), b / slice);
+            }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int b = tid + j * kThreads;
+                if (b / slice != rank) all[b] = x[j];
                 hist[b] = 0;
             }
             cluster_sync();
@@ -441,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : 10) evict_kernel(cons
         if (kCluster) {
             if (tid == 0) mine[3] = total;
             cluster_sync();
-            for (int c = 0; c < rank; ++c) before += peer_word(ptx::smem_u32(mine + 3), c);
+            before += __reduce_add_sync(0xffffffffu, lane < rank ? peer_word(ptx::smem_u32(mine + 3), lane) : 0u);
             cluster_sync();  // mine[3] is written again below
         }
         left = before < need ? need - before : 0u;
@@ -610,20 +625,25 @@ extern "C" int paged_kv_evict(void* k_pool, void* v_pool, const int32_t* block_t
     p.dev_err = dev_err;
     p.vec4 = weights_stride % 4 == 0 && aligned16(weights) && aligned16(token_pos) && aligned16(weights_out) &&
              aligned16(token_pos_out);
-    const bool is_short = max_seq_len <= kShort;
+    // Many small lists want many blocks resident (1792 of 1025 tokens: 18.5 us with 128 threads, 24.6
+    // with 256), larger ones more warps for their moves (896 of 1900 to 2304, E4M3: 28.3 and 23.7).
+    const bool is_small = max_seq_len <= kSmall, is_short = max_seq_len <= kShort;
     p.blocks = is_short ? 1 : 2;
     while (!is_short && p.blocks < kMostBlocks && (max_seq_len + p.blocks - 1) / p.blocks > kChunk) p.blocks *= 2;
     // whole rounds of a block's warps; a block's share is a multiple of four tokens
-    const int round = 4 * (is_short ? kShortThreads : kLongThreads);
+    const int threads = is_small ? kSmallThreads : is_short ? kShortThreads : kLongThreads, round = 4 * threads;
     p.cap = (((max_seq_len + p.blocks - 1) / p.blocks + 3) / 4 * 4 + round - 1) / round * round;
     const size_t smem = (size_t)p.cap * 6;
     const dim3 grid((unsigned)(kv_heads * p.blocks), (unsigned)rows, (unsigned)layers);
-    if (is_short) return launch_early(evict_kernel<kShortThreads, false>, grid, kShortThreads, smem, stream, p);
-    auto* kernel = evict_kernel<kLongThreads, true>;
+    if (is_small)
+        return launch_early(evict_kernel<kSmallThreads, kSmallBlocks, false>, grid, threads, smem, stream, p);
+    if (is_short)
+        return launch_early(evict_kernel<kShortThreads, kShortBlocks, false>, grid, threads, smem, stream, p);
+    auto* kernel = evict_kernel<kLongThreads, kLongBlocks, true>;
     if (smem > 32768 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostChunk * 6) != cudaSuccess) {
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }
-    return launch_early_clusters(kernel, grid, kLongThreads, smem, (unsigned)p.blocks, stream, p);
+    return launch_early_clusters(kernel, grid, threads, smem, (unsigned)p.blocks, stream, p);
 }
