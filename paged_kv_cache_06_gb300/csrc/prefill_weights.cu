@@ -699,7 +699,8 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                 const int q0 = (kSums ? o : c.x) * nq, t0 = (kSums ? c.x : o) * kTile;
                 const int here = min(nq, used - q0);  // queries of the block
                 const float4* lse = reinterpret_cast<const float4*>(smem + S::lse + e * kTile * 4);
-                if (t0 + kTile - 1 <= p0 + q0 && here == nq && !hidden && columns >= kCertain) {
+                // (1: what rows behind the queries get is not used)
+                if (t0 + kTile - 1 <= p0 + q0 && !hidden && (!kSums || (here == nq && columns >= kCertain))) {
 #pragma unroll 1
                     for (int ch = 0; ch < 4; ++ch) {
                         add_plain(ch, ref, acc, sl2, sl, lse);
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                     // columns lo .. hi - 1 count
                     int lo = 0, hi = kTile;
                     if (!kSums) {
-                        hi = my_q < here ? p0 + q0 + my_q - t0 + 1 : 0;  // row i: query; column: token
+                        hi = p0 + q0 + my_q - t0 + 1;  // row i: query; column: token
                     } else {
                         lo = max(0, t0 + i - p0 - q0) * group;  // row i: token; column: flat row
                         hi = hidden >> (i >> 4) & 1 ? 0 : here * group;
@@ -720,7 +721,10 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                             if (hidden >> (2 * ch) & 1) seen &= 0xffff0000u;
                             if (hidden >> (2 * ch + 1) & 1) seen &= 0x0000ffffu;
                         }
-                        add_seen(ch, seen, ref, acc, sl2, lse);
+                        if (__all_sync(0xffffffffu, seen == ~0u))
+                            add_plain(ch, ref, acc, sl2, sl, lse);
+                        else
+                            add_seen(ch, seen, ref, acc, sl2, lse);
                     }
                 }
                 let_go();
