@@ -1,5 +1,6 @@
 """Build libpagedkv.so in-tree from csrc/ (nvcc for sm_103a, g++ for host code),
-and the Python binding of the drafted step's calls, ``_binding.so``.
+and the Python binding of the calls of a drafted step and of a cache within a
+budget, ``_binding.so``.
 
 Translation units compile in parallel into ``_build/`` and link into
 ``paged_kv_cache_06_gb300/libpagedkv.so``, for which nvcc and g++ are enough;

@@ -20,6 +20,13 @@
 // are a lane's, 128 a warp's, at once.  The moves are dealt to the warps 32 at a time:
 // a lane finds one move's slots through the table and moves its weight and
 // position, then the warp moves the keys and values, several vectors in flight a lane.
+//
+// What bounds it.  The choice is a chain: load, differing bits, one to four histograms, the
+// equal keys, the slots.  1792 lists of 1025 tokens, of which one leaves each (14.7 MB of weights
+// and positions): 18.3 us, 16.8 without the move; all blocks are resident at once, 12 an SM.
+// 896 lists of 1900 to 2304, E4M3: 23.6 us, 15.3 of them the choice.  56 lists of 15,360 down to
+// 2048: 39.9 us, 18.4 the choice (three cluster barriers a histogram) and 21.5 the
+// moves, 102 MB in pieces of 256 bytes, 4.7 TB/s.
 #include "pkv_internal.cuh"
 #include "ptx.cuh"
 
@@ -30,7 +37,9 @@ namespace evict {
 constexpr int kSmallThreads = 128, kSmallBlocks = 12, kSmall = 2048;
 constexpr int kShortThreads = 256, kShortBlocks = 5, kShort = 4096;
 constexpr int kLongThreads = 512, kLongBlocks = 2;
-constexpr int kChunk = 4096;       // tokens of a long list's block, while its cluster may still grow
+// Tokens of a long list's block, while its cluster may still grow: 56 lists of 15,360 with 8192 a block
+// (clusters of two) 44.3 us, 4096 39.9, 2048 39.8; of two as good the smaller cluster.
+constexpr int kChunk = 4096;
 constexpr int kMostBlocks = 8;     // of a cluster (the portable limit)
 constexpr int kMostChunk = 24576;  // tokens of a block, at most: 6 bytes of shared memory each
 constexpr int kDigit = 10, kBins = 1 << kDigit;
@@ -626,7 +635,8 @@ extern "C" int paged_kv_evict(void* k_pool, void* v_pool, const int32_t* block_t
     p.vec4 = weights_stride % 4 == 0 && aligned16(weights) && aligned16(token_pos) && aligned16(weights_out) &&
              aligned16(token_pos_out);
     // Many small lists want many blocks resident (1792 of 1025 tokens: 18.5 us with 128 threads, 24.6
-    // with 256), larger ones more warps for their moves (896 of 1900 to 2304, E4M3: 28.3 and 23.7).
+    // with 256), larger ones more warps for their moves (896 of 1900 to 2304, E4M3: 28.3 and 23.7), and a
+    // cluster pays only where a list is too long for a block of that size (the same 896: 86.9).
     const bool is_small = max_seq_len <= kSmall, is_short = max_seq_len <= kShort;
     p.blocks = is_short ? 1 : 2;
     while (!is_short && p.blocks < kMostBlocks && (max_seq_len + p.blocks - 1) / p.blocks > kChunk) p.blocks *= 2;

@@ -55,8 +55,9 @@ def lib() -> ctypes.CDLL:
 
 
 def binding():
-    """The C++ binding module of the drafted step's calls (built first if it is
-    missing or stale; loads the library, which it links against)."""
+    """The C++ binding module of the calls of a drafted step and of a cache within a
+    budget (built first if it is missing or stale; loads the library, which it links
+    against)."""
     global _ext
     lib()
     with _lock:
