@@ -14,8 +14,8 @@
 // it, so the moves have no order among themselves, and there are as few as can be: the
 // tokens that leave, not the tokens that stay.
 //
-// Work.  A short list has a small block, a long one a cluster of blocks; every
-// block holds its share of the keys in shared memory, and a cluster's blocks add up their
+// Work.  A short list has a small block, a long one a larger block or, where there are few, a
+// cluster of them; every block holds its share of the keys in shared memory, and a cluster's blocks add up their
 // histograms and counts through distributed shared memory.  Four neighbouring tokens
 // are a lane's, 128 a warp's, at once.  The moves are dealt to the warps 32 at a time:
 // a lane finds one move's slots through the table and moves its weight and
@@ -24,9 +24,9 @@
 // What bounds it.  The choice is a chain: load, differing bits, one to four histograms, the
 // equal keys, the slots.  1792 lists of 1025 tokens, of which one leaves each (14.7 MB of weights
 // and positions): 18.3 us, 16.8 without the move; all blocks are resident at once, 12 an SM.
-// 896 lists of 1900 to 2304, E4M3: 23.6 us, 15.3 of them the choice.  56 lists of 15,360 down to
-// 2048: 39.9 us, 18.4 the choice (three cluster barriers a histogram) and 21.5 the
-// moves, 102 MB in pieces of 256 bytes, 4.7 TB/s.
+// 896 lists of 1900 to 2304, E4M3: 23.6 us, 15.3 of them the choice.  32 lists of 30,000 to 32,768 down
+// to 4096: 39.9 us, 18.4 the choice (three cluster barriers a histogram) and 21.5 the
+// moves, 117 MB in pieces of 256 bytes, 5.4 TB/s.
 #include "pkv_internal.cuh"
 #include "ptx.cuh"
 
@@ -37,9 +37,7 @@ namespace evict {
 constexpr int kSmallThreads = 128, kSmallBlocks = 12, kSmall = 2048;
 constexpr int kShortThreads = 256, kShortBlocks = 5, kShort = 4096;
 constexpr int kLongThreads = 512, kLongBlocks = 2;
-// Tokens of a long list's block, while its cluster may still grow: 56 lists of 15,360 with 8192 a block
-// (clusters of two) 44.3 us, 4096 39.9, 2048 39.8; of two as good the smaller cluster.
-constexpr int kChunk = 4096;
+constexpr int kChunk = 4096;       // tokens of a long list's block, while its cluster may still grow
 constexpr int kMostBlocks = 8;     // of a cluster (the portable limit)
 constexpr int kMostChunk = 24576;  // tokens of a block, at most: 6 bytes of shared memory each
 constexpr int kDigit = 10, kBins = 1 << kDigit;
@@ -247,7 +245,7 @@ __device__ __forceinline__ void move_tokens(const Params& p, const List& l, int 
 template <int kThreads, int kBlocks, bool kCluster>
 __global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const __grid_constant__ Params p) {
     constexpr int kWarps = kThreads / 32, kPer = kBins / kThreads;
-    constexpr int kRounds = (kCluster ? kMostChunk : kShort) / (4 * kThreads);  // of 128 tokens a warp, at most
+    constexpr int kRounds = (kThreads == kLongThreads ? kMostChunk : kShort) / (4 * kThreads);  // of 128 tokens a warp, at most
     extern __shared__ uint4 dyn[];
     uint32_t* keys = reinterpret_cast<uint32_t*>(dyn);             // [cap]
     uint16_t* list = reinterpret_cast<uint16_t*>(keys + p.cap);    // [cap]: holes from the front, fillers from the back
@@ -635,11 +633,21 @@ extern "C" int paged_kv_evict(void* k_pool, void* v_pool, const int32_t* block_t
     p.vec4 = weights_stride % 4 == 0 && aligned16(weights) && aligned16(token_pos) && aligned16(weights_out) &&
              aligned16(token_pos_out);
     // Many small lists want many blocks resident (1792 of 1025 tokens: 18.5 us with 128 threads, 24.6
-    // with 256), larger ones more warps for their moves (896 of 1900 to 2304, E4M3: 28.3 and 23.7), and a
-    // cluster pays only where a list is too long for a block of that size (the same 896: 86.9).
+    // with 256), larger ones more warps for their moves (896 of 1900 to 2304, E4M3: 28.3 and 23.7), and
+    // clusters of large blocks do not pay at such lengths (the same 896: 86.9).  Long lists: a cluster of
+    // blocks of up to kChunk tokens, as long as all blocks are resident at once.  32 lists of 16,384 to
+    // 2048: two blocks 40.2 us, four 27.5, eight 32.4; 128 of them: two 61.6, four 72.3; 224: one 109.7, two
+    // 113.7, four 124.3; 224 of 8192 to 1024: one 48.9, two 65.1, four 93.2; 32 of 8192: two 22.2, four 20.8.
     const bool is_small = max_seq_len <= kSmall, is_short = max_seq_len <= kShort;
-    p.blocks = is_short ? 1 : 2;
-    while (!is_short && p.blocks < kMostBlocks && (max_seq_len + p.blocks - 1) / p.blocks > kChunk) p.blocks *= 2;
+    p.blocks = 1;
+    const int sms = device_sms();
+    if (sms <= 0) return PKV_ERR_CUDA;
+    const int64_t resident = (int64_t)sms * kLongBlocks;
+    while (!is_short && p.blocks < kMostBlocks) {
+        const int chunk = (max_seq_len + p.blocks - 1) / p.blocks;
+        if (chunk <= kMostChunk && (chunk <= kChunk || lists * 2 * p.blocks > resident)) break;
+        p.blocks *= 2;
+    }
     // whole rounds of a block's warps; a block's share is a multiple of four tokens
     const int threads = is_small ? kSmallThreads : is_short ? kShortThreads : kLongThreads, round = 4 * threads;
     p.cap = (((max_seq_len + p.blocks - 1) / p.blocks + 3) / 4 * 4 + round - 1) / round * round;
@@ -649,7 +657,8 @@ extern "C" int paged_kv_evict(void* k_pool, void* v_pool, const int32_t* block_t
         return launch_early(evict_kernel<kSmallThreads, kSmallBlocks, false>, grid, threads, smem, stream, p);
     if (is_short)
         return launch_early(evict_kernel<kShortThreads, kShortBlocks, false>, grid, threads, smem, stream, p);
-    auto* kernel = evict_kernel<kLongThreads, kLongBlocks, true>;
+    auto* kernel = p.blocks > 1 ? evict_kernel<kLongThreads, kLongBlocks, true>
+                                : evict_kernel<kLongThreads, kLongBlocks, false>;
     if (smem > 32768 &&
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostChunk * 6) != cudaSuccess) {
         cudaGetLastError();

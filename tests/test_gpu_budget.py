@@ -586,6 +586,20 @@ def test_evict_orders_ties_zeros_and_what_is_no_number(cuda_device, weights, len
     x.check(x.run())
 
 
+# Lists too long for a small block, and so many that each has one large block, or a cluster of two with a
+# large share each.
+@pytest.mark.parametrize("lens,hk,layers", [([5000, 4097] + [4500] * 18, 4, 2), ([20000, 24576] + [6000] * 38, 4, 1),
+                                            ([24577] + [5000] * 39, 4, 1), ([16500, 9000] + [4000] * 14, 4, 2)])
+@pytest.mark.parametrize("weights", [None, odd_numbers, ties])
+def test_evict_of_many_long_lists(cuda_device, lens, hk, layers, weights):
+    x = Lists(lens, 3900, layers=layers, hk=hk, d=16, bs=64, sinks=2, recent=30, weights=weights, seed=len(lens))
+    for in_place in (True, False):
+        err = err_word()
+        got = x.run(in_place=in_place, err=err)
+        assert int(err.item()) == 0
+        x.check(got, in_place)
+
+
 def test_evict_of_a_first_time_takes_slots_for_positions(cuda_device):
     x = Lists([100, 60, 300], 64, sinks=4, recent=20, seed=5)
     x.check(x.run(bare=True))
