@@ -22,7 +22,7 @@
 // block's piece of the unit.
 // The second kernel: each block finds its unit's maxima and sums over the pieces, and
 // finishes a quarter of the unit's output or 1024 tokens' weights, in the same order every time.
-// Few short rows take one launch instead: a cluster of up to eight blocks a unit, each with
+// Short rows take one launch instead: a block a unit, or a cluster of up to eight, each with
 // a contiguous share of its granules; the scores stay in shared memory, the blocks tell
 // each other their maxima and sums and the parts of the output that another of them finishes
 // through distributed shared memory, and each turns its own scores into weights.
@@ -51,6 +51,7 @@ constexpr int kMaxRows = 1024;
 constexpr float kMove = 8.f;
 constexpr int kClusterBlocks = 8;    // of a cluster, at most (the portable limit)
 constexpr int kClusterTokens = 4096; // of a row that a cluster takes, at most
+constexpr int kShare = 64;           // granules of its block, at most
 constexpr int kEndThreads = 256;     // of the second kernel: a warp a head
 constexpr int kEndTokens = 4;        // a thread
 constexpr int kTile = kEndThreads * kEndTokens;
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kEndThreads) merge_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------------------
-// Short rows: a cluster of blocks a unit, one launch.
+// Short rows: a block or a cluster of them a unit, one launch.
 
 __device__ __forceinline__ uint32_t block_rank() {
     uint32_t r;
@@ -1002,24 +1003,26 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     int st = tiled_map_3d(k_pool, type, dims, strides, box, &kmap);
     if (st == PKV_OK) st = tiled_map_3d(v_pool, type, dims, strides, box, &vmap);
     if (st != PKV_OK) return st;
-    // Clusters of up to eight blocks, four granules a warp of the longest row while a cluster may
-    // grow, where they are few enough to be resident at once, four an SM: one launch instead
-    // of two.  Clusters against the even cut, 2 KV heads: 4 rows of 100 tokens 4.7 us and 6.6,
-    // one of 4096 9.6 and 14.3, 32 of 1024 (E4M3) 9.0 and 11.7, 32 of 16 to 512 and one of 4096
-    // 10.9 and 12.1; but 32 of 4096 33.9 and 31.0, and, past four an SM, 96 of 16 to 600 and
-    // one of 4000 29.4 and 18.1, 128 of 2048 75.6 and 55.6.
+    // A block a unit, or a cluster of up to eight, four granules a warp of the longest row, while they
+    // are few enough to be resident at once, four an SM: one launch instead of two.
+    // Against the even cut, 2 KV heads: 4 rows of 100 tokens 4.7 us and 6.6, one of 4096 9.6 and 14.3,
+    // 32 of 1024 (E4M3) 9.0 and 11.7, 32 of 16 to 512 and one of 4096 10.9 and 12.1, 512 of 128 15.0
+    // and 31.8, 512 of 1 to 1024 54 and 71, 512 of 1 to 128 and one of 1024 17 and 34; but 32 of 4096
+    // 33 and 31 (E4M3: 23 and 17.5).  Shares of more than 64 granules, or 4096 tokens, are the even
+    // cut's: 96 rows of 16 to 600 and one of 4000 took clusters in waves 29.4 us, the even cut 18.1.
     const int n = l.tokens / kGranule;
     p.blocks = 1;
-    while (p.blocks < kClusterBlocks && p.blocks * 4 * kWarps < n) p.blocks *= 2;
-    if (max_seq_len <= kClusterTokens && (int64_t)rows * kv_heads * p.blocks <= 4 * (int64_t)sms) {
-        int share = (n + p.blocks - 1) / p.blocks;
+    const int64_t units = (int64_t)rows * kv_heads, resident = 4 * (int64_t)sms;
+    while (p.blocks < kClusterBlocks && p.blocks * 4 * kWarps < n && units * 2 * p.blocks <= resident) p.blocks *= 2;
+    int share = (n + p.blocks - 1) / p.blocks;
+    if (max_seq_len <= kClusterTokens && share <= kShare) {
         if (share < kWarps) share = kWarps;
         const int bytes = k_scale ? granule_bytes<true> : granule_bytes<false>, most_slots = kRing / bytes;
         p.slots = (share + kWarps - 1) / kWarps < most_slots ? (share + kWarps - 1) / kWarps : most_slots;
         const size_t smem = 1024 + (size_t)kWarps * p.slots * bytes + (size_t)share * kGranule * p.pairs * sizeof(float2);
         auto* kernel = k_scale ? cluster_kernel<true> : cluster_kernel<false>;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 1024 + kWarps * kRing + kClusterTokens * kMaxGroup * (int)sizeof(float)) != cudaSuccess) {
+                                 1024 + kWarps * kRing + kShare * kGranule * kMaxGroup * (int)sizeof(float)) != cudaSuccess) {
             cudaGetLastError();
             return PKV_ERR_CUDA;
         }

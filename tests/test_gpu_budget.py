@@ -232,6 +232,12 @@ DECODES = [
     ([1024] * 40, 64, 10, 2),
     ([i * 37 % 500 for i in range(300)], 16, 12, 2),    # many short rows, some of nothing
     ([5000, 70, 0], 16, 8, 1),
+    ([300 + 7 * i for i in range(70)] + [4200], 16, 6, 2),  # the same beside rows too long for clusters
+    ([1024] * 40 + [4097], 64, 10, 2),
+    ([i * 37 % 500 for i in range(300)] + [4300], 16, 12, 2),
+    ([1 + i * 331 % 1024 for i in range(200)], 16, 12, 2),      # a block a unit, more than there is room for
+    ([i * 7 % 70 for i in range(400)], 32, 14, 2),
+    ([2048, 1, 0, 1025] + [i * 61 % 700 for i in range(110)], 64, 16, 2),  # clusters of two, their largest shares
 ]
 
 
