@@ -10,7 +10,7 @@
 //
 // Work.  Each unit, one KV head of a row, has its tokens in 16-token granules; all granules
 // of all units, in (row, head, token) order, are cut into equal contiguous ranges, one for
-// each of three blocks an SM.  A block's four warps take its granules in turn, each through
+// each of up to three blocks an SM.  A block's four warps take its granules in turn, each through
 // a ring of its own that it fills by tiled copies, one box of 16 tokens and 64 dims (128
 // codes) each; 192 KB an SM are on their way.  A granule costs a warp
 //   S^T[16 tok][8 heads] = K Q^T, then O^T[128][8] += V^T P^T, P in fp16,
@@ -56,6 +56,7 @@ constexpr int kEndThreads = 256;     // of the second kernel: a warp a head
 constexpr int kEndTokens = 4;        // a thread
 constexpr int kTile = kEndThreads * kEndTokens;
 constexpr int kOutBlocks = 4;        // of the second kernel for a unit's output
+constexpr int kLeast = 8;            // granules of a range
 constexpr int kAhead = 4;            // pieces of an output that a thread asks for at once
 static_assert(kMaxGroup * kHeadDim / 4 <= kOutBlocks * kEndThreads, "a thread a group of four dims");
 constexpr float kLog2e = 1.4426950408889634f;
@@ -93,6 +94,11 @@ __device__ __forceinline__ int owner_of(int g, int W, int n) {
     if ((int64_t)c * W > x) --c;
     return c;
 }
+
+// Ranges that W granules are cut into: one a block, but kLeast granules in each where there are few, since
+// every piece is read again by all that merge it (one row of 8192, 2 KV heads: 14.5 us with 1, 11.2 with
+// 4, 9.3 with 8, 9.0 with 16; 8 rows of 1 to 1024 and one of 8192: 14.2, 13.1, 11.4 and 13.6).
+__device__ __forceinline__ int ranges_of(int W, int grid) { return min((W + kLeast - 1) / kLeast, grid); }
 
 // A granule in shared memory, as the tiled copies lay it: boxes of 16 rows of 128 bytes, the
 // 16-byte chunk c of row r at c ^ (r & 7).  fp16: keys' dims 0 .. 63, 64 .. 127, then the
@@ -323,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     }
     if (blockIdx.x == 0)  // for the second kernel
         for (int r = tid; r <= p.rows; r += kThreads) p.pre[r] = pre[r];
-    const int W = run, n = min(W, p.grid);
+    const int W = run, n = ranges_of(W, p.grid);
     if ((int)blockIdx.x >= n) return;
     const int g0 = (int)((int64_t)W * blockIdx.x / n), all = (int)((int64_t)W * (blockIdx.x + 1) / n) - g0;
     // The row that granule g is in.
@@ -492,7 +498,7 @@ struct Merge {
     __device__ __forceinline__ Merge(const Params& p, int r, int head, int before, int after, int W) {
         kvh = head;
         unit = r * p.hk + kvh;
-        const int count = (after - before) / p.hk, ga = before + kvh * count, n = min(W, p.grid);
+        const int count = (after - before) / p.hk, ga = before + kvh * count, n = ranges_of(W, p.grid);
         c0 = owner_of(ga, W, n);
         pieces = owner_of(ga + count - 1, W, n) - c0 + 1;
         ml = p.ml + (int64_t)(c0 + unit) * kMaxGroup;
@@ -993,7 +999,8 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     const int64_t most = (int64_t)rows * kv_heads * (l.tokens / kGranule);
     if (most >= (int64_t(1) << 31) - kMaxRows) return PKV_ERR_UNSUPPORTED;
     const int wave = blocks_of(sms);
-    p.grid = most < wave ? (most > 0 ? (int)most : 1) : wave;
+    const int64_t ranges = (most + kLeast - 1) / kLeast;
+    p.grid = ranges < wave ? (ranges > 0 ? (int)ranges : 1) : wave;
     const int elt = k_scale ? 1 : 2;
     const CUtensorMapDataType type = k_scale ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const int64_t dims[3] = {head_dim, kv_heads, (int64_t)num_blocks * block_size};
@@ -1005,7 +1012,7 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     if (st != PKV_OK) return st;
     // A block a unit, or a cluster of up to eight, four granules a warp of the longest row, while they
     // are few enough to be resident at once, four an SM: one launch instead of two.
-    // Against the even cut, 2 KV heads: 4 rows of 100 tokens 4.7 us and 6.6, one of 4096 9.6 and 14.3,
+    // Against the even cut, 2 KV heads: 4 rows of 100 tokens 4.7 us and 6.6, one of 4096 9.4 and 8.7,
     // 32 of 1024 (E4M3) 9.0 and 11.7, 32 of 16 to 512 and one of 4096 10.9 and 12.1, 512 of 128 15.0
     // and 31.8, 512 of 1 to 1024 54 and 71, 512 of 1 to 128 and one of 1024 17 and 34; but 32 of 4096
     // 33 and 31 (E4M3: 23 and 17.5).  Shares of more than 64 granules, or 4096 tokens, are the even
