@@ -1012,11 +1012,11 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     if (st != PKV_OK) return st;
     // A block a unit, or a cluster of up to eight, four granules a warp of the longest row, while they
     // are few enough to be resident at once, four an SM: one launch instead of two.
-    // Against the even cut, 2 KV heads: 4 rows of 100 tokens 4.7 us and 6.6, one of 4096 9.4 and 8.7,
-    // 32 of 1024 (E4M3) 9.0 and 11.7, 32 of 16 to 512 and one of 4096 10.9 and 12.1, 512 of 128 15.0
-    // and 31.8, 512 of 1 to 1024 54 and 71, 512 of 1 to 128 and one of 1024 17 and 34; but 32 of 4096
-    // 33 and 31 (E4M3: 23 and 17.5).  Shares of more than 64 granules, or 4096 tokens, are the even
-    // cut's: 96 rows of 16 to 600 and one of 4000 took clusters in waves 29.4 us, the even cut 18.1.
+    // Against the even cut, 2 KV heads: 4 rows of 100 tokens 4.5 us and 7.8, 8 of 2048 7.8 and 8.2, 32
+    // of 1024 (E4M3) 9.0 and 11.6, 32 of 16 to 512 and one of 4096 10.8 and 12.2, 512 of 128 15.0 and
+    // 31.8, 512 of 1 to 1024 54 and 71, 512 of 1 to 128 and one of 1024 17 and 34; but one of 4096 9.5
+    // and 7.8, 32 of them 33 and 30 (E4M3: 23 and 17.4).  Shares of more than 64 granules, or 4096 tokens,
+    // are the even cut's: 96 rows of 16 to 600 and one of 4000 took clusters in waves 29.4 us, it 18.1.
     const int n = l.tokens / kGranule;
     p.blocks = 1;
     const int64_t units = (int64_t)rows * kv_heads, resident = 4 * (int64_t)sms;
