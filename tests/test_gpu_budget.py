@@ -769,3 +769,98 @@ def test_rows_kept_within_a_budget(cuda_device, fp8):
         if i % 4 == 3:
             lens = tracked = evict(lens, tracked, nxt)
     assert int(err.item()) == 0 and nxt == [n + steps for n in prompt]
+
+
+def chain(fp8, seed):
+    """A prompt's weights, its eviction, then steps of decode and eviction, queued on the current stream
+    without a wait: each call reads what the one before has written.  Returns the call and its results."""
+    step = Step([0, 0, 0], [300, 47, 180], 16, fp8=fp8, seed=seed)
+    a = step.gpu()
+    k0, v0 = a["k_pool"].clone(), a["v_pool"].clone()
+    scales = dict(k_scale=a["k_scale"], v_scale=a["v_scale"])
+    q = torch.randn(step.total, 12, 128, generator=step.gen).half().cuda()
+    steps = [torch.randn(3, 12, 128, generator=step.gen).half().cuda() for _ in range(3)]
+    w, pos = torch.zeros(3, 2, 300, device="cuda"), torch.zeros(3, 2, 300, dtype=torch.int32, device="cuda")
+    lens = [torch.zeros(3, dtype=torch.int32, device="cuda") for _ in range(4)]
+    nxt = i32([300, 47, 180])
+    outs = [torch.zeros(3, 12, 128, dtype=torch.float16, device="cuda") for _ in range(3)]
+    wsp = ops.alloc_prefill_weights_workspace(3, step.total, 12, 2, 128, 300, 16, window=40)
+    wsd = ops.alloc_decode_weights_workspace(3, 12, 2, 128, 300, 16)
+    torch.cuda.synchronize()
+
+    def run(wait=lambda: None):
+        a["k_pool"].copy_(k0), a["v_pool"].copy_(v0)
+        w.zero_(), wait()
+        ops.prefill_weights(w, q, a["k_pool"], a["block_tables"], a["seq_lens"], a["q_start"], 0.09, 300, wsp, window=40,
+                            k_scale=scales["k_scale"]), wait()
+        at, tracked = a["seq_lens"], None
+        for i, budget in enumerate((100, 60, 30)):
+            ops.evict(a["k_pool"], a["v_pool"], a["block_tables"], at, w, pos, budget, 300, sinks=2, recent=9,
+                      tracked=tracked, next_pos=nxt, new_seq_lens=lens[i]), wait()
+            at = tracked = lens[i]
+            ops.decode_weights(outs[i], w, steps[i], a["k_pool"], a["v_pool"], a["block_tables"], at, 0.09, 300, wsd,
+                               **scales), wait()
+    return run, [a["k_pool"], a["v_pool"], w, pos] + lens + outs
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_calls_queued_one_behind_the_other_and_two_chains_at_once(cuda_device, fp8):
+    """Without waits, on two streams at once and in a replayed graph: the bits of calls run one by one."""
+    runs, wants = [], []
+    for seed in (801, 802):
+        run, results = chain(fp8, seed)
+        run(torch.cuda.synchronize)
+        wants.append([x.clone() for x in results])
+        runs.append((run, results))
+    streams = [torch.cuda.Stream() for _ in runs]
+    graphs = []
+    for (run, _), stream in zip(runs, streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.stream(stream), torch.cuda.graph(graphs[-1], stream=stream):
+            run()
+    torch.cuda.synchronize()
+    for captured in (False, True):
+        for _, results in runs:
+            for x in results:
+                x.zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for (run, _), stream, graph in zip(runs, streams, graphs):
+                with torch.cuda.stream(stream):
+                    graph.replay() if captured else run()
+        torch.cuda.synchronize()
+        for (_, results), want in zip(runs, wants):
+            for x, y in zip(results, want):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_calls_over_pools_past_32_bits(cuda_device):
+    """The bits that the four calls give over a small pool, over pools of more than 2^31 elements."""
+    rows, n, bs, hk = 2, 200, 64, 2
+    per, far = (n + bs - 1) // bs, (2 ** 31) // (bs * hk * 128) + 100
+    gen = torch.Generator().manual_seed(77)
+    x = torch.randn(rows * n, 12 + 2 * hk, 128, generator=gen).half().cuda()
+    norm = torch.rand(128, generator=gen).half().cuda()
+    last = torch.randn(rows, 12, 128, generator=gen).half().cuda()
+    lens, starts = i32([n] * rows), i32([0, n, 2 * n])
+    rates = ops.rope_rates(ops.rope_frequencies(128))
+    results = []
+    for base in (0, far):
+        pools = [torch.zeros(base + rows * per, bs, hk, 128, dtype=torch.float16, device="cuda") for _ in range(2)]
+        tables = i32(base + np.arange(rows * per).reshape(rows, per)[:, ::-1])
+        w, pos = torch.zeros(rows, hk, n, device="cuda"), torch.zeros(rows, hk, n, dtype=torch.int32, device="cuda")
+        q, out, new, err = torch.empty_like(x[:, :12]).contiguous(), torch.empty_like(last), torch.zeros_like(lens), err_word()
+        ops.norm_rope_append(*pools, tables, lens, starts, x[:, 12:12 + hk], x[:, 12 + hk:], rates, norm, n, q=x[:, :12],
+                             q_out=q, q_weight=norm, dev_err=err)
+        ops.prefill_weights(w, q, pools[0], tables, lens, starts, 0.09, n,
+                            ops.alloc_prefill_weights_workspace(rows, rows * n, 12, hk, 128, n, bs), dev_err=err)
+        ops.evict(*pools, tables, lens, w, pos, 90, n, sinks=3, recent=20, new_seq_lens=new, dev_err=err)
+        ops.decode_weights(out, w, last, *pools, tables, new, 0.09, n,
+                           ops.alloc_decode_weights_workspace(rows, 12, hk, 128, n, bs), dev_err=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and new.tolist() == [90, 90]
+        results.append([q, w, pos, out] + [p[base:].clone() for p in pools])
+        del pools
+    assert float(results[0][4].abs().max()) > 0
+    for a, b in zip(*results):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
