@@ -23,9 +23,10 @@
 //
 // What bounds it.  The choice is a chain: load, differing bits, one to four histograms, the
 // equal keys, the slots.  1792 lists of 1025 tokens, of which one leaves each (14.7 MB of weights
-// and positions): 18.3 us, 16.8 without the move; all blocks are resident at once, 12 an SM.
-// 896 lists of 1900 to 2304, E4M3: 23.6 us, 15.3 of them the choice.  32 lists of 30,000 to 32,768 down
-// to 4096: 39.9 us, 18.4 the choice (three cluster barriers a histogram) and 21.5 the
+// and positions): 17.9 us, all but 1.5 the choice; all blocks are resident at once, 12 an SM, and
+// issue in 71% of the cycles (64 threads a block, 20 an SM: 23.3).
+// 896 lists of 1900 to 2304, E4M3: 23.2 us, 15 of them the choice.  32 lists of 30,000 to 32,768 down
+// to 4096: 39.6 us, 18.4 the choice (three cluster barriers a histogram) and 21.5 the
 // moves, 117 MB in pieces of 256 bytes, 5.4 TB/s.
 #include "pkv_internal.cuh"
 #include "ptx.cuh"
@@ -264,8 +265,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const __grid_c
     if (!l.good(p, rank == 0 && tid == 0)) return;
     const int per = ((l.L + blocks - 1) / blocks + 3) & ~3;       // tokens of a block
     const int b0 = min(l.L, rank * per), cnt = min(l.L - b0, per);
-    const int rounds = (cnt + 4 * kThreads - 1) / (4 * kThreads);
-    const int w0 = warp * rounds * 128 + 4 * lane;                 // this lane's first token, from b0 on
+    // Rounds of 128 tokens, this warp's next to each other (1025 tokens, four warps: 3, 2, 2, 2).
+    const int all_rounds = (cnt + 127) / 128, extra = all_rounds % kWarps;
+    const int rounds = all_rounds / kWarps + (warp < extra);
+    const int w0 = (all_rounds / kWarps * warp + min(warp, extra)) * 128 + 4 * lane;  // this lane's first token, from b0 on
 
     // ---- keys; the bits in which they differ; how many are protected ----
     uint32_t any = 0, every = ~0u, safe = 0;
@@ -632,8 +635,8 @@ extern "C" int paged_kv_evict(void* k_pool, void* v_pool, const int32_t* block_t
     p.dev_err = dev_err;
     p.vec4 = weights_stride % 4 == 0 && aligned16(weights) && aligned16(token_pos) && aligned16(weights_out) &&
              aligned16(token_pos_out);
-    // Many small lists want many blocks resident (1792 of 1025 tokens: 18.5 us with 128 threads, 24.6
-    // with 256), larger ones more warps for their moves (896 of 1900 to 2304, E4M3: 28.3 and 23.7), and
+    // Many small lists want many blocks resident (1792 of 1025 tokens: 17.9 us with 128 threads, 24.6
+    // with 256), larger ones more warps for their moves (896 of 1900 to 2304, E4M3: 28.3 and 23.2), and
     // clusters of large blocks do not pay at such lengths (the same 896: 86.9).  Long lists: a cluster of
     // blocks of up to kChunk tokens, as long as all blocks are resident at once.  32 lists of 16,384 to
     // 2048: two blocks 40.2 us, four 27.5, eight 32.4; 128 of them: two 61.6, four 72.3; 224: one 109.7, two
