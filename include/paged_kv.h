@@ -664,7 +664,7 @@ int paged_kv_tree_commit(void* k_pool, void* v_pool, const int32_t* block_tables
  * block_size and rows * kv_heads * max_seq_len / 16 below 2^31 less 1024
  * (PKV_ERR_UNSUPPORTED otherwise).  Of out,
  * weights, q and the workspace none that is written overlaps another.
- * Both of its launches start early, as the drafted step's calls do.
+ * Its launches (one or two, by the sizes) start early, as the drafted step's calls do.
  *
  * workspace: paged_attention_decode_weights_workspace_size(...) bytes (0 for
  * sizes that are not supported), 256-byte aligned: 4 bytes a query head (an odd group's
