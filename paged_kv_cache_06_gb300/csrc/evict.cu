@@ -252,7 +252,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const __grid_c
     uint16_t* list = reinterpret_cast<uint16_t*>(keys + p.cap);    // [cap]: holes from the front, fillers from the back
     __shared__ __align__(16) uint32_t hist[kBins];
     __shared__ __align__(16) uint32_t all[kCluster ? kBins : 4];   // the cluster's
-    __shared__ uint32_t sums[2][kWarps], ors[kWarps], ands[kWarps];
+    // A row of the warps' sums a use (0: protected, then bins; 1: equal keys; 2: holes | fillers << 16): where
+    // exactly the protected stay, nothing but this keeps one use's reads from the next one's writes.
+    __shared__ uint32_t sums[3][kWarps], ors[kWarps], ands[kWarps];
     __shared__ uint32_t found[3];   // digit (in the end the key), keys above it, keys in it
     __shared__ uint32_t few[32];    // keys that share the digits, when they are few
     __shared__ uint32_t mine[4];    // this block's: or (or the number of `few`), and, protected; equal keys, then holes | fillers << 16
@@ -503,13 +505,13 @@ __global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const __grid_c
     }
     static_assert(4 * kRounds <= 64, "a lane's flags fit");
     const uint32_t sum = __reduce_add_sync(0xffffffffu, count);
-    if (lane == 0) sums[0][warp] = sum;
+    if (lane == 0) sums[2][warp] = sum;
     __syncthreads();
     uint32_t at = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        at += w < warp ? sums[0][w] : 0u;
-        total += sums[0][w];
+        at += w < warp ? sums[2][w] : 0u;
+        total += sums[2][w];
     }
 #pragma unroll 1
     for (int i = 0; i < rounds; ++i) {

@@ -606,6 +606,24 @@ def test_evict_of_many_long_lists(cuda_device, lens, hk, layers, weights):
         x.check(got, in_place)
 
 
+# Lists of a small block, a short one and a large one, many of each.
+PROTECTED = [([1500] * 60 + [2048, 600, 257], 256, 8, 4), ([4000] * 30 + [4096, 2100], 900, 4, 4),
+             ([5000] * 40 + [6000], 1500, 4, 2)]
+
+
+@pytest.mark.parametrize("sinks", [0, 4])
+@pytest.mark.parametrize("lens,budget,layers,hk", PROTECTED)
+def test_evict_where_exactly_the_protected_stay(cuda_device, lens, budget, layers, hk, sinks):
+    """sinks + recent == budget, a sliding window: no list has a weight to choose by.  Many lists, often: warps
+    must not run ahead of those that still read the counts of protected tokens."""
+    x = Lists(lens, budget, layers=layers, hk=hk, d=16, bs=64, sinks=sinks, recent=budget - sinks, seed=budget)
+    first = x.run()
+    x.check(first)
+    for _ in range(20):
+        for a, b in zip(x.run(), first):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 def test_evict_of_a_first_time_takes_slots_for_positions(cuda_device):
     x = Lists([100, 60, 300], 64, sinks=4, recent=20, seed=5)
     x.check(x.run(bare=True))
