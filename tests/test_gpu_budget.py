@@ -624,6 +624,19 @@ def test_evict_where_exactly_the_protected_stay(cuda_device, lens, budget, layer
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
+@pytest.mark.parametrize("lens,budget,layers,hk", [([300, 90], 64, 2, 2), ([3000, 2600], 700, 2, 2), ([9000, 20000], 3000, 1, 2),
+                                                   ([5000] * 40, 1500, 2, 4)])
+def test_evict_of_more_protected_tokens_than_may_stay(cuda_device, lens, budget, layers, hk):
+    """Recorded positions that repeat: the protected of the lowest slots stay."""
+    x = Lists(lens, budget, layers=layers, hk=hk, d=16, bs=64, sinks=4, recent=10, tracked=[n - 20 for n in lens], seed=budget)
+    rng = np.random.default_rng(budget)
+    for r, n in enumerate(x.tracked):
+        x.pos[:, r, :, :n] = rng.integers(0, 6, (layers, hk, n))
+    x.want()
+    for in_place in (True, False):
+        x.check(x.run(in_place=in_place), in_place)
+
+
 def test_evict_of_a_first_time_takes_slots_for_positions(cuda_device):
     x = Lists([100, 60, 300], 64, sinks=4, recent=20, seed=5)
     x.check(x.run(bare=True))
