@@ -597,12 +597,18 @@ extern "C" int paged_kv_evict(void* k_pool, void* v_pool, const int32_t* block_t
         const void* at;
         size_t bytes;
     };
+    // (a pool of more bytes than there are addresses reaches to the last one)
+    const double slots = (double)layers * num_blocks * block_size, pool_bytes = slots * kv_heads * (double)(vecs * 16);
+    auto pool = [&](const void* at) {
+        const size_t rest = ~reinterpret_cast<uintptr_t>(at);
+        return Span{at, pool_bytes < 1e18 && (size_t)pool_bytes < rest ? (size_t)pool_bytes : rest};
+    };
     const Span outs[] = {{weights_out, wide}, {token_pos_out, wide}, {new_seq_lens, n}};
-    const Span ins[] = {{weights, wide},  {token_pos, wide}, {seq_lens, n}, {block_tables, n * max_blocks_per_row},
-                        {tracked, n},     {next_pos, n}};
+    const Span ins[] = {{weights, wide}, {token_pos, wide}, {seq_lens, n},  {block_tables, n * max_blocks_per_row},
+                        {tracked, n},    {next_pos, n},     pool(k_pool),   pool(v_pool), {dev_err, 4}};
     for (int o = 0; o < 3; ++o) {
         if (!outs[o].at) continue;
-        for (int i = 0; i < 6; ++i) {
+        for (int i = 0; i < 9; ++i) {
             if (!ins[i].at || (in_place && o == i && o < 2)) continue;
             if (overlap(outs[o].at, outs[o].bytes, ins[i].at, ins[i].bytes)) return PKV_ERR_INVALID_ARG;
         }

@@ -167,6 +167,19 @@ def test_evict_outputs_lie_over_nothing_else():
     assert evict(wo=FAKE, po=pos) == INVALID and evict(wo=out, po=FAKE + 12) == INVALID
 
 
+def test_evict_outputs_lie_over_no_pool():
+    size = 2 * 64 * 16 * 2 * 128 * 2
+    out, pos, far = 4 * FAR, 5 * FAR, 6 * FAR
+    for n in ("k", "v"):
+        for x in (far, far + size - 4):
+            assert evict(**{n: far}, new=x) == INVALID, n
+            assert evict(**{n: far}, w=x) == INVALID and evict(**{n: far}, pos=x) == INVALID, n          # in place
+            assert evict(**{n: far}, wo=x, po=pos) == INVALID and evict(**{n: far}, wo=out, po=x) == INVALID, n
+    # sizes whose product passes 64 bits
+    huge = dict(layers=60000, nb=1 << 20, hk=1 << 12, d=1 << 19, pos=1 << 43, w=1 << 42)
+    assert evict(k=far, v=1 << 45, **huge) == INVALID
+
+
 def test_ops_refuse_cpu_tensors_and_wrong_shapes():
     h, i = torch.zeros(4, 12, 128, dtype=torch.float16), torch.zeros(4, dtype=torch.int32)
     pool = torch.zeros(4, 16, 2, 128, dtype=torch.float16)
