@@ -43,6 +43,10 @@ class PagedKVError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libpagedkv.so (building it first if it is missing or stale)."""
     global _lib
+    # no lock once it is there: a finaliser (a block manager's) may run in the thread that
+    # loads the binding, which holds it
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build(binding=False)

@@ -2,6 +2,7 @@
 binding is built again for another torch or Python."""
 import os
 import subprocess
+import sys
 import types
 
 import pytest
@@ -71,3 +72,31 @@ def test_another_torch_or_python_means_another_binding(fake, monkeypatch):
     b.build()
     assert compiled(fake) == {"binding.cpp"}          # the library stays
     assert not b.is_stale()
+
+
+def test_a_block_manager_collected_while_the_binding_loads():
+    """Its finaliser needs the library while the thread that loads the binding holds the loading lock."""
+    code = """
+import gc
+from paged_kv_cache_06_gb300 import build, ops
+from paged_kv_cache_06_gb300.block_manager import BlockManager
+real, closed = build.build, []
+
+class Mine(BlockManager):
+    def close(self):
+        super().close()
+        closed.append(1)
+
+def collecting(**kw):
+    m = Mine(4, 16, 4)
+    m.me = m
+    del m
+    gc.collect()
+    return real(**kw)
+
+ops.lib()
+build.build = collecting
+assert ops.binding() is ops.binding() and closed
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    assert subprocess.run([sys.executable, "-c", code], cwd=root, timeout=120).returncode == 0
