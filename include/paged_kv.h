@@ -660,7 +660,7 @@ int paged_kv_tree_commit(void* k_pool, void* v_pool, const int32_t* block_tables
  *
  * out, errors and clamped lengths as in paged_attention_decode (computed by another
  * kernel: the bits may differ).  Supported for head_dim 128, q_heads / kv_heads
- * <= 8, block_size a multiple of 16, rows <= 1024, max_seq_len <= 2^24, num_blocks *
+ * <= 8, block_size a multiple of 16 and at most 1024, rows <= 1024, max_seq_len <= 2^24, num_blocks *
  * block_size and rows * kv_heads * max_seq_len / 16 below 2^31 less 1024
  * (PKV_ERR_UNSUPPORTED otherwise).  Of out,
  * weights, q and the workspace none that is written overlaps another.

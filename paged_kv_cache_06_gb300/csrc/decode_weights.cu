@@ -905,9 +905,14 @@ struct Layout {
     size_t ml, pre, scores, bytes;
     int tokens, pairs;
 };
+// Granules of rows that are all as long as may be.
+static int64_t granules(int rows, int kv_heads, int max_seq_len) {
+    return (int64_t)rows * kv_heads * (((int64_t)max_seq_len + kGranule - 1) / kGranule);
+}
 static bool supported(int rows, int q_heads, int kv_heads, int head_dim, int max_seq_len, int block_size) {
     return head_dim == kHeadDim && q_heads / kv_heads <= kMaxGroup && block_size % 16 == 0 && rows <= kMaxRows &&
-           max_seq_len <= (1 << 24) && kv_heads <= 65536;
+           block_size <= 1024 && max_seq_len <= (1 << 24) && kv_heads <= 65536 &&
+           granules(rows, kv_heads, max_seq_len) < (int64_t(1) << 31) - kMaxRows;
 }
 // Blocks of the first kernel, as many as fill the device once.
 static int blocks_of(int sms) { return sms * kBlocks; }
@@ -996,8 +1001,7 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     p.pre = reinterpret_cast<int*>(ws + l.pre);
     p.scores = reinterpret_cast<float*>(ws + l.scores);
     p.dev_err = dev_err;
-    const int64_t most = (int64_t)rows * kv_heads * (l.tokens / kGranule);
-    if (most >= (int64_t(1) << 31) - kMaxRows) return PKV_ERR_UNSUPPORTED;
+    const int64_t most = granules(rows, kv_heads, max_seq_len);
     const int wave = blocks_of(sms);
     const int64_t ranges = (most + kLeast - 1) / kLeast;
     p.grid = ranges < wave ? (ranges > 0 ? (int)ranges : 1) : wave;

@@ -83,6 +83,17 @@ def test_decode_weights_workspace_size_host_arithmetic():
         assert ops.decode_weights_workspace_size(*bad) == 0, bad
 
 
+def test_decode_weights_sizes_that_are_refused_have_no_workspace():
+    for kw in (dict(rows=1024, hk=1024, hq=1024, msl=1 << 16, mbpr=1 << 12, stride=1 << 16), dict(bs=1040), dict(bs=4096)):
+        a = dict(rows=4, hq=12, hk=2, d=128, msl=200, bs=16)
+        a.update({n: x for n, x in kw.items() if n in a})
+        assert ops.decode_weights_workspace_size(a["rows"], a["hq"], a["hk"], a["d"], a["msl"], a["bs"]) == 0, kw
+        assert decode(w=1 << 60, wsb=1 << 62, **kw) in (INVALID, UNSUPPORTED), kw
+    most = (1024, 1024, 1024, 128, 32640, 16)                         # 2^31 granules less 2^23
+    assert ops.decode_weights_workspace_size(*most) > 0
+    assert ops.decode_weights_workspace_size(*most[:4], 32768, 16) == 0
+
+
 def prefill(**kw):
     a = dict(w=2 * FAR, q=FAR, k=FAKE, ks=0, bt=FAKE, sl=FAKE, qs=FAKE, rows=4, total=90, hq=12, hk=2, d=128, bs=16,
              scale=0.1, window=32, mbpr=16, nb=64, msl=200, stride=200, ws=3 * FAR, wsb=None)
