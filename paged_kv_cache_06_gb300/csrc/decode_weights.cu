@@ -48,7 +48,12 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kBlocks = 3;           // resident per SM
 constexpr int kRing = 16 << 10;      // bytes of a warp's ring
 constexpr int kMaxRows = 1024;
-constexpr float kMove = 8.f;
+// A head's reference lies 7 (in powers of two) below the largest score at the time and moves when a score passes
+// it by more than 15.  The output's weights, rounded to fp16 for the tensor cores (by 2^-11 of each at most, which
+// adds 1.2e-4 to 2.0e-4 to the 2.1e-4 of the output's own rounding; the sums and the weights handed out keep 32
+// bits), so stay below 2^15, and one of 2^-21 of the largest keeps its eleven bits.  With the reference at the
+// largest, weights below 2^-25 of it were in the row's sum and not in its output.
+constexpr float kLift = 7.f, kMove = 15.f;
 constexpr int kClusterBlocks = 8;    // of a cluster, at most (the portable limit)
 constexpr int kClusterTokens = 4096; // of a row that a cluster takes, at most
 constexpr int kShare = 64;           // granules of its block, at most
@@ -80,7 +85,7 @@ struct Params {
     float scale_log2;
     int* pre;          // [rows + 1]: granules of the rows before
     float* part;       // [block + unit][group][128]: the block's piece of the unit, unnormalised
-    float2* ml;        // [block + unit][kMaxGroup]: its maxima and sums
+    float2* ml;        // [block + unit][kMaxGroup]: its references and sums
     float* scores;     // [unit][tokens][2 * pairs]
     int32_t* dev_err;
 };
@@ -234,7 +239,7 @@ __device__ __forceinline__ void attend(State& st, const unsigned char* data, uin
     }
     const float x0 = fmaxf(s[0], s[2]), x1 = fmaxf(s[1], s[3]);
     if (__any_sync(0xffffffffu, x0 > st.m0 + kMove || x1 > st.m1 + kMove)) {
-        float n0 = fmaxf(st.m0, x0), n1 = fmaxf(st.m1, x1);
+        float n0 = fmaxf(st.m0, x0 - kLift), n1 = fmaxf(st.m1, x1 - kLift);
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, off));

@@ -299,6 +299,46 @@ def test_decode_weights_of_bad_lengths_blocks_and_numbers(cuda_device):
     check_weights(step, w, before, ref, [1] * 4)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("top", [900, 3000, 7000])
+def test_decode_weights_keep_many_faint_tokens_in_the_output(cuda_device, top, fp8):
+    """One token without a value, the others 2^-26 to 2^-28 of its weight and all of the output.  A weight is off by
+    2^-11 of itself, and by 2^-32 of the largest below the fp16 numbers of eleven bits: the reference that weights are
+    taken from lies 2^7 below the largest."""
+    step = Step([top, top // 3], [0, 0], 16, fp8=fp8, seed=31)
+    q = torch.zeros(2, 12, 128, dtype=torch.float16)
+    q[:, :, 0] = 1
+    keys = torch.zeros(step.k_pool.shape)
+    values = torch.rand(step.v_pool.shape, generator=step.gen) * 300 + 100
+    for r, n in enumerate(step.lens):
+        at = step.slots(r)
+        keys.view(-1, 2, 128)[at, :, 0] = -26. - 2 * (torch.arange(n) % 2)[:, None]
+        keys.view(-1, 2, 128)[at[n // 2], :, 0] = 0
+        values.view(-1, 2, 128)[at[n // 2]] = 0
+    if fp8:
+        step.k_scale, step.v_scale = torch.ones(2), torch.tensor([100., 50.])
+        step.k_pool, step.v_pool = (x.to(torch.float8_e4m3fn).view(torch.uint8) for x in (keys, values))
+    else:
+        step.k_pool, step.v_pool = keys.half(), (values * 100).half()
+    scale = float(torch.tensor(np.log(2.0), dtype=torch.float32))
+    ref = weights_ref(step, q, scale, [1, 1], [1, 1])
+    before = torch.zeros(2, 2, top)
+    a, err, w = step.gpu(), err_word(), before.cuda()
+    out = torch.zeros(q.shape, dtype=torch.float16, device="cuda")
+    ops.decode_weights(out, w, q.cuda(), a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], scale, top,
+                       ops.alloc_decode_weights_workspace(2, 12, 2, 128, top, 16), k_scale=a["k_scale"],
+                       v_scale=a["v_scale"], dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check_weights(step, w, before, ref, [1, 1])
+    for r, n in enumerate(step.lens):
+        o, big, e = (x[:, 0] for x in ref[r][2])
+        low = 2.0 ** -32 * step.values(step.v_pool, r, step.v_scale).abs().sum(0).repeat_interleave(6, 0)
+        tol = H * o.abs() + (H + 2 * e + (8 + n) * U) * big + low + 2.0 ** -25
+        assert bool((tol < 0.1 * o.abs()).all())                       # a fault of the faint tokens' own size shows
+        check(out[r], o, tol, f"output of row {r}")
+
+
 PROMPTS = [
     # cached, chunk, window, block, q heads, kv heads
     ([0], [1], None, 16, 12, 2),
