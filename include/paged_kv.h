@@ -846,6 +846,20 @@ int pkv_debug_set_decode_hooks(unsigned poll_limit, const void* stuck_word);
 int pkv_debug_set_tree_hooks(unsigned help_ns, int stop_folds, unsigned linger_ns);
 
 /*
+ * pkv_debug_set_weights_hooks -- test hooks of the bounded waits of
+ * paged_attention_decode_weights and paged_attention_prefill_weights.  With granule
+ * > 0 each of decode's blocks gives up at the granule-th 16 tokens of its share, as
+ * if the wait for them had run out; with jobs > 0 each of a prompt's blocks does at
+ * the jobs-th of its 128 x 128 products, by its copies (role 0), products (1),
+ * widening of codes (2) or sums (3).  Such a block flags
+ * PKV_DEV_ERR_TIMEOUT, lets what it has in flight land and ends; the call's results are
+ * undefined, the workspace may be used again as it is.  (0, 0, 0) restores normal operation.
+ * They apply to launches made (and captured) after the call, from any thread, until
+ * changed.  For tests; not for production use.
+ */
+int pkv_debug_set_weights_hooks(int granule, int role, int jobs);
+
+/*
  * pkv_check_error -- synchronise `stream`, copy the device error word to
  * *host_err and clear it on the device.  Returns PKV_ERR_CUDA if the stream
  * reported an error.  The only library call that blocks.  If the word holds

@@ -33,6 +33,8 @@
 // takes 25 of them, 5.3 TB/s, and the second, with its launch, 6.
 #include <math.h>
 
+#include <atomic>
+
 #include "fp8_codec.cuh"
 #include "pkv_internal.cuh"
 #include "tcgen05.cuh"
@@ -88,6 +90,7 @@ struct Params {
     float2* ml;        // [block + unit][kMaxGroup]: its references and sums
     float* scores;     // [unit][tokens][2 * pairs]
     int32_t* dev_err;
+    int give_up;       // (kHook) the granule of each block whose wait runs out at once
 };
 
 // The block whose range of the W granules holds granule g (block c's starts at c W / n): the
@@ -272,7 +275,8 @@ __device__ __forceinline__ void attend(State& st, const unsigned char* data, uin
 // Place d of a half's 64 dims of head h in a warp's state; pairs of heads lie on other banks.
 __device__ __forceinline__ int state_at(int h, int d) { return h * 64 + (d ^ (((h >> 1) & 3) << 3)); }
 
-template <bool kFp8>
+// kHook: for tests, a wait that runs out at once.
+template <bool kFp8, bool kHook>
 __global__ void __launch_bounds__(kThreads, kBlocks)
     attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ Params p) {
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         const float sl2 = kFp8 ? p.scale_log2 * p.k_scale[kvh] : p.scale_log2;
 #pragma unroll 1
         for (; x < end && ok; x += kWarps) {
-            if (!mbar_waitw(smem_u32(&bars[warp][slot]), parity, stopped)) {
+            if ((kHook && x == p.give_up) || !mbar_waitw(smem_u32(&bars[warp][slot]), parity, stopped)) {
                 // gives up: what it has asked for lands before the block exits; the barriers below are
                 // for all
                 ok = false;
@@ -668,7 +672,7 @@ __device__ __forceinline__ void tell(uint32_t addr, float4 v) {
                  : "memory");
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kHook>
 __global__ void __launch_bounds__(kThreads, 4)
     cluster_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ Params p) {
@@ -774,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 4)
     uint32_t parity = 0;
 #pragma unroll 1
     for (int x = warp; x < all; x += kWarps) {
-        if (!mbar_waitw(smem_u32(&bars[warp][slot]), parity, stopped)) {
+        if ((kHook && x == p.give_up) || !mbar_waitw(smem_u32(&bars[warp][slot]), parity, stopped)) {
             // gives up: what it has asked for lands before the block exits; the barriers below are
             // for all
             if (lane == 0) {
@@ -906,6 +910,8 @@ __global__ void __launch_bounds__(kThreads, 4)
 // ---------------------------------------------------------------------------
 // Host side.
 
+std::atomic<int> g_hook_granule{0};  // for tests (pkv_debug_set_weights_hooks); 0 in normal use
+
 struct Layout {
     size_t ml, pre, scores, bytes;
     int tokens, pairs;
@@ -1006,6 +1012,8 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     p.pre = reinterpret_cast<int*>(ws + l.pre);
     p.scores = reinterpret_cast<float*>(ws + l.scores);
     p.dev_err = dev_err;
+    p.give_up = g_hook_granule.load(std::memory_order_relaxed) - 1;
+    const bool hook = p.give_up >= 0;
     const int64_t most = granules(rows, kv_heads, max_seq_len);
     const int wave = blocks_of(sms);
     const int64_t ranges = (most + kLeast - 1) / kLeast;
@@ -1036,7 +1044,9 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
         const int bytes = k_scale ? granule_bytes<true> : granule_bytes<false>, most_slots = kRing / bytes;
         p.slots = (share + kWarps - 1) / kWarps < most_slots ? (share + kWarps - 1) / kWarps : most_slots;
         const size_t smem = 1024 + (size_t)kWarps * p.slots * bytes + (size_t)share * kGranule * p.pairs * sizeof(float2);
-        auto* kernel = k_scale ? cluster_kernel<true> : cluster_kernel<false>;
+        auto* kernel = hook      ? (k_scale ? cluster_kernel<true, true> : cluster_kernel<false, true>)
+                       : k_scale ? cluster_kernel<true, false>
+                                 : cluster_kernel<false, false>;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  1024 + kWarps * kRing + kShare * kGranule * kMaxGroup * (int)sizeof(float)) != cudaSuccess) {
             cudaGetLastError();
@@ -1045,7 +1055,9 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
         return launch_early_clusters(kernel, dim3((unsigned)(kv_heads * p.blocks), (unsigned)rows), kThreads, smem,
                                      (unsigned)p.blocks, stream, kmap, vmap, p);
     }
-    auto* attend = k_scale ? attend_kernel<true> : attend_kernel<false>;
+    auto* attend = hook      ? (k_scale ? attend_kernel<true, true> : attend_kernel<false, true>)
+                   : k_scale ? attend_kernel<true, false>
+                             : attend_kernel<false, false>;
     const int state = 64 * (int)sizeof(float);  // of a head
     const size_t smem = 1024 + (size_t)kWarps * (kRing + p.group * state) + ((size_t)rows + 1) * sizeof(int);
     if (cudaFuncSetAttribute(attend, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -45,7 +45,10 @@
 // What is not seen (later tokens, table entries out of range) is left out of sums and maxima by
 // selection, whatever its scores are, and so are in 3 the rows behind a query block's queries (1 gives
 // them sums that nothing uses).
+#include <limits.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "fp8_codec.cuh"
 #include "pkv_internal.cuh"
@@ -97,6 +100,7 @@ struct Params {
     float* neg_lse;    // [query block][128]: -e
     float* sums;       // [block + token tile][128]
     int32_t* dev_err;
+    int last[4];       // (kHook) jobs of a block that copies, products, widening and sums do before they give up
 };
 
 // The block whose range of the W jobs holds job j (block c's starts at c W / n).
@@ -202,7 +206,8 @@ __device__ __forceinline__ int scan_most(int v, int most) {
     return v;
 }
 
-template <bool kFp8, bool kSums>
+// kHook: for tests, a role that gives up.
+template <bool kFp8, bool kSums, bool kHook>
 __global__ void __launch_bounds__(threads<kFp8>(), 1)
     tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap,
                 const __grid_constant__ Params p) {
@@ -356,6 +361,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             misc[5] = k;
             misc[6] = x;
             misc[7] = off - before;  // jobs of the unit before j0
+            if (kHook) misc[8] = j1 - j0;
         }
     }
     tc_fence_before();
@@ -375,6 +381,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         at.s += misc[7];
     }
     at.left = j1 - j0;
+    auto cut = [&](int role) { return kHook && misc[8] > p.last[role]; };  // it gives up before its last job
 
     if (idle) {
         // nothing to do but the release below
@@ -382,6 +389,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         // ============================ copies ============================
         bool ok = true;
         Walk<kSums> c = at;
+        if (kHook) c.left = min(c.left, p.last[0]);
         // A ring's next slot, the parity of the wait for it to be free (from the second lap on), fills.
         struct Ring {
             int s = 0, fills = 0;
@@ -499,7 +507,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             c = nx;
         }
         if (lane == 0) {
-            if (!ok) give_up();
+            if (!ok || cut(0)) give_up();
             // every copy has landed before the block exits
             auto drain = [&](uint32_t bar, int n, int count) {
                 for (int i = max(0, n - count); i < n; ++i) mbar_drain1(bar + 8 * (i % count), (uint32_t)(i / count) & 1);
@@ -519,6 +527,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             int f = 0, s = 0, b = 0;
             uint32_t fph = 0, sph = 0, bph = 1;
             Walk<kSums> c = at;
+            if (kHook) c.left = min(c.left, p.last[1]);
             while (c.left > 0 && ok) {
                 const int end = min(c.n, c.s + c.left);
                 if (!(ok = mbar_wait1(bar_ffull + 8 * f, fph, stop))) break;
@@ -557,7 +566,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
                 c.s = end - 1;
                 c.next(w, hk);
             }
-            if (!ok) give_up();
+            if (!ok || cut(1)) give_up();
             umma_commit(bar_fin);
             if (!mbar_drain1(bar_fin, 0)) flag_error(p.dev_err, PKV_DEV_ERR_TIMEOUT);
         }
@@ -567,6 +576,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         bool ok = true, fresh = true;
         int units = 0, jobs = 0, codes = 0;
         Walk<kSums> c = at;
+        if (kHook) c.left = min(c.left, p.last[2]);
         const int row = tid - kConvWarp * 32;  // a token a thread
         while (c.left > 0 && ok) {
             if (!kSums || fresh) {
@@ -596,7 +606,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             ++jobs;
             fresh = c.next(w, hk);
         }
-        if (!ok && lane == 0) give_up();
+        if ((!ok || cut(2)) && lane == 0) give_up();
     } else if (warp < kSumWarps) {
         // ============================ sums ============================
         const int i = (warp & 3) * 32 + lane, grp = warp >> 2;  // row of the product; group
@@ -604,6 +614,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
         bool ok = true;
         int units = 0, jobs = 0;
         Walk<kSums> c = at;
+        if (kHook) c.left = min(c.left, p.last[3]);
         const int group = p.group;
         const int my_q = i / group, columns = nq * group;
         // The 32 columns of chunk ch, all of which count but, of flat rows, those that no query has.
@@ -781,7 +792,7 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
             c.s = end - 1;
             c.next(w, hk);
         }
-        if (!ok && lane == 0) give_up();
+        if ((!ok || cut(3)) && lane == 0) give_up();
     }
 
     // ---- release tensor memory ----
@@ -836,6 +847,9 @@ __global__ void __launch_bounds__(kEndThreads) add_kernel(const __grid_constant_
     }
     *w = was + sum;
 }
+
+// For tests (pkv_debug_set_weights_hooks); 0 in normal use.
+std::atomic<int> g_hook_role{0}, g_hook_jobs{0};
 
 struct Layout {
     size_t tile_pre, block_info, tile_info, ml, neg_lse, sums, bytes;
@@ -956,6 +970,9 @@ extern "C" int paged_attention_prefill_weights(float* weights, const void* q, co
     p.neg_lse = reinterpret_cast<float*>(ws + l.neg_lse);
     p.sums = reinterpret_cast<float*>(ws + l.sums);
     p.dev_err = dev_err;
+    const int hook = g_hook_jobs.load(std::memory_order_relaxed);
+    for (int& jobs : p.last) jobs = INT_MAX;
+    if (hook) p.last[g_hook_role.load(std::memory_order_relaxed)] = hook - 1;
     if (l.blocks == 0 || max_seq_len == 0) return PKV_OK;
 
     CUtensorMap kmap, qmap;
@@ -970,8 +987,12 @@ extern "C" int paged_attention_prefill_weights(float* weights, const void* q, co
     const int64_t qstrides[2] = {(int64_t)head_dim * 2, (int64_t)q_heads * head_dim * 2};
     const int qb[3] = {64, group, p.nq};
     if ((st = tiled_map_3d(q, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, qdims, qstrides, qb, &qmap)) != PKV_OK) return st;
-    auto* first = k_scale ? tile_kernel<true, false> : tile_kernel<false, false>;
-    auto* second = k_scale ? tile_kernel<true, true> : tile_kernel<false, true>;
+    auto* first = hook      ? (k_scale ? tile_kernel<true, false, true> : tile_kernel<false, false, true>)
+                  : k_scale ? tile_kernel<true, false, false>
+                            : tile_kernel<false, false, false>;
+    auto* second = hook      ? (k_scale ? tile_kernel<true, true, true> : tile_kernel<false, true, true>)
+                   : k_scale ? tile_kernel<true, true, false>
+                             : tile_kernel<false, true, false>;
     const int most = (int)(k_scale ? Smem<true>::total(kMaxRows) : Smem<false>::total(kMaxRows));
     const size_t smem = k_scale ? Smem<true>::total(rows) : Smem<false>::total(rows);
     const unsigned block = (unsigned)(k_scale ? threads<true>() : threads<false>());
@@ -985,4 +1006,18 @@ extern "C" int paged_attention_prefill_weights(float* weights, const void* q, co
     if ((st = launch_early(second, (unsigned)p.grid, block, smem, stream, kmap, qmap, p)) != PKV_OK) return st;
     const unsigned z = (unsigned)((max_seq_len + kEndThreads - 1) / kEndThreads);
     return launch_early(add_kernel, dim3((unsigned)kv_heads, (unsigned)rows, z), kEndThreads, 0, stream, p);
+}
+
+namespace pkv {
+namespace weights {
+extern std::atomic<int> g_hook_granule;  // decode_weights.cu
+}
+}  // namespace pkv
+
+extern "C" int pkv_debug_set_weights_hooks(int granule, int role, int jobs) {
+    if (granule < 0 || role < 0 || role > 3 || jobs < 0) return PKV_ERR_INVALID_ARG;
+    pkv::weights::g_hook_granule.store(granule, std::memory_order_relaxed);
+    pkv::prompt::g_hook_role.store(role, std::memory_order_relaxed);
+    pkv::prompt::g_hook_jobs.store(jobs, std::memory_order_relaxed);
+    return PKV_OK;
 }

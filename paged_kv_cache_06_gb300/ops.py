@@ -150,6 +150,8 @@ def _declare(L: ctypes.CDLL) -> None:
     L.pkv_debug_set_decode_hooks.restype = I
     L.pkv_debug_set_tree_hooks.argtypes = [ctypes.c_uint, I, ctypes.c_uint]
     L.pkv_debug_set_tree_hooks.restype = I
+    L.pkv_debug_set_weights_hooks.argtypes = [I, I, I]
+    L.pkv_debug_set_weights_hooks.restype = I
 
 
 def status_string(status: int) -> str:
@@ -750,6 +752,17 @@ def debug_set_tree_hooks(help_ns: int = 0, stop_folds: bool = False, linger_ns: 
     other half of a unit cut in two gives up (PKV_DEV_ERR_TIMEOUT), and how long
     one warp of each block stays behind at the end of every unit.  Test hook."""
     _check("pkv_debug_set_tree_hooks", lib().pkv_debug_set_tree_hooks(int(help_ns), int(stop_folds), int(linger_ns)))
+
+
+WEIGHTS_ROLES = {"copies": 0, "products": 1, "widening": 2, "sums": 3}
+
+
+def debug_set_weights_hooks(granule: int = 0, role: str = "copies", jobs: int = 0) -> None:
+    """pkv_debug_set_weights_hooks: the 16 tokens of its share at which each block of
+    decode_weights gives up (0: none), and the warps of each block of prefill_weights that
+    give up at the ``jobs``-th of its products (0: none).  Test hook."""
+    _check("pkv_debug_set_weights_hooks",
+           lib().pkv_debug_set_weights_hooks(int(granule), WEIGHTS_ROLES[role], int(jobs)))
 
 
 def debug_set_decode_hooks(poll_limit: int = 0, stuck_word: Optional[torch.Tensor] = None) -> None:

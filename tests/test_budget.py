@@ -191,6 +191,13 @@ def test_evict_outputs_lie_over_no_pool():
     assert evict(k=far, v=1 << 45, **huge) == INVALID
 
 
+def test_weights_hooks_refusals():
+    for bad in ((-1, 0, 0), (0, -1, 0), (0, 4, 0), (0, 0, -1)):
+        assert ops.lib().pkv_debug_set_weights_hooks(*bad) == INVALID, bad
+    ops.debug_set_weights_hooks(3, "sums", 5)
+    ops.debug_set_weights_hooks()
+
+
 def test_ops_refuse_cpu_tensors_and_wrong_shapes():
     h, i = torch.zeros(4, 12, 128, dtype=torch.float16), torch.zeros(4, dtype=torch.int32)
     pool = torch.zeros(4, 16, 2, 128, dtype=torch.float16)

@@ -935,3 +935,77 @@ def test_calls_over_pools_past_32_bits(cuda_device):
     assert float(results[0][4].abs().max()) > 0
     for a, b in zip(*results):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+# ---- bounded waits that run out ----
+
+TIMEOUT = 8
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("top,rows", [(700, 160), (1024, 20), (6000, 20)])
+@pytest.mark.parametrize("granule", [1, 3, 6, 11])
+def test_decode_weights_give_up_and_the_next_call_is_as_ever(cuda_device, top, rows, granule, fp8):
+    """Blocks alone, in clusters and of the even cut give up with copies in flight: the call ends, flags it, leaves
+    the entries behind the rows alone, and the next one over the same workspace has the bits of the one before."""
+    lens = [max(1, top - 31 * i) for i in range(rows)]
+    step = Step(lens, [0] * rows, 64, fp8=fp8, seed=71)
+    q = torch.randn(rows, 12, 128, generator=step.gen).half().cuda()
+    before = torch.rand(rows, 2, top, generator=step.gen).cuda()
+    a, err = step.gpu(), err_word()
+    ws = ops.alloc_decode_weights_workspace(rows, 12, 2, 128, top, 64)
+
+    def run():
+        w, out = before.clone(), torch.zeros_like(q)
+        ops.decode_weights(out, w, q, a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], 0.09, top, ws,
+                           k_scale=a["k_scale"], v_scale=a["v_scale"], dev_err=err)
+        torch.cuda.synchronize()
+        return out, w
+
+    want = run()
+    assert int(err.item()) == 0
+    try:
+        ops.debug_set_weights_hooks(granule=granule)
+        _, w = run()
+    finally:
+        ops.debug_set_weights_hooks()
+    assert ops.check_error(err) == TIMEOUT
+    for r, n in enumerate(lens):
+        assert torch.equal(w[r, :, n:], before[r, :, n:])
+    assert all(torch.equal(x, y) for x, y in zip(run(), want))
+    assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("jobs", [1, 2, 6, 10])
+@pytest.mark.parametrize("role", ["copies", "products", "widening", "sums"])
+def test_prefill_weights_give_up_and_the_next_call_is_as_ever(cuda_device, role, jobs, fp8):
+    """Any of a block's roles gives up, at once or with tiles and products in flight: as decode's."""
+    step = Step([900, 10, 300], [700, 1500, 33], 48, fp8=fp8, seed=72)
+    q = torch.randn(step.total, 12, 128, generator=step.gen).half().cuda()
+    before = torch.rand(3, 2, step.max_len + 7, generator=step.gen).cuda()
+    a, err = step.gpu(), err_word()
+    ws = ops.alloc_prefill_weights_workspace(3, step.total, 12, 2, 128, step.max_len, 48)
+
+    def run():
+        w = before.clone()
+        ops.prefill_weights(w, q, a["k_pool"], a["block_tables"], a["seq_lens"], a["q_start"], 0.09, step.max_len, ws,
+                            k_scale=a["k_scale"], dev_err=err)
+        torch.cuda.synchronize()
+        return w
+
+    want = run()
+    assert int(err.item()) == 0
+    for fill in (None, 0, 255):
+        if fill is not None:
+            ws.fill_(fill)
+        try:
+            ops.debug_set_weights_hooks(role=role, jobs=jobs)
+            w = run()
+        finally:
+            ops.debug_set_weights_hooks()
+        assert ops.check_error(err) == (TIMEOUT if fp8 or role != "widening" else 0)
+        for r, n in enumerate(step.lens):
+            assert torch.equal(w[r, :, n:], before[r, :, n:])
+        assert torch.equal(run(), want)
+        assert int(err.item()) == 0
