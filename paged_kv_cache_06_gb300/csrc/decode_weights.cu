@@ -58,7 +58,11 @@ constexpr int kMaxRows = 1024;
 constexpr float kLift = 7.f, kMove = 15.f;
 constexpr int kClusterBlocks = 8;    // of a cluster, at most (the portable limit)
 constexpr int kClusterTokens = 4096; // of a row that a cluster takes, at most
+constexpr int kFewLong = 2048;       // rows longer than this are taken for few
 constexpr int kShare = 64;           // granules of its block, at most
+constexpr size_t kClusterDynamic = 1024 + kWarps * kRing + kShare * kGranule * kMaxGroup * sizeof(float);  // at most
+constexpr size_t kSmShared = 228 << 10;                        // bytes of an SM's shared memory
+constexpr size_t kClusterStatic = 5376, kAttendStatic = 640;   // of a block's, beside what it is launched with, at most
 constexpr int kEndThreads = 256;     // of the second kernel: a warp a head
 constexpr int kEndTokens = 4;        // a thread
 constexpr int kTile = kEndThreads * kEndTokens;
@@ -912,6 +916,42 @@ __global__ void __launch_bounds__(kThreads, 4)
 
 std::atomic<int> g_hook_granule{0};  // for tests (pkv_debug_set_weights_hooks); 0 in normal use
 
+// Blocks of `dynamic` and `fixed` bytes of shared memory that an SM holds at once, up to `most` (their registers).
+static int per_sm(size_t dynamic, size_t fixed, int most) {
+    const int fit = (int)(kSmShared / (dynamic + fixed + 1024));  // (1 KB a block is the system's)
+    return fit < 1 ? 1 : fit < most ? fit : most;
+}
+// Blocks of clusters of `blocks` that are resident at once.  Clusters fit into the device's groups of SMs, so fewer
+// of the larger ones are (of 304 blocks, two an SM, 296 in fours and 288 in eights); the device is asked once for each
+// number of blocks an SM.
+template <class K>
+static int64_t resident(K* kernel, bool fp8, int blocks, size_t smem, int sms) {
+    static std::atomic<int> known[64][2][3][4];
+    const int per = per_sm(smem, kClusterStatic, 4);
+    int dev = 0;
+    if (smem > kClusterDynamic || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return (int64_t)sms * per;
+    std::atomic<int>& slot = known[dev][fp8][blocks == 2 ? 0 : blocks == 4 ? 1 : 2][per - 1];
+    int clusters = slot.load(std::memory_order_relaxed);
+    if (clusters == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)blocks);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)blocks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess || clusters <= 0) {
+            cudaGetLastError();
+            return (int64_t)sms * per;
+        }
+        slot.store(clusters, std::memory_order_relaxed);
+    }
+    return (int64_t)clusters * blocks;
+}
+
 struct Layout {
     size_t ml, pre, scores, bytes;
     int tokens, pairs;
@@ -925,7 +965,7 @@ static bool supported(int rows, int q_heads, int kv_heads, int head_dim, int max
            block_size <= 1024 && max_seq_len <= (1 << 24) && kv_heads <= 65536 &&
            granules(rows, kv_heads, max_seq_len) < (int64_t(1) << 31) - kMaxRows;
 }
-// Blocks of the first kernel, as many as fill the device once.
+// Blocks of the first kernel, at most.
 static int blocks_of(int sms) { return sms * kBlocks; }
 // The current device's; on a machine without one, for as many SMs as any has.
 static Layout layout(int rows, int q_heads, int kv_heads, int max_seq_len) {
@@ -1014,10 +1054,6 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     p.dev_err = dev_err;
     p.give_up = g_hook_granule.load(std::memory_order_relaxed) - 1;
     const bool hook = p.give_up >= 0;
-    const int64_t most = granules(rows, kv_heads, max_seq_len);
-    const int wave = blocks_of(sms);
-    const int64_t ranges = (most + kLeast - 1) / kLeast;
-    p.grid = ranges < wave ? (ranges > 0 ? (int)ranges : 1) : wave;
     const int elt = k_scale ? 1 : 2;
     const CUtensorMapDataType type = k_scale ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const int64_t dims[3] = {head_dim, kv_heads, (int64_t)num_blocks * block_size};
@@ -1027,33 +1063,56 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     int st = tiled_map_3d(k_pool, type, dims, strides, box, &kmap);
     if (st == PKV_OK) st = tiled_map_3d(v_pool, type, dims, strides, box, &vmap);
     if (st != PKV_OK) return st;
-    // A block a unit, or a cluster of up to eight, four granules a warp of the longest row, while they
-    // are few enough to be resident at once, four an SM: one launch instead of two.
-    // Against the even cut, 2 KV heads: 4 rows of 100 tokens 4.5 us and 7.8, 8 of 2048 7.8 and 8.2, 32
-    // of 1024 (E4M3) 9.0 and 11.6, 32 of 16 to 512 and one of 4096 10.8 and 12.2, 512 of 128 15.0 and
-    // 31.8, 512 of 1 to 1024 54 and 71, 512 of 1 to 128 and one of 1024 17 and 34; but one of 4096 9.5
-    // and 7.8, 32 of them 33 and 30 (E4M3: 23 and 17.4).  Shares of more than 64 granules, or 4096 tokens,
-    // are the even cut's: 96 rows of 16 to 600 and one of 4000 took clusters in waves 29.4 us, it 18.1.
-    const int n = l.tokens / kGranule;
-    p.blocks = 1;
-    const int64_t units = (int64_t)rows * kv_heads, resident = 4 * (int64_t)sms;
-    while (p.blocks < kClusterBlocks && p.blocks * 4 * kWarps < n && units * 2 * p.blocks <= resident) p.blocks *= 2;
-    int share = (n + p.blocks - 1) / p.blocks;
-    if (max_seq_len <= kClusterTokens && share <= kShare) {
-        if (share < kWarps) share = kWarps;
-        const int bytes = k_scale ? granule_bytes<true> : granule_bytes<false>, most_slots = kRing / bytes;
-        p.slots = (share + kWarps - 1) / kWarps < most_slots ? (share + kWarps - 1) / kWarps : most_slots;
-        const size_t smem = 1024 + (size_t)kWarps * p.slots * bytes + (size_t)share * kGranule * p.pairs * sizeof(float2);
+    // Short rows: a block a unit, or a cluster of up to eight, four granules a warp of the longest row, as many as
+    // are resident at once by the shared memory they take (fp16: two an SM but for the shortest rows).  One launch
+    // instead of two, and no wave that runs alone.  2 KV heads, pools that L2 does not hold, fp16, us, blocks a
+    // unit 1 / 2 / 4 / 8 and the even cut; in brackets E4M3:
+    //   32 rows of 1024  18.1 / 13.5 / 11.7 / 17.3, 15.5  (16.6 / 11.8 / 11.0 / 12.0, 14.5)
+    //   48               19.1 / 15.5 / 19.3 / 19.5, 18.2  (16.8 / 14.2 / 18.6 / 19.4, 17.4)
+    //   76               21.8 / 19.5 / 27.5 / 28.3, 23.7  (17.3 / 15.4 / 25.0 / 24.7, 19.6)
+    //   128              28.5 / 32.9 / 39.4 / 44.4, 34.8  (21.1 / 27.2 / 36.1 / 38.0, 27.5)
+    //   16 of 2048          - / 19.0 / 13.4 / 11.9, 15.2  (   - / 17.3 / 11.7 / 11.2, 14.4)
+    //   64 of 2048          - / 29.5 / 32.8 / 40.7, 33.2  (   - / 22.2 / 27.3 / 38.5, 26.0)
+    // More units than blocks fit take a block each all the same: 300 of 1024 60.9 and 69.7 (42.5 and 52.0), 200 47.6
+    // and 49.2 (38.4 and 35.7), 400 of 256 27.8 and 40.5.  Blocks of more than 64 granules are the even cut's.
+    // Rows longer than 2048 are taken for a few beside many short ones, whose blocks leave at once: eight blocks
+    // each, where that makes no more than four an SM.  31 rows of 16 to 512 and one of 4096: 10.4 us and the even
+    // cut 12.1 with the pools in L2, 16.1 and 13.9 not; 8 of 4096 13.8 and 15.5; but one of them 9.5 and 7.8, and 32
+    // of them 33.8 and 31.0 (28.3 and 22.5).  With more units, or past 4096 tokens, such rows are the even cut's (64 of
+    // 4096: 54.4, in clusters of four 56.7; 96 of 16 to 600 and one of 4000 18.1 and 29.4).
+    if (max_seq_len <= kClusterTokens) {
         auto* kernel = hook      ? (k_scale ? cluster_kernel<true, true> : cluster_kernel<false, true>)
                        : k_scale ? cluster_kernel<true, false>
                                  : cluster_kernel<false, false>;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 1024 + kWarps * kRing + kShare * kGranule * kMaxGroup * (int)sizeof(float)) != cudaSuccess) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kClusterDynamic) != cudaSuccess) {
             cudaGetLastError();
             return PKV_ERR_CUDA;
         }
-        return launch_early_clusters(kernel, dim3((unsigned)(kv_heads * p.blocks), (unsigned)rows), kThreads, smem,
-                                     (unsigned)p.blocks, stream, kmap, vmap, p);
+        const int n = l.tokens / kGranule;
+        const int64_t units = (int64_t)rows * kv_heads;
+        const int bytes = k_scale ? granule_bytes<true> : granule_bytes<false>, most_slots = kRing / bytes;
+        int share = 0;
+        size_t smem = 0;
+        auto cut_into = [&](int blocks) {
+            share = (n + blocks - 1) / blocks > kWarps ? (n + blocks - 1) / blocks : kWarps;
+            p.slots = (share + kWarps - 1) / kWarps < most_slots ? (share + kWarps - 1) / kWarps : most_slots;
+            p.blocks = blocks;
+            smem = 1024 + (size_t)kWarps * p.slots * bytes + (size_t)share * kGranule * p.pairs * sizeof(float2);
+        };
+        cut_into(1);
+        if (max_seq_len > kFewLong && units * kClusterBlocks <= 4 * (int64_t)sms) {
+            cut_into(kClusterBlocks);
+        } else {
+            while (p.blocks < kClusterBlocks && p.blocks * 4 * kWarps < n) {
+                cut_into(2 * p.blocks);
+                if (units * p.blocks <= resident(kernel, k_scale != nullptr, p.blocks, smem, sms)) continue;
+                cut_into(p.blocks / 2);
+                break;
+            }
+        }
+        if (share <= kShare)
+            return launch_early_clusters(kernel, dim3((unsigned)(kv_heads * p.blocks), (unsigned)rows), kThreads, smem,
+                                         (unsigned)p.blocks, stream, kmap, vmap, p);
     }
     auto* attend = hook      ? (k_scale ? attend_kernel<true, true> : attend_kernel<false, true>)
                    : k_scale ? attend_kernel<true, false>
@@ -1066,6 +1125,12 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
         cudaGetLastError();
         return PKV_ERR_CUDA;
     }
+    // As many blocks as fill the device once: three an SM, but two where groups of eight heads and the prefixes of
+    // some 400 rows take the shared memory (512 rows of 4160, one KV head, E4M3: 123.6 us; with three, of which the
+    // last third ran alone, 142.8).
+    const int wave = sms * per_sm(smem, kAttendStatic, kBlocks);
+    const int64_t ranges = (granules(rows, kv_heads, max_seq_len) + kLeast - 1) / kLeast;
+    p.grid = ranges < wave ? (ranges > 0 ? (int)ranges : 1) : wave;
     st = launch_early(attend, (unsigned)p.grid, kThreads, smem, stream, kmap, vmap, p);
     if (st != PKV_OK) return st;
     auto* merge = l.pairs == 1   ? merge_kernel<1>

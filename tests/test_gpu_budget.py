@@ -275,6 +275,45 @@ def test_decode_weights_match_the_formula(cuda_device, case, fp8):
         check(out[r], o, H * o.abs() + (H + 2 * e + (8 + n) * U) * big + low + 2.0 ** -25, f"output of row {r}")
 
 
+SPLITS = [
+    ([1024 - 9 * i for i in range(32)], 12, 2),                    # clusters of four, as many as fit
+    ([1024 - 7 * i for i in range(48)], 12, 2),                    # of two
+    ([2048, 1, 0, 1025] + [i * 61 % 700 for i in range(60)], 16, 2),    # of two, their largest shares
+    ([2048 - 100 * i for i in range(16)], 6, 2),                   # of eight
+    ([1000 - 3 * i for i in range(96)], 12, 2),                    # a block a unit
+    ([2000 - 9 * i for i in range(90)], 8, 2),                     # the even cut, with rows that clusters could take
+    ([4096, 0, 3000] + [i * 31 % 300 for i in range(35)], 12, 2),  # eight blocks for rows taken for few
+    ([4096, 0, 3000] + [i * 31 % 300 for i in range(36)], 12, 2),  # and one row more
+    ([4200] + [i * 17 % 90 for i in range(429)], 8, 1),            # two blocks an SM
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", range(len(SPLITS)))
+def test_decode_weights_at_the_borders_of_the_work_split(cuda_device, case, fp8):
+    """Tolerances as where the weights are compared with the formula."""
+    lens, hq, hk = SPLITS[case]
+    step = Step(lens, [0] * len(lens), 32, hk=hk, fp8=fp8, seed=560 + case)
+    q = torch.randn(len(lens), hq, 128, generator=step.gen).half()
+    before = torch.rand(len(lens), hk, step.max_len + 1, generator=step.gen)
+    a, err, w = step.gpu(), err_word(), before.cuda()
+    out = torch.full(q.shape, float("nan"), dtype=torch.float16, device="cuda")
+    ops.decode_weights(out, w, q.cuda(), a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], 0.0883, step.max_len,
+                       ops.alloc_decode_weights_workspace(len(lens), hq, hk, 128, step.max_len, 32),
+                       k_scale=a["k_scale"], v_scale=a["v_scale"], dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    ref = weights_ref(step, q, 0.0883, [1] * len(lens), [1] * len(lens))
+    check_weights(step, w, before, ref, [1] * len(lens))
+    for r, n in enumerate(lens):
+        if n == 0:
+            assert bool((out[r] == 0).all())
+            continue
+        o, big, e = (x[:, 0] for x in ref[r][2])
+        low = 2.0 ** -32 * step.values(step.v_pool, r, step.v_scale).abs().sum(0).repeat_interleave(hq // hk, 0)
+        check(out[r], o, H * o.abs() + (H + 2 * e + (8 + n) * U) * big + low + 2.0 ** -25, f"output of row {r}")
+
+
 def test_decode_weights_of_bad_lengths_blocks_and_numbers(cuda_device):
     step = Step([100, 60, 300, 40], [0] * 4, 16, seed=13)
     q = torch.randn(4, 12, 128, generator=step.gen).half()
