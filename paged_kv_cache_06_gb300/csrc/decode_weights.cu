@@ -506,10 +506,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 
 // The unit's pieces, and head h's maximum and sum over them by warp h, in end_ml.
 struct Merge {
-    int unit, kvh, c0, pieces;
+    int unit, c0, pieces;
     const float2* ml;
-    __device__ __forceinline__ Merge(const Params& p, int r, int head, int before, int after, int W) {
-        kvh = head;
+    __device__ __forceinline__ Merge(const Params& p, int r, int kvh, int before, int after, int W) {
         unit = r * p.hk + kvh;
         const int count = (after - before) / p.hk, ga = before + kvh * count, n = ranges_of(W, p.grid);
         c0 = owner_of(ga, W, n);

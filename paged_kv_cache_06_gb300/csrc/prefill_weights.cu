@@ -109,7 +109,7 @@ __device__ __forceinline__ int owner_of(int j, int W, int n) { return (int)((((i
 // Rows as the walk needs them, in shared memory.
 struct Rows {
     const int *len, *used, *end;  // tokens, queries that count, the index behind the last query
-    const int *jobs, *units;      // jobs and units of the rows before
+    const int* units;             // units of the rows before
     const int* blocks;            // query blocks of the rows before
     int nq;
     __device__ __forceinline__ int query_blocks(int r) const { return (used[r] + nq - 1) / nq; }
@@ -239,7 +239,6 @@ __global__ void __launch_bounds__(threads<kFp8>(), 1)
     w.len = sm_len;
     w.used = sm_used;
     w.end = sm_end;
-    w.jobs = sm_jobs;
     w.units = kSums ? sm_tiles : sm_blocks;
     w.blocks = sm_blocks;
     w.nq = nq;
