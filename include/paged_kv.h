@@ -759,7 +759,8 @@ int paged_attention_prefill_weights(float* weights, const void* q, const void* k
  * [weights_stride].  Pools as in paged_kv_tree_commit: [layers][num_blocks]
  * [block_size][kv_heads][head_dim] of elt_bytes each, one block table for all
  * layers.  Blocks in which tokens move must not be shared between rows
- * (copy-on-write first); pkv_bm_truncate is the block manager's side.
+ * (copy-on-write first).  pkv_bm_truncate(new length) is the block manager's side: the
+ * row keeps its blocks and takes its later tokens into them.
  * A row with a length outside [0, max_seq_len] is skipped (its new length too)
  * and flagged PKV_DEV_ERR_SEQ_LEN; a table entry out of range sets
  * PKV_DEV_ERR_BLOCK_ID, and the keys and values that would move from or to it
@@ -945,8 +946,8 @@ int pkv_bm_append_slot(pkv_block_manager* bm, int64_t seq_id, int32_t* position_
 
 /*
  * pkv_bm_truncate -- set the sequence's length back to new_len <= its length
- * (PKV_ERR_INVALID_ARG otherwise): the host's side of paged_kv_tree_commit.  Its blocks stay
- * with it, and the next pkv_bm_append_slot calls reuse those that it does not
+ * (PKV_ERR_INVALID_ARG otherwise): the host's side of paged_kv_tree_commit and of
+ * paged_kv_evict.  Its blocks stay with it, and the next pkv_bm_append_slot calls reuse those that it does not
  * share; a shared one is copied on the first write into it, as ever.  A sequence
  * admitted with a reservation keeps its promise: the private blocks that
  * such copies will need are taken now, or the call returns PKV_ERR_NO_BLOCKS and

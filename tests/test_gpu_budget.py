@@ -15,6 +15,7 @@ import pytest
 import torch
 
 from paged_kv_cache_06_gb300 import ops
+from paged_kv_cache_06_gb300.block_manager import BlockManager
 from test_gpu_tree_step import ERR_BLOCK, ERR_LEN, Step, check, err_word, i32
 
 pytestmark = pytest.mark.gpu
@@ -1048,3 +1049,81 @@ def test_prefill_weights_give_up_and_the_next_call_is_as_ever(cuda_device, role,
             assert torch.equal(w[r, :, n:], before[r, :, n:])
         assert torch.equal(run(), want)
         assert int(err.item()) == 0
+
+
+# ---- eviction and the block manager ----
+
+def test_evicted_rows_go_on_over_their_blocks_and_a_finished_ones_go_round(cuda_device):
+    """A row evicts, is truncated and goes on in the slots behind what stayed, over the blocks that it has; when it
+    ends they go to another row, and nothing of the row beside it changes."""
+    bs, hq, hk, budget, sinks, recent, cap, steps = 16, 12, 2, 48, 2, 8, 352, 30
+    gen = torch.Generator().manual_seed(90)
+    randn = lambda *shape: torch.randn(*shape, generator=gen).half()
+    bm = BlockManager(36, bs, cap // bs)
+    prompts = [300, 90]
+    for seq, n in enumerate(prompts):
+        bm.admit(seq, n, steps + 1)
+    tables, lens = bm.tables([0, 1])
+    pools = [randn(36, bs, hk, 128) for _ in range(2)]
+    k_pool, v_pool = (x.cuda() for x in pools)
+    weights = torch.rand(2, hk, cap, generator=gen)
+    w, pos, err = weights.cuda(), torch.zeros(2, hk, cap, dtype=torch.int32, device="cuda"), err_word()
+
+    def slots(table, t):
+        t = np.asarray(t)
+        return torch.from_numpy(table[t // bs].astype(np.int64) * bs + t % bs)
+
+    def stored(r, n):
+        return [p.cpu().view(-1, hk, 128)[slots(tables[r], np.arange(n))] for p in (k_pool, v_pool)]
+
+    want = []                                               # per row: keys and values by slot
+    for r, n in enumerate(prompts):
+        rows = [p.view(-1, hk, 128)[slots(tables[r], np.arange(n))].clone() for p in pools]
+        for h in range(hk):
+            t = np.arange(n)
+            safe = (t < sinks) | (t >= n - recent)
+            stays = np.zeros(n, dtype=bool)
+            stays[np.lexsort((t, -weights[r, h, :n].numpy(), -safe.astype(int)))[:budget]] = True
+            to, frm = t[(t < budget) & ~stays], t[(t >= budget) & stays]
+            for x in rows:
+                x[to, h] = x[frm, h]
+        want.append([x[:budget] for x in rows])
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    ops.evict(k_pool, v_pool, i32(tables), i32(lens), w, pos, budget, cap, sinks=sinks, recent=recent, new_seq_lens=new,
+              dev_err=err)
+    for seq, n in enumerate(new.tolist()):
+        bm.truncate(seq, n)
+    kept, lens = bm.tables([0, 1])
+    assert lens.tolist() == [budget, budget] and np.array_equal(kept, tables)
+    ws = ops.alloc_decode_weights_workspace(2, hq, hk, 128, cap, bs)
+    for i in range(steps):
+        at = [bm.append_slot(seq) for seq in (0, 1)]
+        assert at == [(budget + i, None)] * 2
+        k, v, q = randn(2, hk, 128), randn(2, hk, 128), randn(2, hq, 128)
+        tables, lens = bm.tables([0, 1])
+        ops.append(k_pool, v_pool, i32(tables), i32([p for p, _ in at]), k.cuda(), v.cuda(), dev_err=err)
+        out = torch.empty(2, hq, 128, dtype=torch.float16, device="cuda")
+        ops.decode_weights(out, w, q.cuda(), k_pool, v_pool, i32(tables), i32(lens), 0.0883, cap, ws, dev_err=err)
+        torch.cuda.synchronize()
+        for r in range(2):
+            want[r] = [torch.cat([x, y[r:r + 1]]) for x, y in zip(want[r], (k, v))]
+            for x, y in zip(stored(r, int(lens[r])), want[r]):
+                assert torch.equal(x, y)
+            for h in range(hk):
+                kk, vv = (x[:, h].double() for x in want[r])
+                p = torch.softmax(q[r, 6 * h:6 * h + 6].double() @ kk.T * 0.0883, -1)
+                assert torch.allclose(out[r, 6 * h:6 * h + 6].double().cpu(), p @ vv, rtol=4e-3, atol=4e-3)
+    assert np.array_equal(tables, kept)                     # thirty tokens more in the blocks that they had
+    # row 0 ends; another one takes its blocks
+    bm.free(0)
+    assert bm.try_admit(2, 320, 1)
+    table, n = bm.table(2)
+    assert set(table[:20].tolist()) & set(kept[0][:20].tolist()) and not set(table[:20].tolist()) & set(kept[1][:8].tolist())
+    k, v = randn(1, n, hk, 128), randn(1, n, hk, 128)
+    ops.prefill_scatter(k_pool, v_pool, i32(table[None]), i32([0]), i32([0]), i32([n]), k.cuda(), v.cuda(), dev_err=err)
+    torch.cuda.synchronize()
+    for x, y in zip(stored(1, int(lens[1])), want[1]):
+        assert torch.equal(x, y)
+    for p, x in ((k_pool, k), (v_pool, v)):
+        assert torch.equal(p.cpu().view(-1, hk, 128)[slots(table, np.arange(n))], x[0])
+    assert int(err.item()) == 0
