@@ -10,6 +10,10 @@ and sum within 2 u, its root halves that and takes 4 u itself, the two products 
 half an E4M3 step of the stored quotient (2^-4 of it, 2^-10 below the normal range).
 Eviction moves bits: equality.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -1127,3 +1131,42 @@ def test_evicted_rows_go_on_over_their_blocks_and_a_finished_ones_go_round(cuda_
     for p, x in ((k_pool, k), (v_pool, v)):
         assert torch.equal(p.cpu().view(-1, hk, 128)[slots(table, np.arange(n))], x[0])
     assert int(err.item()) == 0
+
+
+def test_a_first_call_inside_a_capture(cuda_device):
+    """A fresh process whose first decode and prompt weights are captured: what a first call asks the device for
+    may be asked there, and the replays give the eager calls' bits."""
+    code = """
+import torch
+from paged_kv_cache_06_gb300 import ops
+gen = torch.Generator().manual_seed(3)
+rows, n, bs = 76, 900, 32
+per = (n + bs - 1) // bs
+k, v = (torch.randn(rows * per, bs, 2, 128, generator=gen).half().cuda() for _ in range(2))
+tables = torch.arange(rows * per, dtype=torch.int32).view(rows, per).flip(1).contiguous().cuda()
+lens = torch.full((rows,), n, dtype=torch.int32, device="cuda")
+q = torch.randn(rows, 12, 128, generator=gen).half().cuda()
+starts = torch.arange(rows + 1, dtype=torch.int32, device="cuda")
+first = torch.rand(rows, 2, n, generator=gen).cuda()
+w, out = first.clone(), torch.zeros_like(q)
+wsd = ops.alloc_decode_weights_workspace(rows, 12, 2, 128, n, bs)
+wsp = ops.alloc_prefill_weights_workspace(rows, rows, 12, 2, 128, n, bs)
+def both():
+    ops.decode_weights(out, w, q, k, v, tables, lens, 0.09, n, wsd)
+    ops.prefill_weights(w, q, k, tables, lens, starts, 0.09, n, wsp)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    both()
+results = []
+for run in (graph.replay, graph.replay, both):
+    w.copy_(first)
+    out.zero_()
+    run()
+    torch.cuda.synchronize()
+    results.append((w.clone(), out.clone()))
+assert float(results[0][1].abs().max()) > 0 and not torch.equal(results[0][0], first)
+for r in results[1:]:
+    assert torch.equal(r[0], results[0][0]) and torch.equal(r[1], results[0][1])
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    assert subprocess.run([sys.executable, "-c", code], cwd=root, timeout=300).returncode == 0
