@@ -13,7 +13,7 @@
 // each of up to three blocks an SM.  A block's four warps take its granules in turn, each through
 // a ring of its own that it fills by tiled copies, one box of 16 tokens and 64 dims (128
 // codes) each; 192 KB an SM are on their way.  A granule costs a warp
-//   S^T[16 tok][8 heads] = K Q^T, then O^T[128][8] += V^T P^T, P in fp16,
+//   S^T[16 tok][8 heads] = K Q^T, then O^T[128][8] += V^T P^T, P as the sum of two fp16 numbers,
 // with the grouped heads as the products' eight columns (E4M3 codes are widened in registers,
 // exactly, with the dims in an order that lets a lane read 16 bytes of a row at a time).  The
 // reference that exponents are taken from moves only when a score passes it by kMove: as a rule a
@@ -51,10 +51,11 @@ constexpr int kBlocks = 3;           // resident per SM
 constexpr int kRing = 16 << 10;      // bytes of a warp's ring
 constexpr int kMaxRows = 1024;
 // A head's reference lies 7 (in powers of two) below the largest score at the time and moves when a score passes
-// it by more than 15.  The output's weights, rounded to fp16 for the tensor cores (by 2^-11 of each at most, which
-// adds 1.2e-4 to 2.0e-4 to the 2.1e-4 of the output's own rounding; the sums and the weights handed out keep 32
-// bits), so stay below 2^15, and one of 2^-21 of the largest keeps its eleven bits.  With the reference at the
-// largest, weights below 2^-25 of it were in the row's sum and not in its output.
+// it by more than 15: weights stay below 2^15, fp16 numbers, and those down to 2^-21 of the largest are normal ones.
+// (With the reference at the largest, weights below 2^-25 of it were in the row's sum and not in its output.)
+// The output's products take a weight as two fp16 numbers, the rounded weight and what the rounding left, good to
+// 2^-22 of it or 2^-32 of the largest; the sums and the weights handed out keep 32 bits.  The first number alone put
+// the output off by 2.4e-4 to 2.9e-4 where its own rounding is 2.1e-4, for 0.1 to 0.2 us less in 10.5, 8.6 and 31.2.
 constexpr float kLift = 7.f, kMove = 15.f;
 constexpr int kClusterBlocks = 8;    // of a cluster, at most (the portable limit)
 constexpr int kClusterTokens = 4096; // of a row that a cluster takes, at most
@@ -179,10 +180,18 @@ __device__ __forceinline__ void scores_of(float (&s)[4], const unsigned char* da
 }
 // O^T += V^T P^T; tile mt's rows g and g + 8 are the dims 16 mt + g and 16 mt + 8 + g, or, of
 // codes, 16 g + 2 mt and 16 g + 2 mt + 1.
-// The values of tokens from `valid` on are taken for zeros (their slots may hold anything).
+// P: pb, and qb, what rounding left of it, of any sign: it is multiplied by values that are finite, so that an infinite
+// one stays what pb makes of it.  The values of tokens from `valid` on are taken for zeros (their slots may hold
+// anything).
+// Both halves, infinities as the largest finite number of their sign.
+__device__ __forceinline__ uint32_t finite2(uint32_t x) {
+    uint32_t y;
+    asm("min.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7bff7bffu));
+    return y;
+}
 template <bool kFp8>
 __device__ __forceinline__ void add_values(float (&o)[8][4], const unsigned char* data, uint32_t at, uint32_t pb0,
-                                           uint32_t pb1, int valid, int lane) {
+                                           uint32_t pb1, uint32_t qb0, uint32_t qb1, int valid, int lane) {
     const int t = lane & 3;
     if (kFp8) {
         const int g = lane >> 2;
@@ -194,23 +203,38 @@ __device__ __forceinline__ void add_values(float (&o)[8][4], const unsigned char
             if (row >= valid) x[j] = make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-            const uint32_t sel = mt & 1 ? 0x7362u : 0x5140u;
-            uint32_t a0, a1, a2, a3;
-            widen4(__byte_perm(word(x[0], mt >> 1), word(x[1], mt >> 1), sel), a0, a1);
-            widen4(__byte_perm(word(x[2], mt >> 1), word(x[3], mt >> 1), sel), a2, a3);
-            mma16816(o[mt], a0, a1, a2, a3, pb0, pb1);
+        for (int mt = 0; mt < 8; mt += 2) {  // two tiles: a tile's products follow each other at a distance
+            uint32_t a[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t sel = i ? 0x7362u : 0x5140u;
+                widen4(__byte_perm(word(x[0], mt >> 1), word(x[1], mt >> 1), sel), a[i][0], a[i][1]);
+                widen4(__byte_perm(word(x[2], mt >> 1), word(x[3], mt >> 1), sel), a[i][2], a[i][3]);
+                mma16816(o[mt + i], a[i][0], a[i][1], a[i][2], a[i][3], pb0, pb1);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) mma16816(o[mt + i], a[i][0], a[i][1], a[i][2], a[i][3], qb0, qb1);
         }
     } else {
         const int row = (lane & 7) + (lane >> 4) * 8;
         const uint32_t lo = (2 * t < valid ? 0xffffu : 0u) | (2 * t + 1 < valid ? 0xffff0000u : 0u);
         const uint32_t hi = (2 * t + 8 < valid ? 0xffffu : 0u) | (2 * t + 9 < valid ? 0xffff0000u : 0u);
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-            const int chunk = (mt & 3) * 2 + ((lane >> 3) & 1);
-            uint32_t a0, a1, a2, a3;
-            ldsm_x4_t(at + (2 + (mt >> 2)) * kBox + row * 128 + ((chunk ^ (row & 7)) << 4), a0, a1, a2, a3);
-            mma16816(o[mt], a0 & lo, a1 & lo, a2 & hi, a3 & hi, pb0, pb1);
+        for (int mt = 0; mt < 8; mt += 2) {
+            uint32_t a[2][4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int chunk = ((mt + i) & 3) * 2 + ((lane >> 3) & 1);
+                ldsm_x4_t(at + (2 + (mt >> 2)) * kBox + row * 128 + ((chunk ^ (row & 7)) << 4), a[i][0], a[i][1], a[i][2], a[i][3]);
+                a[i][0] &= lo;
+                a[i][1] &= lo;
+                a[i][2] &= hi;
+                a[i][3] &= hi;
+                mma16816(o[mt + i], a[i][0], a[i][1], a[i][2], a[i][3], pb0, pb1);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                mma16816(o[mt + i], finite2(a[i][0]), finite2(a[i][1]), finite2(a[i][2]), finite2(a[i][3]), qb0, qb1);
         }
     }
 }
@@ -273,7 +297,11 @@ __device__ __forceinline__ void attend(State& st, const unsigned char* data, uin
     // the sums take the weights in 32 bits: the weights handed out are divided by them too
     st.l0 += p0 + p2;
     st.l1 += p1 + p3;
-    add_values<kFp8>(st.o, data, at, movmatrix_t(pack_half2(p0, p1)), movmatrix_t(pack_half2(p2, p3)), valid, lane);
+    const __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
+    const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+    add_values<kFp8>(st.o, data, at, movmatrix_t(*reinterpret_cast<const uint32_t*>(&h0)),
+                     movmatrix_t(*reinterpret_cast<const uint32_t*>(&h1)), movmatrix_t(pack_half2(p0 - f0.x, p1 - f0.y)),
+                     movmatrix_t(pack_half2(p2 - f1.x, p3 - f1.y)), valid, lane);
 }
 
 // Place d of a half's 64 dims of head h in a warp's state; pairs of heads lie on other banks.

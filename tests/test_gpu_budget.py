@@ -280,6 +280,62 @@ def test_decode_weights_match_the_formula(cuda_device, case, fp8):
         check(out[r], o, H * o.abs() + (H + 2 * e + (8 + n) * U) * big + low + 2.0 ** -25, f"output of row {r}")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("cap", [48, 5000])
+def test_decode_weights_of_values_that_cancel(cuda_device, cap, fp8):
+    """Nearly equal weights of values of both signs.  A weight reaches the output within 2^-22 of itself and 2^-32 of the
+    largest, so what is left of the sum is good to that share of A = sum p |v|, and to half a step of its own."""
+    lens = [2, 4, 6, 10, 16, 40]
+    step = Step(lens, [0] * 6, 16, fp8=fp8, seed=32)
+    values = (90 + 20 * torch.rand(step.v_pool.shape, generator=step.gen)) * (1 - 2 * (torch.arange(16) % 2))[:, None, None]
+    if fp8:
+        step.k_scale, step.v_scale = torch.full((2,), 0.02), torch.ones(2)
+        step.v_pool = values.to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        step.v_pool = values.half()
+    q = (0.05 * torch.randn(6, 12, 128, generator=step.gen)).half()
+    ref = weights_ref(step, q, 0.0883, [1] * 6, [1] * 6)
+    tables = np.concatenate([step.tables, np.full((6, (cap + 15) // 16 - step.tables.shape[1]), -1, dtype=np.int32)], 1)
+    before = torch.zeros(6, 2, cap)
+    a, err, w = step.gpu(block_tables=i32(tables)), err_word(), before.cuda()
+    out = torch.zeros(q.shape, dtype=torch.float16, device="cuda")
+    ops.decode_weights(out, w, q.cuda(), a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], 0.0883, cap,
+                       ops.alloc_decode_weights_workspace(6, 12, 2, 128, cap, 16), k_scale=a["k_scale"],
+                       v_scale=a["v_scale"], dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check_weights(step, w, before, ref, [1] * 6)
+    for r, n in enumerate(lens):
+        o, big, e = (x[:, 0] for x in ref[r][2])
+        low = 2.0 ** -32 * step.values(step.v_pool, r, step.v_scale).abs().sum(0).repeat_interleave(6, 0)
+        check(out[r], o, H * o.abs() + (2.0 ** -22 + 2 * e + (12 + n) * U) * big + low + 2.0 ** -25, f"output of row {r}")
+
+
+@pytest.mark.parametrize("cap", [80, 5000])
+def test_decode_weights_of_infinite_values(cuda_device, cap):
+    """An infinite value is its dim's output, two of both signs are no number, and other dims keep their bits."""
+    step = Step([70, 30], [0, 0], 16, seed=33)
+    q = torch.randn(2, 12, 128, generator=step.gen).half().cuda()
+    tables = np.concatenate([step.tables, np.full((2, (cap + 15) // 16 - step.tables.shape[1]), -1, dtype=np.int32)], 1)
+    ws = ops.alloc_decode_weights_workspace(2, 12, 2, 128, cap, 16)
+
+    def run():
+        a, w, out = step.gpu(block_tables=i32(tables)), torch.zeros(2, 2, cap, device="cuda"), torch.zeros_like(q)
+        ops.decode_weights(out, w, q, a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], 0.0883, cap, ws)
+        torch.cuda.synchronize()
+        return out.cpu(), w.cpu()
+
+    clean, weights = run()
+    v, slots, inf = step.v_pool.view(-1, 2, 128), step.slots(0), float("inf")
+    v[slots[3], 0, 5], v[slots[60], 0, 77], v[slots[20], 1, 8], v[slots[66], 1, 8] = inf, -inf, inf, -inf
+    out, w = run()
+    assert torch.equal(w, weights)
+    assert bool((out[0, :6, 5] == inf).all()) and bool((out[0, :6, 77] == -inf).all()) and bool(torch.isnan(out[0, 6:, 8]).all())
+    same = torch.ones(2, 12, 128, dtype=torch.bool)
+    same[0, :6, [5, 77]] = same[0, 6:, 8] = False
+    assert torch.equal(out[same], clean[same])
+
+
 SPLITS = [
     ([1024 - 9 * i for i in range(32)], 12, 2),                    # clusters of four, as many as fit
     ([1024 - 7 * i for i in range(48)], 12, 2),                    # of two
