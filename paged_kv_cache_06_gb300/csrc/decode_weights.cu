@@ -27,9 +27,9 @@
 // each other their maxima and sums and the parts of the output that another of them finishes
 // through distributed shared memory, and each turns its own scores into weights.
 //
-// What bounds it.  Few rows: one dependent chain (32 rows of 1024, E4M3, 9.0 us: 1.7 for the launch
-// and the length, 1.9 for the copies, 1.7 for four granules a warp, 1.3 and 2.3 for bringing the
-// block's and the cluster's parts together).  Long rows: 4 of 32768, 31.4 us; the first kernel
+// What bounds it.  Few rows: one dependent chain (32 rows of 1024, E4M3, in L2 8.7 us; stage by stage 1.7 for
+// the launch and the length, 1.9 for the copies, 1.7 for four granules a warp, 1.3 and 2.3 for bringing the
+// block's and the cluster's parts together).  Long rows: 4 of 32768, 31.3 us; the first kernel
 // takes 25 of them, 5.3 TB/s, and the second, with its launch, 6.
 #include <math.h>
 
@@ -1094,19 +1094,19 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     // are resident at once by the shared memory they take (fp16: two an SM but for the shortest rows).  One launch
     // instead of two, and no wave that runs alone.  2 KV heads, pools that L2 does not hold, fp16, us, blocks a
     // unit 1 / 2 / 4 / 8 and the even cut; in brackets E4M3:
-    //   32 rows of 1024  18.1 / 13.5 / 11.7 / 17.3, 15.5  (16.6 / 11.8 / 11.0 / 12.0, 14.5)
-    //   48               19.1 / 15.5 / 19.3 / 19.5, 18.2  (16.8 / 14.2 / 18.6 / 19.4, 17.4)
-    //   76               21.8 / 19.5 / 27.5 / 28.3, 23.7  (17.3 / 15.4 / 25.0 / 24.7, 19.6)
-    //   128              28.5 / 32.9 / 39.4 / 44.4, 34.8  (21.1 / 27.2 / 36.1 / 38.0, 27.5)
-    //   16 of 2048          - / 19.0 / 13.4 / 11.9, 15.2  (   - / 17.3 / 11.7 / 11.2, 14.4)
-    //   64 of 2048          - / 29.5 / 32.8 / 40.7, 33.2  (   - / 22.2 / 27.3 / 38.5, 26.0)
-    // More units than blocks fit take a block each all the same: 300 of 1024 60.9 and 69.7 (42.5 and 52.0), 200 47.6
-    // and 49.2 (38.4 and 35.7), 400 of 256 27.8 and 40.5.  Blocks of more than 64 granules are the even cut's.
+    //   32 rows of 1024  18.5 / 13.7 / 11.8 / 17.7, 15.8  (17.3 / 12.0 / 11.2 / 12.2, 14.8)
+    //   48               19.5 / 15.7 / 19.7 / 19.9, 18.4  (17.5 / 14.6 / 19.0 / 19.7, 17.7)
+    //   76               21.9 / 19.6 / 28.0 / 28.8, 23.9  (18.0 / 15.8 / 25.2 / 25.2, 20.1)
+    //   128              28.7 / 33.3 / 39.9 / 45.0, 35.0  (21.8 / 27.9 / 36.7 / 38.5, 28.0)
+    //   16 of 2048          - / 19.4 / 13.5 / 12.1, 15.5  (   - / 18.1 / 12.1 / 11.5, 14.6)
+    //   64 of 2048          - / 29.6 / 33.2 / 41.5, 33.4  (   - / 22.8 / 28.0 / 39.3, 26.7)
+    // More units than blocks fit take a block each all the same: 300 of 1024 61.1 and 70.2 (42.7 and 52.4), 200 48.9
+    // and 49.8 (39.4 and 36.1), 400 of 256 28.3 and 40.7.  Blocks of more than 64 granules are the even cut's.
     // Rows longer than 2048 are taken for a few beside many short ones, whose blocks leave at once: eight blocks
-    // each, where that makes no more than four an SM.  31 rows of 16 to 512 and one of 4096: 10.4 us and the even
-    // cut 12.1 with the pools in L2, 16.1 and 13.9 not; 8 of 4096 13.8 and 15.5; but one of them 9.5 and 7.8, and 32
-    // of them 33.8 and 31.0 (28.3 and 22.5).  With more units, or past 4096 tokens, such rows are the even cut's (64 of
-    // 4096: 54.4, in clusters of four 56.7; 96 of 16 to 600 and one of 4000 18.1 and 29.4).
+    // each, where that makes no more than four an SM.  31 rows of 16 to 512 and one of 4096: 10.6 us and the even
+    // cut 12.2 with the pools in L2, 16.5 and 14.2 not; 8 of 4096 14.1 and 15.7; but one of them 9.9 and 7.8, and 32
+    // of them 34.0 and 31.3 (28.9 and 23.2).  With more units, or past 4096 tokens, such rows are the even cut's (64 of
+    // 4096: 54.8, in clusters of four 57.2; 96 of 16 to 600 and one of 4000 18.1 and 29.4).
     if (max_seq_len <= kClusterTokens) {
         auto* kernel = hook      ? (k_scale ? cluster_kernel<true, true> : cluster_kernel<false, true>)
                        : k_scale ? cluster_kernel<true, false>
@@ -1153,7 +1153,7 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
         return PKV_ERR_CUDA;
     }
     // As many blocks as fill the device once: three an SM, but two where groups of eight heads and the prefixes of
-    // some 400 rows take the shared memory (512 rows of 4160, one KV head, E4M3: 123.6 us; with three, of which the
+    // some 400 rows take the shared memory (512 rows of 4160, one KV head, E4M3: 123.9 us; with three, of which the
     // last third ran alone, 142.8).
     const int wave = sms * per_sm(smem, kAttendStatic, kBlocks);
     const int64_t ranges = (granules(rows, kv_heads, max_seq_len) + kLeast - 1) / kLeast;

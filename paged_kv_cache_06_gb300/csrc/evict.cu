@@ -23,10 +23,10 @@
 //
 // What bounds it.  The choice is a chain: load, differing bits, one to four histograms, the
 // equal keys, the slots.  1792 lists of 1025 tokens, of which one leaves each (14.7 MB of weights
-// and positions): 17.9 us, all but 1.5 the choice; all blocks are resident at once, 12 an SM, and
-// issue in 71% of the cycles (64 threads a block, 20 an SM: 23.3).
-// 896 lists of 1900 to 2304, E4M3: 23.2 us, 15 of them the choice.  32 lists of 30,000 to 32,768 down
-// to 4096: 39.6 us, 18.4 the choice (three cluster barriers a histogram) and 21.5 the
+// and positions): 17.4 us, all but 1.5 the choice; all blocks are resident at once, 12 an SM, and
+// issue in 66% of the cycles, 6,700 warp instructions a list (64 threads a block, 20 an SM: 23.3).
+// 896 lists of 1900 to 2304, E4M3: 23.0 us, 15 of them the choice.  32 lists of 30,000 to 32,768 down
+// to 4096: 39.2 us, 18.4 the choice (three cluster barriers a histogram) and 21 the
 // moves, 117 MB in pieces of 256 bytes, 5.4 TB/s.
 #include "pkv_internal.cuh"
 #include "ptx.cuh"

@@ -31,9 +31,12 @@
 // clocks, is in every job: their loops keep slots and parities as running values and find
 // pool rows a batch at a time (with divisions and a look-up a job: 0.72 us a job).
 //
-// What bounds it.  Four rows of 3900 to 4096, every query (12 heads over 2): 241 us, 117 a pass
-// for 165 jobs an SM, 0.71 us a job: its 16,384 exponentials alone take the SM 0.5, its copy from L2
-// 0.55 (both passes without the sums: 183 us), and the two do not overlap fully; the products take 0.28.
+// What bounds it.  Four rows of 3900 to 4096, every query (12 heads over 2): 240 us, 117 a pass
+// for 165 jobs an SM, 0.71 us or 1,180 clocks a job.  No unit is full: 16,384 exponentials take the
+// special-function unit 512 clocks (32 a clock, measured; 40 to 42% busy), the products the tensor pipe 490
+// (41 to 43%), L2 gives 28% of its rate and 48 to 52% of the issue slots are used.  What is left are the roles'
+// chains: without the sums both passes take 183 us, 0.55 a job for copies, barriers and products, and a
+// group's wait, loads from tensor memory and sums do not hide behind them fully.
 // Eight chunks of 512 over 300 to 2100 (32 heads over 8): 123 us.  The last 32 queries of 16 rows of 600
 // to 4500, E4M3: 35 us, of which 9 are four launches with nothing to do, 13 the eight or nine
 // jobs an SM of each pass, and the rest each pass's first copy, product and sum and its

@@ -25,9 +25,9 @@
 // bandwidth, less the first 3 to 4 us in which every block looks up and makes its
 // table (15,000 tokens: 24.8 us, 4.8 TB/s read and written, 71% of a plain copy's
 // rate).  48 registers and five blocks an SM: with four, 25.3 us; with six, which
-// spill, 27.2; two items in flight a thread, 25.2.  With norms 3.5 us and, for the 15,000
-// tokens, 28.6 (4.2 TB/s, 62%): an item is a whole turn of loads, sums over lanes and
-// stores, and three blocks an SM hold its 84 registers (four, which spill, 31.0 us, five 34.7).
+// spill, 27.2; two items in flight a thread, 25.2.  With norms 3.3 us and, for the 15,000
+// tokens, 27.8 (4.3 TB/s, 63%): an item is a whole turn of loads, sums over lanes and
+// stores, and three blocks an SM hold its 80 registers (four, which spill, 31.0 us, five 34.7).
 #include <math.h>
 
 #include "fp8_codec.cuh"
