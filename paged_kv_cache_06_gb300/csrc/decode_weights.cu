@@ -59,6 +59,7 @@ constexpr int kMaxRows = 1024;
 constexpr float kLift = 7.f, kMove = 15.f;
 constexpr int kClusterBlocks = 8;    // of a cluster, at most (the portable limit)
 constexpr int kClusterTokens = 4096; // of a row that a cluster takes, at most
+constexpr int kOrdered = 96;         // rows that may be ordered so that clusters take the long ones first
 constexpr int kFewLong = 2048;       // rows longer than this are taken for few
 constexpr int kShare = 64;           // granules of its block, at most
 constexpr size_t kClusterDynamic = 1024 + kWarps * kRing + kShare * kGranule * kMaxGroup * sizeof(float);  // at most
@@ -89,6 +90,7 @@ struct Params {
     int grid;          // blocks of the first kernel
     int blocks;        // of a cluster
     int slots;         // of a cluster's warps' rings
+    int ordered;       // clusters take the long rows first
     float scale_log2;
     int* pre;          // [rows + 1]: granules of the rows before
     float* part;       // [block + unit][group][128]: the block's piece of the unit, unnormalised
@@ -225,7 +227,8 @@ __device__ __forceinline__ void add_values(float (&o)[8][4], const unsigned char
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int chunk = ((mt + i) & 3) * 2 + ((lane >> 3) & 1);
-                ldsm_x4_t(at + (2 + (mt >> 2)) * kBox + row * 128 + ((chunk ^ (row & 7)) << 4), a[i][0], a[i][1], a[i][2], a[i][3]);
+                ldsm_x4_t(at + (2 + (mt >> 2)) * kBox + row * 128 + ((chunk ^ (row & 7)) << 4), a[i][0], a[i][1],
+                          a[i][2], a[i][3]);
                 a[i][0] &= lo;
                 a[i][1] &= lo;
                 a[i][2] &= hi;
@@ -724,7 +727,8 @@ __global__ void __launch_bounds__(kThreads, 4)
     __shared__ int stop;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int gq = lane >> 2, tq = lane & 3;
-    const int rank = (int)block_rank(), kvh = (int)blockIdx.x / p.blocks, r = (int)blockIdx.y;
+    const int rank = (int)block_rank(), kvh = (int)blockIdx.x / p.blocks;
+    int r = (int)blockIdx.y;
     if (tid < kWarps * kMostSlots) {
         mbar_init(smem_u32(&bars[0][0] + tid), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -735,7 +739,33 @@ __global__ void __launch_bounds__(kThreads, 4)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&vmap)) : "memory");
     }
     griddep_wait();
-    int L = p.seq_lens[r];
+    int L = 0;
+    if (p.ordered) {
+        // rows of more than a quarter of the limit come first, then the others; every warp finds the r-th by itself
+        int len[kOrdered / 32], places = 0, before = 0;
+        uint32_t tall[kOrdered / 32];
+#pragma unroll
+        for (int c = 0; c < kOrdered / 32; ++c) len[c] = 32 * c + lane < p.rows ? p.seq_lens[32 * c + lane] : 0;
+#pragma unroll
+        for (int c = 0; c < kOrdered / 32; ++c) {
+            tall[c] = __ballot_sync(0xffffffffu, len[c] > p.limit / 4);
+            places += __popc(tall[c]);
+        }
+        const int want = r;
+#pragma unroll
+        for (int c = 0; c < kOrdered / 32; ++c) {
+            const int row = 32 * c + lane, taller = before + __popc(tall[c] & ((1u << lane) - 1));
+            const int place = tall[c] >> lane & 1 ? taller : places + row - taller;
+            const uint32_t it = __ballot_sync(0xffffffffu, place == want);
+            if (it) {
+                r = 32 * c + __ffs(it) - 1;
+                L = __shfl_sync(0xffffffffu, len[c], __ffs(it) - 1);
+            }
+            before += __popc(tall[c]);
+        }
+    } else {
+        L = p.seq_lens[r];
+    }
     if (L < 0 || L > p.limit) {
         if (rank == 0 && kvh == 0 && tid == 0) flag_error(p.dev_err, PKV_DEV_ERR_SEQ_LEN);
         L = L < 0 ? 0 : p.limit;
@@ -1102,16 +1132,20 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
     //   64 of 2048          - / 29.6 / 33.2 / 41.5, 33.4  (   - / 22.8 / 28.0 / 39.3, 26.7)
     // More units than blocks fit take a block each all the same: 300 of 1024 61.1 and 70.2 (42.7 and 52.4), 200 48.9
     // and 49.8 (39.4 and 36.1), 400 of 256 28.3 and 40.7.  Blocks of more than 64 granules are the even cut's.
-    // Rows longer than 2048 are taken for a few beside many short ones, whose blocks leave at once: eight blocks
-    // each, where that makes no more than four an SM.  31 rows of 16 to 512 and one of 4096: 10.6 us and the even
-    // cut 12.2 with the pools in L2, 16.5 and 14.2 not; 8 of 4096 14.1 and 15.7; but one of them 9.9 and 7.8, and 32
-    // of them 34.0 and 31.3 (28.9 and 23.2).  With more units, or past 4096 tokens, such rows are the even cut's (64 of
-    // 4096: 54.8, in clusters of four 57.2; 96 of 16 to 600 and one of 4000 18.1 and 29.4).
+    // Rows longer than 2048 are taken for a few beside many short ones, whose blocks leave at once: eight blocks each,
+    // where that makes no more than four an SM, and the long rows first where they are not all resident.  31 rows of
+    // 16 to 512 and one of 4096, in any order: 10.6 to 11.4 us and the even cut 12.3 with the pools in L2, 13.2 and
+    // 15.4 not (E4M3 12.3 and 13.3, 13.9 and 15.4; with the rows as they come 10.5 to 15.8 by where the long one is);
+    // 32 of 16 to 4096, their logarithms even, 14.6 and 18.9; 8 of 4096 14.1 and 15.7; but 32 of 1 to 4096 23.4 and
+    // 22.9, one of 4096 9.9 and 7.8, and 32 of them 34.6 and 31.4 (29.4 and 23.1).  With more units, or past 4096
+    // tokens, such rows are the even cut's (64 of 4096: 54.8, in clusters of four 57.2; 96 of 16 to 600 and one of
+    // 4000 18.1 and 29.4).
     if (max_seq_len <= kClusterTokens) {
         auto* kernel = hook      ? (k_scale ? cluster_kernel<true, true> : cluster_kernel<false, true>)
                        : k_scale ? cluster_kernel<true, false>
                                  : cluster_kernel<false, false>;
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kClusterDynamic) != cudaSuccess) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kClusterDynamic) !=
+            cudaSuccess) {
             cudaGetLastError();
             return PKV_ERR_CUDA;
         }
@@ -1127,8 +1161,9 @@ extern "C" int paged_attention_decode_weights(void* out, float* weights, const v
             smem = 1024 + (size_t)kWarps * p.slots * bytes + (size_t)share * kGranule * p.pairs * sizeof(float2);
         };
         cut_into(1);
-        if (max_seq_len > kFewLong && units * kClusterBlocks <= 4 * (int64_t)sms) {
+        if (max_seq_len > kFewLong && units * kClusterBlocks <= 4 * (int64_t)sms && rows <= kOrdered) {
             cut_into(kClusterBlocks);
+            p.ordered = units * kClusterBlocks > resident(kernel, k_scale != nullptr, kClusterBlocks, smem, sms);
         } else {
             while (p.blocks < kClusterBlocks && p.blocks * 4 * kWarps < n) {
                 cut_into(2 * p.blocks);

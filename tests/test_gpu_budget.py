@@ -375,6 +375,42 @@ def test_decode_weights_at_the_borders_of_the_work_split(cuda_device, case, fp8)
         check(out[r], o, H * o.abs() + (H + 2 * e + (8 + n) * U) * big + low + 2.0 ** -25, f"output of row {r}")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("more,hq,hk", [(24, 12, 2), (66, 8, 1), (55, 6, 1)])
+def test_decode_weights_whatever_the_order_of_the_rows(cuda_device, more, hq, hk, fp8):
+    """Rows that clusters take by their lengths, among them equal ones, empty ones and lengths that are out of range:
+    in any order each has the same bits."""
+    lens = [4096, 17, 0, 300, 300, 2500, 1, 300, 4096, 64] + [20 * i for i in range(more)]
+    rows = len(lens)
+    step = Step(lens, [0] * rows, 64, hk=hk, fp8=fp8, seed=34)
+    q = torch.randn(rows, hq, 128, generator=step.gen).half()
+    before = torch.rand(rows, hk, 4096, generator=step.gen)
+    given = np.array(lens)
+    given[6], given[7] = -3, 5000                            # taken for 0 and 4096, and flagged
+    full = step.tables.copy()
+    full[7] = full[0]                                        # blocks for its 4096 tokens
+    ws = ops.alloc_decode_weights_workspace(rows, hq, hk, 128, 4096, 64)
+    results = []
+    for seed in range(4):
+        order = np.arange(rows) if seed == 0 else np.random.default_rng(seed).permutation(rows)
+        a, err = step.gpu(block_tables=i32(full[order]), seq_lens=i32(given[order])), err_word()
+        w, out = before[order].cuda(), torch.full(q.shape, float("nan"), dtype=torch.float16, device="cuda")
+        ops.decode_weights(out, w, q[order].cuda(), a["k_pool"], a["v_pool"], a["block_tables"], a["seq_lens"], 0.0883, 4096,
+                           ws, k_scale=a["k_scale"], v_scale=a["v_scale"], dev_err=err)
+        assert ops.check_error(err) == ERR_LEN
+        back = np.argsort(order)
+        results.append((out.cpu()[back], w.cpu()[back]))
+    for out, w in results[1:]:
+        assert torch.equal(out, results[0][0]) and torch.equal(w, results[0][1])
+    out, w = results[0]
+    ref = weights_ref(step, q, 0.0883, [1] * rows, [1] * rows)
+    ref[6] = None
+    for r in (6, 2):
+        assert bool((out[r] == 0).all()) and torch.equal(w[r], before[r])
+    w[7], ref[7] = before[7], None
+    check_weights(step, w, before, ref, [1] * rows)
+
+
 def test_decode_weights_of_bad_lengths_blocks_and_numbers(cuda_device):
     step = Step([100, 60, 300, 40], [0] * 4, 16, seed=13)
     q = torch.randn(4, 12, 128, generator=step.gen).half()
