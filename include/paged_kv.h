@@ -645,7 +645,10 @@ int paged_kv_tree_commit(void* k_pool, void* v_pool, const int32_t* block_tables
  *              max_seq_len: entry t belongs to the token in the row's slot t.
  *
  * Three calls: paged_attention_decode_weights and paged_attention_prefill_weights
- * add to the sums, paged_kv_evict drops the tokens whose sums are lowest.
+ * add to the sums, paged_kv_evict drops the tokens whose sums are lowest.  Their grids, and
+ * which kernel runs, follow from max_seq_len, since the lengths are on the device: pass the
+ * bound that holds at the call (the budget and what a row takes until its next eviction), not
+ * all that its table could hold.
  */
 
 /*

@@ -180,17 +180,17 @@ __device__ __forceinline__ void scores_of(float (&s)[4], const unsigned char* da
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = c0[i] + c1[i];
 }
-// O^T += V^T P^T; tile mt's rows g and g + 8 are the dims 16 mt + g and 16 mt + 8 + g, or, of
-// codes, 16 g + 2 mt and 16 g + 2 mt + 1.
-// P: pb, and qb, what rounding left of it, of any sign: it is multiplied by values that are finite, so that an infinite
-// one stays what pb makes of it.  The values of tokens from `valid` on are taken for zeros (their slots may hold
-// anything).
 // Both halves, infinities as the largest finite number of their sign.
 __device__ __forceinline__ uint32_t finite2(uint32_t x) {
     uint32_t y;
     asm("min.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7bff7bffu));
     return y;
 }
+// O^T += V^T P^T; tile mt's rows g and g + 8 are the dims 16 mt + g and 16 mt + 8 + g, or, of
+// codes, 16 g + 2 mt and 16 g + 2 mt + 1.
+// P: pb, and qb, what rounding left of it, of any sign: it is multiplied by values that are finite, so that an infinite
+// one stays what pb makes of it.  The values of tokens from `valid` on are taken for zeros (their slots may hold
+// anything).
 template <bool kFp8>
 __device__ __forceinline__ void add_values(float (&o)[8][4], const unsigned char* data, uint32_t at, uint32_t pb0,
                                            uint32_t pb1, uint32_t qb0, uint32_t qb1, int valid, int lane) {
